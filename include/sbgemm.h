@@ -81,9 +81,11 @@ typedef enum {
                                        or its span leaves its allocation */
     SBGEMM_ERR_DEVICE_CHECK = 8     /* a kernel's own check found an input it
                                        could not use (a paged block id or
-                                       sequence length out of range; a debug
-                                       build's out-of-span address) and skipped
-                                       it; see sbgemm_device_status */
+                                       sequence length out of range; a page
+                                       request that is not valid or finds no
+                                       free page; a debug build's out-of-span
+                                       address) and skipped it; see
+                                       sbgemm_device_status */
 } sbgemm_status;
 
 /* Arithmetic of sbgemm_options.math. */
@@ -341,6 +343,172 @@ SBGEMM_API int sbgemm_attention_paged(const float* Q, int64_t rsQ, int64_t csQ, 
                                       float alpha, int causal, int64_t q_len, void* stream,
                                       const sbgemm_options* opt);
 
+/* ---- 16-bit serving operators ------------------------------------------------
+ * Operands below are arrays of 16-bit floats; strides count ELEMENTS (signed
+ * 64-bit) as above.  Products are exact, sums and softmax statistics are fp32,
+ * and each output is rounded once, to nearest even. */
+enum {
+    SBGEMM_TYPE_BF16 = 1,
+    SBGEMM_TYPE_FP16 = 2
+};
+
+/* The strided batched product of sbgemm on 16-bit operands:
+ *     C[b] <- alpha * A[b] * B[b] (+ C[b]),  A, B and C of `type`.
+ * Arguments, edge cases and errors as sbgemm (pointers 2-byte aligned;
+ * SBGEMM_ERR_INVALID_VALUE also for an unknown type).  Operands that a tensor
+ * map can describe (a unit stride, 16-byte aligned base and other strides) run
+ * on the tensor cores; every other layout runs a CUDA-core kernel with the
+ * same sums in another order. */
+SBGEMM_API int sbgemm_half(int type, const void* A, int64_t rsA, int64_t csA, int64_t bsA,
+                           const void* B, int64_t rsB, int64_t csB, int64_t bsB,
+                           void* C, int64_t rsC, int64_t csC, int64_t bsC,
+                           int64_t M, int64_t N, int64_t K, int64_t batch,
+                           float alpha, int accumulate, void* stream);
+
+/* Latent attention, absorbed form, over a paged cache.  The cache keeps one
+ * row a token for all heads, [c (R) | k_rope (P)]; a head's key is W_uk c with
+ * k_rope beside it and its value W_uv c.  With W_uk absorbed into the query
+ * (q_lat = W_uk^T q_nope, see sbgemm_half) the scores and the average need c
+ * alone, and W_uv is applied to the average afterwards:
+ *     O[s,t,h,:] = sum_n p_n c_n,  p = softmax_n(alpha * Q[s,t,h,:] . row_n)
+ * over the keys n < len(s) and, when causal, n <= len(s) - q_len + t: the
+ * q_len query tokens are a sequence's last ones (1 in a decode step, more with
+ * drafted tokens).  A query with no key gives zeros.
+ *   Q[s,t,h,:]   Q + s*bsQ + t*tsQ + h*hsQ, R + P contiguous elements
+ *   O[s,t,h,:]   alike, R contiguous elements
+ *   cache        page j, row i at cache + j*psC + i*rsC, R + P contiguous
+ *   block_table  int32 [n_seqs][max_blocks]; seq_lens int32 [n_seqs] (0..N) or
+ *                NULL for N everywhere; N <= max_blocks * block_size
+ * Rows of the cache past a sequence's end are not read.  A block id outside
+ * [0, num_blocks) reads as zero rows and a length outside [0, N] is clamped;
+ * either makes the next sbgemm_device_status return SBGEMM_ERR_DEVICE_CHECK
+ * (code 10).  NaN or infinity in a row that some queries of a 64-key block
+ * mask and others do not may reach all of the block's queries.
+ * R = 128, 256, 384 or 512 with P <= 64 a multiple of 8 and 16-byte aligned
+ * bases and strides run on the tensor cores; other sizes up to R <= 512, R + P
+ * <= 640 and other alignments run a slower kernel.  opt->workspace
+ * (sbgemm_latent_workspace_bytes) lets the keys of a sequence be split over
+ * the whole GPU; without it one CTA takes a sequence's every 64 query rows.
+ * The results depend on the split, and so on the lengths of all sequences,
+ * in their rounding only, and repeat from run to run.  Of `opt` only the
+ * workspace is read; force_path must be AUTO.  Errors as
+ * sbgemm_attention_paged.  Asynchronous; allocates nothing. */
+SBGEMM_API int sbgemm_latent_attention_paged(
+    int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t bsQ,
+    const void* cache, int64_t rsC, int64_t psC, int64_t num_blocks, int64_t block_size,
+    const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+    void* O, int64_t hsO, int64_t tsO, int64_t bsO,
+    int64_t q_len, int64_t heads, int64_t N, int64_t R, int64_t P, int64_t n_seqs,
+    float alpha, int causal, void* stream, const sbgemm_options* opt);
+
+/* Workspace with which sbgemm_latent_attention_paged splits keys freely. */
+SBGEMM_API int sbgemm_latent_workspace_bytes(int device, size_t* bytes);
+
+/* Latent attention, expanded form: every head's keys and values made from the
+ * latents beforehand (one sbgemm_half of the latents with W_uk and W_uv), the
+ * rope part of the keys shared by all heads.  Sequences are packed one behind
+ * the other: sequence s has the queries q_starts[s] .. q_starts[s+1]-1 and the
+ * keys k_starts[s] .. k_starts[s+1]-1 (int32 [n_seqs + 1] on the device).
+ *     O[i,h,:] = sum_n p_n V[n,h,:],
+ *     p = softmax_n(alpha * (Q[i,h,:Dn] . K_nope[n,h,:] + Q[i,h,Dn:] . K_rope[n,:]))
+ * over the sequence's keys and, when causal, its first key_count - query_count
+ * + (i - q_start) + 1 of them.  A query with no key gives zeros; rows of O
+ * that belong to no sequence are left as they were.
+ *   Q[i,h,:] = Q + i*tsQ + h*hsQ (Dn + P contiguous); K_nope[n,h,:] (Dn),
+ *   V[n,h,:] (Dv) and O[i,h,:] (Dv) alike; K_rope[n,:] = K_rope + n*tsR (P;
+ *   may be NULL when P == 0)
+ *   total_q, total_k: rows of Q / O and of the keys; max_q: the most queries
+ *   of a sequence
+ * Starts that decrease, leave [0, total] or hold more than max_q queries are
+ * clamped and reported as code 10 (sbgemm_device_status).  NaN or infinity in
+ * V of a key that some queries of a 128-query block mask and others do not may
+ * reach all of the block's queries.  Dn and Dv <= 128, P <= 64, all multiples
+ * of 8, with 16-byte aligned bases and strides run on the tensor cores; other
+ * sizes up to Dn + P <= 640 and Dv <= 512 a slower kernel.  Errors as
+ * sbgemm_attention_paged.  Asynchronous; allocates nothing. */
+SBGEMM_API int sbgemm_latent_attention(
+    int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t total_q,
+    const void* K_nope, int64_t hsK, int64_t tsK, const void* K_rope, int64_t tsR,
+    const void* V, int64_t hsV, int64_t tsV, int64_t total_k,
+    const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int64_t max_q,
+    void* O, int64_t hsO, int64_t tsO,
+    int64_t heads, int64_t Dn, int64_t P, int64_t Dv, float alpha, int causal, void* stream);
+
+/* A pool of pages and the sequences that hold them, all in device memory.
+ * Page j of cache i is the page_bytes[i] bytes from caches[i] + j *
+ * page_bytes[i], block_size equal rows, so the caches of sbgemm_attention_paged
+ * and sbgemm_latent_attention_paged alike (one cache a layer, or one for K and
+ * one for V).  Sequence s holds the pages block_table[s][0 .. ceil(seq_lens[s]
+ * / block_size) - 1]; ref_counts[j] counts the holders of page j, 0 = free.
+ * The operations below run on `stream` as kernels, with no copy to the host
+ * and no synchronisation, give the same result every time, and take the free
+ * page with the lowest index first.  Requests they cannot serve are left out
+ * whole and make the next sbgemm_device_status return
+ * SBGEMM_ERR_DEVICE_CHECK: code 11 for one that is not valid, 12 when no page
+ * was left.  Two operations on one pool need the same stream (or events). */
+enum { SBGEMM_MAX_CACHES = 64 };
+typedef struct {
+    void* const* caches;         /* host array of n_caches device pointers,
+                                    16-byte aligned */
+    const int64_t* page_bytes;   /* host array; positive; page_bytes / block_size
+                                    a whole multiple of 16 */
+    int64_t n_caches;            /* 0 .. SBGEMM_MAX_CACHES */
+    int64_t num_blocks, block_size;
+    int32_t* ref_counts;         /* [num_blocks] */
+    int32_t* block_table;        /* [n_seqs][max_blocks] */
+    int64_t n_seqs, max_blocks;
+    int32_t* seq_lens;           /* [n_seqs] */
+} sbgemm_page_pool;
+
+/* Bytes of workspace (opt->workspace) for any operation on such a pool with up
+ * to n requests (pairs, forks or sequences). */
+SBGEMM_API int sbgemm_pages_workspace_bytes(int64_t num_blocks, int64_t n_seqs, int64_t n, size_t* bytes);
+
+/* Copies page pairs[k][0] to page pairs[k][1] in every cache, k < n (int32
+ * [n][2]).  The bookkeeping is not touched and may be NULL.  A pair is not
+ * valid if an id is out of range, if an earlier pair has the same destination,
+ * or if its source is the destination of another pair. */
+SBGEMM_API int sbgemm_pages_copy(const sbgemm_page_pool* pool, const int32_t* pairs, int64_t n,
+                                 void* stream, const sbgemm_options* opt);
+
+/* Forks: sequence children[k] becomes a copy of sequence parents[k] as it was
+ * before the call.  Full pages are shared (their counts raised); the rows of a
+ * last page that is not full are copied into a fresh page, so that parent and
+ * child can both be appended to.  Not valid: an index out of range, a child
+ * that holds tokens, is also a parent, or is an earlier request's child, a
+ * parent whose length or last page is out of range.  (A shared page's id that
+ * is out of range is carried over as it is, and reported.)  Requests are
+ * granted in order while fresh pages last; those from the first one on that
+ * the pool cannot serve are refused. */
+SBGEMM_API int sbgemm_pages_fork(const sbgemm_page_pool* pool, const int32_t* parents, const int32_t* children,
+                                 int64_t n, void* stream, const sbgemm_options* opt);
+
+/* Appends rows: sequence seqs[k] grows by the tokens starts[k] ..
+ * starts[k+1]-1 (int32 [n + 1]) of `rows`, which holds `total` tokens for each
+ * cache: token j's row in cache i is at rows[i] + j * row_stride[i] bytes (host
+ * arrays of n_caches; 16-byte aligned, strides multiples of 16).  Fresh pages
+ * are taken as needed.  Not valid: an index out of range, a sequence that an
+ * earlier request has, more tokens than max_blocks pages hold, a last page
+ * that is not full and not the sequence's alone; starts that decrease or leave
+ * [0, total] make every request not valid.  Granted in order while pages
+ * last, as in sbgemm_pages_fork. */
+SBGEMM_API int sbgemm_pages_append(const sbgemm_page_pool* pool, const int32_t* seqs, const int32_t* starts,
+                                   int64_t n, const void* const* rows, const int64_t* row_stride, int64_t total,
+                                   void* stream, const sbgemm_options* opt);
+
+/* Frees sequences: the counts of their pages fall by one and their lengths
+ * become 0 (their table rows stay as they were).  A sequence given twice is
+ * freed once.  Not valid: an index out of range; a page out of range or not in
+ * use is left out.  The caches may be NULL (n_caches == 0). */
+SBGEMM_API int sbgemm_pages_free(const sbgemm_page_pool* pool, const int32_t* seqs, int64_t n, void* stream);
+
+/* Compacts the pool: with U pages in use, the k-th page in use at an index >=
+ * U moves to the k-th free index < U, in every cache, with its count and every
+ * sequence's table entry; afterwards the pages 0 .. U-1 are in use.  *moved
+ * (device, may be NULL) receives the number of pages moved. */
+SBGEMM_API int sbgemm_pages_compact(const sbgemm_page_pool* pool, int32_t* moved, void* stream,
+                                    const sbgemm_options* opt);
+
 /* Validate and plan without launching or touching device memory: reports the
  * layout classes and the kernel path, tile and CTA count that sbgemm_ex would
  * use.  Pointers are only checked for NULL and alignment (no device query). */
@@ -404,12 +572,13 @@ SBGEMM_API int sbgemm_noalloc(const float* A, int64_t rsA, int64_t csA, int64_t 
  * bounded in-kernel wait gives up or a device-side check skips an input
  * (after synchronising `stream`; the first code recorded is kept).  Returns
  * SBGEMM_OK, SBGEMM_ERR_DEVICE_TIMEOUT (codes 1-8) or SBGEMM_ERR_DEVICE_CHECK
- * (codes 9-10); *where_out (may be NULL) receives the code (0 if none): 1 a
+ * (codes 9-12); *where_out (may be NULL) receives the code (0 if none): 1 a
  * loaded stage, 2 a released stage, 3 copies in flight at exit, 4 the MMAs of
  * a tile, 5 a free accumulator, 6 a stream-K partial sum, 7 / 8 the
  * self-test's mbarrier / flag, 9 an address outside its operand's span (debug
  * builds only; the access was skipped), 10 a paged-attention block id or
- * sequence length out of range. */
+ * sequence length (or a packed sequence's start) out of range, 11 a page
+ * request that is not valid, 12 one that found no free page. */
 SBGEMM_API int sbgemm_device_status(void* stream, int* where_out);
 
 /* Failure-detection self-test (a diagnostic of the library, not part of the

@@ -29,6 +29,10 @@ __all__ = [
     "ACT_NONE", "ACT_RELU", "ACT_SIGMOID", "ACT_SILU", "ACT_GELU_TANH", "ACT_GELU_ERF",
     "ACTIVATIONS", "KSPLIT_ANY", "KSPLIT_EXACT", "KSPLIT_NONE", "STREAM_K_NONE",
     "STREAM_K_CHAINED", "STREAM_K_PIECES", "NOALLOC_SCRATCH_BYTES",
+    "TYPE_BF16", "TYPE_FP16", "MAX_CACHES", "sbgemm_half", "sbgemm_latent_attention_paged",
+    "sbgemm_latent_attention", "sbgemm_latent_workspace_bytes", "sbgemm_pages_workspace_bytes",
+    "matmul_half", "latent_attention_paged", "latent_attention", "pages_copy", "pages_fork",
+    "pages_append", "pages_free", "pages_compact",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,7 +60,13 @@ PATH_NAMES = {PATH_NONE: "none", PATH_GATHER_FFMA: "gather_ffma",
 EXPORTED_SYMBOLS = ("sbgemm", "sbgemm_ex", "sbgemm_fused", "sbgemm_attention",
                     "sbgemm_attention_ex", "sbgemm_attention_paged", "sbgemm_plan",
                     "sbgemm_workspace_bytes", "sbgemm_noalloc", "sbgemm_selftest",
-                    "sbgemm_device_status", "sbgemm_status_string", "sbgemm_version")
+                    "sbgemm_device_status", "sbgemm_status_string", "sbgemm_version",
+                    "sbgemm_half", "sbgemm_latent_attention_paged", "sbgemm_latent_workspace_bytes",
+                    "sbgemm_latent_attention", "sbgemm_pages_workspace_bytes", "sbgemm_pages_copy",
+                    "sbgemm_pages_fork", "sbgemm_pages_append", "sbgemm_pages_free",
+                    "sbgemm_pages_compact")
+TYPE_BF16, TYPE_FP16 = 1, 2
+MAX_CACHES = 64
 ACT_NONE, ACT_RELU, ACT_SIGMOID, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2, 3, 4, 5
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "sigmoid": ACT_SIGMOID, "silu": ACT_SILU,
                "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF}
@@ -159,6 +169,7 @@ def load(path: str = LIB_PATH):
         lib.sbgemm_status_string.argtypes = [ctypes.c_int]
         lib.sbgemm_version.restype = ctypes.c_int
         lib.sbgemm_version.argtypes = []
+        _serving.declare(lib)
         global _fast
         try:
             from . import _fastcall
@@ -461,3 +472,11 @@ def linear_backward(G, X, W, dX, dW, accumulate_dW: bool = False, stream=None,
     matmul(G.t(), X, dW, accumulate=accumulate_dW, math=math, stream=stream, workspace=workspace,
            k_split=k_split)
     return dX, dW
+
+
+# The 16-bit serving operators (their own file; the same library).
+from . import serving as _serving  # noqa: E402
+from .serving import (  # noqa: E402,F401
+    latent_attention, latent_attention_paged, matmul_half, pages_append, pages_compact,
+    pages_copy, pages_fork, pages_free, sbgemm_half, sbgemm_latent_attention,
+    sbgemm_latent_attention_paged, sbgemm_latent_workspace_bytes, sbgemm_pages_workspace_bytes)

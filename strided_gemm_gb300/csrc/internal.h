@@ -22,6 +22,8 @@ enum : unsigned int {
     kWaitSelftestFlag = 8,   // self-test: a global flag nothing sets
     kBoundsViolation = 9,    // debug build: an access outside its operand's span (skipped)
     kPagedInput = 10,        // paged attention: a block id or sequence length out of range (skipped)
+    kPageRequest = 11,       // page operations: a request that is not valid (left out)
+    kPageExhausted = 12,     // page operations: no free page left for a request (left out)
 };
 
 // Element offsets [lo, hi] from an operand's base pointer that lie inside the

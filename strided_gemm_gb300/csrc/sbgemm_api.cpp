@@ -17,6 +17,7 @@
 #include "attention_tc.h"
 #include "internal.h"
 #include "sbgemm.h"
+#include "serving.h"
 
 namespace sbg {
 
@@ -730,16 +731,17 @@ int sbgemm_device_status(void* stream, int* where_out) {
     const unsigned int code_g = read_and_clear_status_gather(s);
     const unsigned int code_a = read_and_clear_status_attention(s);
     const unsigned int code_d = read_and_clear_status_attention_decode(s);
+    const unsigned int code_s = read_and_clear_status_serving(s);
     if (code == 0) code = code_tc;
     if (code == 0) code = code_st;
     if (code == 0) code = code_at;
     if (code == 0) code = code_g;
     if (code == 0) code = code_a;
     if (code == 0) code = code_d;
+    if (code == 0) code = code_s;
     if (code != 0) {
         if (where_out) *where_out = (int)code;
-        return (code == kBoundsViolation || code == kPagedInput) ? SBGEMM_ERR_DEVICE_CHECK
-                                                                  : SBGEMM_ERR_DEVICE_TIMEOUT;
+        return code >= kBoundsViolation ? SBGEMM_ERR_DEVICE_CHECK : SBGEMM_ERR_DEVICE_TIMEOUT;
     }
     return SBGEMM_OK;
 }
