@@ -50,8 +50,8 @@ bool device_allocation_range(const void* ptr, uintptr_t* base, size_t* size) {
 
 namespace {
 
-bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                 const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
     std::call_once(g_once, load_entry_points);
     if (!g_encode_tiled || rank < 1 || rank > 5) return false;
     cuuint64_t gdim[5], gstride[4];
@@ -62,7 +62,7 @@ bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_
         estride[i] = 1;
         if (i + 1 < rank) gstride[i] = strides_bytes[i];
     }
-    CUresult r = g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (cuuint32_t)rank, const_cast<void*>(base),
+    CUresult r = g_encode_tiled(map, type, (cuuint32_t)rank, const_cast<void*>(base),
                                 gdim, gstride, bdim, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -70,7 +70,17 @@ bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rank, dims, strides_bytes, box, swizzle128);
+}
+
 }  // namespace
+
+bool encode_tmap_16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box) {
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box, true);
+}
 
 bool encode_tmap_f32_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
                         const uint64_t strides_bytes[2], const uint32_t box[3], bool swizzle128) {

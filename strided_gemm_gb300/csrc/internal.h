@@ -197,5 +197,9 @@ bool encode_tmap_f32_3d(CUtensorMap* map, const void* base, const uint64_t dims[
 // The same with rank 4 (byte strides of dims 1, 2 and 3).
 bool encode_tmap_f32_4d(CUtensorMap* map, const void* base, const uint64_t dims[4],
                         const uint64_t strides_bytes[3], const uint32_t box[4], bool swizzle128);
+// A 16-bit map of any rank (the element type does not matter to a copy) with
+// 128-byte swizzled boxes.
+bool encode_tmap_16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace sbg

@@ -21,6 +21,9 @@ struct HalfProblem {
 };
 // Any layout, on the CUDA cores (half_gather.cu).
 cudaError_t launch_half_gather(const HalfProblem& p, cudaStream_t stream);
+// On the tensor cores (half_tc.cu); false if the layout has no tensor maps.
+bool launch_half_tc(const HalfProblem& p, int sms, cudaStream_t stream, cudaError_t* err);
+unsigned int read_and_clear_status_half_tc(cudaStream_t stream);
 
 // Latent attention over a paged cache (sbgemm_latent_attention_paged).
 struct LatentPaged {

@@ -209,7 +209,8 @@ int check_pool_memory(const PoolView& v, std::initializer_list<Bytes> inputs, co
 }  // namespace
 
 unsigned int read_and_clear_status_serving(cudaStream_t stream) {
-    const unsigned int codes[] = {read_and_clear_status_latent_rows(stream), read_and_clear_status_pages(stream)};
+    const unsigned int codes[] = {read_and_clear_status_half_tc(stream),
+                                  read_and_clear_status_latent_rows(stream), read_and_clear_status_pages(stream)};
     for (unsigned int c : codes)
         if (c) return c;
     return 0;
@@ -241,11 +242,14 @@ int sbgemm_half(int type, const void* A, int64_t rsA, int64_t csA, int64_t bsA,
     if (K == 0 && accumulate) return SBGEMM_OK;
     const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
     if (M >= kInt || N >= kInt || K >= kInt || tiles >= kInt) return SBGEMM_ERR_UNSUPPORTED;
-    if (!current_sms()) return SBGEMM_ERR_CUDA;
+    const int sms = current_sms();
+    if (!sms) return SBGEMM_ERR_CUDA;
     const int m = K > 0 ? in_device_memory({sa, sb, sc}) : in_device_memory({sc});
     if (m) return m;
     const HalfProblem p{type, A, rsA, csA, bsA, B, rsB, csB, bsB, C, rsC, csC, bsC,
                         M, N, K, batch, alpha, accumulate};
+    cudaError_t e = cudaSuccess;
+    if (launch_half_tc(p, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_half_gather(p, static_cast<cudaStream_t>(stream)));
 }
 
