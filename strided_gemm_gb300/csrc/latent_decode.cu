@@ -1,0 +1,806 @@
+// Latent attention over a paged cache on the tensor cores (absorbed form, see
+// sbgemm_latent_attention_paged): every head of a sequence reads the same rows
+// [c | k_rope], as keys whole and as values without their rope part.
+//
+// A unit of work is a block of 64 keys of one sequence for NB query rows
+// (token, head) of it, NB = 16, 32 or 64.  The products are computed
+// transposed, keys and latents along the MMA's M and query rows along its N,
+// so that a few heads waste nothing and the one copy of the rows in shared
+// memory serves both:
+//   S^T = K Q^T      M: keys (64 of the MMA's 128 lanes), N = NB, K = R + P,
+//                    A = the rows, K-major; B = the queries
+//   O^T += C^T P^T   M: 128 latents a tile, N = NB, K = 64 keys,
+//                    A = the same rows read MN-major; B = P^T, written by the
+//                    softmax as rows of NB weights a key
+// O^T stays in TMEM (R / 128 tiles of NB columns) over all blocks of a
+// sequence.  The softmax keeps a reference maximum a query row, raised only
+// when a score exceeds it by a factor of 2^8 (then O^T, the sums and the
+// reference are scaled, by all eight warps); P is rounded to the operands'
+// type for the MMA and summed before it in fp32.  Weights up to 2^8 of either
+// type lose nothing by it; in fp16 one below 2^-14 keeps an absolute 2^-25.
+//
+// Work is spread as one list of blocks over the CTAs (one an SM), each CTA an
+// equal run of it that may begin and end inside a sequence.  A sequence that
+// lies in one CTA is written out at once; the pieces of others go to the
+// workspace as (maximum, sum, unnormalised O) in fp32, and a second launch
+// joins them in order.  The lists depend on the lengths alone, which the
+// device knows; no result depends on timing.
+//
+// Roles (12 warps, warp 3 idle): warps 0 and 1 load the rows of even and odd
+// blocks by 16-byte cp.async, each row's page looked up in the table, past the
+// end and for bad pages zeros instead of a read (so nothing there can reach a
+// result); warp 2 issues the MMAs, the scores of block j + 1 before P V of
+// block j when its rows are there in time; warps 4-11 the softmax (the four of
+// them that own the 64 key lanes), rescaling, queries and output.  Every wait
+// is bounded.
+//
+// Bound: few heads by the cache's bytes; 128 heads (two CTAs on the same
+// blocks at the same time, the second read hitting L2) by the MMAs, whose
+// operands come from shared memory.
+#include <algorithm>
+#include <atomic>
+
+#include "serving.h"
+#include "tc16.cuh"
+
+namespace sbg {
+namespace {
+
+constexpr int BT = 64;                       // keys per block
+constexpr int kStages = 2;
+constexpr int kMmaWarp = 2, kMathWarp = 4, kMathWarps = 8, kWarps = 12;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxChunks = 9;                // 64-wide pieces of a row: R <= 512 and the rope part
+constexpr int kMaxTiles = 4;                 // R / 128
+constexpr int kChunkBytes = BT * 128;        // a piece of a block: 64 rows of 128 swizzled bytes
+constexpr float kRaise = 8.0f;               // log2 headroom before the reference maximum rises
+__device__ unsigned int g_wait_status = 0;
+
+// A sequence that begins in a CTA and ends in a later one: its first piece is
+// in `slot`, the others in slot 0 of the CTAs behind, up to member `last`.
+struct Join { int32_t seq, slot, member, last; };    // seq < 0: none begins here
+
+struct Params {
+    const void* Q; int64_t hsQ, tsQ, bsQ;
+    const void* cache; int64_t rsC, psC;
+    const int32_t* table; const int32_t* seq_lens;
+    void* O; int64_t hsO, tsO, bsO;
+    int64_t max_blocks;
+    int num_blocks, block_size;
+    int q_len, heads, rows, N, R, P, n_seqs;
+    int chunks, rope_steps;                  // 64-wide pieces of a row; MMA K steps of the rope piece
+    int groups, per_group;                   // query-row groups; CTAs for each
+    int split;                               // sequences may be split (workspace given)
+    float scale_log2;
+    int causal;
+    uint32_t idesc_s, idesc_o;
+    Join* joins;                             // [groups * per_group]
+    float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
+};
+
+template <int NB>
+struct Ctl {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t q_full, s_full[2], p_full, pv_done, o_free, done;
+    uint32_t tmem_base;
+    int seq0, tile0, count;                  // this CTA's run of the list
+    int scan[kWarps];
+    float ref[NB], factor[NB];               // reference maxima; a rise's factors, then 1 / sum
+    union {
+        float part[2][NB];                   // maxima or sums of the two key quarters
+        int64_t out[NB];                     // element offset of a row of O (-1: none)
+    };
+    int limit[NB];                           // last key a row sees
+};
+
+template <int NB>
+constexpr size_t smem_bytes(int chunks) {
+    return (size_t)chunks * (NB * 128 + kStages * kChunkBytes) + kChunkBytes + sizeof(Ctl<NB>) + 1024;
+}
+
+// A vote and barrier of the eight math warps.
+__device__ __forceinline__ bool math_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\t"
+        "barrier.cta.red.or.pred b, 1, 256, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r) : "r"((uint32_t)v) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ int seq_len(const Params& p, int s, bool report) {
+    if (!p.seq_lens) return p.N;
+    const int n = p.seq_lens[s];
+    if (n >= 0 && n <= p.N) return n;
+    if (report) record_status(&g_wait_status, kPagedInput);
+    return n < 0 ? 0 : p.N;
+}
+// Blocks a sequence counts for in the list: an empty one has its zeros to write.
+__device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + BT - 1) / BT : 1; }
+
+// A CTA's walk over its run: pieces of sequences in order.
+struct Walk {
+    int seq, tile, left;     // the next piece begins at block `tile` of `seq`; units left
+    int len, j0, j1;         // the piece: blocks j0 .. j1 - 1 of a sequence of `len` keys
+    int s, units;            // its sequence and that one's units
+    __device__ __forceinline__ bool next(const Params& p, bool report = false) {
+        if (left <= 0 || seq >= p.n_seqs) return false;
+        s = seq;
+        len = seq_len(p, s, report);
+        units = units_of(len);
+        j0 = tile;
+        const int n = min(units - tile, left);
+        j1 = len > 0 ? j0 + n : j0;
+        left -= n;
+        tile += n;
+        if (tile >= units) {
+            seq += p.split ? 1 : p.per_group;
+            tile = 0;
+        }
+        return true;
+    }
+};
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
+    constexpr int CPW = NB / 2;              // score columns of a softmax warp
+    constexpr uint32_t kColO = 0, kColS = kMaxTiles * NB;
+    static_assert(kColS + 2 * NB <= 512, "TMEM columns");
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sq = base;                                      // queries: [chunk][NB rows][128 bytes]
+    uint8_t* skv = sq + p.chunks * (NB * 128);               // rows: [stage][chunk][64][128]
+    uint8_t* sp = skv + kStages * p.chunks * kChunkBytes;    // weights: [64 keys][128 bytes]
+    Ctl<NB>& c = *reinterpret_cast<Ctl<NB>*>(sp + kChunkBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = blockIdx.x % p.groups, member = blockIdx.x / p.groups;
+    const int tiles_o = p.R / 128;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&c.full[i], 1);
+            mbar_init(&c.empty[i], 1);
+        }
+        mbar_init(&c.q_full, kMathWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&c.s_full[i], 1);
+        mbar_init(&c.p_full, kMathWarps);
+        mbar_init(&c.pv_done, 1);
+        mbar_init(&c.o_free, kMathWarps);
+        mbar_init(&c.done, 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&c.tmem_base, 512);
+        tmem_relinquish();
+    }
+
+    // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
+    int members = 1, lo = 0, units_total = 0;
+    if (p.split) {
+        int sum = 0;
+        for (int s = tid; s < p.n_seqs; s += kThreads) sum += units_of(seq_len(p, s, false));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) c.scan[warp] = sum;
+        __syncthreads();
+        int total = 0;
+        for (int w = 0; w < kWarps; ++w) total += c.scan[w];
+        // No CTA between a sequence's first and last one is empty.
+        members = min(p.per_group, total);
+        lo = member < members ? (int)((int64_t)member * total / members) : 0;
+        const int hi = member < members ? (int)((int64_t)(member + 1) * total / members) : 0;
+        units_total = total;
+        if (tid == 0) c.count = hi - lo;
+        int before = 0;                      // units of the sequences of earlier rounds
+        for (int s0 = 0; s0 < p.n_seqs && before <= lo; s0 += kThreads) {
+            const int s = s0 + tid;
+            const int u = s < p.n_seqs ? units_of(seq_len(p, s, false)) : 0;
+            int inc = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += v;
+            }
+            __syncthreads();
+            if (lane == 31) c.scan[warp] = inc;
+            __syncthreads();
+            int at = before, round = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) at += c.scan[w];
+                round += c.scan[w];
+            }
+            at += inc - u;
+            if (u && lo >= at && lo < at + u) {
+                c.seq0 = s;
+                c.tile0 = lo - at;
+            }
+            before += round;
+        }
+        if (tid == 0 && hi == lo) c.seq0 = c.tile0 = 0;
+    } else if (tid == 0) {
+        c.seq0 = member;
+        c.tile0 = 0;
+        c.count = INT32_MAX;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem_base;
+    Walk w{c.seq0, c.tile0, c.count};
+
+    if (warp < kStages) {
+        // ---- rows of the cache into shared memory ---------------------------------
+        const int st = warp;                 // this warp's stage
+        const int r0 = lane >> 3, piece = lane & 7;
+        const uint32_t stage = smem_u32(skv) + st * p.chunks * kChunkBytes;
+        const char* cache = static_cast<const char*>(p.cache);
+        const int row_pieces = (p.R + p.P) / 8;
+        int i = 0;                           // blocks so far, over all pieces
+        bool ok = true;
+        while (ok && w.next(p)) {
+            const int32_t* table = p.table + w.s * p.max_blocks;
+            for (int j = w.j0; j < w.j1; ++j, ++i) {
+                if ((i & 1) != st) continue;
+                // The rows' places first: their table entries arrive while the stage drains.
+                const char* src[BT / 4];
+#pragma unroll
+                for (int g = 0; g < BT / 4; ++g) {
+                    const int n = j * BT + r0 + 4 * g;
+                    src[g] = nullptr;
+                    if (n < w.len) {
+                        const int page = table[n / p.block_size];
+                        if (page >= 0 && page < p.num_blocks)
+                            src[g] = cache + 2 * (page * p.psC + (n % p.block_size) * p.rsC) + piece * 16;
+                        else
+                            record_status(&g_wait_status, kPagedInput);
+                    }
+                }
+                if (i >= kStages && !mbar_wait(&c.empty[st], (uint32_t)((i / kStages - 1) & 1))) {
+                    record_status(&g_wait_status, kWaitEmpty);
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int g = 0; g < BT / 4; ++g) {
+                    const int r = r0 + 4 * g;
+                    const uint32_t dst = stage + r * 128 + ((piece ^ (r & 7)) << 4);
+                    for (int k = 0; k < p.chunks; ++k) {
+                        const bool read = src[g] != nullptr && k * 8 + piece < row_pieces;
+                        cp_async16(dst + k * kChunkBytes, read ? src[g] + k * 128 : cache, read);
+                    }
+                }
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.full[st]);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- MMAs ------------------------------------------------------------------
+        if (lane == 0) {
+            const uint32_t q_lo = smem_u32(sq), kv_lo = smem_u32(skv), p_lo = smem_u32(sp);
+            const uint32_t stage_bytes = p.chunks * kChunkBytes;
+            int i = 0, filled = 0;           // blocks and pieces with blocks so far
+            bool ok = true;
+            auto scores = [&](int b) {       // S^T of block number b
+                tc_fence_after();
+                const uint32_t d = tmem + kColS + (b & 1) * NB;
+                uint64_t da = desc16(kv_lo + (b & 1) * stage_bytes), dq = desc16(q_lo);
+                for (int k = 0; k < p.R / 64; ++k) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, (k | x) ? 1u : 0u);
+                    da += kChunkBytes >> 4;
+                    dq += NB * 128 >> 4;
+                }
+                for (int x = 0; x < p.rope_steps; ++x)
+                    mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, 1u);
+                mma_commit(&c.s_full[b & 1]);
+            };
+            auto timed_out = [&](unsigned int code) {
+                record_status(&g_wait_status, code);
+                ok = false;
+            };
+            while (ok && w.next(p)) {
+                const int n = w.j1 - w.j0;
+                if (n == 0) continue;        // an empty sequence
+                if (!mbar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
+                    !mbar_wait(&c.full[i & 1], (uint32_t)((i / kStages) & 1))) {
+                    timed_out(kWaitFull);
+                    break;
+                }
+                scores(i);
+                for (int j = 0; j < n && ok; ++j, ++i) {
+                    // The next block's scores as soon as its rows are there, but
+                    // this block's P V does not wait for them.
+                    bool ahead = j + 1 >= n;
+                    const uint32_t ph_next = (uint32_t)(((i + 1) / kStages) & 1);
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&c.p_full, (uint32_t)(i & 1))) {
+                        if (!ahead && mbar_try_wait(&c.full[(i + 1) & 1], ph_next)) {
+                            scores(i + 1);
+                            ahead = true;
+                        }
+                        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+                            timed_out(kWaitMma);
+                            break;
+                        }
+                    }
+                    if (!ok) break;
+                    if (j == 0 && filled > 0 && !mbar_wait(&c.o_free, (uint32_t)((filled - 1) & 1))) {
+                        timed_out(kWaitAccFree);
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t rows = kv_lo + (i & 1) * stage_bytes;
+                    for (int t = 0; t < tiles_o; ++t) {
+                        const uint64_t da = desc16(rows + 2 * t * kChunkBytes, kChunkBytes), dp = desc16(p_lo);
+#pragma unroll
+                        for (int x = 0; x < BT / 16; ++x)
+                            mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
+                                     (j | x) ? 1u : 0u);
+                    }
+                    mma_commit(&c.empty[i & 1]);
+                    mma_commit(&c.pv_done);
+                    if (!ahead) {
+                        if (!mbar_wait(&c.full[(i + 1) & 1], ph_next)) {
+                            timed_out(kWaitFull);
+                            break;
+                        }
+                        scores(i + 1);
+                    }
+                }
+                ++filled;
+            }
+            // Nothing may still be writing TMEM when it is freed.
+            mma_commit(&c.done);
+            if (!mbar_wait(&c.done, 0)) record_status(&g_wait_status, kWaitMma);
+        }
+    } else if (warp >= kMathWarp) {
+        // ---- queries, softmax, output ------------------------------------------------
+        const int m = tid - kMathWarp * 32;                  // 0 .. 255
+        const int quarter = warp & 3, half = (warp - kMathWarp) >> 2;
+        const bool active = quarter < 2;                     // owns key lanes 32 quarter .. + 31
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int row_pieces = (p.R + p.P) / 8;
+        int i = 0, piece_no = 0, used = 0;                   // blocks, pieces, units so far
+        bool ok = true;
+        Join join{-1, 0, 0, 0};
+        while (w.next(p, group == 0)) {
+            const int n = w.j1 - w.j0;
+            // The rows of this group: where they go and what they see.
+            if (m < NB) {
+                const int r = group * NB + m, t = r / p.heads;
+                c.limit[m] = r < p.rows && p.causal ? w.len - p.q_len + t : w.len - 1;
+                c.ref[m] = -INFINITY;
+            }
+            if (n > 0) {
+                for (int x = m; x < NB * p.chunks * 8; x += 256) {
+                    const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
+                    const int gr = group * NB + r, t = gr / p.heads, h = gr % p.heads;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (gr < p.rows && k < row_pieces)
+                        v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + w.s * p.bsQ + t * p.tsQ +
+                                                            h * p.hsQ + k * 8);
+                    *reinterpret_cast<uint4*>(sq + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.q_full);
+            }
+            math_sync();
+
+            float l[CPW];
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) l[x] = 0.0f;
+            bool failed = false;
+            for (int j = 0; j < n; ++j, ++i) {
+                if (!mbar_wait(&c.s_full[i & 1], (uint32_t)((i >> 1) & 1))) {
+                    record_status(&g_wait_status, kWaitMma);
+                    ok = false;
+                }
+                tc_fence_after();
+                float a[CPW];
+                bool rise = false;
+                if (active) {
+                    tmem_ld<CPW>(tmem + lanes + kColS + (i & 1) * NB + half * CPW, a);
+                    const int key = (w.j0 + j) * BT + quarter * 32 + lane;
+                    const int safe = p.causal ? w.len - p.q_len : w.len - 1;    // keys up to here: every row's
+                    const bool all = (w.j0 + j) * BT + BT - 1 <= safe;
+#pragma unroll
+                    for (int x = 0; x < CPW; ++x) {
+                        a[x] *= p.scale_log2;
+                        if (!all && key > c.limit[half * CPW + x]) a[x] = -INFINITY;
+                        rise |= a[x] > c.ref[half * CPW + x] + kRaise;
+                    }
+                }
+                if (math_any(rise || !ok)) {
+                    if (math_any(!ok)) {
+                        failed = true;
+                        break;
+                    }
+                    // Raise the references to the block's maxima and scale what was summed.
+                    if (active) {
+#pragma unroll
+                        for (int x = 0; x < CPW; ++x) {
+                            float v = a[x];
+#pragma unroll
+                            for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+                            if (lane == 0) c.part[quarter][half * CPW + x] = v;
+                        }
+                    }
+                    math_sync();
+                    if (m < NB) {
+                        const float old = c.ref[m], top = fmaxf(old, fmaxf(c.part[0][m], c.part[1][m]));
+                        c.factor[m] = top == -INFINITY ? 1.0f : exp2f(old - top);    // 0 at the first rise
+                        c.ref[m] = top;
+                    }
+                    math_sync();
+                    if (active) {
+#pragma unroll
+                        for (int x = 0; x < CPW; ++x) l[x] *= c.factor[half * CPW + x];
+                    }
+                    if (j > 0) {
+                        if (!mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                            record_status(&g_wait_status, kWaitMma);
+                            ok = false;
+                        }
+                        tc_fence_after();
+                        constexpr int W = NB < 32 ? NB : 32;
+#pragma unroll 1
+                        for (int t = half; t < tiles_o; t += 2)
+#pragma unroll 1
+                            for (int x0 = 0; x0 < NB; x0 += W) {
+                                const uint32_t at = tmem + lanes + kColO + t * NB + x0;
+                                float o[W];
+                                uint32_t bits[W];
+                                tmem_ld<W>(at, o);
+#pragma unroll
+                                for (int x = 0; x < W; ++x) bits[x] = __float_as_uint(o[x] * c.factor[x0 + x]);
+                                tmem_st_bits<W>(at, bits);
+                            }
+                        tmem_wait_st();
+                    }
+                }
+                if (active) {
+                    uint32_t w2[CPW / 2];
+#pragma unroll
+                    for (int x = 0; x < CPW; x += 2) {
+                        const float r0 = c.ref[half * CPW + x], r1 = c.ref[half * CPW + x + 1];
+                        // A row that has seen no key yet has no reference: its weights are 0.
+                        const float p0 = ex2_approx(a[x] - (r0 == -INFINITY ? 0.0f : r0));
+                        const float p1 = ex2_approx(a[x + 1] - (r1 == -INFINITY ? 0.0f : r1));
+                        l[x] += p0;
+                        l[x + 1] += p1;
+                        w2[x / 2] = pack2<T>(p0, p1);
+                    }
+                    // The block before has read its weights.
+                    if (i > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                        record_status(&g_wait_status, kWaitMma);
+                        ok = false;
+                    }
+                    const int r = quarter * 32 + lane;
+#pragma unroll
+                    for (int x = 0; x < CPW / 8; ++x)
+                        *reinterpret_cast<uint4*>(sp + r * 128 + (((half * (CPW / 8) + x) ^ (r & 7)) << 4)) =
+                            make_uint4(w2[4 * x], w2[4 * x + 1], w2[4 * x + 2], w2[4 * x + 3]);
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.p_full);
+            }
+            if (failed) break;
+
+            // The piece is done: its sums, then O^T out of TMEM.
+            if (n > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                record_status(&g_wait_status, kWaitMma);
+                ok = false;
+            }
+            tc_fence_after();
+            if (active) {
+#pragma unroll
+                for (int x = 0; x < CPW; ++x) {
+                    float v = l[x];
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+                    if (lane == 0) c.part[quarter][half * CPW + x] = v;
+                }
+            }
+            if (math_any(!ok)) break;
+            const bool whole = w.j0 == 0 && (w.len == 0 || w.j1 == w.units);
+            // A split sequence: this CTA's first piece goes to slot 0, its last to slot 1.
+            const int slot = 2 * blockIdx.x + (piece_no > 0 ? 1 : 0);
+            float* part = p.parts + (int64_t)slot * NB * (2 + p.R);
+            if (m < NB) {
+                const float sum = c.part[0][m] + c.part[1][m];
+                c.factor[m] = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
+                if (!whole) {
+                    part[m] = c.ref[m];
+                    part[NB + m] = sum;
+                }
+            }
+            math_sync();
+            if (m < NB) {
+                const int r = group * NB + m, t = r / p.heads, h = r % p.heads;
+                c.out[m] = r < p.rows ? w.s * p.bsO + t * p.tsO + h * p.hsO : -1;
+            }
+            math_sync();
+            constexpr int W = NB < 32 ? NB : 32;
+#pragma unroll 1
+            for (int t = half; t < tiles_o; t += 2)
+#pragma unroll 1
+                for (int x0 = 0; x0 < NB; x0 += W) {
+                    float o[W];
+                    if (n > 0) tmem_ld<W>(tmem + lanes + kColO + t * NB + x0, o);
+                    const int e = t * 128 + quarter * 32 + lane;
+#pragma unroll
+                    for (int x = 0; x < W; ++x) {
+                        const float f = c.factor[x0 + x];
+                        const float v = f == 0.0f ? 0.0f : o[x] * f;       // no key: zeros
+                        if (!whole) part[2 * NB + (int64_t)(x0 + x) * p.R + e] = v;
+                        else if (c.out[x0 + x] >= 0) static_cast<T*>(p.O)[c.out[x0 + x] + e] = from_float<T>(v);
+                    }
+                }
+            if (w.j0 == 0 && !whole) {
+                // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
+                const int64_t end = (int64_t)lo + used + w.units;
+                join = Join{w.s, slot, member, (int)((end * members + units_total - 1) / units_total) - 1};
+            }
+            used += max(n, 1);
+            tc_fence_before();
+            __syncwarp();
+            if (n > 0 && lane == 0) mbar_arrive(&c.o_free);
+            math_sync();                                         // c.* is free for the next piece
+            ++piece_no;
+        }
+        if (p.split && m == 0) p.joins[blockIdx.x] = join;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the pieces of split sequences in order: with the largest maximum M of
+// a row's pieces, O = sum 2^(m - M) O_piece / sum 2^(m - M) l_piece.  Few
+// pieces: a thread takes four columns of a row over all of them, two rows of
+// 512 columns a block; many (one long sequence): eight warps share the pieces
+// of 128 columns of a row.
+constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 1024;
+
+template <typename T>
+__device__ __forceinline__ void store4(T* o, float4 v) {
+    o[0] = from_float<T>(v.x);
+    o[1] = from_float<T>(v.y);
+    o[2] = from_float<T>(v.z);
+    o[3] = from_float<T>(v.w);
+}
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+    __shared__ int list[kMaxJoins], found;
+    __shared__ float4 sums[8][32];
+    __shared__ float tops[8], ls[8];
+    // The CTAs in which split sequences begin, in order: every block has the same list.
+    const int ctas = p.groups * p.per_group;
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + threadIdx.x;
+            const bool begins = c < ctas && p.joins[c].seq >= 0;
+            const unsigned all = __ballot_sync(~0u, begins);
+            if (begins) list[n + __popc(all & ((1u << threadIdx.x) - 1))] = c;
+            n += __popc(all);
+        }
+        if (threadIdx.x == 0) found = n;
+    }
+    __syncthreads();
+    const int per_row = p.R / 4;                             // threads a row
+    const int64_t slot_floats = (int64_t)NB * (2 + p.R);
+    const int steps = (NB * per_row + kJoinThreads - 1) / kJoinThreads;
+    for (int64_t it = blockIdx.x; it < (int64_t)found * steps; it += gridDim.x) {
+        const int cta = list[it / steps], group = cta % p.groups;
+        const Join jn = p.joins[cta];
+        const int pieces = jn.last - jn.member + 1;
+        if (pieces > kFewPieces) continue;
+        const int at = (int)(it % steps) * kJoinThreads + threadIdx.x;
+        const int row = at / per_row, e = at % per_row * 4, r = group * NB + row;
+        if (row >= NB || r >= p.rows) continue;
+        const float* src[kFewPieces];
+        float top = -INFINITY, mx[kFewPieces];
+        float4 v[kFewPieces];
+#pragma unroll
+        for (int k = 0; k < kFewPieces; ++k) {
+            if (k >= pieces) continue;
+            const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
+            src[k] = p.parts + slot * slot_floats;
+            mx[k] = src[k][row];
+            v[k] = *reinterpret_cast<const float4*>(src[k] + 2 * NB + (int64_t)row * p.R + e);
+            top = fmaxf(top, mx[k]);
+        }
+        float l = 0.0f;
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kFewPieces; ++k) {
+            if (k >= pieces) continue;
+            const float w = mx[k] == -INFINITY ? 0.0f : exp2f(mx[k] - top);
+            l = fmaf(w, src[k][NB + row], l);
+            o.x = fmaf(w, v[k].x, o.x);
+            o.y = fmaf(w, v[k].y, o.y);
+            o.z = fmaf(w, v[k].z, o.z);
+            o.w = fmaf(w, v[k].w, o.w);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
+               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarters = p.R / 128;
+    for (int64_t it = blockIdx.x; it < (int64_t)found * NB * quarters; it += gridDim.x) {
+        const int cta = list[it / (NB * quarters)], group = cta % p.groups;
+        const Join jn = p.joins[cta];
+        const int pieces = jn.last - jn.member + 1;
+        const int row = (int)(it / quarters % NB), e = (int)(it % quarters) * 128 + lane * 4, r = group * NB + row;
+        if (pieces <= kFewPieces || r >= p.rows) continue;
+        auto piece = [&](int k) {
+            const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
+            return p.parts + slot * slot_floats;
+        };
+        // This warp's pieces: a running maximum over groups of four.
+        float top = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0, 0, 0, 0);
+        for (int k0 = warp; k0 < pieces; k0 += 32) {
+            float mx[4], lx[4];
+            float4 v[4];
+            float now = top;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 8 * q;
+                mx[q] = -INFINITY;
+                lx[q] = 0.0f;
+                v[q] = make_float4(0, 0, 0, 0);
+                if (k < pieces) {
+                    const float* src = piece(k);
+                    mx[q] = src[row];
+                    lx[q] = src[NB + row];
+                    v[q] = *reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)row * p.R + e);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) now = fmaxf(now, mx[q]);
+            const float f = top == -INFINITY ? 0.0f : exp2f(top - now);
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            top = now;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float w = mx[q] == -INFINITY ? 0.0f : exp2f(mx[q] - top);
+                l = fmaf(w, lx[q], l);
+                o.x = fmaf(w, v[q].x, o.x);
+                o.y = fmaf(w, v[q].y, o.y);
+                o.z = fmaf(w, v[q].z, o.z);
+                o.w = fmaf(w, v[q].w, o.w);
+            }
+        }
+        __syncthreads();                                     // the last item's sums are read
+        sums[warp][lane] = o;
+        if (lane == 0) {
+            tops[warp] = top;
+            ls[warp] = l;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            top = -INFINITY;
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k]);
+            l = 0.0f;
+            o = make_float4(0, 0, 0, 0);
+            for (int k = 0; k < 8; ++k) {
+                const float w = tops[k] == -INFINITY ? 0.0f : exp2f(tops[k] - top);
+                const float4 v = sums[k][lane];
+                l = fmaf(w, ls[k], l);
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
+                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        }
+    }
+}
+
+constexpr size_t kJoinBytes = kMaxJoins * sizeof(Join);
+
+int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+size_t part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
+
+template <typename T, int NB>
+cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    static_assert(smem_bytes<NB>(kMaxChunks) <= 232448, "shared memory per CTA");
+    if (!(attr_done.load() & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem_bytes<NB>(kMaxChunks));
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit);
+    }
+    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(p);
+    if (p.split) join_kernel<T, NB><<<(unsigned)sms * 8, kJoinThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_rows(int nb, const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch<T, 16>(p, sms, stream);
+    if (nb == 32) return launch<T, 32>(p, sms, stream);
+    return launch<T, 64>(p, sms, stream);
+}
+
+bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
+
+}  // namespace
+
+size_t latent_decode_workspace_bytes(int sms) { return kJoinBytes + 2 * (size_t)sms * part_bytes(64, 512); }
+
+bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err) {
+    if (a.R % 128 != 0 || a.R > 512 || a.P % 8 != 0 || a.P > 64) return false;
+    if (!vec16(a.Q, a.heads > 1 ? a.hsQ : 0, a.q_len > 1 ? a.tsQ : 0, a.n_seqs > 1 ? a.bsQ : 0) ||
+        !vec16(a.cache, a.block_size > 1 ? a.rsC : 0, a.num_blocks > 1 ? a.psC : 0, 0))
+        return false;
+    const int64_t rows = a.q_len * a.heads;
+    const int nb = rows_block(rows);
+    const int64_t groups = (rows + nb - 1) / nb;
+    if (groups > 65535 || (__int128)a.n_seqs * ((a.N + BT - 1) / BT + 1) >= INT32_MAX) return false;
+    Params p{};
+    p.Q = a.Q; p.hsQ = a.hsQ; p.tsQ = a.tsQ; p.bsQ = a.bsQ;
+    p.cache = a.cache; p.rsC = a.rsC; p.psC = a.psC;
+    p.table = a.table; p.seq_lens = a.seq_lens;
+    p.O = a.O; p.hsO = a.hsO; p.tsO = a.tsO; p.bsO = a.bsO;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = (int)a.num_blocks; p.block_size = (int)a.block_size;
+    p.q_len = (int)a.q_len; p.heads = (int)a.heads; p.rows = (int)rows;
+    p.N = (int)a.N; p.R = (int)a.R; p.P = (int)a.P; p.n_seqs = (int)a.n_seqs;
+    p.chunks = (int)(a.R / 64 + (a.P > 0));
+    p.rope_steps = (int)((a.P + 15) / 16);
+    p.groups = (int)groups;
+    p.scale_log2 = a.alpha * 1.4426950408889634f;
+    p.causal = a.causal;
+    const bool bf = a.type == SBGEMM_TYPE_BF16;
+    p.idesc_s = idesc16(bf, nb, false, false);
+    p.idesc_o = idesc16(bf, nb, true, true);
+    // CTAs for each group of rows: an SM each, as far as the workspace has two
+    // slots for every one of them; without it whole sequences.
+    int64_t each = std::max<int64_t>(1, sms / groups);
+    const int64_t slots = a.workspace && a.workspace_bytes > kJoinBytes
+                              ? (int64_t)((a.workspace_bytes - kJoinBytes) / part_bytes(nb, a.R)) : 0;
+    each = std::min(each, slots / (2 * groups));
+    if (each > 1 && each * groups <= kMaxJoins) {
+        p.split = 1;
+        p.joins = static_cast<Join*>(a.workspace);
+        p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kJoinBytes);
+    } else {
+        each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
+    }
+    p.per_group = (int)each;
+    *err = bf ? launch_rows<__nv_bfloat16>(nb, p, sms, stream) : launch_rows<__half>(nb, p, sms, stream);
+    return true;
+}
+
+unsigned int read_and_clear_status_latent_decode(cudaStream_t stream) {
+    return read_and_clear_word(reinterpret_cast<const void*>(&g_wait_status), stream);
+}
+
+}  // namespace sbg

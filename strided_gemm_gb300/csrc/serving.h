@@ -52,6 +52,11 @@ struct LatentPacked {
     float alpha;
     int causal;
 };
+// On the tensor cores, over a paged cache (latent_decode.cu); false for sizes
+// and alignments it does not take.
+bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err);
+size_t latent_decode_workspace_bytes(int sms);
+unsigned int read_and_clear_status_latent_decode(cudaStream_t stream);
 // One warp a query row, any sizes and alignments (latent_rows.cu).
 constexpr int64_t kLatentMaxQK = 640, kLatentMaxV = 512;
 cudaError_t launch_latent_rows_paged(const LatentPaged& a, cudaStream_t stream);

@@ -209,7 +209,7 @@ int check_pool_memory(const PoolView& v, std::initializer_list<Bytes> inputs, co
 }  // namespace
 
 unsigned int read_and_clear_status_serving(cudaStream_t stream) {
-    const unsigned int codes[] = {read_and_clear_status_half_tc(stream),
+    const unsigned int codes[] = {read_and_clear_status_half_tc(stream), read_and_clear_status_latent_decode(stream),
                                   read_and_clear_status_latent_rows(stream), read_and_clear_status_pages(stream)};
     for (unsigned int c : codes)
         if (c) return c;
@@ -289,7 +289,8 @@ int sbgemm_latent_attention_paged(
         return SBGEMM_ERR_OUTPUT_OVERLAP;
     for (const Bytes& s : {sq, sc, st, sl})
         if (meet(so, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
-    if (!current_sms()) return SBGEMM_ERR_CUDA;
+    const int sms = current_sms();
+    if (!sms) return SBGEMM_ERR_CUDA;
     if (const int m = in_device_memory({sq, sc, so, st, sl})) return m;
     if (ws) {
         const Bytes w = block(ws, (int64_t)std::min<size_t>(ws_bytes, (size_t)1 << 60));
@@ -300,6 +301,8 @@ int sbgemm_latent_attention_paged(
     }
     const LatentPaged a{type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
                         seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal, ws, ws_bytes};
+    cudaError_t e = cudaSuccess;
+    if (launch_latent_decode(a, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_latent_rows_paged(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -310,7 +313,7 @@ int sbgemm_latent_workspace_bytes(int device, size_t* bytes) {
         cudaGetLastError();
         return SBGEMM_ERR_CUDA;
     }
-    *bytes = 256;
+    *bytes = latent_decode_workspace_bytes(d->sm_count);
     return SBGEMM_OK;
 }
 
