@@ -27,9 +27,12 @@
 // device knows; no result depends on timing.
 //
 // Roles (12 warps, warp 3 idle): warps 0 and 1 load the rows of even and odd
-// blocks by 16-byte cp.async, each row's page looked up in the table, past the
-// end and for bad pages zeros instead of a read (so nothing there can reach a
-// result); warp 2 issues the MMAs, the scores of block j + 1 before P V of
+// blocks, each run of rows inside a page looked up in the table and fetched by
+// TMA, one lane a run (a bad page's coordinate lies outside the tensor map and
+// reads as zeros).  A sequence's last, partial block, and pages whose runs are
+// shorter than 8 rows, come by 16-byte cp.async with zeros past the end, so
+// that nothing there can reach a result (cp.async for every block was bound by
+// its issue: 6.4 us a block); warp 2 issues the MMAs, the scores of block j + 1 before P V of
 // block j when its rows are there in time; warps 4-11 the softmax (the four of
 // them that own the 64 key lanes), rescaling, queries and output.  Every wait
 // is bounded.
@@ -67,6 +70,7 @@ struct Params {
     void* O; int64_t hsO, tsO, bsO;
     int64_t max_blocks;
     int num_blocks, block_size;
+    int run;                                 // rows a TMA box takes: the run of a block inside a page; 0: no TMA
     int q_len, heads, rows, N, R, P, n_seqs;
     int chunks, rope_steps;                  // 64-wide pieces of a row; MMA K steps of the rope piece
     int groups, per_group;                   // query-row groups; CTAs for each
@@ -147,7 +151,8 @@ struct Walk {
 };
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
     constexpr int CPW = NB / 2;              // score columns of a softmax warp
     constexpr uint32_t kColO = 0, kColS = kMaxTiles * NB;
     static_assert(kColS + 2 * NB <= 512, "TMEM columns");
@@ -241,11 +246,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         const char* cache = static_cast<const char*>(p.cache);
         const int row_pieces = (p.R + p.P) / 8;
         int i = 0;                           // blocks so far, over all pieces
+        int landing = 0;                     // from 1, the stage's last block if it came by TMA
         bool ok = true;
         while (ok && w.next(p)) {
             const int32_t* table = p.table + w.s * p.max_blocks;
             for (int j = w.j0; j < w.j1; ++j, ++i) {
                 if ((i & 1) != st) continue;
+                const uint32_t ph_empty = (uint32_t)((i / kStages - 1) & 1);
+                if (p.run && (j + 1) * BT <= w.len) {
+                    // A whole block: lane x takes run x.
+                    const int runs = BT / p.run, n = j * BT + lane * p.run;
+                    int page = 0;
+                    if (lane < runs) {
+                        page = table[n / p.block_size];
+                        if (page < 0 || page >= p.num_blocks) {
+                            record_status(&g_wait_status, kPagedInput);
+                            page = p.num_blocks;
+                        }
+                    }
+                    if (i >= kStages && !mbar_wait(&c.empty[st], ph_empty)) {
+                        record_status(&g_wait_status, kWaitEmpty);
+                        ok = false;
+                    }
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&c.full[st], (uint32_t)(p.chunks * kChunkBytes));
+                    __syncwarp();
+                    if (lane < runs) {
+                        uint8_t* dst = skv + st * p.chunks * kChunkBytes + lane * p.run * 128;
+                        for (int k = 0; k < p.chunks; ++k)
+                            tma_load_3d(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64, n % p.block_size, page);
+                    }
+                    landing = i + 1;
+                    continue;
+                }
                 // The rows' places first: their table entries arrive while the stage drains.
                 const char* src[BT / 4];
 #pragma unroll
@@ -260,11 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             record_status(&g_wait_status, kPagedInput);
                     }
                 }
-                if (i >= kStages && !mbar_wait(&c.empty[st], (uint32_t)((i / kStages - 1) & 1))) {
+                if (i >= kStages && !mbar_wait(&c.empty[st], ph_empty)) {
                     record_status(&g_wait_status, kWaitEmpty);
                     ok = false;
-                    break;
                 }
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
 #pragma unroll
                 for (int g = 0; g < BT / 4; ++g) {
                     const int r = r0 + 4 * g;
@@ -278,8 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.full[st]);
+                landing = 0;                 // the stage's earlier blocks are through
             }
         }
+        // Copies still landing keep the CTA's shared memory.
+        if (landing && !mbar_wait(&c.full[st], (uint32_t)(((landing - 1) / kStages) & 1)))
+            record_status(&g_wait_status, kWaitDrain);
     } else if (warp == kMmaWarp) {
         // ---- MMAs ------------------------------------------------------------------
         if (lane == 0) {
@@ -723,7 +762,7 @@ int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 size_t part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
 
 template <typename T, int NB>
-cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -735,16 +774,16 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
-    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(p);
+    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
     if (p.split) join_kernel<T, NB><<<(unsigned)sms * 8, kJoinThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_rows(int nb, const Params& p, int sms, cudaStream_t stream) {
-    if (nb == 16) return launch<T, 16>(p, sms, stream);
-    if (nb == 32) return launch<T, 32>(p, sms, stream);
-    return launch<T, 64>(p, sms, stream);
+cudaError_t launch_rows(int nb, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch<T, 16>(map, p, sms, stream);
+    if (nb == 32) return launch<T, 32>(map, p, sms, stream);
+    return launch<T, 64>(map, p, sms, stream);
 }
 
 bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
@@ -795,7 +834,24 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
     }
     p.per_group = (int)each;
-    *err = bf ? launch_rows<__nv_bfloat16>(nb, p, sms, stream) : launch_rows<__half>(nb, p, sms, stream);
+    // Runs of rows that lie in one page wherever a block of 64 begins.
+    CUtensorMap map{};
+    int run = BT;
+    while (a.block_size % run != 0) run /= 2;
+    const int64_t row_stride = a.block_size > 1 ? a.rsC : (a.R + a.P + 7) / 8 * 8;
+    const int64_t page_stride = a.num_blocks > 1 ? a.psC : row_stride;
+    const int64_t lim = (int64_t)1 << 39;
+    if (run >= 8 && row_stride > 0 && page_stride > 0 && row_stride < lim && page_stride < lim) {
+        const uint64_t dims[3] = {(uint64_t)(a.R + a.P), (uint64_t)a.block_size, (uint64_t)a.num_blocks};
+        const uint64_t strides[2] = {(uint64_t)row_stride * 2, (uint64_t)page_stride * 2};
+        const uint32_t box[3] = {64, (uint32_t)run, 1};
+        if (!encode_tmap_16(&map, a.cache, 3, dims, strides, box)) {
+            *err = cudaErrorInvalidValue;
+            return true;
+        }
+        p.run = run;
+    }
+    *err = bf ? launch_rows<__nv_bfloat16>(nb, map, p, sms, stream) : launch_rows<__half>(nb, map, p, sms, stream);
     return true;
 }
 
