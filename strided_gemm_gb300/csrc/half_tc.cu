@@ -51,7 +51,6 @@ struct Shape {
     static constexpr int kStage = BX * BK * 2 + kYBytes;
     static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
     static constexpr int kSmem = kStages * kStage + 2 * kOutBytes + 1024;
-    static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;
     static_assert(kSmem <= 232448 - 1024, "shared memory per CTA");
 };
 
@@ -76,7 +75,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
     uint8_t* out = ring + S::kStages * S::kStage;
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_free[2], done;
     __shared__ uint32_t tmem_base;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -94,13 +93,12 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
         if (p.c_tma) prefetch_tensormap(&to);
     }
     if (warp == 5) {
-        tmem_alloc(&tmem_base, S::kTmem);
+        tmem_alloc(&tmem_base, kTmemAll);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
     // Tile t: x fastest, so that CTAs side by side share the Y operand's tile.
     auto place = [&](int64_t t, int* x0, int* y0, int* b) {
         *x0 = (int)(t % p.x_tiles) * BX;
@@ -150,7 +148,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                 }
         }
     } else if (warp == 5) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t x_step = p.x_mn ? kStepMN : kStepK, y_step = p.y_mn ? kStepMN : kStepK;
             int64_t i = 0;
             int n = 0;                             // tiles begun
@@ -160,7 +158,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                     record_status(&g_wait_status, kWaitAccFree);
                     break;
                 }
-                const uint32_t acc = tmem + (uint32_t)(n & 1) * NT;
+                const uint32_t acc = kTmemBase + (uint32_t)(n & 1) * NT;
                 for (int j = 0; j < p.k_blocks; ++j, ++i) {
                     const int s = (int)(i % S::kStages);
                     if (!mbar_wait(&full[s], (uint32_t)((i / S::kStages) & 1))) {
@@ -197,7 +195,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             if (!in) record_status(&g_wait_status, kWaitMma);
             if (!all_of_group(in)) break;          // they meet at barriers below: all go on or none
             tc_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(n & 1) * NT + ((uint32_t)(warp * 32) << 16);
+            const uint32_t acc = kTmemBase + (uint32_t)(n & 1) * NT + ((uint32_t)(warp * 32) << 16);
             const int x = x0 + threadIdx.x;
             T* C = static_cast<T*>(p.C) + b * p.bsC;
 #pragma unroll 1
@@ -274,7 +272,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
     __syncthreads();
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, S::kTmem);
+        tmem_dealloc(kTmemBase, kTmemAll);
     }
 }
 

@@ -162,7 +162,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     uint8_t* skv = sq + p.chunks * (NB * 128);               // rows: [stage][chunk][64][128]
     uint8_t* sp = skv + kStages * p.chunks * kChunkBytes;    // weights: [64 keys][128 bytes]
     Ctl<NB>& c = *reinterpret_cast<Ctl<NB>*>(sp + kChunkBytes);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int group = blockIdx.x % p.groups, member = blockIdx.x / p.groups;
     const int tiles_o = p.R / 128;
 
@@ -180,7 +180,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(&c.tmem_base, 512);
+        tmem_alloc(&c.tmem_base, kTmemAll);
         tmem_relinquish();
     }
 
@@ -235,7 +235,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = c.tmem_base;
+    constexpr uint32_t tmem = kTmemBase;
     Walk w{c.seq0, c.tile0, c.count};
 
     if (warp < kStages) {
@@ -321,7 +321,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             record_status(&g_wait_status, kWaitDrain);
     } else if (warp == kMmaWarp) {
         // ---- MMAs ------------------------------------------------------------------
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t q_lo = smem_u32(sq), kv_lo = smem_u32(skv), p_lo = smem_u32(sp);
             const uint32_t stage_bytes = p.chunks * kChunkBytes;
             int i = 0, filled = 0;           // blocks and pieces with blocks so far
@@ -604,7 +604,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(kTmemBase, kTmemAll);
     }
 }
 
