@@ -2,16 +2,18 @@
 // sbgemm_latent_attention_paged): every head of a sequence reads the same rows
 // [c | k_rope], as keys whole and as values without their rope part.
 //
-// A unit of work is a block of 64 keys of one sequence for NB query rows
+// A unit of work is a block of BT keys of one sequence for NB query rows
 // (token, head) of it, NB = 16, 32 or 64.  The products are computed
 // transposed, keys and latents along the MMA's M and query rows along its N,
 // so that a few heads waste nothing and the one copy of the rows in shared
 // memory serves both:
-//   S^T = K Q^T      M: keys (64 of the MMA's 128 lanes), N = NB, K = R + P,
+//   S^T = K Q^T      M: 64 keys, N = NB, K = R + P,
 //                    A = the rows, K-major; B = the queries
-//   O^T += C^T P^T   M: 128 latents a tile, N = NB, K = 64 keys,
+//   O^T += C^T P^T   M: 128 latents a tile, N = NB, K = BT keys,
 //                    A = the same rows read MN-major; B = P^T, written by the
 //                    softmax as rows of NB weights a key
+// Such MMAs are bound by shared memory's 128 bytes a cycle for A and B: 24
+// cycles for the scores' 64 x 16 x 16 (40 with M = 128), 40 for 128 x 16 x 16.
 // O^T stays in TMEM (R / 128 tiles of NB columns) over all blocks of a
 // sequence.  The softmax keeps a reference maximum a query row, raised only
 // when a score exceeds it by a factor of 2^8 (then O^T, the sums and the
@@ -26,16 +28,20 @@
 // joins them in order.  The lists depend on the lengths alone, which the
 // device knows; no result depends on timing.
 //
-// Roles (12 warps, warp 3 idle): warps 0 and 1 load the rows of even and odd
-// blocks, each run of rows inside a page looked up in the table and fetched by
-// TMA, one lane a run (a bad page's coordinate lies outside the tensor map and
-// reads as zeros).  A sequence's last, partial block, and pages whose runs are
-// shorter than 8 rows, come by 16-byte cp.async with zeros past the end, so
-// that nothing there can reach a result (cp.async for every block was bound by
-// its issue: 6.4 us a block); warp 2 issues the MMAs, the scores of block j + 1 before P V of
-// block j when its rows are there in time; warps 4-11 the softmax (the four of
-// them that own the 64 key lanes), rescaling, queries and output.  Every wait
-// is bounded.
+// Roles (12 warps): a warp for each of the 2 or 3 stages loads every second
+// or third block's rows, each run of rows inside a page looked up in the table
+// and fetched by TMA, one lane a run (a bad page's coordinate lies outside the
+// tensor map and reads as zeros).  A sequence's last, partial block, and pages
+// whose runs are shorter than 8 rows, come by 16-byte cp.async with zeros past
+// the end, so that nothing there can reach a result (cp.async for every block
+// was bound by its issue: 6.4 us a block).  Warp 3 issues the MMAs, the scores
+// of block j + 1 before P V of block j when its rows are there in time; warps
+// 4-11 do the softmax, rescaling, queries and output.  Every wait is bounded.
+//
+// Up to 32 rows three stages of 48 keys keep two blocks' loads in flight under
+// the third's MMAs (two stages of 64: loads and MMAs took turns, 76 us against
+// XX us for 32 ragged sequences of 16 heads); 64 rows' queries leave room for
+// two stages of 64.
 //
 // Bound: few heads by the cache's bytes; 128 heads (two CTAs on the same
 // blocks at the same time, the second read hitting L2) by the MMAs, whose
@@ -49,13 +55,16 @@
 namespace sbg {
 namespace {
 
-constexpr int BT = 64;                       // keys per block
-constexpr int kStages = 2;
-constexpr int kMmaWarp = 2, kMathWarp = 4, kMathWarps = 8, kWarps = 12;
+constexpr int kMmaWarp = 3, kMathWarp = 4, kMathWarps = 8, kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxChunks = 9;                // 64-wide pieces of a row: R <= 512 and the rope part
 constexpr int kMaxTiles = 4;                 // R / 128
-constexpr int kChunkBytes = BT * 128;        // a piece of a block: 64 rows of 128 swizzled bytes
+// Keys a block and stages of the ring, by query rows.
+template <int NB> struct Shape {
+    static constexpr int BT = NB == 64 ? 64 : 48;
+    static constexpr int kStages = NB == 64 ? 2 : 3;
+    static constexpr int kChunkBytes = BT * 128;             // a piece of a block: BT rows of 128 swizzled bytes
+};
 constexpr float kRaise = 8.0f;               // log2 headroom before the reference maximum rises
 __device__ unsigned int g_wait_status = 0;
 
@@ -84,22 +93,22 @@ struct Params {
 
 template <int NB>
 struct Ctl {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[Shape<NB>::kStages], empty[Shape<NB>::kStages];
     uint64_t q_full, s_full[2], p_full, pv_done, o_free, done;
     uint32_t tmem_base;
     int seq0, tile0, count;                  // this CTA's run of the list
     int scan[kWarps];
     float ref[NB], factor[NB];               // reference maxima; a rise's factors, then 1 / sum
     union {
-        float part[2][NB];                   // maxima or sums of the two key quarters
+        float part[4][NB];                   // maxima or sums of the four key quarters
         int64_t out[NB];                     // element offset of a row of O (-1: none)
     };
-    int limit[NB];                           // last key a row sees
 };
 
 template <int NB>
 constexpr size_t smem_bytes(int chunks) {
-    return (size_t)chunks * (NB * 128 + kStages * kChunkBytes) + kChunkBytes + sizeof(Ctl<NB>) + 1024;
+    using H = Shape<NB>;
+    return (size_t)chunks * (NB * 128 + H::kStages * H::kChunkBytes) + H::kChunkBytes + sizeof(Ctl<NB>) + 1024;
 }
 
 // A vote and barrier of the eight math warps.
@@ -125,9 +134,11 @@ __device__ __forceinline__ int seq_len(const Params& p, int s, bool report) {
     return n < 0 ? 0 : p.N;
 }
 // Blocks a sequence counts for in the list: an empty one has its zeros to write.
+template <int BT>
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + BT - 1) / BT : 1; }
 
 // A CTA's walk over its run: pieces of sequences in order.
+template <int BT>
 struct Walk {
     int seq, tile, left;     // the next piece begins at block `tile` of `seq`; units left
     int len, j0, j1;         // the piece: blocks j0 .. j1 - 1 of a sequence of `len` keys
@@ -136,7 +147,7 @@ struct Walk {
         if (left <= 0 || seq >= p.n_seqs) return false;
         s = seq;
         len = seq_len(p, s, report);
-        units = units_of(len);
+        units = units_of<BT>(len);
         j0 = tile;
         const int n = min(units - tile, left);
         j1 = len > 0 ? j0 + n : j0;
@@ -153,14 +164,14 @@ struct Walk {
 template <typename T, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
-    constexpr int CPW = NB / 2;              // score columns of a softmax warp
+    constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
     constexpr uint32_t kColO = 0, kColS = kMaxTiles * NB;
     static_assert(kColS + 2 * NB <= 512, "TMEM columns");
     extern __shared__ uint8_t raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* sq = base;                                      // queries: [chunk][NB rows][128 bytes]
-    uint8_t* skv = sq + p.chunks * (NB * 128);               // rows: [stage][chunk][64][128]
-    uint8_t* sp = skv + kStages * p.chunks * kChunkBytes;    // weights: [64 keys][128 bytes]
+    uint8_t* skv = sq + p.chunks * (NB * 128);               // rows: [stage][chunk][BT][128]
+    uint8_t* sp = skv + kStages * p.chunks * kChunkBytes;    // weights: [BT keys][128 bytes]
     Ctl<NB>& c = *reinterpret_cast<Ctl<NB>*>(sp + kChunkBytes);
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int group = blockIdx.x % p.groups, member = blockIdx.x / p.groups;
@@ -188,7 +199,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     int members = 1, lo = 0, units_total = 0;
     if (p.split) {
         int sum = 0;
-        for (int s = tid; s < p.n_seqs; s += kThreads) sum += units_of(seq_len(p, s, false));
+        for (int s = tid; s < p.n_seqs; s += kThreads) sum += units_of<BT>(seq_len(p, s, false));
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         if (lane == 0) c.scan[warp] = sum;
@@ -204,7 +215,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         int before = 0;                      // units of the sequences of earlier rounds
         for (int s0 = 0; s0 < p.n_seqs && before <= lo; s0 += kThreads) {
             const int s = s0 + tid;
-            const int u = s < p.n_seqs ? units_of(seq_len(p, s, false)) : 0;
+            const int u = s < p.n_seqs ? units_of<BT>(seq_len(p, s, false)) : 0;
             int inc = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -236,7 +247,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = kTmemBase;
-    Walk w{c.seq0, c.tile0, c.count};
+    Walk<BT> w{c.seq0, c.tile0, c.count};
 
     if (warp < kStages) {
         // ---- rows of the cache into shared memory ---------------------------------
@@ -251,7 +262,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         while (ok && w.next(p)) {
             const int32_t* table = p.table + w.s * p.max_blocks;
             for (int j = w.j0; j < w.j1; ++j, ++i) {
-                if ((i & 1) != st) continue;
+                if (i % kStages != st) continue;
                 const uint32_t ph_empty = (uint32_t)((i / kStages - 1) & 1);
                 if (p.run && (j + 1) * BT <= w.len) {
                     // A whole block: lane x takes run x.
@@ -329,7 +340,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             auto scores = [&](int b) {       // S^T of block number b
                 tc_fence_after();
                 const uint32_t d = tmem + kColS + (b & 1) * NB;
-                uint64_t da = desc16(kv_lo + (b & 1) * stage_bytes), dq = desc16(q_lo);
+                uint64_t da = desc16(kv_lo + b % kStages * stage_bytes), dq = desc16(q_lo);
                 for (int k = 0; k < p.R / 64; ++k) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -349,7 +360,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 const int n = w.j1 - w.j0;
                 if (n == 0) continue;        // an empty sequence
                 if (!mbar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
-                    !mbar_wait(&c.full[i & 1], (uint32_t)((i / kStages) & 1))) {
+                    !mbar_wait(&c.full[i % kStages], (uint32_t)((i / kStages) & 1))) {
                     timed_out(kWaitFull);
                     break;
                 }
@@ -361,7 +372,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     const uint32_t ph_next = (uint32_t)(((i + 1) / kStages) & 1);
                     const uint64_t t0 = global_timer_ns();
                     while (!mbar_try_wait(&c.p_full, (uint32_t)(i & 1))) {
-                        if (!ahead && mbar_try_wait(&c.full[(i + 1) & 1], ph_next)) {
+                        if (!ahead && mbar_try_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             scores(i + 1);
                             ahead = true;
                         }
@@ -376,7 +387,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t rows = kv_lo + (i & 1) * stage_bytes;
+                    const uint32_t rows = kv_lo + i % kStages * stage_bytes;
                     for (int t = 0; t < tiles_o; ++t) {
                         const uint64_t da = desc16(rows + 2 * t * kChunkBytes, kChunkBytes), dp = desc16(p_lo);
 #pragma unroll
@@ -384,10 +395,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
                                      (j | x) ? 1u : 0u);
                     }
-                    mma_commit(&c.empty[i & 1]);
+                    mma_commit(&c.empty[i % kStages]);
                     mma_commit(&c.pv_done);
                     if (!ahead) {
-                        if (!mbar_wait(&c.full[(i + 1) & 1], ph_next)) {
+                        if (!mbar_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             timed_out(kWaitFull);
                             break;
                         }
@@ -404,20 +415,20 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         // ---- queries, softmax, output ------------------------------------------------
         const int m = tid - kMathWarp * 32;                  // 0 .. 255
         const int quarter = warp & 3, half = (warp - kMathWarp) >> 2;
-        const bool active = quarter < 2;                     // owns key lanes 32 quarter .. + 31
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        // Keys lie in lanes 0-15 of each quarter (the accumulator of an M = 64
+        // MMA); a warp takes half of the columns, its lower and upper lanes a
+        // half of those each, for the same keys.
+        constexpr int CPW = NB / 2, CPT = NB / 4;
+        const int row = quarter * 16 + (lane & 15), col = half * CPW + (lane >> 4) * CPT;
+        const bool mine = row < BT;
         const int row_pieces = (p.R + p.P) / 8;
         int i = 0, piece_no = 0, used = 0;                   // blocks, pieces, units so far
         bool ok = true;
         Join join{-1, 0, 0, 0};
         while (w.next(p, group == 0)) {
             const int n = w.j1 - w.j0;
-            // The rows of this group: where they go and what they see.
-            if (m < NB) {
-                const int r = group * NB + m, t = r / p.heads;
-                c.limit[m] = r < p.rows && p.causal ? w.len - p.q_len + t : w.len - 1;
-                c.ref[m] = -INFINITY;
-            }
+            if (m < NB) c.ref[m] = -INFINITY;
             if (n > 0) {
                 for (int x = m; x < NB * p.chunks * 8; x += 256) {
                     const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
@@ -434,9 +445,9 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             }
             math_sync();
 
-            float l[CPW];
+            float l[CPT];
 #pragma unroll
-            for (int x = 0; x < CPW; ++x) l[x] = 0.0f;
+            for (int x = 0; x < CPT; ++x) l[x] = 0.0f;
             bool failed = false;
             for (int j = 0; j < n; ++j, ++i) {
                 if (!mbar_wait(&c.s_full[i & 1], (uint32_t)((i >> 1) & 1))) {
@@ -444,46 +455,57 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     ok = false;
                 }
                 tc_fence_after();
-                float a[CPW];
+                float a[CPT];
                 bool rise = false;
-                if (active) {
-                    tmem_ld<CPW>(tmem + lanes + kColS + (i & 1) * NB + half * CPW, a);
-                    const int key = (w.j0 + j) * BT + quarter * 32 + lane;
-                    const int safe = p.causal ? w.len - p.q_len : w.len - 1;    // keys up to here: every row's
-                    const bool all = (w.j0 + j) * BT + BT - 1 <= safe;
+                {
+                    float v[CPW];
+                    tmem_ld<CPW>(tmem + lanes + kColS + (i & 1) * NB + half * CPW, v);
 #pragma unroll
-                    for (int x = 0; x < CPW; ++x) {
-                        a[x] *= p.scale_log2;
-                        if (!all && key > c.limit[half * CPW + x]) a[x] = -INFINITY;
-                        rise |= a[x] > c.ref[half * CPW + x] + kRaise;
+                    for (int x = 0; x < CPT; ++x) {
+                        const float other = __shfl_xor_sync(~0u, v[CPT + x], 16);
+                        a[x] = (lane < 16 ? v[x] : other) * p.scale_log2;
                     }
                 }
+                const int first = (w.j0 + j) * BT;
+                const int safe = p.causal ? w.len - p.q_len : w.len - 1;    // keys up to here: every row's
+                const bool edge = first + BT - 1 > safe;
+                if (edge || !mine) {
+#pragma unroll
+                    for (int x = 0; x < CPT; ++x) {
+                        int limit = w.len - 1;
+                        if (p.causal) {
+                            const int r = group * NB + col + x;
+                            if (r < p.rows) limit = safe + r / p.heads;
+                        }
+                        if (!mine || first + row > limit) a[x] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < CPT; ++x) rise |= a[x] > c.ref[col + x] + kRaise;
                 if (math_any(rise || !ok)) {
                     if (math_any(!ok)) {
                         failed = true;
                         break;
                     }
                     // Raise the references to the block's maxima and scale what was summed.
-                    if (active) {
 #pragma unroll
-                        for (int x = 0; x < CPW; ++x) {
-                            float v = a[x];
+                    for (int x = 0; x < CPT; ++x) {
+                        float v = a[x];
 #pragma unroll
-                            for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-                            if (lane == 0) c.part[quarter][half * CPW + x] = v;
-                        }
+                        for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+                        if ((lane & 15) == 0) c.part[quarter][col + x] = v;
                     }
                     math_sync();
                     if (m < NB) {
-                        const float old = c.ref[m], top = fmaxf(old, fmaxf(c.part[0][m], c.part[1][m]));
+                        const float old = c.ref[m];
+                        const float top = fmaxf(old, fmaxf(fmaxf(c.part[0][m], c.part[1][m]),
+                                                           fmaxf(c.part[2][m], c.part[3][m])));
                         c.factor[m] = top == -INFINITY ? 1.0f : exp2f(old - top);    // 0 at the first rise
                         c.ref[m] = top;
                     }
                     math_sync();
-                    if (active) {
 #pragma unroll
-                        for (int x = 0; x < CPW; ++x) l[x] *= c.factor[half * CPW + x];
-                    }
+                    for (int x = 0; x < CPT; ++x) l[x] *= c.factor[col + x];
                     if (j > 0) {
                         if (!mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
                             record_status(&g_wait_status, kWaitMma);
@@ -506,30 +528,35 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         tmem_wait_st();
                     }
                 }
-                if (active) {
-                    uint32_t w2[CPW / 2];
+                uint32_t w2[CPT / 2];
 #pragma unroll
-                    for (int x = 0; x < CPW; x += 2) {
-                        const float r0 = c.ref[half * CPW + x], r1 = c.ref[half * CPW + x + 1];
-                        // A row that has seen no key yet has no reference: its weights are 0.
-                        const float p0 = ex2_approx(a[x] - (r0 == -INFINITY ? 0.0f : r0));
-                        const float p1 = ex2_approx(a[x + 1] - (r1 == -INFINITY ? 0.0f : r1));
-                        l[x] += p0;
-                        l[x + 1] += p1;
-                        w2[x / 2] = pack2<T>(p0, p1);
-                    }
-                    // The block before has read its weights.
-                    if (i > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
-                        record_status(&g_wait_status, kWaitMma);
-                        ok = false;
-                    }
-                    const int r = quarter * 32 + lane;
-#pragma unroll
-                    for (int x = 0; x < CPW / 8; ++x)
-                        *reinterpret_cast<uint4*>(sp + r * 128 + (((half * (CPW / 8) + x) ^ (r & 7)) << 4)) =
-                            make_uint4(w2[4 * x], w2[4 * x + 1], w2[4 * x + 2], w2[4 * x + 3]);
-                    fence_proxy_async_smem();
+                for (int x = 0; x < CPT; x += 2) {
+                    const float r0 = c.ref[col + x], r1 = c.ref[col + x + 1];
+                    // A row that has seen no key yet has no reference: its weights are 0.
+                    const float p0 = ex2_approx(a[x] - (r0 == -INFINITY ? 0.0f : r0));
+                    const float p1 = ex2_approx(a[x + 1] - (r1 == -INFINITY ? 0.0f : r1));
+                    l[x] += p0;
+                    l[x + 1] += p1;
+                    w2[x / 2] = pack2<T>(p0, p1);
                 }
+                // The block before has read its weights.
+                if (i > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                    record_status(&g_wait_status, kWaitMma);
+                    ok = false;
+                }
+                if (mine) {
+                    uint8_t* to = sp + row * 128;
+                    const int at = col * 2, swz = (row & 7) << 4;
+                    if constexpr (CPT >= 8) {
+#pragma unroll
+                        for (int x = 0; x < CPT / 8; ++x)
+                            *reinterpret_cast<uint4*>(to + ((at + 16 * x) ^ swz)) =
+                                make_uint4(w2[4 * x], w2[4 * x + 1], w2[4 * x + 2], w2[4 * x + 3]);
+                    } else {
+                        *reinterpret_cast<uint2*>(to + (at ^ swz)) = make_uint2(w2[0], w2[1]);
+                    }
+                }
+                fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.p_full);
@@ -542,14 +569,12 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 ok = false;
             }
             tc_fence_after();
-            if (active) {
 #pragma unroll
-                for (int x = 0; x < CPW; ++x) {
-                    float v = l[x];
+            for (int x = 0; x < CPT; ++x) {
+                float v = l[x];
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-                    if (lane == 0) c.part[quarter][half * CPW + x] = v;
-                }
+                for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+                if ((lane & 15) == 0) c.part[quarter][col + x] = v;
             }
             if (math_any(!ok)) break;
             const bool whole = w.j0 == 0 && (w.len == 0 || w.j1 == w.units);
@@ -557,7 +582,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             const int slot = 2 * blockIdx.x + (piece_no > 0 ? 1 : 0);
             float* part = p.parts + (int64_t)slot * NB * (2 + p.R);
             if (m < NB) {
-                const float sum = c.part[0][m] + c.part[1][m];
+                const float sum = c.part[0][m] + c.part[1][m] + c.part[2][m] + c.part[3][m];
                 c.factor[m] = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
                 if (!whole) {
                     part[m] = c.ref[m];
@@ -802,7 +827,7 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     const int64_t rows = a.q_len * a.heads;
     const int nb = rows_block(rows);
     const int64_t groups = (rows + nb - 1) / nb;
-    if (groups > 65535 || (__int128)a.n_seqs * ((a.N + BT - 1) / BT + 1) >= INT32_MAX) return false;
+    if (groups > 65535 || (__int128)a.n_seqs * (a.N / 32 + 1) >= INT32_MAX) return false;
     Params p{};
     p.Q = a.Q; p.hsQ = a.hsQ; p.tsQ = a.tsQ; p.bsQ = a.bsQ;
     p.cache = a.cache; p.rsC = a.rsC; p.psC = a.psC;
@@ -818,7 +843,7 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     p.scale_log2 = a.alpha * 1.4426950408889634f;
     p.causal = a.causal;
     const bool bf = a.type == SBGEMM_TYPE_BF16;
-    p.idesc_s = idesc16(bf, nb, false, false);
+    p.idesc_s = idesc16(bf, nb, false, false, 64);
     p.idesc_o = idesc16(bf, nb, true, true);
     // CTAs for each group of rows: an SM each, as far as the workspace has two
     // slots for every one of them; without it whole sequences.
@@ -834,14 +859,15 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
     }
     p.per_group = (int)each;
-    // Runs of rows that lie in one page wherever a block of 64 begins.
+    // Runs of rows that lie in one page wherever a block begins; whole groups
+    // of 8 rows, the swizzle's period.
     CUtensorMap map{};
-    int run = BT;
-    while (a.block_size % run != 0) run /= 2;
+    int run = nb == 64 ? Shape<64>::BT : Shape<32>::BT;
+    for (const int bt = run; a.block_size % run != 0 || bt % run != 0;) --run;
     const int64_t row_stride = a.block_size > 1 ? a.rsC : (a.R + a.P + 7) / 8 * 8;
     const int64_t page_stride = a.num_blocks > 1 ? a.psC : row_stride;
     const int64_t lim = (int64_t)1 << 39;
-    if (run >= 8 && row_stride > 0 && page_stride > 0 && row_stride < lim && page_stride < lim) {
+    if (run % 8 == 0 && row_stride > 0 && page_stride > 0 && row_stride < lim && page_stride < lim) {
         const uint64_t dims[3] = {(uint64_t)(a.R + a.P), (uint64_t)a.block_size, (uint64_t)a.num_blocks};
         const uint64_t strides[2] = {(uint64_t)row_stride * 2, (uint64_t)page_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)run, 1};

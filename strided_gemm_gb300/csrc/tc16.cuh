@@ -24,11 +24,12 @@ __device__ __forceinline__ int uniform_warp() { return __shfl_sync(~0u, (int)(th
 // A CTA that allocates all columns has them at address 0.
 constexpr uint32_t kTmemAll = 512, kTmemBase = 0;
 
-// kind::f16, D fp32, M = 128: N columns; *_mn: the operand's unit stride in
+// kind::f16, D fp32, M rows (128, or 64: accumulator row r in lane r / 16 * 32 +
+// r % 16) and N columns; *_mn: the operand's unit stride in
 // shared memory runs along M or N instead of K.
-__host__ __device__ constexpr uint32_t idesc16(bool bf16, int n, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc16(bool bf16, int n, bool a_mn, bool b_mn, int m = 128) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
-           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Shared-memory descriptor of a tile whose rows of 128 bytes (64 elements) are
