@@ -433,12 +433,12 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 for (int x = m; x < NB * p.chunks * 8; x += 256) {
                     const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
                     const int gr = group * NB + r, t = gr / p.heads, h = gr % p.heads;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (gr < p.rows && k < row_pieces)
-                        v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + w.s * p.bsQ + t * p.tsQ +
-                                                            h * p.hsQ + k * 8);
-                    *reinterpret_cast<uint4*>(sq + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = v;
+                    const bool read = gr < p.rows && k < row_pieces;
+                    const T* src = static_cast<const T*>(p.Q);
+                    if (read) src += w.s * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
+                    cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
                 }
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.q_full);
@@ -638,7 +638,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 // pieces: a thread takes four columns of a row over all of them, two rows of
 // 512 columns a block; many (one long sequence): eight warps share the pieces
 // of 128 columns of a row.
-constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 1024;
+constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 512;
 
 template <typename T>
 __device__ __forceinline__ void store4(T* o, float4 v) {
@@ -650,32 +650,43 @@ __device__ __forceinline__ void store4(T* o, float4 v) {
 
 template <typename T, int NB>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
-    __shared__ int list[kMaxJoins], found;
+    // The split sequences, those of few pieces from the front and those of many
+    // from the back, in the order of the CTAs in which they begin: every block
+    // has the same list.
+    __shared__ Join list[kMaxJoins];
+    __shared__ int few, many;
     __shared__ float4 sums[8][32];
     __shared__ float tops[8], ls[8];
-    // The CTAs in which split sequences begin, in order: every block has the same list.
     const int ctas = p.groups * p.per_group;
     if (threadIdx.x < 32) {
-        int n = 0;
+        const unsigned below = (1u << threadIdx.x) - 1;
+        int nf = 0, nm = 0;
         for (int c0 = 0; c0 < ctas; c0 += 32) {
             const int c = c0 + threadIdx.x;
-            const bool begins = c < ctas && p.joins[c].seq >= 0;
-            const unsigned all = __ballot_sync(~0u, begins);
-            if (begins) list[n + __popc(all & ((1u << threadIdx.x) - 1))] = c;
-            n += __popc(all);
+            Join jn{-1, 0, 0, 0};
+            if (c < ctas) jn = p.joins[c];
+            const bool is_few = jn.seq >= 0 && jn.last - jn.member < kFewPieces;
+            const bool is_many = jn.seq >= 0 && !is_few;
+            const unsigned f = __ballot_sync(~0u, is_few), g = __ballot_sync(~0u, is_many);
+            // The slot names the CTA and with it the group of rows.
+            if (is_few) list[nf + __popc(f & below)] = jn;
+            if (is_many) list[kMaxJoins - 1 - (nm + __popc(g & below))] = jn;
+            nf += __popc(f);
+            nm += __popc(g);
         }
-        if (threadIdx.x == 0) found = n;
+        if (threadIdx.x == 0) {
+            few = nf;
+            many = nm;
+        }
     }
     __syncthreads();
     const int per_row = p.R / 4;                             // threads a row
     const int64_t slot_floats = (int64_t)NB * (2 + p.R);
     const int steps = (NB * per_row + kJoinThreads - 1) / kJoinThreads;
-    for (int64_t it = blockIdx.x; it < (int64_t)found * steps; it += gridDim.x) {
-        const int cta = list[it / steps], group = cta % p.groups;
-        const Join jn = p.joins[cta];
-        const int pieces = jn.last - jn.member + 1;
-        if (pieces > kFewPieces) continue;
-        const int at = (int)(it % steps) * kJoinThreads + threadIdx.x;
+    for (int it = blockIdx.x; it < few * steps; it += gridDim.x) {
+        const Join jn = list[it / steps];
+        const int group = (jn.slot >> 1) % p.groups, pieces = jn.last - jn.member + 1;
+        const int at = it % steps * kJoinThreads + threadIdx.x;
         const int row = at / per_row, e = at % per_row * 4, r = group * NB + row;
         if (row >= NB || r >= p.rows) continue;
         const float* src[kFewPieces];
@@ -707,12 +718,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarters = p.R / 128;
-    for (int64_t it = blockIdx.x; it < (int64_t)found * NB * quarters; it += gridDim.x) {
-        const int cta = list[it / (NB * quarters)], group = cta % p.groups;
-        const Join jn = p.joins[cta];
-        const int pieces = jn.last - jn.member + 1;
-        const int row = (int)(it / quarters % NB), e = (int)(it % quarters) * 128 + lane * 4, r = group * NB + row;
-        if (pieces <= kFewPieces || r >= p.rows) continue;
+    for (int it = blockIdx.x; it < many * NB * quarters; it += gridDim.x) {
+        const Join jn = list[kMaxJoins - 1 - it / (NB * quarters)];
+        const int group = (jn.slot >> 1) % p.groups, pieces = jn.last - jn.member + 1;
+        const int row = it / quarters % NB, e = it % quarters * 128 + lane * 4, r = group * NB + row;
+        if (r >= p.rows) continue;
         auto piece = [&](int k) {
             const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
             return p.parts + slot * slot_floats;
