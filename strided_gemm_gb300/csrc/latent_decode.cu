@@ -426,10 +426,9 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         int i = 0, piece_no = 0, used = 0;                   // blocks, pieces, units so far
         bool ok = true;
         Join join{-1, 0, 0, 0};
-        while (w.next(p, group == 0)) {
-            const int n = w.j1 - w.j0;
-            if (m < NB) c.ref[m] = -INFINITY;
-            if (n > 0) {
+        // Queries of the walk's piece on their way into shared memory.
+        auto fetch_queries = [&](const Walk<BT>& w) {
+            if (w.j1 > w.j0) {
                 for (int x = m; x < NB * p.chunks * 8; x += 256) {
                     const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
                     const int gr = group * NB + r, t = gr / p.heads, h = gr % p.heads;
@@ -438,7 +437,17 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     if (read) src += w.s * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
                     cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
                 }
-                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        bool more = w.next(p, group == 0);
+        if (more) fetch_queries(w);
+        while (more) {
+            const Walk<BT> now = w;          // this piece; the walk looks one ahead
+            const int n = now.j1 - now.j0;
+            if (m < NB) c.ref[m] = -INFINITY;
+            if (n > 0) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.q_full);
@@ -466,13 +475,13 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         a[x] = (lane < 16 ? v[x] : other) * p.scale_log2;
                     }
                 }
-                const int first = (w.j0 + j) * BT;
-                const int safe = p.causal ? w.len - p.q_len : w.len - 1;    // keys up to here: every row's
+                const int first = (now.j0 + j) * BT;
+                const int safe = p.causal ? now.len - p.q_len : now.len - 1;    // keys up to here: every row's
                 const bool edge = first + BT - 1 > safe;
                 if (edge || !mine) {
 #pragma unroll
                     for (int x = 0; x < CPT; ++x) {
-                        int limit = w.len - 1;
+                        int limit = now.len - 1;
                         if (p.causal) {
                             const int r = group * NB + col + x;
                             if (r < p.rows) limit = safe + r / p.heads;
@@ -562,6 +571,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 if (lane == 0) mbar_arrive(&c.p_full);
             }
             if (failed) break;
+            // Every score of the piece is done (its last weights are written):
+            // the next one's queries may come in under the rest.
+            more = w.next(p, group == 0);
+            if (more) fetch_queries(w);
 
             // The piece is done: its sums, then O^T out of TMEM.
             if (n > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
@@ -577,7 +590,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 if ((lane & 15) == 0) c.part[quarter][col + x] = v;
             }
             if (math_any(!ok)) break;
-            const bool whole = w.j0 == 0 && (w.len == 0 || w.j1 == w.units);
+            const bool whole = now.j0 == 0 && (now.len == 0 || now.j1 == now.units);
             // A split sequence: this CTA's first piece goes to slot 0, its last to slot 1.
             const int slot = 2 * blockIdx.x + (piece_no > 0 ? 1 : 0);
             float* part = p.parts + (int64_t)slot * NB * (2 + p.R);
@@ -592,7 +605,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             math_sync();
             if (m < NB) {
                 const int r = group * NB + m, t = r / p.heads, h = r % p.heads;
-                c.out[m] = r < p.rows ? w.s * p.bsO + t * p.tsO + h * p.hsO : -1;
+                c.out[m] = r < p.rows ? now.s * p.bsO + t * p.tsO + h * p.hsO : -1;
             }
             math_sync();
             constexpr int W = NB < 32 ? NB : 32;
@@ -611,10 +624,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         else if (c.out[x0 + x] >= 0) static_cast<T*>(p.O)[c.out[x0 + x] + e] = from_float<T>(v);
                     }
                 }
-            if (w.j0 == 0 && !whole) {
+            if (now.j0 == 0 && !whole) {
                 // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
-                const int64_t end = (int64_t)lo + used + w.units;
-                join = Join{w.s, slot, member, (int)((end * members + units_total - 1) / units_total) - 1};
+                const int64_t end = (int64_t)lo + used + now.units;
+                join = Join{now.s, slot, member, (int)((end * members + units_total - 1) / units_total) - 1};
             }
             used += max(n, 1);
             tc_fence_before();
@@ -623,6 +636,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             math_sync();                                         // c.* is free for the next piece
             ++piece_no;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");   // on a failure too: shared memory outlives them
         if (p.split && m == 0) p.joins[blockIdx.x] = join;
     }
     tc_fence_before();
@@ -658,25 +672,47 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     __shared__ float4 sums[8][32];
     __shared__ float tops[8], ls[8];
     const int ctas = p.groups * p.per_group;
-    if (threadIdx.x < 32) {
-        const unsigned below = (1u << threadIdx.x) - 1;
-        int nf = 0, nm = 0;
-        for (int c0 = 0; c0 < ctas; c0 += 32) {
-            const int c = c0 + threadIdx.x;
-            Join jn{-1, 0, 0, 0};
-            if (c < ctas) jn = p.joins[c];
-            const bool is_few = jn.seq >= 0 && jn.last - jn.member < kFewPieces;
-            const bool is_many = jn.seq >= 0 && !is_few;
-            const unsigned f = __ballot_sync(~0u, is_few), g = __ballot_sync(~0u, is_many);
-            // The slot names the CTA and with it the group of rows.
-            if (is_few) list[nf + __popc(f & below)] = jn;
-            if (is_many) list[kMaxJoins - 1 - (nm + __popc(g & below))] = jn;
-            nf += __popc(f);
-            nm += __popc(g);
+    __shared__ int counts[2][kMaxJoins / 32];
+    {
+        const int lane = threadIdx.x & 31;
+        const unsigned below = (1u << lane) - 1;
+        Join jn[kMaxJoins / kJoinThreads];
+        unsigned f[kMaxJoins / kJoinThreads], g[kMaxJoins / kJoinThreads];
+#pragma unroll
+        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
+            const int c = k * kJoinThreads + threadIdx.x;
+            jn[k] = Join{-1, 0, 0, 0};
+            if (c < ctas) jn[k] = p.joins[c];
         }
-        if (threadIdx.x == 0) {
-            few = nf;
-            many = nm;
+#pragma unroll
+        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
+            const bool is_few = jn[k].last - jn[k].member < kFewPieces;
+            f[k] = __ballot_sync(~0u, jn[k].seq >= 0 && is_few);
+            g[k] = __ballot_sync(~0u, jn[k].seq >= 0 && !is_few);
+            if (lane == 0) {
+                counts[0][k * (kJoinThreads / 32) + (threadIdx.x >> 5)] = __popc(f[k]);
+                counts[1][k * (kJoinThreads / 32) + (threadIdx.x >> 5)] = __popc(g[k]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
+            int nf = 0, nm = 0, tf = 0, tm = 0;
+            for (int q = 0; q < kMaxJoins / 32; ++q) {
+                const bool before = q < k * (kJoinThreads / 32) + (int)(threadIdx.x >> 5);
+                if (before) {
+                    nf += counts[0][q];
+                    nm += counts[1][q];
+                }
+                tf += counts[0][q];
+                tm += counts[1][q];
+            }
+            if (f[k] >> lane & 1) list[nf + __popc(f[k] & below)] = jn[k];
+            if (g[k] >> lane & 1) list[kMaxJoins - 1 - (nm + __popc(g[k] & below))] = jn[k];
+            if (threadIdx.x == 0) {
+                few = tf;
+                many = tm;
+            }
         }
     }
     __syncthreads();
