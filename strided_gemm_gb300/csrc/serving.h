@@ -57,6 +57,9 @@ struct LatentPacked {
 bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err);
 size_t latent_decode_workspace_bytes(int sms);
 unsigned int read_and_clear_status_latent_decode(cudaStream_t stream);
+// On the tensor cores, over packed sequences (latent_prompt.cu); false likewise.
+bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_t* err);
+unsigned int read_and_clear_status_latent_prompt(cudaStream_t stream);
 // One warp a query row, any sizes and alignments (latent_rows.cu).
 constexpr int64_t kLatentMaxQK = 640, kLatentMaxV = 512;
 cudaError_t launch_latent_rows_paged(const LatentPaged& a, cudaStream_t stream);

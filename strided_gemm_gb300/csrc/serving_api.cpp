@@ -210,6 +210,7 @@ int check_pool_memory(const PoolView& v, std::initializer_list<Bytes> inputs, co
 
 unsigned int read_and_clear_status_serving(cudaStream_t stream) {
     const unsigned int codes[] = {read_and_clear_status_half_tc(stream), read_and_clear_status_latent_decode(stream),
+                                  read_and_clear_status_latent_prompt(stream),
                                   read_and_clear_status_latent_rows(stream), read_and_clear_status_pages(stream)};
     for (unsigned int c : codes)
         if (c) return c;
@@ -357,6 +358,8 @@ int sbgemm_latent_attention(
     if (const int m = in_device_memory({sq, sk, sr, sv, so, s0, s1})) return m;
     const LatentPacked a{type, Q, hsQ, tsQ, total_q, K_nope, hsK, tsK, K_rope, tsR, V, hsV, tsV, total_k,
                          q_starts, k_starts, n_seqs, max_q, O, hsO, tsO, heads, Dn, P, Dv, alpha, causal};
+    cudaError_t e = cudaSuccess;
+    if (launch_latent_prompt(a, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_latent_rows_packed(a, static_cast<cudaStream_t>(stream)));
 }
 
