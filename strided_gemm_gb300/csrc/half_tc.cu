@@ -118,7 +118,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                 const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
                 for (int j = 0; j < p.k_blocks; ++j, ++i) {
                     const int s = (int)(i % S::kStages);
-                    if (i >= S::kStages && !mbar_wait(&empty[s], (uint32_t)((i / S::kStages - 1) & 1))) {
+                    if (i >= S::kStages && !bar_wait(&empty[s], (uint32_t)((i / S::kStages - 1) & 1))) {
                         record_status(&g_wait_status, kWaitEmpty);
                         ok = false;
                         break;
@@ -142,7 +142,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             }
             // Copies still landing keep the CTA's shared memory.
             for (int64_t q = i > S::kStages ? i - S::kStages : 0; q < i; ++q)
-                if (!mbar_wait(&full[q % S::kStages], (uint32_t)((q / S::kStages) & 1))) {
+                if (!bar_wait(&full[q % S::kStages], (uint32_t)((q / S::kStages) & 1))) {
                     record_status(&g_wait_status, kWaitDrain);
                     break;
                 }
@@ -154,14 +154,14 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             int n = 0;                             // tiles begun
             bool ok = true;
             for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++n) {
-                if (n >= 2 && !mbar_wait(&acc_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) {
+                if (n >= 2 && !bar_wait(&acc_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) {
                     record_status(&g_wait_status, kWaitAccFree);
                     break;
                 }
                 const uint32_t acc = kTmemBase + (uint32_t)(n & 1) * NT;
                 for (int j = 0; j < p.k_blocks; ++j, ++i) {
                     const int s = (int)(i % S::kStages);
-                    if (!mbar_wait(&full[s], (uint32_t)((i / S::kStages) & 1))) {
+                    if (!bar_wait(&full[s], (uint32_t)((i / S::kStages) & 1))) {
                         record_status(&g_wait_status, kWaitFull);
                         ok = false;
                         break;
@@ -181,7 +181,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             }
             // Nothing may still be writing TMEM when it is freed.
             mma_commit(&done);
-            if (!mbar_wait(&done, 0)) record_status(&g_wait_status, kWaitMma);
+            if (!bar_wait(&done, 0)) record_status(&g_wait_status, kWaitMma);
         }
     } else {
         // The way out in chunks of 64 accumulator columns (32 where NT is).
@@ -191,7 +191,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
         for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
             int x0, y0, b;
             place(t, &x0, &y0, &b);
-            const bool in = mbar_wait(&acc_full[n & 1], (uint32_t)((n / 2) & 1));
+            const bool in = bar_wait(&acc_full[n & 1], (uint32_t)((n / 2) & 1));
             if (!in) record_status(&g_wait_status, kWaitMma);
             if (!all_of_group(in)) break;          // they meet at barriers below: all go on or none
             tc_fence_after();

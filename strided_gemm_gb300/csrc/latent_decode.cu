@@ -94,7 +94,7 @@ struct Params {
 template <int NB>
 struct Ctl {
     uint64_t full[Shape<NB>::kStages], empty[Shape<NB>::kStages];
-    uint64_t q_full, s_full[2], p_full, pv_done, o_free, done;
+    uint64_t q_full, s_full[2], p_full, o_free, done;
     uint32_t tmem_base;
     int seq0, tile0, count;                  // this CTA's run of the list
     int scan[kWarps];
@@ -185,7 +185,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         mbar_init(&c.q_full, kMathWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&c.s_full[i], 1);
         mbar_init(&c.p_full, kMathWarps);
-        mbar_init(&c.pv_done, 1);
         mbar_init(&c.o_free, kMathWarps);
         mbar_init(&c.done, 1);
         fence_mbar_init();
@@ -275,7 +274,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             page = p.num_blocks;
                         }
                     }
-                    if (i >= kStages && !mbar_wait(&c.empty[st], ph_empty)) {
+                    if (i >= kStages && !bar_wait(&c.empty[st], ph_empty)) {
                         record_status(&g_wait_status, kWaitEmpty);
                         ok = false;
                     }
@@ -305,7 +304,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             record_status(&g_wait_status, kPagedInput);
                     }
                 }
-                if (i >= kStages && !mbar_wait(&c.empty[st], ph_empty)) {
+                if (i >= kStages && !bar_wait(&c.empty[st], ph_empty)) {
                     record_status(&g_wait_status, kWaitEmpty);
                     ok = false;
                 }
@@ -328,7 +327,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             }
         }
         // Copies still landing keep the CTA's shared memory.
-        if (landing && !mbar_wait(&c.full[st], (uint32_t)(((landing - 1) / kStages) & 1)))
+        if (landing && !bar_wait(&c.full[st], (uint32_t)(((landing - 1) / kStages) & 1)))
             record_status(&g_wait_status, kWaitDrain);
     } else if (warp == kMmaWarp) {
         // ---- MMAs ------------------------------------------------------------------
@@ -359,8 +358,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             while (ok && w.next(p)) {
                 const int n = w.j1 - w.j0;
                 if (n == 0) continue;        // an empty sequence
-                if (!mbar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
-                    !mbar_wait(&c.full[i % kStages], (uint32_t)((i / kStages) & 1))) {
+                if (!bar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
+                    !bar_wait(&c.full[i % kStages], (uint32_t)((i / kStages) & 1))) {
                     timed_out(kWaitFull);
                     break;
                 }
@@ -370,19 +369,19 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     // this block's P V does not wait for them.
                     bool ahead = j + 1 >= n;
                     const uint32_t ph_next = (uint32_t)(((i + 1) / kStages) & 1);
-                    const uint64_t t0 = global_timer_ns();
+                    const long long t0 = clock64();
                     while (!mbar_try_wait(&c.p_full, (uint32_t)(i & 1))) {
                         if (!ahead && mbar_try_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             scores(i + 1);
                             ahead = true;
                         }
-                        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+                        if (clock64() - t0 > kWaitCycles) {
                             timed_out(kWaitMma);
                             break;
                         }
                     }
                     if (!ok) break;
-                    if (j == 0 && filled > 0 && !mbar_wait(&c.o_free, (uint32_t)((filled - 1) & 1))) {
+                    if (j == 0 && filled > 0 && !bar_wait(&c.o_free, (uint32_t)((filled - 1) & 1))) {
                         timed_out(kWaitAccFree);
                         break;
                     }
@@ -396,9 +395,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                                      (j | x) ? 1u : 0u);
                     }
                     mma_commit(&c.empty[i % kStages]);
-                    mma_commit(&c.pv_done);
                     if (!ahead) {
-                        if (!mbar_wait(&c.full[(i + 1) % kStages], ph_next)) {
+                        if (!bar_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             timed_out(kWaitFull);
                             break;
                         }
@@ -409,7 +407,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             }
             // Nothing may still be writing TMEM when it is freed.
             mma_commit(&c.done);
-            if (!mbar_wait(&c.done, 0)) record_status(&g_wait_status, kWaitMma);
+            if (!bar_wait(&c.done, 0)) record_status(&g_wait_status, kWaitMma);
         }
     } else if (warp >= kMathWarp) {
         // ---- queries, softmax, output ------------------------------------------------
@@ -440,6 +438,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // P V of block number b is done: its weights are read and O is settled.
+        auto pv_done = [&](int b) { return bar_wait(&c.empty[b % kStages], (uint32_t)((b / kStages) & 1)); };
         bool more = w.next(p, group == 0);
         if (more) fetch_queries(w);
         while (more) {
@@ -459,7 +459,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             for (int x = 0; x < CPT; ++x) l[x] = 0.0f;
             bool failed = false;
             for (int j = 0; j < n; ++j, ++i) {
-                if (!mbar_wait(&c.s_full[i & 1], (uint32_t)((i >> 1) & 1))) {
+                if (!bar_wait(&c.s_full[i & 1], (uint32_t)((i >> 1) & 1))) {
                     record_status(&g_wait_status, kWaitMma);
                     ok = false;
                 }
@@ -516,7 +516,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 #pragma unroll
                     for (int x = 0; x < CPT; ++x) l[x] *= c.factor[col + x];
                     if (j > 0) {
-                        if (!mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                        if (!pv_done(i - 1)) {
                             record_status(&g_wait_status, kWaitMma);
                             ok = false;
                         }
@@ -549,7 +549,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     w2[x / 2] = pack2<T>(p0, p1);
                 }
                 // The block before has read its weights.
-                if (i > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+                if (i > 0 && !pv_done(i - 1)) {
                     record_status(&g_wait_status, kWaitMma);
                     ok = false;
                 }
@@ -577,7 +577,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             if (more) fetch_queries(w);
 
             // The piece is done: its sums, then O^T out of TMEM.
-            if (n > 0 && !mbar_wait(&c.pv_done, (uint32_t)((i - 1) & 1))) {
+            if (n > 0 && !pv_done(i - 1)) {
                 record_status(&g_wait_status, kWaitMma);
                 ok = false;
             }

@@ -17,9 +17,14 @@
 // tile coming in say that its P V before them is done.
 //
 // Shared memory holds Q (96 KB at 192 dimensions) and a ring of eight 16 KB
-// pieces, 128 keys x 64 dimensions each, of K_0, V_0, K_1, V_1, ...: a piece
-// is released as soon as both tiles have read it, which lets five pieces of a
-// block be followed by three of the next.  Two whole stages would not fit.
+// pieces, 128 keys x 64 dimensions each, of K_0, V_0, K_1, V_1, ...: a block's
+// K is free once both tiles have its scores, its V once both P V are done,
+// which lets five pieces of a block be followed by three of the next.  Two
+// whole stages would not fit.  A commit that follows another one without MMAs
+// between them holds the issue up for about 360 cycles (a barrier for each
+// piece: 549 us where XX now, 3 sequences of up to 4096 queries, 32 heads), so
+// every commit serves all that wait for it: the scores of the last tile tell
+// its softmax and the TMA warp.
 //
 // Roles (12 warps, all waits bounded): warp 0 TMA, warp 1 MMAs, warps 4-7 and
 // 8-11 the rows of the two tiles.  In the last block they also zero the rows of
@@ -30,6 +35,7 @@
 // 20 MMAs of 66 cycles; the exponentials come next (16 a cycle and SM).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "serving.h"
 #include "tc16.cuh"
@@ -65,7 +71,7 @@ struct Params {
 struct Smem {
     alignas(1024) uint8_t q[kTiles][kQPieces][kPiece];
     alignas(1024) uint8_t ring[kSlots][kPiece];
-    uint64_t q_full, full[kSlots], empty[kSlots];
+    uint64_t q_full, k_full[2], v_full[2], v_empty;     // of even and odd blocks
     uint64_t s_full[kTiles], p_full[kTiles], o_done[kTiles], v_clean, done;
     uint32_t tmem_base;
 };
@@ -81,7 +87,9 @@ __device__ __forceinline__ bool packed_range(const int32_t* starts, int s, int t
     return a == x && b == y && *n == y - x;
 }
 
-template <typename T>
+// Whole: three pieces of K and two of V, every one of 64 columns (128 + 64
+// dimensions of keys, 128 of values), known to the compiler.
+template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ CUtensorMap tqr,
               const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tkr,
@@ -99,23 +107,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
     if (!good && threadIdx.x == 0) record_status(&g_wait_status, kPagedInput);
     const int m0 = qb * (kTiles * BM);
     if (m0 >= nq) return;
-    int nb[kTiles], blocks = 0;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
+    // Blocks of each tile.
+    auto blocks_of = [&](int t) {
         const int first = m0 + t * BM, last = min(first + BM, nq) - 1;
         int keys = first < nq ? nk : 0;
         if (p.causal) keys = min(keys, max(0, last + nk - nq + 1));
-        nb[t] = (keys + BN - 1) / BN;
-        blocks = max(blocks, nb[t]);
-    }
-    const int k_pieces = p.n_pieces + p.rope, per_block = k_pieces + p.v_pieces;
+        return (keys + BN - 1) / BN;
+    };
+    const int nb0 = blocks_of(0), nb1 = blocks_of(1), blocks = max(nb0, nb1);
+    const int last_tile = nb1 > 0 ? 1 : 0;       // it has every block that any tile has
+    const int k_pieces = kWhole ? 3 : p.n_pieces + p.rope, v_pieces = kWhole ? 2 : p.v_pieces;
+    const int per_block = k_pieces + v_pieces;
 
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.v_full[s], 1);
         }
+        mbar_init(&sh.v_empty, 1);
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(&sh.s_full[t], 1);
             mbar_init(&sh.p_full[t], 4);
@@ -143,70 +153,109 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
     if (warp == 0) {
         // ---- TMA ----------------------------------------------------------------
         if (lane == 0 && blocks > 0) {
-            int tiles = 0;
-            for (int t = 0; t < kTiles; ++t) tiles += nb[t] > 0;
-            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * k_pieces * kPiece));
+            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(((nb0 > 0) + (nb1 > 0)) * k_pieces * kPiece));
+#pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                if (nb[t] == 0) continue;
-                for (int c = 0; c < p.n_pieces; ++c)
+                if ((t == 0 ? nb0 : nb1) == 0) continue;
+                for (int c = 0; c < k_pieces - p.rope; ++c)
                     tma_load_3d(sh.q[t][c], &tqn, &sh.q_full, 64 * c, head, q0 + m0 + t * BM);
                 if (p.rope) tma_load_3d(sh.q[t][p.n_pieces], &tqr, &sh.q_full, 0, head, q0 + m0 + t * BM);
             }
-            int i = 0;
-            const int total = blocks * per_block;
-            for (int j = 0; i < total; ++j) {
+            // The piece that was in a slot before: of a K, free with the last
+            // tile's scores of its block, or of a V, free with its P V.
+            int k_free = 0, v_free = 0;              // blocks known to be free
+            int old = -kSlots, old_block = 0, old_piece = 0;
+            bool ok = true;
+            auto need_k = [&](int b) {               // blocks come here in order, none left out
+                if (ok && b >= k_free) {
+                    ok = bar_wait(&sh.s_full[last_tile], (uint32_t)(b & 1));
+                    k_free = b + 1;
+                }
+            };
+            auto need_v = [&](int b) {
+                if (ok && b >= v_free) {
+                    ok = bar_wait(&sh.v_empty, (uint32_t)(b & 1));
+                    v_free = b + 1;
+                }
+            };
+            auto next_slot = [&](int i) {
+                if (old >= 0) {
+                    if (old_piece < k_pieces) need_k(old_block);
+                    else need_v(old_block);
+                    if (++old_piece == per_block) {
+                        old_piece = 0;
+                        ++old_block;
+                    }
+                }
+                ++old;
+                return sh.ring[i & (kSlots - 1)];
+            };
+            int i = 0, j = 0;
+            for (; j < blocks && ok; ++j) {
                 const int n0 = k0 + j * BN;
-                bool ok = true;
+                uint64_t* kb = &sh.k_full[j & 1];
+                uint64_t* vb = &sh.v_full[j & 1];
                 for (int c = 0; c < per_block; ++c, ++i) {
-                    const int s = i % kSlots;
-                    if (i >= kSlots && !mbar_wait(&sh.empty[s], (uint32_t)((i / kSlots - 1) & 1))) {
+                    // The last block on this one's barriers is through.
+                    if (j >= 2 && c == 0) need_k(j - 2);
+                    if (j >= 2 && c == k_pieces) need_v(j - 2);
+                    uint8_t* dst = next_slot(i);
+                    if (!ok) {
                         record_status(&g_wait_status, kWaitEmpty);
-                        ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sh.full[s], kPiece);
-                    if (c < p.n_pieces) tma_load_3d(sh.ring[s], &tkn, &sh.full[s], 64 * c, head, n0);
-                    else if (c < k_pieces) tma_load_3d(sh.ring[s], &tkr, &sh.full[s], 0, 0, n0);
-                    else tma_load_3d(sh.ring[s], &tv, &sh.full[s], 64 * (c - k_pieces), head, n0);
+                    if (c == 0) mbar_arrive_expect_tx(kb, (uint32_t)(k_pieces * kPiece));
+                    if (c == k_pieces) mbar_arrive_expect_tx(vb, (uint32_t)(v_pieces * kPiece));
+                    if (c < k_pieces - p.rope) tma_load_3d(dst, &tkn, kb, 64 * c, head, n0);
+                    else if (c < k_pieces) tma_load_3d(dst, &tkr, kb, 0, 0, n0);
+                    else tma_load_3d(dst, &tv, vb, 64 * (c - k_pieces), head, n0);
                 }
-                if (!ok) break;
             }
-            // Copies still landing keep the CTA's shared memory.
-            for (int q = i > kSlots ? i - kSlots : 0; q < i; ++q)
-                if (!mbar_wait(&sh.full[q % kSlots], (uint32_t)((q / kSlots) & 1))) {
+            // Copies still landing keep the CTA's shared memory (of the blocks
+            // before the last two the MMAs have seen every one).
+            for (int q = max(0, j - 2); ok && q < j; ++q)
+                if (!bar_wait(&sh.k_full[q & 1], (uint32_t)((q >> 1) & 1)) ||
+                    !bar_wait(&sh.v_full[q & 1], (uint32_t)((q >> 1) & 1))) {
                     record_status(&g_wait_status, kWaitDrain);
                     break;
                 }
-            if (!mbar_wait(&sh.q_full, 0)) record_status(&g_wait_status, kWaitDrain);
+            if (!bar_wait(&sh.q_full, 0)) record_status(&g_wait_status, kWaitDrain);
         }
     } else if (warp == 1) {
         // ---- MMAs -----------------------------------------------------------------
+        // One thread's chain of waits and issues: every instruction between two
+        // MMAs is latency (a wait that is over costs some 250 cycles with its
+        // address arithmetic), so there is one barrier a block for K and for V,
+        // and slots follow by additions.
         if (elect_one()) {
             bool ok = true;
             const uint32_t q_lo = smem_u32(sh.q), ring_lo = smem_u32(sh.ring);
-            auto wait_piece = [&](int i) {
-                if (ok && !mbar_wait(&sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1))) {
-                    record_status(&g_wait_status, kWaitFull);
-                    ok = false;
-                }
+            auto fail = [&](unsigned int code) {
+                record_status(&g_wait_status, code);
+                ok = false;
             };
-            // S_t of block j.
-            auto scores = [&](int t, int j) {
-                if (j >= nb[t]) return;
-                const int first = j * per_block;
-                for (int c = 0; c < k_pieces; ++c) {
-                    wait_piece(first + c);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t da = desc16(q_lo + (t * kQPieces + c) * kPiece);
-                    const uint64_t db = desc16(ring_lo + (first + c) % kSlots * kPiece);
-                    const int steps = c < p.n_pieces - 1 ? 4 : c == p.n_pieces - 1 ? p.n_steps : p.r_steps;
-                    if (steps == 4) {
+            // S_t of block j, whose K begins at slot `s`.
+            auto scores = [&](auto tile, int j, uint32_t s) {
+                constexpr int t = decltype(tile)::value;
+                if (j >= (t == 0 ? nb0 : nb1)) return;
+                if ((t == 0 || j >= nb0) && !bar_wait(&sh.k_full[j & 1], (uint32_t)((j >> 1) & 1)))
+                    return fail(kWaitFull);
+                tc_fence_after();
+                if constexpr (kWhole) {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const uint64_t da = desc16(q_lo + (t * kQPieces + c) * kPiece);
+                        const uint64_t db = desc16(ring_lo + ((s + c) & (kSlots - 1)) * kPiece);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             mma16_ss(tmem + kColS + t * BN, da + x * kStepK, db + x * kStepK, p.idesc_s,
                                      (c | x) ? 1u : 0u);
-                    } else {
+                    }
+                } else {
+                    for (int c = 0; c < k_pieces; ++c) {
+                        const uint64_t da = desc16(q_lo + (t * kQPieces + c) * kPiece);
+                        const uint64_t db = desc16(ring_lo + ((s + c) & (kSlots - 1)) * kPiece);
+                        const int steps = c < p.n_pieces - 1 ? 4 : c == p.n_pieces - 1 ? p.n_steps : p.r_steps;
                         for (int x = 0; x < steps; ++x)
                             mma16_ss(tmem + kColS + t * BN, da + x * kStepK, db + x * kStepK, p.idesc_s,
                                      (c | x) ? 1u : 0u);
@@ -214,68 +263,62 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                 }
                 mma_commit(&sh.s_full[t]);
             };
-            auto release = [&](int first, int n) {
-                for (int c = 0; c < n; ++c) mma_commit(&sh.empty[(first + c) % kSlots]);
+            // O_t += P_t V of block j, whose V begins at slot `s`.
+            auto values = [&](auto tile, int j, uint32_t s) {
+                constexpr int t = decltype(tile)::value;
+                const int n = t == 0 ? nb0 : nb1;
+                if (j >= n) return;
+                if (!bar_wait(&sh.p_full[t], (uint32_t)(j & 1))) return fail(kWaitMma);
+                tc_fence_after();
+                constexpr uint32_t d = tmem + kColO + t * BN, a = tmem + kColS + t * BN;
+                if (v_pieces == 1 || s + 1 < kSlots) {
+                    // V's pieces lie side by side: all columns at once.
+                    const uint64_t db = desc16(ring_lo + s * kPiece, kPiece);
+#pragma unroll
+                    for (int x = 0; x < BN / 16; ++x)
+                        mma16_ts(d, a + 8 * x, db + x * kStepMN, p.idesc_v, (j | x) ? 1u : 0u);
+                } else {
+                    const uint64_t d0 = desc16(ring_lo + s * kPiece), d1 = desc16(ring_lo);
+#pragma unroll
+                    for (int x = 0; x < BN / 16; ++x)
+                        mma16_ts(d, a + 8 * x, d0 + x * kStepMN, p.idesc_v_half, (j | x) ? 1u : 0u);
+#pragma unroll
+                    for (int x = 0; x < BN / 16; ++x)
+                        mma16_ts(d + 64, a + 8 * x, d1 + x * kStepMN, p.idesc_v_tail, (j | x) ? 1u : 0u);
+                }
+                if (j == n - 1) mma_commit(&sh.o_done[t]);
+                else if (t == last_tile) mma_commit(&sh.v_empty);
             };
+            constexpr std::integral_constant<int, 0> t0{};
+            constexpr std::integral_constant<int, 1> t1{};
             if (blocks > 0) {
-                if (!mbar_wait(&sh.q_full, 0)) {
-                    record_status(&g_wait_status, kWaitFull);
-                    ok = false;
-                }
-                if (ok) scores(0, 0);
-                if (ok) scores(1, 0);
-                if (ok) release(0, k_pieces);
+                if (!bar_wait(&sh.q_full, 0)) fail(kWaitFull);
+                if (ok) scores(t0, 0, 0);
+                if (ok) scores(t1, 0, 0);
             }
+            uint32_t ks = 0;                         // slot of K_j's first piece
             for (int j = 0; j < blocks && ok; ++j) {
-                const int first = j * per_block + k_pieces;      // V_j's pieces
-                for (int c = 0; c < p.v_pieces; ++c) wait_piece(first + c);
-                if (ok && clean && j == blocks - 1 && !mbar_wait(&sh.v_clean, 0)) {
-                    record_status(&g_wait_status, kWaitFull);
-                    ok = false;
+                const uint32_t vs = (ks + k_pieces) & (kSlots - 1);
+                ks = (ks + per_block) & (kSlots - 1);
+                if (!bar_wait(&sh.v_full[j & 1], (uint32_t)((j >> 1) & 1)) ||
+                    (clean && j == blocks - 1 && !bar_wait(&sh.v_clean, 0))) {
+                    fail(kWaitFull);
+                    break;
                 }
-                for (int t = 0; t < kTiles && ok; ++t) {
-                    if (j < nb[t]) {
-                        if (!mbar_wait(&sh.p_full[t], (uint32_t)(j & 1))) {
-                            record_status(&g_wait_status, kWaitMma);
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t d = tmem + kColO + t * BN, a = tmem + kColS + t * BN;
-                        const int s = first % kSlots;
-                        if (p.v_pieces == 1 || s + 1 < kSlots) {
-                            // V's pieces lie side by side: all columns at once.
-                            const uint64_t db = desc16(ring_lo + s * kPiece, kPiece);
-#pragma unroll
-                            for (int x = 0; x < BN / 16; ++x)
-                                mma16_ts(d, a + 8 * x, db + x * kStepMN, p.idesc_v, (j | x) ? 1u : 0u);
-                        } else {
-                            const uint64_t d0 = desc16(ring_lo + s * kPiece), d1 = desc16(ring_lo);
-#pragma unroll
-                            for (int x = 0; x < BN / 16; ++x)
-                                mma16_ts(d, a + 8 * x, d0 + x * kStepMN, p.idesc_v_half, (j | x) ? 1u : 0u);
-#pragma unroll
-                            for (int x = 0; x < BN / 16; ++x)
-                                mma16_ts(d + 64, a + 8 * x, d1 + x * kStepMN, p.idesc_v_tail, (j | x) ? 1u : 0u);
-                        }
-                        if (j == nb[t] - 1) mma_commit(&sh.o_done[t]);
-                    }
-                    if (t == kTiles - 1) release(first, p.v_pieces);
-                    if (j + 1 < blocks) {
-                        scores(t, j + 1);
-                        if (t == kTiles - 1 && ok) release((j + 1) * per_block, k_pieces);
-                    }
-                }
+                values(t0, j, vs);
+                if (ok) scores(t0, j + 1, ks);
+                if (ok) values(t1, j, vs);
+                if (ok) scores(t1, j + 1, ks);
             }
             // Nothing may still be writing TMEM when it is freed.
             mma_commit(&sh.done);
-            if (!mbar_wait(&sh.done, 0)) record_status(&g_wait_status, kWaitMma);
+            if (!bar_wait(&sh.done, 0)) record_status(&g_wait_status, kWaitMma);
         }
     } else if (warp >= 4) {
         // ---- softmax and output, one row a thread ------------------------------------
         const int t = (warp - 4) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane, m = m0 + t * BM + row;      // in the sequence
-        const int n_blocks = t == 0 ? nb[0] : nb[1];
+        const int n_blocks = t == 0 ? nb0 : nb1;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_at = tmem + lanes + kColS + t * BN, o_at = tmem + lanes + kColO + t * BN;
         const int last = p.causal ? min(nk - 1, m + nk - nq) : nk - 1;   // last key the row sees
@@ -285,7 +328,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
         for (int j = 0; j < n_blocks; ++j) {
-            if (!mbar_wait(&sh.s_full[t], (uint32_t)(j & 1))) {
+            if (!bar_wait(&sh.s_full[t], (uint32_t)(j & 1))) {
                 record_status(&g_wait_status, kWaitMma);
                 ok = false;
                 break;
@@ -358,17 +401,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[t]);
-            if (clean && j == blocks - 1 && t == (nb[1] == blocks ? 1 : 0)) {
-                // These pieces are the ring's last: their phase is the slots' current one.
-                for (int c = 0; c < p.v_pieces; ++c) {
-                    const int i = j * per_block + k_pieces + c;
-                    if (!mbar_wait(&sh.full[i % kSlots], (uint32_t)((i / kSlots) & 1))) {
-                        record_status(&g_wait_status, kWaitFull);
-                        ok = false;
-                        break;
-                    }
+            if (clean && j == blocks - 1 && t == last_tile) {
+                // V_j - 2, the last one on this barrier, was read long ago: its
+                // phase is over and this one's is the current one.
+                if (!bar_wait(&sh.v_full[j & 1], (uint32_t)((j >> 1) & 1))) {
+                    record_status(&g_wait_status, kWaitFull);
+                    ok = false;
+                }
+                for (int c = 0; ok && c < v_pieces; ++c) {
                     // Whole rows: the swizzle stays inside a row's 128 bytes.
-                    uint4* rows = reinterpret_cast<uint4*>(sh.ring[i % kSlots]);
+                    uint4* rows = reinterpret_cast<uint4*>(sh.ring[(j * per_block + k_pieces + c) & (kSlots - 1)]);
                     for (int x = v_rows * 8 + row; x < BN * 8; x += BM) rows[x] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -376,7 +418,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                 if (lane == 0) mbar_arrive(&sh.v_clean);
             }
         }
-        if (ok && n_blocks > 0 && !mbar_wait(&sh.o_done[t], 0)) {
+        if (ok && n_blocks > 0 && !bar_wait(&sh.o_done[t], 0)) {
             record_status(&g_wait_status, kWaitMma);
             ok = false;
         }
@@ -435,13 +477,18 @@ cudaError_t launch(const CUtensorMap* m, const Params& p, int64_t n_seqs, cudaSt
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_done.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)kSmemBytes);
+        cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSmemBytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(prompt_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
     const dim3 grid((unsigned)(p.q_blocks * p.heads), (unsigned)n_seqs);
-    prompt_kernel<T><<<grid, kThreads, kSmemBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
+    const bool whole = p.n_pieces == 2 && p.rope && p.v_pieces == 2 && p.n_steps == 4 && p.r_steps == 4 && p.Dv == 128;
+    if (whole) prompt_kernel<T, true><<<grid, kThreads, kSmemBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
+    else prompt_kernel<T, false><<<grid, kThreads, kSmemBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
     return cudaGetLastError();
 }
 

@@ -21,6 +21,20 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
 
+// mbar_wait with its limit counted in SM cycles: reading the nanosecond timer
+// costs a wait that just misses its first look about 1000 cycles.
+constexpr long long kWaitCycles = 4000000000ll;      // about 2 s
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (clock64() - t0 < kWaitCycles);
+    return false;
+}
+
 // A CTA that allocates all columns has them at address 0.
 constexpr uint32_t kTmemAll = 512, kTmemBase = 0;
 
