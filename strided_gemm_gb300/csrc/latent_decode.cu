@@ -87,6 +87,7 @@ struct Params {
     float scale_log2;
     int causal;
     uint32_t idesc_s, idesc_o;
+    int o_vec;                               // rows of O take 8-byte stores
     Join* joins;                             // [groups * per_group]
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
 };
@@ -98,8 +99,9 @@ struct Ctl {
     uint32_t tmem_base;
     int seq0, tile0, count;                  // this CTA's run of the list
     int scan[kWarps];
-    float ref[NB], factor[NB];               // reference maxima; a rise's factors, then 1 / sum
-    union {
+    alignas(16) float ref[NB];               // reference maxima
+    alignas(16) float factor[NB];            // a rise's factors, then 1 / sum
+    union alignas(16) {
         float part[4][NB];                   // maxima or sums of the four key quarters
         int64_t out[NB];                     // element offset of a row of O (-1: none)
     };
@@ -193,6 +195,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         tmem_alloc(&c.tmem_base, kTmemAll);
         tmem_relinquish();
     }
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
     int members = 1, lo = 0, units_total = 0;
@@ -608,6 +612,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 c.out[m] = r < p.rows ? now.s * p.bsO + t * p.tsO + h * p.hsO : -1;
             }
             math_sync();
+            // (Each branch its own loop: the rows' factors and places are read as
+            // vectors, and one address runs over a piece's rows.)
             constexpr int W = NB < 32 ? NB : 32;
 #pragma unroll 1
             for (int t = half; t < tiles_o; t += 2)
@@ -617,11 +623,25 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     if (n > 0) tmem_ld<W>(tmem + lanes + kColO + t * NB + x0, o);
                     const int e = t * 128 + quarter * 32 + lane;
 #pragma unroll
-                    for (int x = 0; x < W; ++x) {
-                        const float f = c.factor[x0 + x];
-                        const float v = f == 0.0f ? 0.0f : o[x] * f;       // no key: zeros
-                        if (!whole) part[2 * NB + (int64_t)(x0 + x) * p.R + e] = v;
-                        else if (c.out[x0 + x] >= 0) static_cast<T*>(p.O)[c.out[x0 + x] + e] = from_float<T>(v);
+                    for (int x = 0; x < W; x += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&c.factor[x0 + x]);
+                        o[x] = f.x == 0.0f ? 0.0f : o[x] * f.x;                // no key: zeros
+                        o[x + 1] = f.y == 0.0f ? 0.0f : o[x + 1] * f.y;
+                        o[x + 2] = f.z == 0.0f ? 0.0f : o[x + 2] * f.z;
+                        o[x + 3] = f.w == 0.0f ? 0.0f : o[x + 3] * f.w;
+                    }
+                    if (!whole) {
+                        float* dst = part + 2 * NB + (int64_t)x0 * p.R + e;
+#pragma unroll
+                        for (int x = 0; x < W; ++x, dst += p.R) *dst = o[x];
+                    } else {
+                        T* dst = static_cast<T*>(p.O) + e;
+#pragma unroll
+                        for (int x = 0; x < W; x += 2) {
+                            const longlong2 at = *reinterpret_cast<const longlong2*>(&c.out[x0 + x]);
+                            if (at.x >= 0) dst[at.x] = from_float<T>(o[x]);
+                            if (at.y >= 0) dst[at.y] = from_float<T>(o[x + 1]);
+                        }
                     }
                 }
             if (now.j0 == 0 && !whole) {
@@ -655,15 +675,22 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 512;
 
 template <typename T>
-__device__ __forceinline__ void store4(T* o, float4 v) {
-    o[0] = from_float<T>(v.x);
-    o[1] = from_float<T>(v.y);
-    o[2] = from_float<T>(v.z);
-    o[3] = from_float<T>(v.w);
+__device__ __forceinline__ void store4(T* o, float4 v, bool vec) {
+    if (vec) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+    } else {
+        o[0] = from_float<T>(v.x);
+        o[1] = from_float<T>(v.y);
+        o[2] = from_float<T>(v.z);
+        o[3] = from_float<T>(v.w);
+    }
 }
 
 template <typename T, int NB>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+    // Launched while the pieces are still being made (the launch hides behind
+    // them): nothing of theirs is read before they are complete.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // The split sequences, those of few pieces from the front and those of many
     // from the back, in the order of the CTAs in which they begin: every block
     // has the same list.
@@ -751,7 +778,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
-               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), p.o_vec);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarters = p.R / 128;
     for (int it = blockIdx.x; it < many * NB * quarters; it += gridDim.x) {
@@ -822,7 +849,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
-                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), p.o_vec);
         }
     }
 }
@@ -846,7 +873,19 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
         attr_done.fetch_or(bit);
     }
     decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
-    if (p.split) join_kernel<T, NB><<<(unsigned)sms * 8, kJoinThreads, 0, stream>>>(p);
+    if (p.split) {
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)sms * 8);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.stream = stream;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T, NB>, p);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 
@@ -883,6 +922,7 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     p.num_blocks = (int)a.num_blocks; p.block_size = (int)a.block_size;
     p.q_len = (int)a.q_len; p.heads = (int)a.heads; p.rows = (int)rows;
     p.N = (int)a.N; p.R = (int)a.R; p.P = (int)a.P; p.n_seqs = (int)a.n_seqs;
+    p.o_vec = reinterpret_cast<uintptr_t>(a.O) % 8 == 0 && a.hsO % 4 == 0 && a.tsO % 4 == 0 && a.bsO % 4 == 0;
     p.chunks = (int)(a.R / 64 + (a.P > 0));
     p.rope_steps = (int)((a.P + 15) / 16);
     p.groups = (int)groups;

@@ -5,13 +5,15 @@
 // One CTA per 256 queries of a sequence and head: two tiles of 128 rows (the
 // MMA's M) that share every block of 128 keys.  Per block j and tile t:
 //   S_t = Q_t K_j^T    SS MMAs, 64-wide pieces of the head dimension, into TMEM
-//   P_t = exp2(alpha log2(e) S_t - ref)   one thread a row: one pass over the
-//         scores for their maximum, one for the weights, which are rounded to
-//         the operands' type (summed before) and written over the scores
+//   P_t = exp2(alpha log2(e) S_t - ref)   one thread a row, one pass over the
+//         scores: the weights, rounded to the operands' type (summed before),
+//         and the scores' maximum; then the weights go over the scores
 //   O_t += P_t V_j     TS MMAs, A = P_t from TMEM, B = V_j read MN-major from
 //         the rows as TMA lands them
 // A row's reference maximum rises only when a score exceeds it by 2^8; then
-// the row's own thread scales its sums and its row of O_t.  The tensor pipe
+// the row's own thread scales its sums and its row of O_t and weighs the block
+// again (a pass for the maximum before the weights cost 350 of 4300 cycles a
+// block).  The tensor pipe
 // takes P V_0, S_0 of the next block, P V_1, S_1 of the next block in turn, so
 // that each tile's softmax runs under the other's MMAs, and the scores of a
 // tile coming in say that its P V before them is done.
@@ -324,7 +326,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         const int last = p.causal ? min(nk - 1, m + nk - nq) : nk - 1;   // last key the row sees
         // Blocks below this one hide nothing from any of the tile's rows.
         const int open = (p.causal ? min(nk, max(0, m0 + t * BM + nk - nq + 1)) : nk) / BN;
-        const float scale = p.scale_log2;
+        const float scale = fabsf(p.scale_log2);
+        const bool negative = p.scale_log2 < 0.0f;
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
         for (int j = 0; j < n_blocks; ++j) {
@@ -336,34 +339,67 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
             tc_fence_after();
             const bool edge = j >= open;
             const int see = last - j * BN;               // columns up to this one count
-            float top = -INFINITY;
+            if (j == 0) {
+                // The first reference is the block's maximum.
+                float top = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v[64];
-                tmem_ld64(s_at + 64 * h, v);
-                if (scale < 0.0f) {                      // the largest weight has the least score
+                for (int h = 0; h < 2; ++h) {
+                    float v[64];
+                    tmem_ld64(s_at + 64 * h, v);
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) v[x] = -v[x];
+                    for (int x = 0; x < 64; ++x) {
+                        if (negative) v[x] = -v[x];
+                        if (64 * h + x <= see) top = fmaxf(top, v[x]);
+                    }
                 }
-                if (edge) {
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (64 * h + x > see) v[x] = -INFINITY;
-                }
-                // Two chains of three-input maxima.
-                float a = top, b = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < 64; x += 4) {
-                    asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(v[x]), "f"(v[x + 1]));
-                    asm("max.f32 %0, %0, %1, %2;" : "+f"(b) : "f"(v[x + 2]), "f"(v[x + 3]));
-                }
-                top = fmaxf(a, b);
+                ref = top == -INFINITY ? -INFINITY : top * scale;
             }
-            top *= fabsf(scale);
-            const bool rise = top > ref + kRaise;
-            if (__any_sync(~0u, rise)) {
-                const float f = rise ? exp2f(ref - top) : 1.0f;      // 0 at the first rise
-                if (rise) ref = top;
+            // One pass over the row's scores, 16 columns under way while 16 are
+            // worked on: the weights against the reference, packed in registers,
+            // their sum, and the scores' maximum.
+            uint32_t w[64];
+            float top, part;
+            auto weigh = [&](auto masked) {
+                constexpr bool kMask = decltype(masked)::value;
+                const float shift = ref == -INFINITY ? 0.0f : ref;   // no key yet: every weight is 0
+                float t0 = -INFINITY, t1 = -INFINITY, s0 = 0.0f, s1 = 0.0f;
+                uint32_t v[2][16];
+                tmem_ld16_begin(s_at, v[0]);
+                tmem_ld16_end(v[0]);
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    if (h < 7) tmem_ld16_begin(s_at + 16 * (h + 1), v[(h + 1) & 1]);
+                    if (negative) {                  // alpha < 0: the largest weight has the least score
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) v[h & 1][x] ^= 0x80000000u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        float a = __uint_as_float(v[h & 1][x]), b = __uint_as_float(v[h & 1][x + 1]);
+                        if (kMask && 16 * h + x > see) a = -INFINITY;
+                        if (kMask && 16 * h + x + 1 > see) b = -INFINITY;
+                        if (x & 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(t1) : "f"(a), "f"(b));
+                        else asm("max.f32 %0, %0, %1, %2;" : "+f"(t0) : "f"(a), "f"(b));
+                        a = ex2_approx(fmaf(a, scale, -shift));
+                        b = ex2_approx(fmaf(b, scale, -shift));
+                        s0 += a;
+                        s1 += b;
+                        w[8 * h + x / 2] = pack2<T>(a, b);
+                    }
+                    if (h < 7) tmem_ld16_end(v[(h + 1) & 1]);
+                }
+                top = fmaxf(t0, t1);
+                part = s0 + s1;
+            };
+            while (true) {
+                if (edge) weigh(std::true_type{});
+                else weigh(std::false_type{});
+                // (A maximum of -infinity times a scale of 0 is no rise.)
+                const bool rise = top * scale > ref + kRaise;
+                if (!__any_sync(~0u, rise)) break;
+                // Rare: the block again, with the new references.
+                const float f = rise ? exp2f(ref - top * scale) : 1.0f;      // 0 for a first key
+                if (rise) ref = top * scale;
                 sum *= f;
                 if (j > 0) {
 #pragma unroll 1
@@ -377,26 +413,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                     }
                 }
             }
-            const float shift = ref == -INFINITY ? 0.0f : ref;       // no key yet: every weight is 0
-            float part[2] = {0.0f, 0.0f};
+            sum += part;
+            // Over the scores' first columns, all read by now.
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float v[32];
-                uint32_t w[16];
-                tmem_ld32(s_at + 32 * h, v);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    v[x] = fmaf(v[x], scale, -shift);
-                    if (edge && 32 * h + x > see) v[x] = -INFINITY;
-                    v[x] = ex2_approx(v[x]);
-                    part[x & 1] += v[x];
-                }
-#pragma unroll
-                for (int x = 0; x < 16; ++x) w[x] = pack2<T>(v[2 * x], v[2 * x + 1]);
-                // Columns 16 h .. of the row's scores, all read by now.
-                tmem_st_bits<16>(s_at + 16 * h, w);
-            }
-            sum += part[0] + part[1];
+            for (int h = 0; h < 2; ++h)
+                tmem_st_bits<32>(s_at + 32 * h, *reinterpret_cast<const uint32_t(*)[32]>(&w[32 * h]));
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
