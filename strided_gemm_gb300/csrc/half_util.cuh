@@ -30,6 +30,20 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
     return r;
 }
 
+// The same where it stands: left to itself the compiler may move the packing of
+// a long row behind its last element and hold twice the registers.
+template <typename T> __device__ __forceinline__ uint32_t pack2_here(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2_here<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pack2_here<__half>(float lo, float hi) {
+    uint32_t r;
+    asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Reads and clears a kernel file's status word (0 on a CUDA error).
 inline unsigned int read_and_clear_word(const void* symbol, cudaStream_t stream) {
     unsigned int v = 0, zero = 0;

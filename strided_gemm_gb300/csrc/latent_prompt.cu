@@ -339,28 +339,41 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
             tc_fence_after();
             const bool edge = j >= open;
             const int see = last - j * BN;               // columns up to this one count
+            const float hidden = negative ? INFINITY : -INFINITY;
+            if (edge) {
+                // Scores that the row does not see are hidden in TMEM first, so
+                // that the pass below has no masked form of its own (which took
+                // it over the registers).
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    if (!__any_sync(~0u, see < 32 * h + 31)) continue;
+                    float v[32];
+                    uint32_t bits[32];
+                    tmem_ld<32>(s_at + 32 * h, v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) bits[x] = __float_as_uint(32 * h + x <= see ? v[x] : hidden);
+                    tmem_st_bits<32>(s_at + 32 * h, bits);
+                }
+                tmem_wait_st();
+            }
             if (j == 0) {
                 // The first reference is the block's maximum.
-                float top = -INFINITY;
+                float top = hidden;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[64];
                     tmem_ld64(s_at + 64 * h, v);
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        if (negative) v[x] = -v[x];
-                        if (64 * h + x <= see) top = fmaxf(top, v[x]);
-                    }
+                    for (int x = 0; x < 64; ++x) top = negative ? fminf(top, v[x]) : fmaxf(top, v[x]);
                 }
-                ref = top == -INFINITY ? -INFINITY : top * scale;
+                ref = top == hidden ? -INFINITY : negative ? -top * scale : top * scale;
             }
             // One pass over the row's scores, 16 columns under way while 16 are
             // worked on: the weights against the reference, packed in registers,
             // their sum, and the scores' maximum.
-            uint32_t w[64];
+            uint32_t w[2][32];
             float top, part;
-            auto weigh = [&](auto masked) {
-                constexpr bool kMask = decltype(masked)::value;
+            auto weigh = [&] {
                 const float shift = ref == -INFINITY ? 0.0f : ref;   // no key yet: every weight is 0
                 float t0 = -INFINITY, t1 = -INFINITY, s0 = 0.0f, s1 = 0.0f;
                 uint32_t v[2][16];
@@ -376,28 +389,31 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
 #pragma unroll
                     for (int x = 0; x < 16; x += 2) {
                         float a = __uint_as_float(v[h & 1][x]), b = __uint_as_float(v[h & 1][x + 1]);
-                        if (kMask && 16 * h + x > see) a = -INFINITY;
-                        if (kMask && 16 * h + x + 1 > see) b = -INFINITY;
                         if (x & 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(t1) : "f"(a), "f"(b));
                         else asm("max.f32 %0, %0, %1, %2;" : "+f"(t0) : "f"(a), "f"(b));
                         a = ex2_approx(fmaf(a, scale, -shift));
                         b = ex2_approx(fmaf(b, scale, -shift));
                         s0 += a;
                         s1 += b;
-                        w[8 * h + x / 2] = pack2<T>(a, b);
+                        w[h >> 2][8 * (h & 3) + x / 2] = pack2_here<T>(a, b);
                     }
                     if (h < 7) tmem_ld16_end(v[(h + 1) & 1]);
                 }
                 top = fmaxf(t0, t1);
                 part = s0 + s1;
             };
-            while (true) {
-                if (edge) weigh(std::true_type{});
-                else weigh(std::false_type{});
-                // (A maximum of -infinity times a scale of 0 is no rise.)
-                const bool rise = top * scale > ref + kRaise;
-                if (!__any_sync(~0u, rise)) break;
-                // Rare: the block again, with the new references.
+            weigh();
+            // (A maximum of -infinity times a scale of 0 is no rise.)
+            const bool rise = top * scale > ref + kRaise;
+            if (!__any_sync(~0u, rise)) {
+                // Over the scores' first columns, all read by now.
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tmem_st_bits<32>(s_at + 32 * h, w[h]);
+                sum += part;
+            } else {
+                // Rare: what was summed is scaled to the new references, and the
+                // block weighed again (written over the scores chunk by chunk,
+                // always behind what is read).
                 const float f = rise ? exp2f(ref - top * scale) : 1.0f;      // 0 for a first key
                 if (rise) ref = top * scale;
                 sum *= f;
@@ -406,18 +422,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                     for (int c = 0; c < p.Dv; c += 32) {
                         float o[32];
                         uint32_t bits[32];
-                        tmem_ld32(o_at + c, o);
+                        tmem_ld<32>(o_at + c, o);
 #pragma unroll
                         for (int x = 0; x < 32; ++x) bits[x] = __float_as_uint(o[x] * f);
                         tmem_st_bits<32>(o_at + c, bits);
                     }
                 }
-            }
-            sum += part;
-            // Over the scores' first columns, all read by now.
+                const float shift = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    float v[32];
+                    uint32_t bits[16];
+                    tmem_ld<32>(s_at + 32 * h, v);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                tmem_st_bits<32>(s_at + 32 * h, *reinterpret_cast<const uint32_t(*)[32]>(&w[32 * h]));
+                    for (int x = 0; x < 32; ++x) {
+                        v[x] = ex2_approx(fmaf(negative ? -v[x] : v[x], scale, -shift));
+                        sum += v[x];
+                    }
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) bits[x] = pack2<T>(v[2 * x], v[2 * x + 1]);
+                    tmem_st_bits<16>(s_at + 16 * h, bits);
+                }
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
