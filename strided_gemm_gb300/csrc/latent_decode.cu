@@ -481,8 +481,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 }
                 const int first = (now.j0 + j) * BT;
                 const int safe = p.causal ? now.len - p.q_len : now.len - 1;    // keys up to here: every row's
-                const bool edge = first + BT - 1 > safe;
-                if (edge || !mine) {
+                if (!mine) {
+#pragma unroll
+                    for (int x = 0; x < CPT; ++x) a[x] = -INFINITY;
+                } else if (first + BT - 1 > safe) {
 #pragma unroll
                     for (int x = 0; x < CPT; ++x) {
                         int limit = now.len - 1;
@@ -490,7 +492,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             const int r = group * NB + col + x;
                             if (r < p.rows) limit = safe + r / p.heads;
                         }
-                        if (!mine || first + row > limit) a[x] = -INFINITY;
+                        if (first + row > limit) a[x] = -INFINITY;
                     }
                 }
 #pragma unroll
@@ -669,9 +671,9 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 
 // Joins the pieces of split sequences in order: with the largest maximum M of
 // a row's pieces, O = sum 2^(m - M) O_piece / sum 2^(m - M) l_piece.  Few
-// pieces: a thread takes four columns of a row over all of them, two rows of
-// 512 columns a block; many (one long sequence): eight warps share the pieces
-// of 128 columns of a row.
+// pieces: a thread takes eight columns of a row over all of them, four pieces'
+// loads in flight at once; many (one long sequence): eight warps share the pieces of
+// 128 columns of a row.
 constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 512;
 
 template <typename T>
@@ -685,9 +687,18 @@ __device__ __forceinline__ void store4(T* o, float4 v, bool vec) {
         o[3] = from_float<T>(v.w);
     }
 }
+__device__ __forceinline__ void add4(float4& o, float w, const float4& v) {
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+}
+__device__ __forceinline__ float4 scale4(const float4& o, float f) {
+    return make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+}
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ Params p) {
     // Launched while the pieces are still being made (the launch hides behind
     // them): nothing of theirs is read before they are complete.
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -743,42 +754,56 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
     }
     __syncthreads();
-    const int per_row = p.R / 4;                             // threads a row
+    const int per_row = p.R / 8;                             // threads a row
     const int64_t slot_floats = (int64_t)NB * (2 + p.R);
     const int steps = (NB * per_row + kJoinThreads - 1) / kJoinThreads;
     for (int it = blockIdx.x; it < few * steps; it += gridDim.x) {
         const Join jn = list[it / steps];
         const int group = (jn.slot >> 1) % p.groups, pieces = jn.last - jn.member + 1;
         const int at = it % steps * kJoinThreads + threadIdx.x;
-        const int row = at / per_row, e = at % per_row * 4, r = group * NB + row;
+        const int row = at / per_row, e = at % per_row * 8, r = group * NB + row;
         if (row >= NB || r >= p.rows) continue;
-        const float* src[kFewPieces];
-        float top = -INFINITY, mx[kFewPieces];
-        float4 v[kFewPieces];
+        float top = -INFINITY, l = 0.0f;
+        float4 o0 = make_float4(0, 0, 0, 0), o1 = o0;
+        for (int k0 = 0; k0 < pieces; k0 += 4) {
+            float mx[4], lx[4];
+            float4 v[4][2];
 #pragma unroll
-        for (int k = 0; k < kFewPieces; ++k) {
-            if (k >= pieces) continue;
-            const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
-            src[k] = p.parts + slot * slot_floats;
-            mx[k] = src[k][row];
-            v[k] = *reinterpret_cast<const float4*>(src[k] + 2 * NB + (int64_t)row * p.R + e);
-            top = fmaxf(top, mx[k]);
-        }
-        float l = 0.0f;
-        float4 o = make_float4(0, 0, 0, 0);
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + q;
+                mx[q] = -INFINITY;
+                lx[q] = 0.0f;
+                v[q][0] = v[q][1] = make_float4(0, 0, 0, 0);
+                if (k < pieces) {
+                    const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
+                    const float* src = p.parts + slot * slot_floats;
+                    mx[q] = src[row];
+                    lx[q] = src[NB + row];
+                    const float4* o = reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)row * p.R + e);
+                    v[q][0] = o[0];
+                    v[q][1] = o[1];
+                }
+            }
+            float now = top;
 #pragma unroll
-        for (int k = 0; k < kFewPieces; ++k) {
-            if (k >= pieces) continue;
-            const float w = mx[k] == -INFINITY ? 0.0f : exp2f(mx[k] - top);
-            l = fmaf(w, src[k][NB + row], l);
-            o.x = fmaf(w, v[k].x, o.x);
-            o.y = fmaf(w, v[k].y, o.y);
-            o.z = fmaf(w, v[k].z, o.z);
-            o.w = fmaf(w, v[k].w, o.w);
+            for (int q = 0; q < 4; ++q) now = fmaxf(now, mx[q]);
+            const float f = top == -INFINITY ? 0.0f : exp2f(top - now);
+            l *= f;
+            o0 = scale4(o0, f);
+            o1 = scale4(o1, f);
+            top = now;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float w = mx[q] == -INFINITY ? 0.0f : exp2f(mx[q] - top);
+                l = fmaf(w, lx[q], l);
+                add4(o0, w, v[q][0]);
+                add4(o1, w, v[q][1]);
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
-               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), p.o_vec);
+        T* out = static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
+        store4(out, scale4(o0, inv), p.o_vec);
+        store4(out + 4, scale4(o1, inv), p.o_vec);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarters = p.R / 128;
     for (int it = blockIdx.x; it < many * NB * quarters; it += gridDim.x) {
@@ -814,16 +839,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             for (int q = 0; q < 4; ++q) now = fmaxf(now, mx[q]);
             const float f = top == -INFINITY ? 0.0f : exp2f(top - now);
             l *= f;
-            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            o = scale4(o, f);
             top = now;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float w = mx[q] == -INFINITY ? 0.0f : exp2f(mx[q] - top);
                 l = fmaf(w, lx[q], l);
-                o.x = fmaf(w, v[q].x, o.x);
-                o.y = fmaf(w, v[q].y, o.y);
-                o.z = fmaf(w, v[q].z, o.z);
-                o.w = fmaf(w, v[q].w, o.w);
+                add4(o, w, v[q]);
             }
         }
         __syncthreads();                                     // the last item's sums are read
@@ -840,16 +862,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             o = make_float4(0, 0, 0, 0);
             for (int k = 0; k < 8; ++k) {
                 const float w = tops[k] == -INFINITY ? 0.0f : exp2f(tops[k] - top);
-                const float4 v = sums[k][lane];
                 l = fmaf(w, ls[k], l);
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
+                add4(o, w, sums[k][lane]);
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
-                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), p.o_vec);
+                   scale4(o, inv), p.o_vec);
         }
     }
 }
