@@ -14,6 +14,7 @@
 // Data moves in pieces of 4 KB a warp (eight 16-byte loads in flight a lane,
 // then eight stores).
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "half_util.cuh"
@@ -136,16 +137,34 @@ __device__ __forceinline__ void move_page_piece(const PageCaches& c, int64_t blo
 
 __device__ __forceinline__ bool in_pool(int64_t page, int64_t num_blocks) { return page >= 0 && page < num_blocks; }
 
-__global__ void copy_claim_kernel(const int32_t* pairs, int64_t n, int64_t num_blocks, int32_t* claim) {
-    const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (k >= n) return;
+// The lowest pair with each destination.
+__device__ __forceinline__ void claim_pair(const int32_t* pairs, int64_t k, int64_t num_blocks, int32_t* claim) {
     const int src = pairs[2 * k], dst = pairs[2 * k + 1];
     if (in_pool(src, num_blocks) && in_pool(dst, num_blocks) && src != dst) atomicMin(&claim[dst], (int)k);
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void copy_claim_kernel(const int32_t* pairs, int64_t n, int64_t num_blocks, int32_t* claim) {
+    const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (k < n) claim_pair(pairs, k, num_blocks, claim);
+}
+
+// Few pairs of a small pool: every block makes the claims for itself in shared
+// memory, and the copy is one launch (1500 pairs of 8192 pages: 12 us less than
+// with a memset and a launch for them).
+constexpr int64_t kOwnClaimPairs = 8192, kOwnClaimBlocks = 24576;
+
+template <bool kOwnClaims>
+__global__ void __launch_bounds__(512)
 copy_move_kernel(const __grid_constant__ PageCaches c, const int32_t* pairs, int64_t n, int64_t num_blocks,
-                 int64_t block_size, const int32_t* claim, int64_t pieces) {
+                 int64_t block_size, const int32_t* claims, int64_t pieces) {
+    extern __shared__ int32_t own[];
+    if (kOwnClaims) {
+        for (int64_t i = threadIdx.x; i < num_blocks; i += blockDim.x) own[i] = kNoClaim;
+        __syncthreads();
+        for (int64_t k = threadIdx.x; k < n; k += blockDim.x) claim_pair(pairs, k, num_blocks, own);
+        __syncthreads();
+    }
+    const int32_t* claim = kOwnClaims ? own : claims;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n * pieces; w += warps) {
         const int64_t k = w / pieces, j = w % pieces;
@@ -162,22 +181,33 @@ copy_move_kernel(const __grid_constant__ PageCaches c, const int32_t* pairs, int
 
 // ---- fork and append: planning -------------------------------------------------
 
+constexpr int kEach = 8;                     // pages a thread looks at in a round of the search
+
+// Bit i: page at + i is free.
+__device__ __forceinline__ unsigned free_pages(const int32_t* refs, int64_t num_blocks, int64_t at) {
+    int v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = at + i < num_blocks ? refs[at + i] : 1;
+    unsigned bits = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) bits |= (v[i] == 0 ? 1u : 0u) << i;
+    return bits;
+}
+
 // The free pages in ascending order, as many as `want`, into `fresh`; returns
-// how many were found.
-__device__ int find_fresh(const int32_t* refs, int64_t num_blocks, int64_t want, int32_t* fresh, int* sums) {
-    constexpr int kEach = 8;
+// how many were found.  `first_bits`: this thread's pages of the first round,
+// looked at beforehand.
+__device__ int find_fresh(const int32_t* refs, int64_t num_blocks, int64_t want, unsigned first_bits,
+                          int32_t* fresh, int* sums) {
     int64_t found = 0;
     for (int64_t base = 0; base < num_blocks && found < want; base += (int64_t)kPlanThreads * kEach) {
         const int64_t at = base + (int64_t)threadIdx.x * kEach;
-        unsigned free_bits = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (at + i < num_blocks && refs[at + i] == 0) free_bits |= 1u << i;
+        const unsigned bits = base == 0 ? first_bits : free_pages(refs, num_blocks, at);
         int total;
-        int64_t to = found + block_exclusive(__popc(free_bits), sums, &total);
+        int64_t to = found + block_exclusive(__popc(bits), sums, &total);
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (free_bits >> i & 1) {
+            if (bits >> i & 1) {
                 if (to < want) fresh[to] = (int32_t)(at + i);
                 ++to;
             }
@@ -219,14 +249,26 @@ __device__ __forceinline__ bool check_request(const PagePool& p, const int32_t* 
     return true;
 }
 
+constexpr int kSharedSeqs = 4096;            // pools of up to so many sequences have their claims in shared memory
+
 // One CTA: claims, checks, the prefix sum of the pages needed, the search of
 // the free pages, and what is granted.  Fork: a = parents, b = children;
 // append: a = sequences, b = starts.  Lengths are read before any is written.
+// A chain of dependent steps, so the first pages are looked at while the
+// requests come in, claims are in shared memory where they fit, and a thread
+// keeps its first request in registers.
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const PagePool p, const int32_t* a, const int32_t* b, int64_t n, int64_t total, const Workspace w) {
+plan_kernel(const PagePool p, const int32_t* a, const int32_t* b, int64_t n, int64_t total, Workspace w) {
     __shared__ int sums[33];
+    __shared__ int32_t claims[kSharedSeqs], flags[kSharedSeqs];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.n_seqs <= kSharedSeqs) {
+        w.claim = claims;
+        w.flag = flags;
+    }
     const int t = threadIdx.x;
+    const unsigned first_bits = free_pages(p.refs, p.num_blocks, (int64_t)t * kEach);
     bool bad_starts = false;
     for (int64_t k = t; k < n; k += kPlanThreads) {
         const int to = kFork ? b[k] : a[k];
@@ -246,6 +288,7 @@ plan_kernel(const PagePool p, const int32_t* a, const int32_t* b, int64_t n, int
     }
     __syncthreads();
     int64_t want = 0;
+    Request mine{};
     for (int64_t base = 0; base < n; base += kPlanThreads) {
         const int64_t k = base + t;
         Request r{};
@@ -256,23 +299,20 @@ plan_kernel(const PagePool p, const int32_t* a, const int32_t* b, int64_t n, int
         // Past the pool's size nothing can be granted: keep the sum in range.
         r.first = (int32_t)min(before, (int64_t)INT_MAX / 2);
         want += sum;
-        if (k < n) {
-            if (!r.ok) record_status(&g_status, kPageRequest);
-            w.req[k] = r;
-        }
+        if (k < n && !r.ok) record_status(&g_status, kPageRequest);
+        if (base == 0) mine = r;
+        else if (k < n) w.req[k] = r;
     }
     __syncthreads();
-    const int found = find_fresh(p.refs, p.num_blocks, min(want, p.num_blocks), w.fresh, sums);
-    __syncthreads();
+    const int found = find_fresh(p.refs, p.num_blocks, min(want, p.num_blocks), first_bits, w.fresh, sums);
     for (int64_t k = t; k < n; k += kPlanThreads) {
-        const Request r = w.req[k];
-        if (!r.ok) continue;
-        if ((int64_t)r.first + r.need > found) {
-            w.req[k].ok = 0;
+        Request r = k < kPlanThreads ? mine : w.req[k];
+        if (r.ok && (int64_t)r.first + r.need > found) {
+            r.ok = 0;
             record_status(&g_status, kPageExhausted);
-            continue;
         }
-        p.lens[r.to] = r.len + (kFork ? 0 : r.count);
+        w.req[k] = r;
+        if (r.ok) p.lens[r.to] = r.len + (kFork ? 0 : r.count);
     }
 }
 
@@ -282,6 +322,7 @@ plan_kernel(const PagePool p, const int32_t* a, const int32_t* b, int64_t n, int
 // shared pages (blockIdx.y == 0), and the rows of the last page.
 __global__ void __launch_bounds__(256)
 fork_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, const Workspace w, int64_t pieces) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Request r = w.req[blockIdx.x];
     if (!r.ok) return;
     const int64_t full = r.len / p.block_size, rest = r.len % p.block_size;
@@ -311,6 +352,7 @@ fork_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, const W
 __global__ void __launch_bounds__(256)
 append_move_kernel(const __grid_constant__ PageCaches c, const __grid_constant__ PageRows rows, const PagePool p,
                    const Workspace w, const int32_t* starts, int64_t n, int64_t total) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int lane = threadIdx.x & 31;
     const int64_t per = c.n ? c.n : 1;
@@ -381,6 +423,8 @@ __global__ void __launch_bounds__(256) free_kernel(const PagePool p, const int32
 
 // ---- compact ---------------------------------------------------------------------
 
+constexpr int64_t kOwnCounts = 32;           // segments that every ranking block counts for itself
+
 __global__ void __launch_bounds__(256) compact_count_kernel(const int32_t* refs, int64_t num_blocks, int32_t* counts) {
     __shared__ int sums[33];
     int used = 0;
@@ -402,11 +446,21 @@ __global__ void __launch_bounds__(256)
 compact_rank_kernel(const int32_t* refs, int64_t num_blocks, int64_t segments, const Workspace w) {
     __shared__ int sums[33];
     const int t = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int part_before = 0, part_all = 0;
-    for (int64_t s = t; s < segments; s += 256) {
-        const int v = w.counts[s];
-        part_all += v;
-        if (s < blockIdx.x) part_before += v;
+    if (segments <= kOwnCounts) {
+#pragma unroll 8
+        for (int64_t i = t; i < num_blocks; i += 256) {
+            const int v = refs[i] > 0;
+            part_all += v;
+            if (i < (int64_t)blockIdx.x * kSegment) part_before += v;
+        }
+    } else {
+        for (int64_t s = t; s < segments; s += 256) {
+            const int v = w.counts[s];
+            part_all += v;
+            if (s < blockIdx.x) part_before += v;
+        }
     }
     int before, U;
     block_exclusive(part_all, sums, &U);
@@ -440,6 +494,7 @@ compact_rank_kernel(const int32_t* refs, int64_t num_blocks, int64_t segments, c
 __global__ void __launch_bounds__(256)
 compact_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, const Workspace w, int64_t pieces,
                     int32_t* moved) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int U = w.head[0], h = w.head[1];
     const int64_t threads = (int64_t)gridDim.x * blockDim.x, t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (t == 0 && moved) *moved = h;
@@ -473,6 +528,22 @@ unsigned move_grid(int64_t warps, int sms) {
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8, (int64_t)sms * 8));
 }
 
+// A launch that may begin before the one ahead of it ends; the kernel waits for
+// that one's results itself (griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 }  // namespace
 
 size_t pages_workspace_bytes(int64_t num_blocks, int64_t n_seqs, int64_t n) {
@@ -483,13 +554,29 @@ size_t pages_workspace_bytes(int64_t num_blocks, int64_t n_seqs, int64_t n) {
 
 cudaError_t launch_pages_copy(const PageCaches& c, const PagePool& p, const int32_t* pairs, int64_t n, void* ws,
                               int sms, cudaStream_t stream) {
+    const int64_t pieces = page_pieces(c, p.block_size);
+    // Blocks of 16 warps, two a SM.
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n * pieces + 15) / 16, (int64_t)sms * 2));
+    if (n <= kOwnClaimPairs && p.num_blocks <= kOwnClaimBlocks) {
+        static std::atomic<uint64_t> attr_done{0};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (!(attr_done.load() & bit)) {
+            const cudaError_t e = cudaFuncSetAttribute(copy_move_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)(kOwnClaimBlocks * 4));
+            if (e != cudaSuccess) return e;
+            attr_done.fetch_or(bit);
+        }
+        copy_move_kernel<true><<<grid, 512, (size_t)p.num_blocks * 4, stream>>>(c, pairs, n, p.num_blocks, p.block_size,
+                                                                              nullptr, pieces);
+        return cudaGetLastError();
+    }
     const Workspace w = layout(ws, p.num_blocks, 0, 0, nullptr);
-    cudaError_t e = cudaMemsetAsync(w.claim, 0x7f, (size_t)p.num_blocks * 4, stream);
+    const cudaError_t e = cudaMemsetAsync(w.claim, 0x7f, (size_t)p.num_blocks * 4, stream);
     if (e != cudaSuccess) return e;
     copy_claim_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(pairs, n, p.num_blocks, w.claim);
-    const int64_t pieces = page_pieces(c, p.block_size);
-    copy_move_kernel<<<move_grid(n * pieces, sms), 256, 0, stream>>>(c, pairs, n, p.num_blocks, p.block_size,
-                                                                     w.claim, pieces);
+    copy_move_kernel<false><<<grid, 512, 0, stream>>>(c, pairs, n, p.num_blocks, p.block_size, w.claim, pieces);
     return cudaGetLastError();
 }
 
@@ -500,8 +587,9 @@ cudaError_t launch_pages_fork(const PageCaches& c, const PagePool& p, const int3
     const int64_t pieces = page_pieces(c, p.block_size);
     // A block moves 8 pieces at a time; at most two blocks a SM in all.
     const int64_t y = std::min<int64_t>((pieces + 7) / 8, std::max<int64_t>(1, 2 * sms / n));
-    fork_move_kernel<<<dim3((unsigned)n, (unsigned)std::max<int64_t>(1, y)), 256, 0, stream>>>(c, p, w, pieces);
-    return cudaGetLastError();
+    const cudaError_t e = launch_early(fork_move_kernel, dim3((unsigned)n, (unsigned)std::max<int64_t>(1, y)), 256,
+                                       stream, c, p, w, pieces);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_pages_append(const PageCaches& c, const PagePool& p, const int32_t* seqs, const int32_t* starts,
@@ -509,9 +597,11 @@ cudaError_t launch_pages_append(const PageCaches& c, const PagePool& p, const in
                                 cudaStream_t stream) {
     const Workspace w = layout(ws, p.num_blocks, p.n_seqs, n, nullptr);
     plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p, seqs, starts, n, total, w);
-    if (total > 0)
-        append_move_kernel<<<move_grid(total * std::max(c.n, 1), sms), 256, 0, stream>>>(c, rows, p, w, starts, n,
-                                                                                        total);
+    if (total > 0) {
+        const cudaError_t e = launch_early(append_move_kernel, dim3(move_grid(total * std::max(c.n, 1), sms)), 256,
+                                           stream, c, rows, p, w, starts, n, total);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 
@@ -524,10 +614,12 @@ cudaError_t launch_pages_compact(const PageCaches& c, const PagePool& p, int32_t
                                  cudaStream_t stream) {
     const Workspace w = layout(ws, p.num_blocks, p.n_seqs, 0, nullptr);
     const int64_t segments = (p.num_blocks + kSegment - 1) / kSegment;
-    compact_count_kernel<<<(unsigned)segments, 256, 0, stream>>>(p.refs, p.num_blocks, w.counts);
+    if (segments > kOwnCounts)
+        compact_count_kernel<<<(unsigned)segments, 256, 0, stream>>>(p.refs, p.num_blocks, w.counts);
     compact_rank_kernel<<<(unsigned)segments, 256, 0, stream>>>(p.refs, p.num_blocks, segments, w);
-    compact_move_kernel<<<(unsigned)(sms * 8), 256, 0, stream>>>(c, p, w, page_pieces(c, p.block_size), moved);
-    return cudaGetLastError();
+    const cudaError_t e = launch_early(compact_move_kernel, dim3((unsigned)(sms * 8)), 256, stream, c, p, w,
+                                       page_pieces(c, p.block_size), moved);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 unsigned int read_and_clear_status_pages(cudaStream_t stream) {
