@@ -38,7 +38,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
 // A CTA that allocates all columns has them at address 0.
 constexpr uint32_t kTmemAll = 512, kTmemBase = 0;
 
-// kind::f16, D fp32, M rows (128, or 64: accumulator row r in lane r / 16 * 32 +
+// kind::f16, D fp32, M rows (128, 256 on a CTA pair, or 64: accumulator row r in lane r / 16 * 32 +
 // r % 16) and N columns; *_mn: the operand's unit stride in
 // shared memory runs along M or N instead of K.
 __host__ __device__ constexpr uint32_t idesc16(bool bf16, int n, bool a_mn, bool b_mn, int m = 128) {
@@ -63,6 +63,17 @@ __device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uin
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same over a CTA pair (M = 256: each CTA's 128 rows of A and of D, each
+// one's half of B's columns), issued by the pair's first CTA.
+__device__ __forceinline__ void mma16_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }

@@ -123,7 +123,7 @@ def check_product(torch, t, batch, M, N, K, la, lb, lc, alpha=1.0, accumulate=Fa
 PRODUCTS = [
     (1, 1, 1, 1), (1, 1, 8, 16), (3, 5, 9, 31), (2, 17, 33, 64), (1, 64, 64, 72), (2, 127, 65, 40),
     (1, 128, 128, 128), (3, 129, 136, 200), (1, 300, 264, 8), (2, 16, 512, 128), (5, 1, 128, 512),
-    (1, 257, 392, 520), (1, 1000, 48, 136),
+    (1, 257, 392, 520), (1, 1000, 48, 136), (1, 2600, 2056, 72), (2, 1290, 2040, 1032),
 ]
 
 
