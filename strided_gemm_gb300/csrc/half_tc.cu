@@ -63,6 +63,12 @@ struct Shape {
     static constexpr int kStage = BX * BK * 2 + kYBytes;
     static constexpr int kStages = kYRows == 256 ? 4 : kYRows == 128 ? 5 : 6;
     static constexpr int kBufs = kYRows == 256 ? 1 : 2;             // on the way out, for each group
+    // With 256 columns a fourth stage and a second buffer do not both fit; up to
+    // three blocks of K have no use for the stage (128 products of 64 x 512 x
+    // 128: 10.3 us with four stages, 8.3 with two buffers; 4099 x 8192 x 512:
+    // 30.8 and 33.8).
+    __host__ __device__ static constexpr int stages(int k_blocks) { return kYRows == 256 && k_blocks <= 3 ? 3 : kStages; }
+    __host__ __device__ static constexpr int bufs(int k_blocks) { return kYRows == 256 && k_blocks <= 3 ? 2 : kBufs; }
     static constexpr int kSmem = kStages * kStage + kBufs * kGroups * kOutBytes + 1024;
     static_assert(kSmem <= 232448 - 1024, "shared memory per CTA");
 };
@@ -87,7 +93,8 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
     const int rank = kPair ? (int)(cluster_rank() & 1) : 0;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* out = ring + S::kStages * S::kStage;
+    const int stages = S::stages(p.k_blocks), bufs = S::bufs(p.k_blocks);
+    uint8_t* out = ring + stages * S::kStage;
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_free[2], done;
     __shared__ uint32_t tmem_base;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -169,8 +176,8 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                     } else {
                         load(y, &ty, s, j * BK, yr, zy);
                     }
-                    if (issued < S::kStages) ++issued;
-                    if (++s == S::kStages) {
+                    if (issued < stages) ++issued;
+                    if (++s == stages) {
                         s = 0;
                         ++round;
                     }
@@ -180,7 +187,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             // CTA waits for both).
             for (int q = 0; rank == 0 && q < issued; ++q) {
                 if (--s < 0) {
-                    s = S::kStages - 1;
+                    s = stages - 1;
                     --round;
                 }
                 if (!bar_wait(&full[s], round & 1)) {
@@ -223,7 +230,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                     }
                     if constexpr (kPair) mma_commit_pair_both(&empty[s]);
                     else mma_commit(&empty[s]);
-                    if (++s == S::kStages) {
+                    if (++s == stages) {
                         s = 0;
                         ++round;
                     }
@@ -255,11 +262,11 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
             T* C = static_cast<T*>(p.C) + b * p.bsC;
 #pragma unroll 1
             for (int c = g * kChunk; c < NT; c += kGroups * kChunk) {
-                uint8_t* buf = out + (S::kBufs * g + (S::kBufs == 2 ? sent & 1 : 0)) * kOutBytes;
+                uint8_t* buf = out + (bufs * g + (bufs == 2 ? sent & 1 : 0)) * kOutBytes;
                 if (p.c_tma) {
                     // The buffer's last store has read it.
                     if (row == 0) {
-                        if (S::kBufs == 2) bulk_wait_read_all_but_one();
+                        if (bufs == 2) bulk_wait_read_all_but_one();
                         else bulk_wait_read_all();
                     }
                     group_sync(g);
