@@ -98,7 +98,7 @@ struct Ctl {
     uint64_t q_full, s_full[2], p_full, o_free, done;
     uint32_t tmem_base;
     int seq0, tile0, count;                  // this CTA's run of the list
-    int scan[kWarps];
+    int scan[kWarps], rest[kWarps];
     alignas(16) float ref[NB];               // reference maxima
     alignas(16) float factor[NB];            // a rise's factors, then 1 / sum
     union alignas(16) {
@@ -201,14 +201,28 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
     int members = 1, lo = 0, units_total = 0;
     if (p.split) {
-        int sum = 0;
-        for (int s = tid; s < p.n_seqs; s += kThreads) sum += units_of<BT>(seq_len(p, s, false));
+        // Units of this thread's sequence of the first round, and their sum over
+        // the warp's lanes up to it; pools of more sequences look again below.
+        const int u0 = tid < p.n_seqs ? units_of<BT>(seq_len(p, tid, false)) : 0;
+        int rest = 0;
+        for (int s = tid + kThreads; s < p.n_seqs; s += kThreads) rest += units_of<BT>(seq_len(p, s, false));
+        auto warp_sum = [&](int v) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (lane == 0) c.scan[warp] = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(~0u, v, o);
+                if (lane >= o) v += x;
+            }
+            return v;
+        };
+        int inc = warp_sum(u0);
+        const int rest_sum = p.n_seqs > kThreads ? __reduce_add_sync(~0u, rest) : 0;
+        if (lane == 31) {
+            c.scan[warp] = inc;
+            c.rest[warp] = rest_sum;
+        }
         __syncthreads();
         int total = 0;
-        for (int w = 0; w < kWarps; ++w) total += c.scan[w];
+        for (int w = 0; w < kWarps; ++w) total += c.scan[w] + c.rest[w];
         // No CTA between a sequence's first and last one is empty.
         members = min(p.per_group, total);
         lo = member < members ? (int)((int64_t)member * total / members) : 0;
@@ -218,16 +232,14 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         int before = 0;                      // units of the sequences of earlier rounds
         for (int s0 = 0; s0 < p.n_seqs && before <= lo; s0 += kThreads) {
             const int s = s0 + tid;
-            const int u = s < p.n_seqs ? units_of<BT>(seq_len(p, s, false)) : 0;
-            int inc = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += v;
+            int u = u0;
+            if (s0 > 0) {
+                u = s < p.n_seqs ? units_of<BT>(seq_len(p, s, false)) : 0;
+                inc = warp_sum(u);
+                __syncthreads();
+                if (lane == 31) c.scan[warp] = inc;
+                __syncthreads();
             }
-            __syncthreads();
-            if (lane == 31) c.scan[warp] = inc;
-            __syncthreads();
             int at = before, round = 0;
             for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) at += c.scan[w];
