@@ -44,6 +44,15 @@ template <> __device__ __forceinline__ uint32_t pack2_here<__half>(float lo, flo
     return r;
 }
 
+// The two values of a packed pair.
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // Reads and clears a kernel file's status word (0 on a CUDA error).
 inline unsigned int read_and_clear_word(const void* symbol, cudaStream_t stream) {
     unsigned int v = 0, zero = 0;

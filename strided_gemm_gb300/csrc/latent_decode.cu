@@ -18,8 +18,9 @@
 // sequence.  The softmax keeps a reference maximum a query row, raised only
 // when a score exceeds it by a factor of 2^8 (then O^T, the sums and the
 // reference are scaled, by all eight warps); P is rounded to the operands'
-// type for the MMA and summed before it in fp32.  Weights up to 2^8 of either
-// type lose nothing by it; in fp16 one below 2^-14 keeps an absolute 2^-25.
+// type for the MMA and summed as rounded, in fp32, so that the weights add up to
+// one.  Weights up to 2^8 of either type lose nothing by it; in fp16 one below
+// 2^-14 keeps an absolute 2^-25.
 //
 // Work is spread as one list of blocks over the CTAs (one an SM), each CTA an
 // equal run of it that may begin and end inside a sequence.  A sequence that
@@ -39,13 +40,20 @@
 // 4-11 do the softmax, rescaling, queries and output.  Every wait is bounded.
 //
 // Up to 32 rows three stages of 48 keys keep two blocks' loads in flight under
-// the third's MMAs (two stages of 64: loads and MMAs took turns, 76 us against
-// XX us for 32 ragged sequences of 16 heads); 64 rows' queries leave room for
-// two stages of 64.
+// the third's MMAs: 8.7 k cycles for 144 keys, where two stages of 64 loaded and
+// computed in turns, 11 k cycles for 128 (16 heads, all SMs).  64 rows' queries
+// leave room for two stages of 64 only: 7.0 k cycles for 128 keys, of them 3.6 k
+// until a block's rows are in and 3.4 k of scores, softmax and P V in a chain.
+// (Four stages of 32 there took 443 us for the 177 below; each stage's load and
+// release in two halves 181.)
 //
-// Bound: few heads by the cache's bytes; 128 heads (two CTAs on the same
-// blocks at the same time, the second read hitting L2) by the MMAs, whose
-// operands come from shared memory.
+// Measured on a GB300, bf16 or fp16, R = 512, P = 64, join included: 64
+// sequences of 2048 to 8192 keys with 128 heads 177 us (399 MB: 2.2 TB/s, 520
+// TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 55 us (193 MB: 3.5
+// TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 16.5 us.
+// Bound: few heads by the cache's bytes and a start of 7 us; 128 heads (two
+// CTAs on the same blocks at the same time, the second read hitting L2) by the
+// chain above.
 #include <algorithm>
 #include <atomic>
 
@@ -562,9 +570,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     // A row that has seen no key yet has no reference: its weights are 0.
                     const float p0 = ex2_approx(a[x] - (r0 == -INFINITY ? 0.0f : r0));
                     const float p1 = ex2_approx(a[x + 1] - (r1 == -INFINITY ? 0.0f : r1));
-                    l[x] += p0;
-                    l[x + 1] += p1;
                     w2[x / 2] = pack2<T>(p0, p1);
+                    const float2 rounded = unpack2<T>(w2[x / 2]);
+                    l[x] += rounded.x;
+                    l[x + 1] += rounded.y;
                 }
                 // The block before has read its weights.
                 if (i > 0 && !pv_done(i - 1)) {

@@ -309,6 +309,67 @@ def test_paged_large_scores(torch, workspace):
     c.check(torch, True)
 
 
+def test_paged_scales_of_any_sign(torch, workspace):
+    for alpha in (-0.05, 0.0, 3.0):
+        c = Paged(torch, "bf16", [130, 700], 16, 2, 512, 64, 16, seed=31)
+        c.alpha = alpha
+        c.run(True, workspace)
+        c.check(torch, True)
+        d = Packed(torch, "fp16", [140, 30], [300, 30], 2, 128, 64, 128, seed=32)
+        d.alpha = alpha
+        d.run(True)
+        d.check(torch, True)
+
+
+def test_paged_smaller_workspaces(torch, workspace):
+    """Fewer slots mean fewer CTAs, down to whole sequences: the same results
+    within the bound."""
+    c = Paged(torch, "bf16", [3000, 40, 700], 128, 1, 512, 64, 64, seed=33)
+    for n in (0, 256, 1 << 14, 1 << 20, 5 << 20, workspace.numel()):
+        c.o.fill_(float("nan"))
+        c.run(True, workspace[:n] if n else None)
+        c.check(torch, True)
+
+
+def test_paged_more_row_groups_than_sms(torch, workspace):
+    c = Paged(torch, "bf16", [200, 64], 64, 160, 128, 64, 16, seed=34)      # 160 groups of 64 rows
+    c.run(True, workspace)
+    c.check(torch, True)
+
+
+def test_paged_offsets_past_32_bits(torch, workspace):
+    """A cache of more than 2^31 elements, a sequence in its last pages; the page
+    operations reach them too."""
+    block, row = 64, 576
+    blocks = (1 << 31) // (block * row) + 40
+    c = Paged(torch, "bf16", [300], 16, 1, 512, 64, block, seed=35)
+    cache = torch.empty(blocks, block, row, device="cuda", dtype=torch.bfloat16)
+    old = c.table[0, :5].long()
+    pairs = torch.stack([torch.arange(5, device="cuda"), torch.arange(blocks - 5, blocks, device="cuda")], 1).int()
+    cache[:5] = c.cache[old]
+    ws = torch.empty(sg.sbgemm_pages_workspace_bytes(blocks, 1, 8), device="cuda", dtype=torch.uint8)
+    sg.pages_copy([cache], pairs, workspace=ws)
+    cache[:5] = float("nan")
+    c.table[0, :5] = pairs[:, 1]
+    c.cache = cache
+    c.run(True, workspace)
+    c.check(torch, True)
+    status_is(0)
+
+
+def test_product_offsets_past_32_bits(torch):
+    M, N, K = 70000, 32768, 16
+    g = torch.Generator(device="cuda").manual_seed(36)
+    A = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    B = torch.randn(K, N, generator=g, device="cuda").bfloat16()
+    C = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+    sg.matmul_half(A, B, C)
+    for m in (0, 65535, 65536, M - 1):
+        ref = A[m].double() @ B.double()
+        size = A[m].double().abs() @ B.double().abs()
+        assert_within(torch, C[m], ref, (K + 3) * U * size + HALF["bf16"] * ref.abs() + 2.0 ** -25, f"row {m}")
+
+
 def test_paged_strided_operands(torch, workspace):
     for gap in (8, 3):      # 16-byte multiples, and a stride that no vector load can take
         c = Paged(torch, "bf16", [100, 333], 16, 2, 512, 64, 16, seed=9, gap=gap)
@@ -480,6 +541,24 @@ def test_packed_large_scores_and_strides(torch):
     c.q[..., 128] = 8.0
     c.run(True)
     c.check(torch, True)
+
+
+def test_packed_infinities_of_other_sequences_stay_there(torch):
+    c = Packed(torch, "bf16", [130, 50], [130, 50], 2, 128, 64, 128, seed=25)
+    c.v[c.front + 130:] = float("inf")
+    c.kn[c.front + 130:] = float("nan")
+    c.run(True)
+    assert bool(torch.isfinite(c.o[:130]).all())
+    c.q_lens, c.k_lens = [130], [130]
+    c.whole[130:] = 7.0
+    c.check(torch, True)
+
+
+def test_packed_without_any_key(torch):
+    c = Packed(torch, "bf16", [20, 3], [0, 0], 2, 128, 64, 128, seed=26, back=0)
+    c.run(False)
+    c.check(torch, False)
+    status_is(0)
 
 
 def test_packed_starts_out_of_range_are_reported(torch):
@@ -791,6 +870,44 @@ def test_pages_replay(torch):
         p.m.free([2])
         torch.cuda.synchronize()
         p.same()
+
+
+def test_pages_on_two_streams(torch):
+    rng = np.random.default_rng(12)
+    pools = [Pool(torch, rng, 200, 4, 8, 20, [9, 6, 0, 0, 13, 70, 1, 0], [(8,)]) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    rows = [rng.standard_normal((3, 8)).astype(np.float16) for _ in pools]
+    dev = [torch.from_numpy(r).cuda() for r in rows]
+    seqs, starts, parents, children = (pools[0].dev(x) for x in ([0, 4, 5], [0, 1, 2, 3], [5, 0], [2, 3]))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, s, d, r in zip(pools, streams, dev, rows):
+            with torch.cuda.stream(s):
+                sg.pages_append(*p.all(), seqs, starts, [d], workspace=p.ws)
+                sg.pages_fork(*p.all(), parents, children, workspace=p.ws)
+                sg.pages_free(*p.all(), children)
+                sg.pages_compact(*p.all(), workspace=p.ws)
+            p.m.append([0, 4, 5], [0, 1, 2, 3], [r])
+            p.m.fork([5, 0], [2, 3])
+            p.m.free([2, 3])
+            p.m.compact()
+    torch.cuda.synchronize()
+    for p in pools:
+        p.same()
+
+
+def test_calls_through_ctypes_alone(torch, workspace, monkeypatch):
+    """Without the fast-call module the same calls go through ctypes."""
+    monkeypatch.setattr(sg, "_fast", None)
+    check_product(torch, "bf16", 2, 33, 40, 64, "c", "r", "c")
+    c = Paged(torch, "bf16", [70, 5], 16, 1, 512, 64, 16, seed=41)
+    c.run(True, workspace)
+    c.check(torch, True)
+    d = Packed(torch, "fp16", [40], [70], 2, 128, 64, 128, seed=42)
+    d.run(True)
+    d.check(torch, True)
+    test_pages_requests_that_are_not_valid(torch)
+    test_pages_run_out_in_request_order(torch)
 
 
 def test_pages_of_paged_attention_caches(torch):

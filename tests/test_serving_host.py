@@ -156,3 +156,53 @@ def test_pages_workspace_bytes():
     assert sg.sbgemm_pages_workspace_bytes(2000, 10, 5) > b
     with pytest.raises(sg.SbgemmError):
         sg.sbgemm_pages_workspace_bytes(-1, 10, 5)
+
+
+def test_fastcall_statuses_match_ctypes(monkeypatch):
+    """The fast-call module and ctypes give the same statuses, and the former
+    refuses arguments it cannot convert."""
+    if sg._fast is None:
+        pytest.skip("the fast-call module is not built (no Python headers)")
+    cases = [(half, dict(type=9)), (half, dict(C=A)), (half, dict(M=0)), (paged, dict(N=129)), (paged, dict(O=0)),
+             (paged, dict(n_seqs=0)), (packed, dict(Dv=513)), (packed, dict(V=0)), (packed, dict(Dv=0))]
+    fast = [f(**kw) for f, kw in cases]
+    pages = [status(serving._pages_on, op, (A, B), (1024, 512 + bad), 100, 16, C, C + 4096, 8, 10, C + 8192, D, E, n,
+                    (F, G) if op == 2 else (), (64, 32) if op == 2 else (), 4, 0, 0, 0)
+             for op in range(5) for bad in (0, 8) for n in (0, -1)]
+    monkeypatch.setattr(sg, "_fast", None)
+    assert fast == [f(**kw) for f, kw in cases]
+    assert pages == [status(serving._pages_on, op, (A, B), (1024, 512 + bad), 100, 16, C, C + 4096, 8, 10, C + 8192, D,
+                            E, n, (F, G) if op == 2 else (), (64, 32) if op == 2 else (), 4, 0, 0, 0)
+                     for op in range(5) for bad in (0, 8) for n in (0, -1)]
+
+
+def test_fastcall_refuses_what_it_cannot_convert():
+    if sg._fast is None:
+        pytest.skip("the fast-call module is not built (no Python headers)")
+    f = sg._fast
+    for call in (lambda: f.half(1), lambda: f.paged(1), lambda: f.packed(1), lambda: f.pages(1),
+                 lambda: f.half("1", A, 1, 1, 1, B, 1, 1, 1, C, 1, 1, 1, 0, 0, 0, 0, 1.0, 0, 0),
+                 lambda: f.pages(0, [A], (1024,), 100, 16, 0, 0, 0, 0, 0, D, 0, 1, (), (), 0, 0, 0),
+                 lambda: f.pages(0, (A, B), (1024,), 100, 16, 0, 0, 0, 0, 0, D, 0, 1, (), (), 0, 0, 0),
+                 lambda: f.pages(0, (A,) * 65, (1024,) * 65, 100, 16, 0, 0, 0, 0, 0, D, 0, 1, (), (), 0, 0, 0),
+                 lambda: f.pages(2, (A,), (1024,), 100, 16, C, C, 1, 1, C, D, E, 1, (), (), 0, 0, 0)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_torch_helpers_refuse_tensors():
+    torch = pytest.importorskip("torch")
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    x = torch.zeros(4, 8, **bf)
+    with pytest.raises(TypeError):
+        sg.matmul_half(x, x.t(), torch.zeros(4, 4, **bf))              # on the CPU
+    with pytest.raises(TypeError):
+        sg.matmul_half(x.float(), x.float().t(), torch.zeros(4, 4))
+    with pytest.raises(TypeError):
+        sg.latent_attention_paged(torch.zeros(1, 1, 1, 576, **bf), torch.zeros(4, 16, 576, **bf),
+                                  torch.zeros(1, 4, **i32), None, torch.zeros(1, 1, 1, 512, **bf), 1.0)
+    with pytest.raises(ValueError):
+        sg.pages_copy([], torch.zeros(1, 2, **i32), workspace=None)
+    with pytest.raises(TypeError):
+        sg.pages_free([torch.zeros(4, 16, 8, **bf)], torch.zeros(4, **i32), torch.zeros(1, 4, **i32),
+                      torch.zeros(1, **i32), torch.zeros(1, **i32))
