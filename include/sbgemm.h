@@ -382,13 +382,14 @@ SBGEMM_API int sbgemm_half(int type, const void* A, int64_t rsA, int64_t csA, in
  * Rows of the cache past a sequence's end are not read.  A block id outside
  * [0, num_blocks) reads as zero rows and a length outside [0, N] is clamped;
  * either makes the next sbgemm_device_status return SBGEMM_ERR_DEVICE_CHECK
- * (code 10).  NaN or infinity in a row that some queries of a 64-key block
- * mask and others do not may reach all of the block's queries.
+ * (code 10).  NaN or infinity in a row that some queries of a sequence
+ * mask and others do not may reach all of its queries.
  * R = 128, 256, 384 or 512 with P <= 64 a multiple of 8 and 16-byte aligned
  * bases and strides run on the tensor cores; other sizes up to R <= 512, R + P
  * <= 640 and other alignments run a slower kernel.  opt->workspace
  * (sbgemm_latent_workspace_bytes) lets the keys of a sequence be split over
- * the whole GPU; without it one CTA takes a sequence's every 64 query rows.
+ * the whole GPU (calls that may run at the same time need workspaces of their
+ * own); without it one CTA reads all keys of a sequence for each 64 query rows.
  * The results depend on the split, and so on the lengths of all sequences,
  * in their rounding only, and repeat from run to run.  Of `opt` only the
  * workspace is read; force_path must be AUTO.  Errors as

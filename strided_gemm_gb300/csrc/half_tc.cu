@@ -13,9 +13,9 @@
 // Roles: warp 8 issues the TMA loads, warp 9 the MMAs, warps 0-3 and 4-7 take
 // the accumulator (one of two in TMEM, so that the next tile's MMAs run
 // meanwhile) in turns of 64 columns, round it once and send it out by TMA
-// through swizzled 16 KB buffers, two for each group (one group alone took 4.2
-// us a tile of 128 x 256, twice its MMAs at K = 512); a C without a tensor map,
-// or one that is added to, goes straight from registers.
+// through swizzled 16 KB buffers, two for each group (128 products of
+// 64 x 512 x 128: 8.3 us, 10.3 with one buffer each); a C without a
+// tensor map, or one that is added to, goes straight from registers.
 //
 // Products of long K run on CTA pairs (cta_group::2): one MMA of 256 x 256 x 16
 // over both CTAs' shared memory, each holding its 128 rows of the tile and half

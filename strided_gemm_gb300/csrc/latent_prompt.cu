@@ -67,12 +67,11 @@ struct Params {
     int heads, q_blocks;
     int n_pieces, v_pieces, rope;            // pieces of K's nope part and of V; rope: one more piece
     int n_steps, r_steps;                    // MMA K steps of the last nope piece and of the rope piece
-    int Dn, Dv;
+    int Dv;
     float scale_log2;
     int causal;
     uint32_t idesc_s, idesc_v, idesc_v_half; // P V of all columns at once; of 64 of them
-    int v_tail;                              // columns of V's last piece
-    uint32_t idesc_v_tail;
+    uint32_t idesc_v_tail;                   // and of V's last piece
     int o_vec;                               // O rows take 16-byte stores
 };
 
@@ -580,15 +579,14 @@ bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_
     p.v_pieces = (int)((a.Dv + 63) / 64);
     p.n_steps = a.Dn > 0 ? (int)((a.Dn - (p.n_pieces - 1) * 64 + 15) / 16) : 0;
     p.r_steps = (int)((a.P + 15) / 16);
-    p.Dn = (int)a.Dn; p.Dv = (int)a.Dv;
+    p.Dv = (int)a.Dv;
     p.scale_log2 = a.alpha * 1.4426950408889634f;
     p.causal = a.causal;
     const bool bf = a.type == SBGEMM_TYPE_BF16;
     p.idesc_s = idesc16(bf, BN, false, false);
     p.idesc_v = idesc16(bf, (int)((a.Dv + 15) / 16 * 16), false, true);
     p.idesc_v_half = idesc16(bf, 64, false, true);
-    p.v_tail = (int)(a.Dv > 64 ? a.Dv - 64 : 0);
-    p.idesc_v_tail = idesc16(bf, std::max(16, (p.v_tail + 15) / 16 * 16), false, true);
+    p.idesc_v_tail = idesc16(bf, std::max<int>(16, (int)(a.Dv - 64 + 15) / 16 * 16), false, true);
     p.o_vec = reinterpret_cast<uintptr_t>(a.O) % 16 == 0 && a.tsO % 8 == 0 && (a.heads == 1 || a.hsO % 8 == 0);
     *err = bf ? launch<__nv_bfloat16>(m, p, a.n_seqs, stream) : launch<__half>(m, p, a.n_seqs, stream);
     return true;

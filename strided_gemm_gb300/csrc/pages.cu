@@ -149,8 +149,8 @@ __global__ void copy_claim_kernel(const int32_t* pairs, int64_t n, int64_t num_b
 }
 
 // Few pairs of a small pool: every block makes the claims for itself in shared
-// memory, and the copy is one launch (1500 pairs of 8192 pages: 12 us less than
-// with a memset and a launch for them).
+// memory, and the copy is one launch (1500 pairs of 73.7 KB pages in a pool of 8192: 38.9
+// us, 43.5 with a memset and a launch for them).
 constexpr int64_t kOwnClaimPairs = 8192, kOwnClaimBlocks = 24576;
 
 template <bool kOwnClaims>

@@ -272,7 +272,8 @@ int sbgemm_latent_attention_paged(
         return SBGEMM_ERR_INVALID_VALUE;
     if ((i128)max_blocks * block_size < (i128)N) return SBGEMM_ERR_INVALID_VALUE;
     if (R > kLatentMaxV || R + P > kLatentMaxQK) return SBGEMM_ERR_UNSUPPORTED;
-    if (q_len >= kInt || heads >= kInt || N >= kInt || n_seqs >= kInt || block_size >= kInt ||
+    // (A block of keys beyond the last one still has an int for its index.)
+    if (q_len >= kInt || heads >= kInt || N > kInt - 64 || n_seqs >= kInt || block_size >= kInt ||
         (i128)q_len * heads >= kInt || (i128)q_len * heads * n_seqs >= kInt)
         return SBGEMM_ERR_UNSUPPORTED;
     if (!Q || !cache || !block_table || !O) return SBGEMM_ERR_NULL_POINTER;

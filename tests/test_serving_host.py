@@ -62,7 +62,8 @@ def paged(**kw):
     (INVALID, dict(type=0)), (INVALID, dict(q_len=-1)), (INVALID, dict(N=-1)), (INVALID, dict(causal=2)),
     (INVALID, dict(N=129)), (INVALID, dict(num_blocks=0)), (INVALID, dict(block_size=0)),
     (INVALID, dict(max_blocks=0)), (UNSUPPORTED, dict(R=513)), (UNSUPPORTED, dict(P=129)),
-    (UNSUPPORTED, dict(heads=1 << 31)), (NULL, dict(Q=0)), (NULL, dict(cache=0)), (NULL, dict(block_table=0)),
+    (UNSUPPORTED, dict(heads=1 << 31)), (UNSUPPORTED, dict(N=(1 << 31) - 64, max_blocks=1 << 30)),
+    (NULL, dict(Q=0)), (NULL, dict(cache=0)), (NULL, dict(block_table=0)),
     (NULL, dict(O=0)), (INVALID, dict(Q=A + 1)), (INVALID, dict(block_table=C + 2)), (INVALID, dict(seq_lens=D + 1)),
     (OVERLAP, dict(hsO=256)), (OVERLAP, dict(bsO=0)), (OVERLAP, dict(O=B)), (OVERLAP, dict(O=A)), (OVERLAP, dict(O=D)),
     (INVALID, dict(workspace=F + 16, workspace_bytes=1 << 20)), (INVALID, dict(psC=1 << 60)),
