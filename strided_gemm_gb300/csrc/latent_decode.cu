@@ -42,18 +42,23 @@
 // Up to 32 rows three stages of 48 keys keep two blocks' loads in flight under
 // the third's MMAs: 8.7 k cycles for 144 keys, where two stages of 64 loaded and
 // computed in turns, 11 k cycles for 128 (16 heads, all SMs).  64 rows' queries
-// leave room for two stages of 64 only: 7.0 k cycles for 128 keys, of them 3.6 k
-// until a block's rows are in and 3.4 k of scores, softmax and P V in a chain.
-// (Four stages of 32 there took 443 us for the 177 below; each stage's load and
-// release in two halves 181.)
+// leave room for two stages of 64 only, which load and compute in turns: a block
+// takes the time until its rows are in and a chain of scores, softmax and P V of
+// 3.4 k cycles. So the block that a stage takes next is prefetched into L2, and
+// where the groups of 64 rows are even in number two CTAs with the same blocks
+// form a pair: each fetches half of a block's pieces for both (multicast), and a
+// stage is free once both have read it. 128 heads as below: 178 us with neither,
+// 172 with the prefetch, 176 with pairs, 165 with both. (Before them four stages
+// of 32 keys took 443 us for 177; each stage's load and release in two halves
+// 181.)
 //
 // Measured on a GB300, bf16 or fp16, R = 512, P = 64, join included: 64
-// sequences of 2048 to 8192 keys with 128 heads 177 us (399 MB: 2.2 TB/s, 520
+// sequences of 2048 to 8192 keys with 128 heads 165 us (399 MB: 2.4 TB/s, 560
 // TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 55 us (193 MB: 3.5
 // TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 16.5 us.
-// Bound: few heads by the cache's bytes and a start of 7 us; 128 heads (two
-// CTAs on the same blocks at the same time, the second read hitting L2) by the
-// chain above.
+// Bound: few heads by the cache's bytes and a start of 7 us; 128 heads by the
+// chain above and, at a sequence's end, the way of 64 x 512 sums to the workspace
+// and back (join 12 us).
 #include <algorithm>
 #include <atomic>
 
@@ -171,7 +176,7 @@ struct Walk {
     }
 };
 
-template <typename T, int NB>
+template <typename T, int NB, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
     constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
@@ -186,18 +191,19 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int group = blockIdx.x % p.groups, member = blockIdx.x / p.groups;
     const int tiles_o = p.R / 128;
+    const int rank = kPair ? (int)(cluster_rank() & 1) : 0;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&c.full[i], 1);
-            mbar_init(&c.empty[i], 1);
+            mbar_init(&c.empty[i], kPair ? 2 : 1);
         }
         mbar_init(&c.q_full, kMathWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&c.s_full[i], 1);
         mbar_init(&c.p_full, kMathWarps);
         mbar_init(&c.o_free, kMathWarps);
         mbar_init(&c.done, 1);
-        fence_mbar_init();
+        fence_mbar_init_cluster();
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&c.tmem_base, kTmemAll);
@@ -268,6 +274,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    // A pair's barriers are there before either CTA signals the other's.
+    if constexpr (kPair) cluster_sync();
     tc_fence_after();
     constexpr uint32_t tmem = kTmemBase;
     Walk<BT> w{c.seq0, c.tile0, c.count};
@@ -284,20 +292,22 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         bool ok = true;
         while (ok && w.next(p)) {
             const int32_t* table = p.table + w.s * p.max_blocks;
+            // The page of a run's first row; num_blocks, outside the tensor map, for a bad one.
+            auto page_of = [&](int n) {
+                const int page = table[n / p.block_size];
+                if (page >= 0 && page < p.num_blocks) return page;
+                record_status(&g_wait_status, kPagedInput);
+                return p.num_blocks;
+            };
+            int next = -1, next_page = 0;    // the stage's next block, already looked up
             for (int j = w.j0; j < w.j1; ++j, ++i) {
                 if (i % kStages != st) continue;
                 const uint32_t ph_empty = (uint32_t)((i / kStages - 1) & 1);
                 if (p.run && (j + 1) * BT <= w.len) {
                     // A whole block: lane x takes run x.
                     const int runs = BT / p.run, n = j * BT + lane * p.run;
-                    int page = 0;
-                    if (lane < runs) {
-                        page = table[n / p.block_size];
-                        if (page < 0 || page >= p.num_blocks) {
-                            record_status(&g_wait_status, kPagedInput);
-                            page = p.num_blocks;
-                        }
-                    }
+                    int page = next_page;
+                    if (lane < runs && next != j) page = page_of(n);
                     if (i >= kStages && !bar_wait(&c.empty[st], ph_empty)) {
                         record_status(&g_wait_status, kWaitEmpty);
                         ok = false;
@@ -308,10 +318,31 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     __syncwarp();
                     if (lane < runs) {
                         uint8_t* dst = skv + st * p.chunks * kChunkBytes + lane * p.run * 128;
-                        for (int k = 0; k < p.chunks; ++k)
-                            tma_load_3d(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64, n % p.block_size, page);
+                        // A pair's CTA fetches every other piece for both.
+                        for (int k = rank; k < p.chunks; k += kPair ? 2 : 1) {
+                            if constexpr (kPair)
+                                tma_load_3d_both(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64,
+                                                 n % p.block_size, page);
+                            else
+                                tma_load_3d(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64, n % p.block_size,
+                                            page);
+                        }
                     }
                     landing = i + 1;
+                    // Into L2 already what this stage takes next (with three stages
+                    // another two blocks are under way as it is).
+                    next = j + kStages;
+                    if (NB == 64 && next < w.j1 && (next + 1) * BT <= w.len) {
+                        if (lane < runs) {
+                            const int at = next * BT + lane * p.run;
+                            next_page = page_of(at);
+                            if (next_page < p.num_blocks)
+                                for (int k = rank; k < p.chunks; k += kPair ? 2 : 1)
+                                    tma_prefetch_3d(&rows_map, k * 64, at % p.block_size, next_page);
+                        }
+                    } else {
+                        next = -1;
+                    }
                     continue;
                 }
                 // The rows' places first: their table entries arrive while the stage drains.
@@ -418,7 +449,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
                                      (j | x) ? 1u : 0u);
                     }
-                    mma_commit(&c.empty[i % kStages]);
+                    if constexpr (kPair) mma_commit_both(&c.empty[i % kStages]);
+                    else mma_commit(&c.empty[i % kStages]);
                     if (!ahead) {
                         if (!bar_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             timed_out(kWaitFull);
@@ -684,6 +716,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    // Neither CTA of a pair leaves while the other may write its memory.
+    if constexpr (kPair) cluster_sync();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(kTmemBase, kTmemAll);
@@ -896,23 +930,63 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
 constexpr size_t kJoinBytes = kMaxJoins * sizeof(Join);
 
 int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+cudaLaunchAttribute pair_attribute() {
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = 2;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    return a;
+}
+
 size_t part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
 
-template <typename T, int NB>
-cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
-    static std::atomic<uint64_t> attr_done{0};
+// How often the current device holds the kernel at a time, in CTAs or pairs; 0
+// on a CUDA error.  A pair's kernel always asks for the shared memory of the
+// widest rows, so that no SM takes both of its CTAs: each wants all of TMEM.
+template <typename T, int NB, bool kPair>
+int fit(int sms) {
+    static std::atomic<int> known[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    const uint64_t bit = 1ull << (dev & 63);
-    static_assert(smem_bytes<NB>(kMaxChunks) <= 232448, "shared memory per CTA");
-    if (!(attr_done.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem_bytes<NB>(kMaxChunks));
-        if (e != cudaSuccess) return e;
-        attr_done.fetch_or(bit);
+    int n = known[dev & 63].load();
+    if (n) return n;
+    constexpr size_t bytes = smem_bytes<NB>(kMaxChunks);
+    static_assert(bytes <= 232448, "shared memory per CTA");
+    static_assert(!kPair || bytes > 116 * 1024, "one CTA a SM");
+    if (cudaFuncSetAttribute(decode_kernel<T, NB, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+        cudaSuccess)
+        return 0;
+    n = sms;
+    if (kPair) {
+        cudaLaunchAttribute cluster = pair_attribute();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = bytes;
+        cfg.attrs = &cluster;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<T, NB, kPair>, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            return 0;
+        }
     }
-    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
-    if (p.split) {
+    known[dev & 63].store(n);
+    return n;
+}
+
+template <typename T, int NB, bool kPair>
+cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    if (!fit<T, NB, kPair>(sms)) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute cluster = pair_attribute();
+    cudaLaunchConfig_t main{};
+    main.gridDim = dim3((unsigned)(p.groups * p.per_group));
+    main.blockDim = dim3(kThreads);
+    main.dynamicSmemBytes = smem_bytes<NB>(kPair ? kMaxChunks : p.chunks);
+    main.stream = stream;
+    main.attrs = &cluster;
+    main.numAttrs = kPair ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&main, decode_kernel<T, NB, kPair>, map, p);
+    if (e == cudaSuccess && p.split) {
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;
@@ -922,17 +996,17 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
         cfg.stream = stream;
         cfg.attrs = &early;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T, NB>, p);
-        if (e != cudaSuccess) return e;
+        e = cudaLaunchKernelEx(&cfg, join_kernel<T, NB>, p);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T>
-cudaError_t launch_rows(int nb, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
-    if (nb == 16) return launch<T, 16>(map, p, sms, stream);
-    if (nb == 32) return launch<T, 32>(map, p, sms, stream);
-    return launch<T, 64>(map, p, sms, stream);
+cudaError_t launch_rows(int nb, bool pair, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch<T, 16, false>(map, p, sms, stream);
+    if (nb == 32) return launch<T, 32, false>(map, p, sms, stream);
+    if (pair) return launch<T, 64, true>(map, p, sms, stream);
+    return launch<T, 64, false>(map, p, sms, stream);
 }
 
 bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
@@ -970,20 +1044,6 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     const bool bf = a.type == SBGEMM_TYPE_BF16;
     p.idesc_s = idesc16(bf, nb, false, false, 64);
     p.idesc_o = idesc16(bf, nb, true, true);
-    // CTAs for each group of rows: an SM each, as far as the workspace has two
-    // slots for every one of them; without it whole sequences.
-    int64_t each = std::max<int64_t>(1, sms / groups);
-    const int64_t slots = a.workspace && a.workspace_bytes > kJoinBytes
-                              ? (int64_t)((a.workspace_bytes - kJoinBytes) / part_bytes(nb, a.R)) : 0;
-    each = std::min(each, slots / (2 * groups));
-    if (each > 1 && each * groups <= kMaxJoins) {
-        p.split = 1;
-        p.joins = static_cast<Join*>(a.workspace);
-        p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kJoinBytes);
-    } else {
-        each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
-    }
-    p.per_group = (int)each;
     // Runs of rows that lie in one page wherever a block begins; whole groups
     // of 8 rows, the swizzle's period.
     CUtensorMap map{};
@@ -1002,7 +1062,31 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         }
         p.run = run;
     }
-    *err = bf ? launch_rows<__nv_bfloat16>(nb, map, p, sms, stream) : launch_rows<__half>(nb, map, p, sms, stream);
+    // CTAs for each group of rows: an SM each, as far as the workspace has two
+    // slots for every one of them; without it whole sequences.
+    int64_t at_once = sms;
+    const bool pair = p.run > 0 && nb == 64 && groups % 2 == 0;
+    if (pair) {
+        at_once = 2 * (bf ? fit<__nv_bfloat16, 64, true>(sms) : fit<__half, 64, true>(sms));
+        if (!at_once) {
+            *err = cudaErrorInvalidConfiguration;
+            return true;
+        }
+    }
+    int64_t each = std::max<int64_t>(1, at_once / groups);
+    const int64_t slots = a.workspace && a.workspace_bytes > kJoinBytes
+                              ? (int64_t)((a.workspace_bytes - kJoinBytes) / part_bytes(nb, a.R)) : 0;
+    each = std::min(each, slots / (2 * groups));
+    if (each > 1 && each * groups <= kMaxJoins) {
+        p.split = 1;
+        p.joins = static_cast<Join*>(a.workspace);
+        p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kJoinBytes);
+    } else {
+        each = std::min<int64_t>(std::max<int64_t>(1, at_once / groups), a.n_seqs);
+    }
+    p.per_group = (int)each;
+    *err = bf ? launch_rows<__nv_bfloat16>(nb, pair, map, p, sms, stream)
+              : launch_rows<__half>(nb, pair, map, p, sms, stream);
     return true;
 }
 

@@ -453,6 +453,62 @@ def test_paged_many_sequences(torch, workspace):
     c.check(torch, True)
 
 
+PAIRS = [
+    # lens, heads, q_len, R, P, block, causal: an even number of 64-row groups,
+    # whose CTAs load the cache's blocks together
+    ([0, 700, 1, 64, 65, 3000], 128, 1, 512, 64, 64, True),
+    ([127, 128, 129, 0], 120, 1, 512, 64, 16, True),
+    ([40, 260], 64, 4, 128, 64, 8, True),
+    ([200, 3, 64], 64, 2, 384, 0, 128, True),
+    ([5, 90, 1000], 70, 5, 256, 32, 32, False),
+    ([130, 500], 128, 1, 512, 64, 20, True),
+]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(PAIRS)))
+def test_paged_pairs_of_row_groups(torch, workspace, t, case):
+    lens, heads, q_len, R, P, block, causal = PAIRS[case]
+    c = Paged(torch, t, lens, heads, q_len, R, P, block, seed=40 + case)
+    for ws in (workspace, None):
+        c.o.fill_(float("nan"))
+        first = c.run(causal, ws).clone()
+        c.check(torch, causal)
+        for _ in range(3):
+            assert torch.equal(c.run(causal, ws), first)
+    status_is(0)
+
+
+def test_paged_pairs_replayed_beside_another_stream(torch, workspace):
+    a = Paged(torch, "bf16", [4000, 100, 900], 128, 1, 512, 64, 64, seed=50)
+    b = Paged(torch, "fp16", [50, 3000], 64, 4, 128, 64, 16, seed=51)
+    first = a.run(True, workspace).clone()
+    other = torch.empty_like(workspace)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        a.run(True, workspace)
+    s2 = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        graph.replay()
+        b.run(True, other, stream=s2.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a.o, first)
+    a.check(torch, True)
+    b.check(torch, True)
+    status_is(0)
+
+
+def test_paged_pairs_report_bad_device_data(torch, workspace):
+    c = Paged(torch, "bf16", [200, 70], 128, 1, 512, 64, 16, seed=52)
+    c.table[0, 3] = -1                        # rows 48..63 of sequence 0 read as zeros
+    c.run(True, workspace)
+    c.ctx[0][48:64] = 0.0
+    c.check(torch, True)
+    status_is(10)
+    status_is(0)
+
+
 # ---- latent attention, expanded form over packed sequences --------------------------
 
 class Packed:
