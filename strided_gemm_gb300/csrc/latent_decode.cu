@@ -48,14 +48,14 @@
 // where the groups of 64 rows are even in number two CTAs with the same blocks
 // form a pair: each fetches half of a block's pieces for both (multicast), and a
 // stage is free once both have read it. 128 heads as below: 178 us with neither,
-// 172 with the prefetch, 176 with pairs, 165 with both. (Before them four stages
+// 172 with the prefetch, 176 with pairs, 166 with both. (Before them four stages
 // of 32 keys took 443 us for 177; each stage's load and release in two halves
 // 181.)
 //
 // Measured on a GB300, bf16 or fp16, R = 512, P = 64, join included: 64
-// sequences of 2048 to 8192 keys with 128 heads 165 us (399 MB: 2.4 TB/s, 560
-// TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 55 us (193 MB: 3.5
-// TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 16.5 us.
+// sequences of 2048 to 8192 keys with 128 heads 166 us (399 MB: 2.4 TB/s, 555
+// TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 52 us (193 MB: 3.7
+// TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 14.5 us.
 // Bound: few heads by the cache's bytes and a start of 7 us; 128 heads by the
 // chain above and, at a sequence's end, the way of 64 x 512 sums to the workspace
 // and back (join 12 us).
@@ -81,9 +81,10 @@ template <int NB> struct Shape {
 constexpr float kRaise = 8.0f;               // log2 headroom before the reference maximum rises
 __device__ unsigned int g_wait_status = 0;
 
-// A sequence that begins in a CTA and ends in a later one: its first piece is
-// in `slot`, the others in slot 0 of the CTAs behind, up to member `last`.
-struct Join { int32_t seq, slot, member, last; };    // seq < 0: none begins here
+// A sequence that begins in a group's CTA `member` and ends in a later one: its
+// first piece is that CTA's first or (second = 1) last one, the others are the
+// first ones of the CTAs behind, up to `last`.
+struct Join { int32_t seq, member, last, second; };
 
 struct Params {
     const void* Q; int64_t hsQ, tsQ, bsQ;
@@ -101,7 +102,6 @@ struct Params {
     int causal;
     uint32_t idesc_s, idesc_o;
     int o_vec;                               // rows of O take 8-byte stores
-    Join* joins;                             // [groups * per_group]
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
 };
 
@@ -213,7 +213,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
-    int members = 1, lo = 0, units_total = 0;
     if (p.split) {
         // Units of this thread's sequence of the first round, and their sum over
         // the warp's lanes up to it; pools of more sequences look again below.
@@ -238,10 +237,9 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         int total = 0;
         for (int w = 0; w < kWarps; ++w) total += c.scan[w] + c.rest[w];
         // No CTA between a sequence's first and last one is empty.
-        members = min(p.per_group, total);
-        lo = member < members ? (int)((int64_t)member * total / members) : 0;
+        const int members = min(p.per_group, total);
+        const int lo = member < members ? (int)((int64_t)member * total / members) : 0;
         const int hi = member < members ? (int)((int64_t)(member + 1) * total / members) : 0;
-        units_total = total;
         if (tid == 0) c.count = hi - lo;
         int before = 0;                      // units of the sequences of earlier rounds
         for (int s0 = 0; s0 < p.n_seqs && before <= lo; s0 += kThreads) {
@@ -477,9 +475,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         const int row = quarter * 16 + (lane & 15), col = half * CPW + (lane >> 4) * CPT;
         const bool mine = row < BT;
         const int row_pieces = (p.R + p.P) / 8;
-        int i = 0, piece_no = 0, used = 0;                   // blocks, pieces, units so far
+        int i = 0, piece_no = 0;                             // blocks and pieces so far
         bool ok = true;
-        Join join{-1, 0, 0, 0};
         // Queries of the walk's piece on their way into shared memory.
         auto fetch_queries = [&](const Walk<BT>& w) {
             if (w.j1 > w.j0) {
@@ -699,12 +696,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         }
                     }
                 }
-            if (now.j0 == 0 && !whole) {
-                // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
-                const int64_t end = (int64_t)lo + used + now.units;
-                join = Join{now.s, slot, member, (int)((end * members + units_total - 1) / units_total) - 1};
-            }
-            used += max(n, 1);
             tc_fence_before();
             __syncwarp();
             if (n > 0 && lane == 0) mbar_arrive(&c.o_free);
@@ -712,7 +703,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             ++piece_no;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");   // on a failure too: shared memory outlives them
-        if (p.split && m == 0) p.joins[blockIdx.x] = join;
     }
     tc_fence_before();
     __syncthreads();
@@ -730,6 +720,12 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 // loads in flight at once; many (one long sequence): eight warps share the pieces of
 // 128 columns of a row.
 constexpr int kJoinThreads = 256, kFewPieces = 8, kMaxJoins = 512;
+// Blocks a SM: as many as stay resident, every one making the list once. Two,
+// with the registers to have all of a thread's loads in flight, take the three
+// measurements above, one sequence first, to 14.5, 51.7 and 167 us; three, for
+// the larger amounts of 64 rows, to 16.0, 52.0 and 165.5; eight in turns to
+// 16.5, 54.6 and 168.
+template <int NB> constexpr int kJoinBlocks = NB == 64 ? 3 : 2;
 
 template <typename T>
 __device__ __forceinline__ void store4(T* o, float4 v, bool vec) {
@@ -753,68 +749,83 @@ __device__ __forceinline__ float4 scale4(const float4& o, float f) {
 }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ Params p) {
-    // Launched while the pieces are still being made (the launch hides behind
-    // them): nothing of theirs is read before they are complete.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // The split sequences, those of few pieces from the front and those of many
-    // from the back, in the order of the CTAs in which they begin: every block
-    // has the same list.
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(const __grid_constant__ Params p) {
+    // Launched while the pieces are still being made: which sequences are split
+    // follows from the lengths, as in the kernel that splits them, so that every
+    // block has its list, those of few pieces from the front and those of many
+    // from the back, before it waits for the pieces.
+    constexpr int BT = Shape<NB>::BT, kJoinWarps = kJoinThreads / 32;
     __shared__ Join list[kMaxJoins];
-    __shared__ int few, many;
     __shared__ float4 sums[8][32];
     __shared__ float tops[8], ls[8];
-    const int ctas = p.groups * p.per_group;
-    __shared__ int counts[2][kMaxJoins / 32];
+    __shared__ int scan[kJoinWarps], found[2][kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int few = 0, many = 0;
     {
-        const int lane = threadIdx.x & 31;
-        const unsigned below = (1u << lane) - 1;
-        Join jn[kMaxJoins / kJoinThreads];
-        unsigned f[kMaxJoins / kJoinThreads], g[kMaxJoins / kJoinThreads];
-#pragma unroll
-        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
-            const int c = k * kJoinThreads + threadIdx.x;
-            jn[k] = Join{-1, 0, 0, 0};
-            if (c < ctas) jn[k] = p.joins[c];
-        }
-#pragma unroll
-        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
-            const bool is_few = jn[k].last - jn[k].member < kFewPieces;
-            f[k] = __ballot_sync(~0u, jn[k].seq >= 0 && is_few);
-            g[k] = __ballot_sync(~0u, jn[k].seq >= 0 && !is_few);
-            if (lane == 0) {
-                counts[0][k * (kJoinThreads / 32) + (threadIdx.x >> 5)] = __popc(f[k]);
-                counts[1][k * (kJoinThreads / 32) + (threadIdx.x >> 5)] = __popc(g[k]);
-            }
-        }
+        auto units_at = [&](int s) { return s < p.n_seqs ? units_of<BT>(seq_len(p, s, false)) : 0; };
+        const int u0 = units_at(threadIdx.x);
+        int mine = u0;
+        for (int s = threadIdx.x + kJoinThreads; s < p.n_seqs; s += kJoinThreads) mine += units_at(s);
+        mine = __reduce_add_sync(~0u, mine);
+        if (lane == 0) scan[warp] = mine;
         __syncthreads();
+        int total = 0;
+        for (int w = 0; w < kJoinWarps; ++w) total += scan[w];
+        const int members = min(p.per_group, total);
+        int before = 0;                      // units of the sequences of earlier rounds
+        for (int s0 = 0; s0 < p.n_seqs; s0 += kJoinThreads) {
+            const int s = s0 + threadIdx.x, u = s0 == 0 ? u0 : units_at(s);
+            int inc = u;
 #pragma unroll
-        for (int k = 0; k < kMaxJoins / kJoinThreads; ++k) {
-            int nf = 0, nm = 0, tf = 0, tm = 0;
-            for (int q = 0; q < kMaxJoins / 32; ++q) {
-                const bool before = q < k * (kJoinThreads / 32) + (int)(threadIdx.x >> 5);
-                if (before) {
-                    nf += counts[0][q];
-                    nm += counts[1][q];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += x;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            int at = before + inc - u;
+            for (int w = 0; w < kJoinWarps; ++w) {
+                if (w < warp) at += scan[w];
+                before += scan[w];
+            }
+            // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
+            auto member_of = [&](int unit) { return (int)(((int64_t)(unit + 1) * members + total - 1) / total) - 1; };
+            const int first = u ? member_of(at) : 0, last = u ? member_of(at + u - 1) : 0;
+            const Join jn{s, first, last, (int64_t)first * total / members < at};
+            const unsigned below = (1u << lane) - 1;
+            const unsigned f = __ballot_sync(~0u, last > first && last - first < kFewPieces);
+            const unsigned g = __ballot_sync(~0u, last - first >= kFewPieces);
+            if (lane == 0) {
+                found[0][warp] = __popc(f);
+                found[1][warp] = __popc(g);
+            }
+            __syncthreads();
+            int nf = few + __popc(f & below), nm = many + __popc(g & below);
+            for (int w = 0; w < kJoinWarps; ++w) {
+                if (w < warp) {
+                    nf += found[0][w];
+                    nm += found[1][w];
                 }
-                tf += counts[0][q];
-                tm += counts[1][q];
+                few += found[0][w];
+                many += found[1][w];
             }
-            if (f[k] >> lane & 1) list[nf + __popc(f[k] & below)] = jn[k];
-            if (g[k] >> lane & 1) list[kMaxJoins - 1 - (nm + __popc(g[k] & below))] = jn[k];
-            if (threadIdx.x == 0) {
-                few = tf;
-                many = tm;
-            }
+            if (f >> lane & 1) list[nf] = jn;
+            if (g >> lane & 1) list[kMaxJoins - 1 - nm] = jn;
         }
     }
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The slot of piece k of a sequence in a group of rows.
+    auto slot_of = [&](const Join& jn, int group, int k) {
+        return 2 * ((int64_t)(jn.member + k) * p.groups + group) + (k == 0 ? jn.second : 0);
+    };
     const int per_row = p.R / 8;                             // threads a row
     const int64_t slot_floats = (int64_t)NB * (2 + p.R);
     const int steps = (NB * per_row + kJoinThreads - 1) / kJoinThreads;
-    for (int it = blockIdx.x; it < few * steps; it += gridDim.x) {
-        const Join jn = list[it / steps];
-        const int group = (jn.slot >> 1) % p.groups, pieces = jn.last - jn.member + 1;
+    for (int it = blockIdx.x; it < few * p.groups * steps; it += gridDim.x) {
+        const Join jn = list[it / steps / p.groups];
+        const int group = it / steps % p.groups, pieces = jn.last - jn.member + 1;
         const int at = it % steps * kJoinThreads + threadIdx.x;
         const int row = at / per_row, e = at % per_row * 8, r = group * NB + row;
         if (row >= NB || r >= p.rows) continue;
@@ -830,8 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
                 lx[q] = 0.0f;
                 v[q][0] = v[q][1] = make_float4(0, 0, 0, 0);
                 if (k < pieces) {
-                    const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
-                    const float* src = p.parts + slot * slot_floats;
+                    const float* src = p.parts + slot_of(jn, group, k) * slot_floats;
                     mx[q] = src[row];
                     lx[q] = src[NB + row];
                     const float4* o = reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)row * p.R + e);
@@ -860,16 +870,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
         store4(out, scale4(o0, inv), p.o_vec);
         store4(out + 4, scale4(o1, inv), p.o_vec);
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarters = p.R / 128;
-    for (int it = blockIdx.x; it < many * NB * quarters; it += gridDim.x) {
-        const Join jn = list[kMaxJoins - 1 - it / (NB * quarters)];
-        const int group = (jn.slot >> 1) % p.groups, pieces = jn.last - jn.member + 1;
+    const int quarters = p.R / 128;
+    for (int it = blockIdx.x; it < many * p.groups * NB * quarters; it += gridDim.x) {
+        const Join jn = list[kMaxJoins - 1 - it / (NB * quarters) / p.groups];
+        const int group = it / (NB * quarters) % p.groups, pieces = jn.last - jn.member + 1;
         const int row = it / quarters % NB, e = it % quarters * 128 + lane * 4, r = group * NB + row;
         if (r >= p.rows) continue;
-        auto piece = [&](int k) {
-            const int64_t slot = k == 0 ? jn.slot : 2ll * ((int64_t)(jn.member + k) * p.groups + group);
-            return p.parts + slot * slot_floats;
-        };
+        auto piece = [&](int k) { return p.parts + slot_of(jn, group, k) * slot_floats; };
         // This warp's pieces: a running maximum over groups of four.
         float top = -INFINITY, l = 0.0f;
         float4 o = make_float4(0, 0, 0, 0);
@@ -926,8 +933,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
         }
     }
 }
-
-constexpr size_t kJoinBytes = kMaxJoins * sizeof(Join);
 
 int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 cudaLaunchAttribute pair_attribute() {
@@ -991,7 +996,9 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)sms * 8);
+        // No more blocks than there can be rows to join.
+        const int64_t most = (int64_t)std::min(p.n_seqs, p.per_group - 1) * p.groups * NB * (p.R / 128);
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)sms * kJoinBlocks<NB>, most));
         cfg.blockDim = dim3(kJoinThreads);
         cfg.stream = stream;
         cfg.attrs = &early;
@@ -1015,7 +1022,7 @@ bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
 
 }  // namespace
 
-size_t latent_decode_workspace_bytes(int sms) { return kJoinBytes + 2 * (size_t)sms * part_bytes(64, 512); }
+size_t latent_decode_workspace_bytes(int sms) { return 2 * (size_t)sms * part_bytes(64, 512); }
 
 bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err) {
     if (a.R % 128 != 0 || a.R > 512 || a.P % 8 != 0 || a.P > 64) return false;
@@ -1074,13 +1081,11 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         }
     }
     int64_t each = std::max<int64_t>(1, at_once / groups);
-    const int64_t slots = a.workspace && a.workspace_bytes > kJoinBytes
-                              ? (int64_t)((a.workspace_bytes - kJoinBytes) / part_bytes(nb, a.R)) : 0;
+    const int64_t slots = a.workspace ? (int64_t)(a.workspace_bytes / part_bytes(nb, a.R)) : 0;
     each = std::min(each, slots / (2 * groups));
     if (each > 1 && each * groups <= kMaxJoins) {
         p.split = 1;
-        p.joins = static_cast<Join*>(a.workspace);
-        p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kJoinBytes);
+        p.parts = static_cast<float*>(a.workspace);
     } else {
         each = std::min<int64_t>(std::max<int64_t>(1, at_once / groups), a.n_seqs);
     }
