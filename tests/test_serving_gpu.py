@@ -462,6 +462,10 @@ PAIRS = [
     ([200, 3, 64], 64, 2, 384, 0, 128, True),
     ([5, 90, 1000], 70, 5, 256, 32, 32, False),
     ([130, 500], 128, 1, 512, 64, 20, True),
+    ([1], 128, 1, 512, 64, 64, True),
+    ([0], 128, 1, 512, 64, 64, True),
+    ([20000], 128, 1, 512, 64, 64, True),
+    ([64] * 300, 65, 1, 128, 64, 64, True),
 ]
 
 
