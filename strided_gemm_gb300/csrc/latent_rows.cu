@@ -18,8 +18,9 @@ constexpr int kWarps = 4;
 constexpr int XQ = (int)kLatentMaxQK / 32, XV = (int)kLatentMaxV / 32;
 __device__ unsigned int g_status = 0;
 
-// Running softmax of one row over keys; `key(n, K, K2, V)` gives the key's
-// nope part, rope part and value rows, or K == nullptr for a row of zeros.
+// Running softmax of one row over keys; `key(n, K, K2, V)` gives the key's nope
+// part, rope part and value rows, or false for a row of zeros.  (No pointer
+// says so: a part of no elements may lie anywhere, at address 0 too.)
 template <typename T, typename Key>
 __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, int64_t keys, float scale_log2,
                                            T* o, Key key) {
@@ -32,9 +33,9 @@ __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, i
     float top = -INFINITY, sum = 0.0f;
     for (int64_t n = 0; n < keys; ++n) {
         const T *kn, *kr, *v;
-        key(n, &kn, &kr, &v);
+        const bool there = key(n, &kn, &kr, &v);
         float z = 0.0f;
-        if (kn) {
+        if (there) {
 #pragma unroll
             for (int x = 0; x < XQ; ++x) {
                 const int d = lane + 32 * x;
@@ -54,7 +55,7 @@ __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, i
         // A score of -infinity weighs nothing, also as the first one.
         const float w = z == -INFINITY ? 0.0f : exp2f(z - top);
         sum += w;
-        if (v) {
+        if (there) {
 #pragma unroll
             for (int x = 0; x < XV; ++x)
                 if (lane + 32 * x < dv) acc[x] = fmaf(w, to_float(v[lane + 32 * x]), acc[x]);
@@ -85,11 +86,11 @@ rows_paged_kernel(const LatentPaged a, float scale_log2) {
                           const int64_t page = a.table[s * a.max_blocks + n / a.block_size];
                           if (page < 0 || page >= a.num_blocks) {
                               record_status(&g_status, kPagedInput);
-                              *kn = *kr = *v = nullptr;
-                              return;
+                              return false;
                           }
                           *kn = *v = base + page * a.psC + n % a.block_size * a.rsC;
                           *kr = *kn + a.R;
+                          return true;
                       });
     }
 }
@@ -121,6 +122,7 @@ rows_packed_kernel(const LatentPacked a, float scale_log2) {
                           *kn = static_cast<const T*>(a.Kn) + (k0 + n) * a.tsK + h * a.hsK;
                           *kr = static_cast<const T*>(a.Kr) + (k0 + n) * a.tsR;
                           *v = static_cast<const T*>(a.V) + (k0 + n) * a.tsV + h * a.hsV;
+                          return true;
                       });
     }
 }

@@ -591,6 +591,34 @@ def test_packed_against_64_bits(torch, t, case):
     status_is(0)
 
 
+ROPE_ONLY = [
+    # q_lens, k_lens, heads, P, Dv, gap: sizes and alignments of the row kernel
+    ([5, 33], [9, 40], 2, 66, 128, 0),                 # P past the tensor cores' 64
+    ([7], [20], 1, 64, 136, 0),                        # Dv past their 128
+    ([30, 3], [30, 50], 3, 64, 64, 3),                 # rows of V without alignment
+]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(ROPE_ONLY)))
+def test_packed_rows_of_keys_without_a_nope_part(torch, t, case):
+    """Dn == 0: keys of the shared part alone.  K_nope has no element and may be
+    at any address, 0 included, which hides no key."""
+    q_lens, k_lens, heads, P, Dv, gap = ROPE_ONLY[case]
+    c = Packed(torch, t, q_lens, k_lens, heads, 0, P, Dv, seed=60 + case, gap=gap, scale=3.0)
+    assert c.kn.data_ptr() == 0
+    c.run(True)
+    c.check(torch, True)
+    c.whole.fill_(7.0)
+    nq, nk, row = c.q.shape[0], c.v.shape[0], Dv + gap
+    sg.sbgemm_latent_attention(sg.TYPE_BF16 if t == "bf16" else sg.TYPE_FP16, c.q.data_ptr(), P, heads * P, nq, 0, 0, 0,
+                               c.kr.data_ptr(), P, c.v.data_ptr(), row, heads * row, nk, c.qs.data_ptr(),
+                               c.ks.data_ptr(), len(q_lens), max(q_lens), c.o.data_ptr(), row, heads * row, heads, 0, P,
+                               Dv, c.alpha, 1, torch.cuda.current_stream().cuda_stream)
+    c.check(torch, True)
+    status_is(0)
+
+
 def test_packed_large_scores_and_strides(torch):
     for gap in (8, 3):
         c = Packed(torch, "bf16", [200, 90], [333, 90], 2, 128, 64, 128, seed=21, gap=gap, scale=40.0)
