@@ -28,7 +28,8 @@
 // between them holds the issue up for about 360 cycles (a barrier for each
 // piece: 549 us, 515 without, for the prompts below), so
 // every commit serves all that wait for it: the scores of the last tile tell
-// its softmax and the TMA warp.
+// its softmax, which tells the TMA warp (a commit to barriers of even and odd
+// blocks for both cost registers: 426 us for 416, 14.3 for 12.5).
 //
 // Roles (12 warps, all waits bounded): warp 0 TMA, warp 1 MMAs, warps 4-7 and
 // 8-11 the rows of the two tiles.  In the last block they also zero the rows of
@@ -78,7 +79,10 @@ struct Params {
 struct Smem {
     alignas(1024) uint8_t q[kTiles][kQPieces][kPiece];
     alignas(1024) uint8_t ring[kSlots][kPiece];
-    uint64_t q_full, k_full[2], v_full[2], v_empty;     // of even and odd blocks
+    // [2]: one for the even blocks, one for the odd ones.  Nothing is asked of
+    // block b + 2 before block b is through, so a wait for block b never finds its
+    // barrier a round further (where the parity says "not yet" for ever).
+    uint64_t q_full, k_full[2], v_full[2], v_empty[2], k_empty[2];
     uint64_t s_full[kTiles], p_full[kTiles], o_done[kTiles], v_clean, done;
     uint32_t tmem_base;
 };
@@ -131,8 +135,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.k_full[s], 1);
             mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_empty[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
         }
-        mbar_init(&sh.v_empty, 1);
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(&sh.s_full[t], 1);
             mbar_init(&sh.p_full[t], 4);
@@ -175,13 +180,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
             bool ok = true;
             auto need_k = [&](int b) {               // blocks come here in order, none left out
                 if (ok && b >= k_free) {
-                    ok = bar_wait(&sh.s_full[last_tile], (uint32_t)(b & 1));
+                    ok = bar_wait(&sh.k_empty[b & 1], (uint32_t)((b >> 1) & 1));
                     k_free = b + 1;
                 }
             };
             auto need_v = [&](int b) {
                 if (ok && b >= v_free) {
-                    ok = bar_wait(&sh.v_empty, (uint32_t)(b & 1));
+                    ok = bar_wait(&sh.v_empty[b & 1], (uint32_t)((b >> 1) & 1));
                     v_free = b + 1;
                 }
             };
@@ -294,7 +299,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                         mma16_ts(d + 64, a + 8 * x, d1 + x * kStepMN, p.idesc_v_tail, (j | x) ? 1u : 0u);
                 }
                 if (j == n - 1) mma_commit(&sh.o_done[t]);
-                else if (t == last_tile) mma_commit(&sh.v_empty);
+                else if (t == last_tile) mma_commit(&sh.v_empty[j & 1]);
             };
             constexpr std::integral_constant<int, 0> t0{};
             constexpr std::integral_constant<int, 1> t1{};
@@ -342,6 +347,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
                 ok = false;
                 break;
             }
+            // Both tiles have their scores: the block's K is read.
+            if (warp == 4 * last_tile + 4 && lane == 0) mbar_arrive(&sh.k_empty[j & 1]);
             tc_fence_after();
             const bool edge = j >= open;
             const int see = last - j * BN;               // columns up to this one count

@@ -619,6 +619,31 @@ def test_packed_rows_of_keys_without_a_nope_part(torch, t, case):
     status_is(0)
 
 
+SHORT_BLOCKS = [
+    # q_lens, k_lens, heads, Dn, P, Dv, causal: two or three pieces a block of keys
+    # in the ring of eight, so that several blocks are under way at once
+    ([300, 100], [20000, 9000], 2, 64, 0, 64, False),
+    ([256], [30000], 1, 64, 0, 64, True),
+    ([4000], [4000], 2, 64, 0, 64, True),
+    ([1, 129, 700], [6000, 300, 1500], 3, 0, 64, 64, True),
+    ([140], [140], 2, 0, 64, 128, True),
+    ([300, 90], [3000, 700], 2, 32, 32, 128, False),
+    ([130, 5], [130, 260], 1, 0, 16, 8, False),
+]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(SHORT_BLOCKS)))
+def test_packed_blocks_of_few_pieces(torch, t, case):
+    q_lens, k_lens, heads, Dn, P, Dv, causal = SHORT_BLOCKS[case]
+    c = Packed(torch, t, q_lens, k_lens, heads, Dn, P, Dv, seed=70 + case)
+    first = c.run(causal).clone()
+    c.check(torch, causal)
+    for _ in range(20):
+        assert torch.equal(c.run(causal), first)
+    status_is(0)
+
+
 def test_packed_large_scores_and_strides(torch):
     for gap in (8, 3):
         c = Packed(torch, "bf16", [200, 90], [333, 90], 2, 128, 64, 128, seed=21, gap=gap, scale=40.0)
