@@ -336,8 +336,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         const int last = p.causal ? min(nk - 1, m + nk - nq) : nk - 1;   // last key the row sees
         // Blocks below this one hide nothing from any of the tile's rows.
         const int open = (p.causal ? min(nk, max(0, m0 + t * BM + nk - nq + 1)) : nk) / BN;
-        // Never 0, so that a hidden score's infinity stays one when alpha is.
-        const float scale = fmaxf(fabsf(p.scale_log2), 1.0e-37f);
+        // Never 0, so that a hidden score's infinity stays one when alpha is: the
+        // least float, under which the largest score is below 2^-20.  A NaN stays.
+        const float scale = p.scale_log2 == 0.0f ? 1.0e-45f : fabsf(p.scale_log2);
         const bool negative = p.scale_log2 < 0.0f;
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
@@ -484,6 +485,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         ok = __all_sync(~0u, ok);
         if (ok) {
             tc_fence_after();
+            if (last < 0) sum = 0.0f;                // no key: zeros, whatever alpha is
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             T* out = static_cast<T*>(p.O) + (int64_t)(q0 + m) * p.tsO + (int64_t)head * p.hsO;
 #pragma unroll 1

@@ -321,6 +321,39 @@ def test_paged_scales_of_any_sign(torch, workspace):
         d.check(torch, True)
 
 
+@pytest.mark.parametrize("dims", [(128, 64, 128), (130, 66, 70)])       # tensor cores; row kernel
+def test_alpha_that_is_no_number(torch, workspace, dims):
+    """A NaN alpha makes NaN of every row that has a key, and nothing of the others."""
+    nan = float("nan")
+    c = Packed(torch, "bf16", [100, 7, 3], [60, 0, 200], 2, *dims, seed=33)    # the first 40 rows see no key
+    c.alpha = nan
+    c.run(True)
+    assert bool((c.o[:40] == 0).all()) and bool((c.o[100:107] == 0).all())
+    assert bool(torch.isnan(c.o[40:100]).all()) and bool(torch.isnan(c.o[107:110]).all())
+    R, P = (512, 64) if dims[0] == 128 else (40, 7)
+    d = Paged(torch, "fp16", [2, 0, 70], 16, 3, R, P, 16, seed=34)
+    d.alpha = nan
+    for ws in (workspace, None):
+        d.o.zero_()
+        d.run(True, ws)
+        assert bool((d.o[0, 0] == 0).all()) and bool((d.o[1] == 0).all())
+        assert bool(torch.isnan(d.o[0, 1:]).all()) and bool(torch.isnan(d.o[2]).all())
+    status_is(0)
+
+
+def test_alpha_of_zero_weighs_huge_scores_alike(torch, workspace):
+    for alpha in (0.0, -0.0):
+        c = Packed(torch, "bf16", [140], [300], 2, 128, 64, 128, seed=35, scale=1e18)
+        c.kn.mul_(1e18)                        # scores of 1e37 and more
+        c.alpha = alpha
+        c.run(True)
+        for i in (0, 77, 139):
+            v = c.v[: 161 + i].double()
+            # Equal weights of 1, exact in the type: additions and one rounding.
+            lim = (v.shape[0] + 8) * U * v.abs().mean(0) + 2 ** -18 * v.abs().mean(0) + HALF["bf16"] * v.mean(0).abs()
+            assert_within(torch, c.o[i], v.mean(0), lim + 2.0 ** -25, f"row {i}")
+
+
 def test_paged_smaller_workspaces(torch, workspace):
     """Fewer slots mean fewer CTAs, down to whole sequences: the same results
     within the bound."""
