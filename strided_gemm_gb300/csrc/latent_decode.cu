@@ -44,17 +44,13 @@
 // computed in turns, 11 k cycles for 128 (16 heads, all SMs).  64 rows' queries
 // leave room for two stages of 64 only, which load and compute in turns: a block
 // takes the time until its rows are in and a chain of scores, softmax and P V of
-// 3.4 k cycles. So the block that a stage takes next is prefetched into L2, and
-// where the groups of 64 rows are even in number two CTAs with the same blocks
-// form a pair: each fetches half of a block's pieces for both (multicast), and a
-// stage is free once both have read it. 128 heads as below: 178 us with neither,
-// 172 with the prefetch, 176 with pairs, 166 with both. (Before them four stages
-// of 32 keys took 443 us for 177; each stage's load and release in two halves
-// 181.)
+// 3.4 k cycles. So the block that a stage takes next is prefetched into L2: 128
+// heads as below 171 us, 178 without. (Before it four stages of 32 keys took 443
+// us for 177; each stage's load and release in two halves 181.)
 //
 // Measured on a GB300, bf16 or fp16, R = 512, P = 64, join included: 64
-// sequences of 2048 to 8192 keys with 128 heads 166 us (399 MB: 2.4 TB/s, 555
-// TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 52 us (193 MB: 3.7
+// sequences of 2048 to 8192 keys with 128 heads 171 us (399 MB: 2.3 TB/s, 539
+// TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 54 us (193 MB: 3.6
 // TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 14.5 us.
 // Bound: few heads by the cache's bytes and a start of 7 us; 128 heads by the
 // chain above and, at a sequence's end, the way of 64 x 512 sums to the workspace
@@ -176,7 +172,7 @@ struct Walk {
     }
 };
 
-template <typename T, int NB, bool kPair>
+template <typename T, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
     constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
@@ -191,19 +187,18 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int group = blockIdx.x % p.groups, member = blockIdx.x / p.groups;
     const int tiles_o = p.R / 128;
-    const int rank = kPair ? (int)(cluster_rank() & 1) : 0;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&c.full[i], 1);
-            mbar_init(&c.empty[i], kPair ? 2 : 1);
+            mbar_init(&c.empty[i], 1);
         }
         mbar_init(&c.q_full, kMathWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&c.s_full[i], 1);
         mbar_init(&c.p_full, kMathWarps);
         mbar_init(&c.o_free, kMathWarps);
         mbar_init(&c.done, 1);
-        fence_mbar_init_cluster();
+        fence_mbar_init();
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&c.tmem_base, kTmemAll);
@@ -272,8 +267,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    // A pair's barriers are there before either CTA signals the other's.
-    if constexpr (kPair) cluster_sync();
     tc_fence_after();
     constexpr uint32_t tmem = kTmemBase;
     Walk<BT> w{c.seq0, c.tile0, c.count};
@@ -316,15 +309,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     __syncwarp();
                     if (lane < runs) {
                         uint8_t* dst = skv + st * p.chunks * kChunkBytes + lane * p.run * 128;
-                        // A pair's CTA fetches every other piece for both.
-                        for (int k = rank; k < p.chunks; k += kPair ? 2 : 1) {
-                            if constexpr (kPair)
-                                tma_load_3d_both(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64,
-                                                 n % p.block_size, page);
-                            else
-                                tma_load_3d(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64, n % p.block_size,
-                                            page);
-                        }
+                        for (int k = 0; k < p.chunks; ++k)
+                            tma_load_3d(dst + k * kChunkBytes, &rows_map, &c.full[st], k * 64, n % p.block_size, page);
                     }
                     landing = i + 1;
                     // Into L2 already what this stage takes next (with three stages
@@ -335,7 +321,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             const int at = next * BT + lane * p.run;
                             next_page = page_of(at);
                             if (next_page < p.num_blocks)
-                                for (int k = rank; k < p.chunks; k += kPair ? 2 : 1)
+                                for (int k = 0; k < p.chunks; ++k)
                                     tma_prefetch_3d(&rows_map, k * 64, at % p.block_size, next_page);
                         }
                     } else {
@@ -447,8 +433,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                             mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
                                      (j | x) ? 1u : 0u);
                     }
-                    if constexpr (kPair) mma_commit_both(&c.empty[i % kStages]);
-                    else mma_commit(&c.empty[i % kStages]);
+                    mma_commit(&c.empty[i % kStages]);
                     if (!ahead) {
                         if (!bar_wait(&c.full[(i + 1) % kStages], ph_next)) {
                             timed_out(kWaitFull);
@@ -706,8 +691,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    // Neither CTA of a pair leaves while the other may write its memory.
-    if constexpr (kPair) cluster_sync();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(kTmemBase, kTmemAll);
@@ -935,62 +918,25 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
 }
 
 int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-cudaLaunchAttribute pair_attribute() {
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = 2;
-    a.val.clusterDim.y = a.val.clusterDim.z = 1;
-    return a;
-}
 
 size_t part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
 
-// How often the current device holds the kernel at a time, in CTAs or pairs; 0
-// on a CUDA error.  A pair's kernel always asks for the shared memory of the
-// widest rows, so that no SM takes both of its CTAs: each wants all of TMEM.
-template <typename T, int NB, bool kPair>
-int fit(int sms) {
-    static std::atomic<int> known[64];
+template <typename T, int NB>
+cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    constexpr size_t most_bytes = smem_bytes<NB>(kMaxChunks);
+    static_assert(most_bytes <= 232448, "shared memory per CTA");
     int dev = 0;
     cudaGetDevice(&dev);
-    int n = known[dev & 63].load();
-    if (n) return n;
-    constexpr size_t bytes = smem_bytes<NB>(kMaxChunks);
-    static_assert(bytes <= 232448, "shared memory per CTA");
-    static_assert(!kPair || bytes > 116 * 1024, "one CTA a SM");
-    if (cudaFuncSetAttribute(decode_kernel<T, NB, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-        return 0;
-    n = sms;
-    if (kPair) {
-        cudaLaunchAttribute cluster = pair_attribute();
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = bytes;
-        cfg.attrs = &cluster;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<T, NB, kPair>, &cfg) != cudaSuccess || n <= 0) {
-            cudaGetLastError();
-            return 0;
-        }
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load() & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)most_bytes);
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit);
     }
-    known[dev & 63].store(n);
-    return n;
-}
-
-template <typename T, int NB, bool kPair>
-cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
-    if (!fit<T, NB, kPair>(sms)) return cudaErrorInvalidConfiguration;
-    cudaLaunchAttribute cluster = pair_attribute();
-    cudaLaunchConfig_t main{};
-    main.gridDim = dim3((unsigned)(p.groups * p.per_group));
-    main.blockDim = dim3(kThreads);
-    main.dynamicSmemBytes = smem_bytes<NB>(kPair ? kMaxChunks : p.chunks);
-    main.stream = stream;
-    main.attrs = &cluster;
-    main.numAttrs = kPair ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&main, decode_kernel<T, NB, kPair>, map, p);
+    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
+    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.split) {
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1009,11 +955,10 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
 }
 
 template <typename T>
-cudaError_t launch_rows(int nb, bool pair, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
-    if (nb == 16) return launch<T, 16, false>(map, p, sms, stream);
-    if (nb == 32) return launch<T, 32, false>(map, p, sms, stream);
-    if (pair) return launch<T, 64, true>(map, p, sms, stream);
-    return launch<T, 64, false>(map, p, sms, stream);
+cudaError_t launch_rows(int nb, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch<T, 16>(map, p, sms, stream);
+    if (nb == 32) return launch<T, 32>(map, p, sms, stream);
+    return launch<T, 64>(map, p, sms, stream);
 }
 
 bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
@@ -1071,27 +1016,18 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     }
     // CTAs for each group of rows: an SM each, as far as the workspace has two
     // slots for every one of them; without it whole sequences.
-    int64_t at_once = sms;
-    const bool pair = p.run > 0 && nb == 64 && groups % 2 == 0;
-    if (pair) {
-        at_once = 2 * (bf ? fit<__nv_bfloat16, 64, true>(sms) : fit<__half, 64, true>(sms));
-        if (!at_once) {
-            *err = cudaErrorInvalidConfiguration;
-            return true;
-        }
-    }
-    int64_t each = std::max<int64_t>(1, at_once / groups);
+    int64_t each = std::max<int64_t>(1, sms / groups);
     const int64_t slots = a.workspace ? (int64_t)(a.workspace_bytes / part_bytes(nb, a.R)) : 0;
     each = std::min(each, slots / (2 * groups));
     if (each > 1 && each * groups <= kMaxJoins) {
         p.split = 1;
         p.parts = static_cast<float*>(a.workspace);
     } else {
-        each = std::min<int64_t>(std::max<int64_t>(1, at_once / groups), a.n_seqs);
+        each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
     }
     p.per_group = (int)each;
-    *err = bf ? launch_rows<__nv_bfloat16>(nb, pair, map, p, sms, stream)
-              : launch_rows<__half>(nb, pair, map, p, sms, stream);
+    *err = bf ? launch_rows<__nv_bfloat16>(nb, map, p, sms, stream)
+              : launch_rows<__half>(nb, map, p, sms, stream);
     return true;
 }
 

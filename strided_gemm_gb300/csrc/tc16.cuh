@@ -78,27 +78,6 @@ __device__ __forceinline__ void mma16_ss_pair(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 
-// Arrives once on `bar` in both CTAs of a pair when this thread's MMAs so far
-// (each CTA's own, cta_group::1) have completed.
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
-    const uint16_t mask = 3;
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"(mask) : "memory");
-}
-
-// A 3-D tiled TMA load that lands at `dst` in both CTAs of a pair and counts on
-// each one's `bar`.
-__device__ __forceinline__ void tma_load_3d_both(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                                 int c2) {
-    const uint16_t mask = 3;
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5}], [%2], %6;"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)),
-          "r"(c0), "r"(c1), "r"(c2), "h"(mask)
-        : "memory");
-}
-
 // Brings a 3-D box into L2, for a load to come.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];"

@@ -2,6 +2,9 @@
 arguments comes before the first CUDA call, on addresses that nothing reads."""
 
 import ctypes
+import glob
+import os
+import re
 
 import pytest
 
@@ -207,3 +210,21 @@ def test_torch_helpers_refuse_tensors():
     with pytest.raises(TypeError):
         sg.pages_free([torch.zeros(4, 16, 8, **bf)], torch.zeros(4, **i32), torch.zeros(1, 4, **i32),
                       torch.zeros(1, **i32), torch.zeros(1, **i32))
+
+
+def test_no_load_is_multicast():
+    """Every TMA load lands in the shared memory of the CTA that asks for it (a
+    pair's by its barrier's address): none is multicast over a cluster, since an
+    operand may lie in another GPU's memory and the library serves runs of
+    several ranks.  (Barrier arrivals over a pair are no loads.)"""
+    files = [f for x in ("*.cu", "*.cuh", "*.cpp", "*.h") for f in glob.glob(os.path.join(sgbuild.CSRC, x))]
+    assert len(files) > 20
+    for f in files:
+        with open(f) as fh:
+            text = fh.read()
+        # The strings of an asm statement, joined: an instruction may run over several.
+        for statement in re.findall(r"\basm\b[^;]*?\((.*?)\);\n", text, re.S):
+            code = "".join(re.findall(r'"([^"]*)"', statement))
+            for instruction in re.split(r";|\\n", code):
+                if "multicast::cluster" in instruction:
+                    assert "cp.async.bulk" not in instruction, (os.path.basename(f), instruction)
