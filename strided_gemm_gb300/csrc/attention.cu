@@ -412,16 +412,6 @@ cudaError_t launch_attention(const AttnProblem& a, cudaStream_t stream) {
                    : launch_paged<false>(p, a.D, grid, stream);
 }
 
-unsigned int read_and_clear_status_attention(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_attention() { return word_address(&g_status); }
 
 }  // namespace sbg

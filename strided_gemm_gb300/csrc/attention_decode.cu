@@ -645,16 +645,6 @@ cudaError_t launch_attention_decode(const AttnProblem& a, cudaStream_t stream) {
                    : launch_dh<false>(p, a.D, mr, a.batch, stream);
 }
 
-unsigned int read_and_clear_status_attention_decode(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_attention_decode() { return word_address(&g_status); }
 
 }  // namespace sbg

@@ -702,17 +702,6 @@ cudaError_t launch_attention_tc(const AttnProblem& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-unsigned int read_and_clear_wait_status_attention_tc(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_wait_status, sizeof(v), 0, cudaMemcpyDeviceToHost,
-                                  stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_attention_tc() { return word_address(&g_wait_status); }
 
 }  // namespace sbg

@@ -15,7 +15,4 @@ bool attention_tc_supported(const AttnProblem& a);
 
 cudaError_t launch_attention_tc(const AttnProblem& a, cudaStream_t stream);
 
-// Reads and clears the kernel's status word (0 when no wait ran out).
-unsigned int read_and_clear_wait_status_attention_tc(cudaStream_t stream);
-
 }  // namespace sbg

@@ -571,16 +571,6 @@ cudaError_t launch_gather_ffma(const Problem& p, const Plan& plan, cudaStream_t 
 
 namespace sbg {
 
-unsigned int read_and_clear_status_gather(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_gather() { return word_address(&g_status); }
 
 }  // namespace sbg

@@ -105,13 +105,4 @@ cudaError_t launch_tma_ffma(const Problem& p, const Plan& plan, int sm_count, cu
     }
 }
 
-unsigned int read_and_clear_wait_status_tma_ffma(cudaStream_t stream) {
-    unsigned int v = read_and_clear_wait_status_tma_ffma_256x128(stream);
-    const unsigned int v1 = read_and_clear_wait_status_tma_ffma_128x256(stream);
-    const unsigned int v2 = read_and_clear_wait_status_tma_ffma_512x64(stream);
-    if (v == 0) v = v1;
-    if (v == 0) v = v2;
-    return v;
-}
-
 }  // namespace sbg

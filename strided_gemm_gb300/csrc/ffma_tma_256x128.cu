@@ -9,8 +9,6 @@ cudaError_t launch_tma_ffma_256x128(const Problem& p, const Plan& plan, int sm_c
     return launch_tile<256, 128>(p, plan, sm_count, stream);
 }
 
-unsigned int read_and_clear_wait_status_tma_ffma_256x128(cudaStream_t stream) {
-    return read_and_clear_status(stream);
-}
+unsigned int* status_word_tma_ffma_256x128() { return status_word(); }
 
 }  // namespace sbg

@@ -14,8 +14,6 @@ cudaError_t launch_tma_ffma_512x64(const Problem& p, const Plan& plan, int sm_co
     return launch_impl<512, 64, true, false>(p, plan, sm_count, stream);
 }
 
-unsigned int read_and_clear_wait_status_tma_ffma_512x64(cudaStream_t stream) {
-    return read_and_clear_status(stream);
-}
+unsigned int* status_word_tma_ffma_512x64() { return status_word(); }
 
 }  // namespace sbg

@@ -912,19 +912,8 @@ cudaError_t launch_tile(const Problem& p, const Plan& plan, int sm_count, cudaSt
 }
 
 // This translation unit's copy of the kernels' status word (each tile shape is
-// compiled on its own), read and cleared by the host.
-inline unsigned int read_and_clear_status(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_wait_status, sizeof(v), 0, cudaMemcpyDeviceToHost,
-                                  stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+// compiled on its own).
+inline unsigned int* status_word() { return word_address(&g_wait_status); }
 
 }  // namespace
 }  // namespace sbg

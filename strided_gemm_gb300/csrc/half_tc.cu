@@ -502,8 +502,6 @@ bool launch_half_tc(const HalfProblem& given, int sms, cudaStream_t stream, cuda
     return true;
 }
 
-unsigned int read_and_clear_status_half_tc(cudaStream_t stream) {
-    return read_and_clear_word(reinterpret_cast<const void*>(&g_wait_status), stream);
-}
+unsigned int* status_word_half_tc() { return word_address(&g_wait_status); }
 
 }  // namespace sbg

@@ -1,4 +1,4 @@
-// 16-bit floats on the device: conversions and the status word readers' body.
+// 16-bit floats on the device: conversions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -51,18 +51,6 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 }
 template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// Reads and clears a kernel file's status word (0 on a CUDA error).
-inline unsigned int read_and_clear_word(const void* symbol, cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, symbol, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
 }
 
 }  // namespace sbg

@@ -123,7 +123,6 @@ cudaError_t launch_attention(const AttnProblem& a, cudaStream_t stream);
 // Few query rows per batch entry (decode): keys split across CTAs.
 bool attention_decode_supported(const AttnProblem& a);
 cudaError_t launch_attention_decode(const AttnProblem& a, cudaStream_t stream);
-unsigned int read_and_clear_status_attention_decode(cudaStream_t stream);
 
 // ---- strided-gather FFMA path (ffma_gather.cu) --------------------------------
 // Tile configurations of the gather kernel.
@@ -158,13 +157,6 @@ cudaError_t launch_tma_ffma(const Problem& p, const Plan& plan, int sm_count, cu
 cudaError_t launch_tma_ffma_256x128(const Problem& p, const Plan& plan, int sm_count, cudaStream_t stream);
 cudaError_t launch_tma_ffma_128x256(const Problem& p, const Plan& plan, int sm_count, cudaStream_t stream);
 cudaError_t launch_tma_ffma_512x64(const Problem& p, const Plan& plan, int sm_count, cudaStream_t stream);
-unsigned int read_and_clear_wait_status_tma_ffma_256x128(cudaStream_t stream);
-unsigned int read_and_clear_wait_status_tma_ffma_128x256(cudaStream_t stream);
-unsigned int read_and_clear_wait_status_tma_ffma_512x64(cudaStream_t stream);
-
-// Reads and clears the status words of the kernels that use bounded waits.
-// Returns the first non-zero code found (0 if none).
-unsigned int read_and_clear_wait_status_tma_ffma(cudaStream_t stream);
 
 // ---- TF32 tensor-core path (tf32_tc.cu) ----------------------------------------
 TmaFfmaConfig tf32_tc_config();
@@ -176,14 +168,33 @@ void tf32_tc_schedule(const Problem& p, Plan& plan, int sm_count, size_t ws_byte
 // (with their own split over the workspace); false leaves the plan as it was.
 bool tf32_tc_pair(const Problem& pr, Plan& plan, int sm_count, size_t ws_bytes, const void* ws,
                   int k_split);
-unsigned int read_and_clear_wait_status_tf32(cudaStream_t stream);
 
-// ---- status words of the kernels without bounded waits (debug bounds checks) ----
-unsigned int read_and_clear_status_gather(cudaStream_t stream);
-unsigned int read_and_clear_status_attention(cudaStream_t stream);
-
-// ---- failure-detection self-test (selftest.cu) ----------------------------------
-unsigned int read_and_clear_wait_status_selftest(cudaStream_t stream);
+// ---- status words (status.cu) -------------------------------------------------
+// Each kernel file has a word of its own, in which its kernels record the first
+// code; its address on the current device, nullptr on a CUDA error.
+inline unsigned int* word_address(const unsigned int* symbol) {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, static_cast<const void*>(symbol)) == cudaSuccess ? static_cast<unsigned int*>(p)
+                                                                                     : nullptr;
+}
+unsigned int* status_word_tma_ffma_256x128();
+unsigned int* status_word_tma_ffma_128x256();
+unsigned int* status_word_tma_ffma_512x64();
+unsigned int* status_word_tf32();
+unsigned int* status_word_selftest();
+unsigned int* status_word_attention_tc();
+unsigned int* status_word_gather();
+unsigned int* status_word_attention();
+unsigned int* status_word_attention_decode();
+unsigned int* status_word_half_tc();
+unsigned int* status_word_latent_decode();
+unsigned int* status_word_latent_prompt();
+unsigned int* status_word_latent_rows();
+unsigned int* status_word_pages();
+// Clears all of them behind the work on `stream` and waits for it; *code
+// receives the first non-zero one in the order above (0 if none).  False on a
+// CUDA error.
+bool take_status_words(cudaStream_t stream, unsigned int* code);
 
 // ---- driver entry points (driver.cpp) ---------------------------------------
 // [base, base+size) of the allocation that contains `ptr`; false if `ptr` is not

@@ -1031,8 +1031,6 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     return true;
 }
 
-unsigned int read_and_clear_status_latent_decode(cudaStream_t stream) {
-    return read_and_clear_word(reinterpret_cast<const void*>(&g_wait_status), stream);
-}
+unsigned int* status_word_latent_decode() { return word_address(&g_wait_status); }
 
 }  // namespace sbg

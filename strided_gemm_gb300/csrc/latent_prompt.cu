@@ -601,8 +601,6 @@ bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_
     return true;
 }
 
-unsigned int read_and_clear_status_latent_prompt(cudaStream_t stream) {
-    return read_and_clear_word(reinterpret_cast<const void*>(&g_wait_status), stream);
-}
+unsigned int* status_word_latent_prompt() { return word_address(&g_wait_status); }
 
 }  // namespace sbg

@@ -147,8 +147,6 @@ cudaError_t launch_latent_rows_packed(const LatentPacked& a, cudaStream_t stream
     return cudaGetLastError();
 }
 
-unsigned int read_and_clear_status_latent_rows(cudaStream_t stream) {
-    return read_and_clear_word(reinterpret_cast<const void*>(&g_status), stream);
-}
+unsigned int* status_word_latent_rows() { return word_address(&g_status); }
 
 }  // namespace sbg

@@ -622,8 +622,6 @@ cudaError_t launch_pages_compact(const PageCaches& c, const PagePool& p, int32_t
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-unsigned int read_and_clear_status_pages(cudaStream_t stream) {
-    return read_and_clear_word(reinterpret_cast<const void*>(&g_status), stream);
-}
+unsigned int* status_word_pages() { return word_address(&g_status); }
 
 }  // namespace sbg

@@ -724,21 +724,11 @@ int sbgemm_device_status(void* stream, int* where_out) {
         cudaGetLastError();
         return SBGEMM_ERR_CUDA;
     }
-    unsigned int code = read_and_clear_wait_status_tma_ffma(s);
-    const unsigned int code_tc = read_and_clear_wait_status_tf32(s);
-    const unsigned int code_st = read_and_clear_wait_status_selftest(s);
-    const unsigned int code_at = read_and_clear_wait_status_attention_tc(s);
-    const unsigned int code_g = read_and_clear_status_gather(s);
-    const unsigned int code_a = read_and_clear_status_attention(s);
-    const unsigned int code_d = read_and_clear_status_attention_decode(s);
-    const unsigned int code_s = read_and_clear_status_serving(s);
-    if (code == 0) code = code_tc;
-    if (code == 0) code = code_st;
-    if (code == 0) code = code_at;
-    if (code == 0) code = code_g;
-    if (code == 0) code = code_a;
-    if (code == 0) code = code_d;
-    if (code == 0) code = code_s;
+    unsigned int code = 0;
+    if (!take_status_words(s, &code)) {
+        cudaGetLastError();
+        return SBGEMM_ERR_CUDA;
+    }
     if (code != 0) {
         if (where_out) *where_out = (int)code;
         return code >= kBoundsViolation ? SBGEMM_ERR_DEVICE_CHECK : SBGEMM_ERR_DEVICE_TIMEOUT;

@@ -36,18 +36,7 @@ __global__ void selftest_kernel(int what, uint64_t limit_ns) {
 
 }  // namespace
 
-unsigned int read_and_clear_wait_status_selftest(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_wait_status, sizeof(v), 0, cudaMemcpyDeviceToHost,
-                                  stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_selftest() { return word_address(&g_wait_status); }
 
 }  // namespace sbg
 

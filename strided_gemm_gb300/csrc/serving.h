@@ -23,7 +23,6 @@ struct HalfProblem {
 cudaError_t launch_half_gather(const HalfProblem& p, cudaStream_t stream);
 // On the tensor cores (half_tc.cu); false if the layout has no tensor maps.
 bool launch_half_tc(const HalfProblem& p, int sms, cudaStream_t stream, cudaError_t* err);
-unsigned int read_and_clear_status_half_tc(cudaStream_t stream);
 
 // Latent attention over a paged cache (sbgemm_latent_attention_paged).
 struct LatentPaged {
@@ -56,15 +55,12 @@ struct LatentPacked {
 // and alignments it does not take.
 bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err);
 size_t latent_decode_workspace_bytes(int sms);
-unsigned int read_and_clear_status_latent_decode(cudaStream_t stream);
 // On the tensor cores, over packed sequences (latent_prompt.cu); false likewise.
 bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_t* err);
-unsigned int read_and_clear_status_latent_prompt(cudaStream_t stream);
 // One warp a query row, any sizes and alignments (latent_rows.cu).
 constexpr int64_t kLatentMaxQK = 640, kLatentMaxV = 512;
 cudaError_t launch_latent_rows_paged(const LatentPaged& a, cudaStream_t stream);
 cudaError_t launch_latent_rows_packed(const LatentPacked& a, cudaStream_t stream);
-unsigned int read_and_clear_status_latent_rows(cudaStream_t stream);
 
 // Page operations (pages.cu).
 struct PageCaches {
@@ -93,9 +89,5 @@ cudaError_t launch_pages_append(const PageCaches& c, const PagePool& p, const in
 cudaError_t launch_pages_free(const PagePool& p, const int32_t* seqs, int64_t n, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PageCaches& c, const PagePool& p, int32_t* moved, void* ws, int sms,
                                  cudaStream_t stream);
-unsigned int read_and_clear_status_pages(cudaStream_t stream);
-
-// The first non-zero code of the serving kernels' status words, all cleared (serving_api.cpp).
-unsigned int read_and_clear_status_serving(cudaStream_t stream);
 
 }  // namespace sbg

@@ -208,15 +208,6 @@ int check_pool_memory(const PoolView& v, std::initializer_list<Bytes> inputs, co
 
 }  // namespace
 
-unsigned int read_and_clear_status_serving(cudaStream_t stream) {
-    const unsigned int codes[] = {read_and_clear_status_half_tc(stream), read_and_clear_status_latent_decode(stream),
-                                  read_and_clear_status_latent_prompt(stream),
-                                  read_and_clear_status_latent_rows(stream), read_and_clear_status_pages(stream)};
-    for (unsigned int c : codes)
-        if (c) return c;
-    return 0;
-}
-
 }  // namespace sbg
 
 using namespace sbg;

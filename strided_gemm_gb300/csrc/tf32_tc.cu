@@ -1180,17 +1180,6 @@ bool tf32_tc_pair(const Problem& pr, Plan& plan, int sm_count, size_t ws_bytes, 
     return true;
 }
 
-unsigned int read_and_clear_wait_status_tf32(cudaStream_t stream) {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_wait_status, sizeof(v), 0, cudaMemcpyDeviceToHost,
-                                  stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return v;
-}
+unsigned int* status_word_tf32() { return word_address(&g_wait_status); }
 
 }  // namespace sbg

@@ -1184,3 +1184,51 @@ def test_latent_layer_prompt_fork_decode(torch, workspace, t):
     assert_within(torch, step["ol"][1].transpose(0, 1), O, lim)
     assert_within(torch, before.transpose(0, 1), O, lim)
     status_is(0)
+
+
+# ---- the status words -------------------------------------------------------------------
+
+def test_status_of_several_kernels_is_read_at_once(torch, workspace):
+    """A code of each kernel file, pending together: one is reported, all are
+    cleared, and the next call reports what came since."""
+    rng = np.random.default_rng(14)
+    p = Pool(torch, rng, 20, 4, 4, 6, [9, 0, 0, 0], [(8,)])
+    c = Paged(torch, "bf16", [40, 20], 16, 1, 512, 64, 16, seed=80)
+    c.seq_lens[1] = -1
+    d = Packed(torch, "bf16", [20], [20], 2, 128, 64, 128, seed=81, back=0)
+    d.ks[1] = 25
+    e = Packed(torch, "bf16", [20], [20], 2, 130, 66, 70, seed=82, back=0)
+    e.ks[1] = 25
+    for codes, calls in ((10, (lambda: c.run(True, workspace), lambda: d.run(True), lambda: e.run(True))),
+                         (11, (lambda: sg.pages_free(*p.all(), p.dev([-1])),))):
+        for f in calls:
+            f()
+        sg.sbgemm_selftest(sg.SELFTEST_FLAG, 1000)
+        st, where = sg.sbgemm_device_status()            # the self-test's word comes first
+        assert (st, where) == (sg.SBGEMM_ERR_DEVICE_TIMEOUT, 8)
+        status_is(0)
+        for f in calls:
+            f()
+            status_is(codes)
+            status_is(0)
+
+
+def test_status_costs_a_launch_and_a_copy(torch):
+    """Reading the status is one launch, one copy and a wait, not one of each for
+    every kernel file: within eight times a copy of one number to the host (it
+    was 22 times with a read a file)."""
+    import time
+    x = torch.zeros(1, device="cuda")
+
+    def median(f):
+        times = []
+        for _ in range(200):
+            t = time.perf_counter()
+            f()
+            times.append(time.perf_counter() - t)
+        return sorted(times)[100]
+    for f in (sg.sbgemm_device_status, x.item):
+        median(f)
+    status, copy = median(sg.sbgemm_device_status), median(x.item)
+    print(f"status {status * 1e6:.1f} us, copy {copy * 1e6:.1f} us")
+    assert status < 8 * copy
