@@ -8,6 +8,7 @@
 // FFMA issue, an order below the tensor cores.
 #include <algorithm>
 
+#include "debug_check.cuh"
 #include "half_util.cuh"
 #include "serving.h"
 
@@ -15,6 +16,7 @@ namespace sbg {
 namespace {
 
 constexpr int BM = 64, BN = 64, BK = 16;
+__device__ unsigned int g_status = 0;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -33,10 +35,12 @@ half_gather_kernel(const HalfProblem p, int64_t tiles_n) {
                 // The unit-stride index, if any, runs across the threads.
                 const int ka = p.csA == 1 ? i % BK : i / BM, ma = p.csA == 1 ? i / BK : i % BM;
                 const int kb = p.csB == 1 ? i / BN : i % BK, nb = p.csB == 1 ? i % BN : i / BK;
-                sa[ka][ma] = m0 + ma < p.M && k0 + ka < p.K
-                                 ? to_float(A[(m0 + ma) * p.rsA + (k0 + ka) * p.csA]) : 0.0f;
-                sb[kb][nb] = n0 + nb < p.N && k0 + kb < p.K
-                                 ? to_float(B[(k0 + kb) * p.rsB + (n0 + nb) * p.csB]) : 0.0f;
+                const T* a = A + (m0 + ma) * p.rsA + (k0 + ka) * p.csA;
+                const T* bb = B + (k0 + kb) * p.rsB + (n0 + nb) * p.csB;
+                sa[ka][ma] = m0 + ma < p.M && k0 + ka < p.K && dbg_in_bytes(a, sizeof(T), p.sa, &g_status)
+                                 ? to_float(*a) : 0.0f;
+                sb[kb][nb] = n0 + nb < p.N && k0 + kb < p.K && dbg_in_bytes(bb, sizeof(T), p.sb, &g_status)
+                                 ? to_float(*bb) : 0.0f;
             }
             __syncthreads();
 #pragma unroll
@@ -58,6 +62,7 @@ half_gather_kernel(const HalfProblem p, int64_t tiles_n) {
                 const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
                 if (m < p.M && n < p.N) {
                     T* c = C + m * p.rsC + n * p.csC;
+                    if (!dbg_in_bytes(c, sizeof(T), p.sc, &g_status)) continue;
                     *c = from_float<T>(p.accumulate ? fmaf(p.alpha, acc[i][j], to_float(*c)) : p.alpha * acc[i][j]);
                 }
             }
@@ -76,5 +81,7 @@ cudaError_t launch_half_gather(const HalfProblem& p, cudaStream_t stream) {
         half_gather_kernel<__half><<<grid, 256, 0, stream>>>(p, tn);
     return cudaGetLastError();
 }
+
+unsigned int* status_word_half_gather() { return word_address(&g_status); }
 
 }  // namespace sbg

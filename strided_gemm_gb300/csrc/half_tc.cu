@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "debug_check.cuh"
 #include "serving.h"
 #include "tc16.cuh"
 
@@ -54,6 +55,7 @@ struct Params {
     int x_batch, y_batch;          // the batch coordinate moves (else shared)
     int c_tma;                     // C goes out through its tensor map
     uint32_t idesc;
+    ByteSpan sc;                   // debug builds: what C occupies
 };
 
 template <int NT, bool kPair>
@@ -283,6 +285,7 @@ half_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ C
                             const int64_t m = p.swapped ? y : x, nn = p.swapped ? x : y;
                             if (m < p.rows && nn < p.cols) {
                                 T* o = C + m * p.rsC + nn;
+                                if (!dbg_in_bytes(o, sizeof(T), p.sc, &g_wait_status)) continue;
                                 *o = from_float<T>(p.accumulate ? fmaf(p.alpha, v[i], to_float(*o)) : p.alpha * v[i]);
                             }
                         }
@@ -488,7 +491,7 @@ bool launch_half_tc(const HalfProblem& given, int sms, cudaStream_t stream, cuda
         *err = cudaErrorInvalidValue;
         return true;
     }
-    q.C = p.C; q.rsC = p.rsC; q.bsC = p.bsC;
+    q.C = p.C; q.rsC = p.rsC; q.bsC = p.bsC; q.sc = p.sc;
     q.rows = p.M; q.cols = p.N;
     q.k_blocks = (int)((p.K + BK - 1) / BK);
     q.alpha = p.alpha;

@@ -30,6 +30,8 @@ enum : unsigned int {
 // memory the caller described (the host's span check before every launch).
 // Only the bounds checks of a debug build (SBGEMM_DEBUG) read them.
 struct ElemSpan { int64_t lo, hi; };
+// The same as addresses [lo, hi), for operands of any type.
+struct ByteSpan { uintptr_t lo, hi; };
 
 // One call of the product, strides in fp32 elements (see include/sbgemm.h).
 // Fused epilogue of sbgemm_fused: out = act(alpha*acc (+ C_old) + D), with D
@@ -186,6 +188,7 @@ unsigned int* status_word_attention_tc();
 unsigned int* status_word_gather();
 unsigned int* status_word_attention();
 unsigned int* status_word_attention_decode();
+unsigned int* status_word_half_gather();
 unsigned int* status_word_half_tc();
 unsigned int* status_word_latent_decode();
 unsigned int* status_word_latent_prompt();

@@ -58,6 +58,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "debug_check.cuh"
 #include "serving.h"
 #include "tc16.cuh"
 
@@ -99,6 +100,7 @@ struct Params {
     uint32_t idesc_s, idesc_o;
     int o_vec;                               // rows of O take 8-byte stores
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
+    ByteSpan sq, sc, so, sw;                 // debug builds: what Q, the cache, O and the workspace occupy
 };
 
 template <int NB>
@@ -354,7 +356,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     const int r = r0 + 4 * g;
                     const uint32_t dst = stage + r * 128 + ((piece ^ (r & 7)) << 4);
                     for (int k = 0; k < p.chunks; ++k) {
-                        const bool read = src[g] != nullptr && k * 8 + piece < row_pieces;
+                        const bool read = src[g] != nullptr && k * 8 + piece < row_pieces &&
+                                          dbg_in_bytes(src[g] + k * 128, 16, p.sc, &g_wait_status);
                         cp_async16(dst + k * kChunkBytes, read ? src[g] + k * 128 : cache, read);
                     }
                 }
@@ -468,9 +471,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 for (int x = m; x < NB * p.chunks * 8; x += 256) {
                     const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
                     const int gr = group * NB + r, t = gr / p.heads, h = gr % p.heads;
-                    const bool read = gr < p.rows && k < row_pieces;
+                    bool read = gr < p.rows && k < row_pieces;
                     const T* src = static_cast<const T*>(p.Q);
                     if (read) src += w.s * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
+                    read = read && dbg_in_bytes(src, 16, p.sq, &g_wait_status);
                     cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
                 }
             }
@@ -638,7 +642,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             if (m < NB) {
                 const float sum = c.part[0][m] + c.part[1][m] + c.part[2][m] + c.part[3][m];
                 c.factor[m] = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
-                if (!whole) {
+                if (!whole && dbg_in_bytes(part, 4 * NB * (2 + p.R), p.sw, &g_wait_status)) {
                     part[m] = c.ref[m];
                     part[NB + m] = sum;
                 }
@@ -670,14 +674,17 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     if (!whole) {
                         float* dst = part + 2 * NB + (int64_t)x0 * p.R + e;
 #pragma unroll
-                        for (int x = 0; x < W; ++x, dst += p.R) *dst = o[x];
+                        for (int x = 0; x < W; ++x, dst += p.R)
+                            if (dbg_in_bytes(dst, 4, p.sw, &g_wait_status)) *dst = o[x];
                     } else {
                         T* dst = static_cast<T*>(p.O) + e;
 #pragma unroll
                         for (int x = 0; x < W; x += 2) {
                             const longlong2 at = *reinterpret_cast<const longlong2*>(&c.out[x0 + x]);
-                            if (at.x >= 0) dst[at.x] = from_float<T>(o[x]);
-                            if (at.y >= 0) dst[at.y] = from_float<T>(o[x + 1]);
+                            if (at.x >= 0 && dbg_in_bytes(dst + at.x, sizeof(T), p.so, &g_wait_status))
+                                dst[at.x] = from_float<T>(o[x]);
+                            if (at.y >= 0 && dbg_in_bytes(dst + at.y, sizeof(T), p.so, &g_wait_status))
+                                dst[at.y] = from_float<T>(o[x + 1]);
                         }
                     }
                 }
@@ -823,7 +830,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
                 mx[q] = -INFINITY;
                 lx[q] = 0.0f;
                 v[q][0] = v[q][1] = make_float4(0, 0, 0, 0);
-                if (k < pieces) {
+                if (k < pieces && dbg_in_bytes(p.parts + slot_of(jn, group, k) * slot_floats, 4 * slot_floats, p.sw,
+                                               &g_wait_status)) {
                     const float* src = p.parts + slot_of(jn, group, k) * slot_floats;
                     mx[q] = src[row];
                     lx[q] = src[NB + row];
@@ -850,6 +858,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         T* out = static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
+        if (!dbg_in_bytes(out, 8 * sizeof(T), p.so, &g_wait_status)) continue;
         store4(out, scale4(o0, inv), p.o_vec);
         store4(out + 4, scale4(o1, inv), p.o_vec);
     }
@@ -873,7 +882,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
                 mx[q] = -INFINITY;
                 lx[q] = 0.0f;
                 v[q] = make_float4(0, 0, 0, 0);
-                if (k < pieces) {
+                if (k < pieces && dbg_in_bytes(piece(k), 4 * slot_floats, p.sw, &g_wait_status)) {
                     const float* src = piece(k);
                     mx[q] = src[row];
                     lx[q] = src[NB + row];
@@ -911,8 +920,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
                 add4(o, w, sums[k][lane]);
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            store4(static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e,
-                   scale4(o, inv), p.o_vec);
+            T* out = static_cast<T*>(p.O) + jn.seq * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
+            if (dbg_in_bytes(out, 4 * sizeof(T), p.so, &g_wait_status)) store4(out, scale4(o, inv), p.o_vec);
         }
     }
 }
@@ -993,6 +1002,8 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     p.groups = (int)groups;
     p.scale_log2 = a.alpha * 1.4426950408889634f;
     p.causal = a.causal;
+    p.sq = a.sq; p.sc = a.sc; p.so = a.so;
+    p.sw = ByteSpan{reinterpret_cast<uintptr_t>(a.workspace), reinterpret_cast<uintptr_t>(a.workspace) + a.workspace_bytes};
     const bool bf = a.type == SBGEMM_TYPE_BF16;
     p.idesc_s = idesc16(bf, nb, false, false, 64);
     p.idesc_o = idesc16(bf, nb, true, true);

@@ -46,6 +46,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "debug_check.cuh"
 #include "serving.h"
 #include "tc16.cuh"
 
@@ -74,6 +75,7 @@ struct Params {
     uint32_t idesc_s, idesc_v, idesc_v_half; // P V of all columns at once; of 64 of them
     uint32_t idesc_v_tail;                   // and of V's last piece
     int o_vec;                               // O rows take 16-byte stores
+    ByteSpan so;                             // debug builds: what O occupies
 };
 
 struct Smem {
@@ -492,7 +494,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
             for (int c = 0; c < p.Dv; c += 32) {
                 float o[32];
                 if (n_blocks > 0) tmem_ld32(o_at + c, o);
-                if (m >= nq) continue;
+                if (m >= nq || !dbg_in_bytes(out + c, sizeof(T) * min(32, p.Dv - c), p.so, &g_wait_status)) continue;
 #pragma unroll
                 for (int x = 0; x < 32; ++x) o[x] = sum == 0.0f ? 0.0f : o[x] * inv;
                 if (p.o_vec && c + 32 <= p.Dv) {
@@ -591,6 +593,7 @@ bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_
     p.Dv = (int)a.Dv;
     p.scale_log2 = a.alpha * 1.4426950408889634f;
     p.causal = a.causal;
+    p.so = a.so;
     const bool bf = a.type == SBGEMM_TYPE_BF16;
     p.idesc_s = idesc16(bf, BN, false, false);
     p.idesc_v = idesc16(bf, (int)((a.Dv + 15) / 16 * 16), false, true);

@@ -7,6 +7,7 @@
 // the tensor-core kernels take the sizes they can.
 #include <algorithm>
 
+#include "debug_check.cuh"
 #include "half_util.cuh"
 #include "ptx.cuh"
 #include "serving.h"
@@ -21,13 +22,19 @@ __device__ unsigned int g_status = 0;
 // Running softmax of one row over keys; `key(n, K, K2, V)` gives the key's nope
 // part, rope part and value rows, or false for a row of zeros.  (No pointer
 // says so: a part of no elements may lie anywhere, at address 0 too.)
+// What the operands occupy, for the checks of debug builds.
+struct Spans { ByteSpan q, k, r, v, o; };
+
 template <typename T, typename Key>
 __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, int64_t keys, float scale_log2,
-                                           T* o, Key key) {
+                                           T* o, const Spans& in, Key key) {
+    auto load = [](const T* x, const ByteSpan& span) {
+        return dbg_in_bytes(x, sizeof(T), span, &g_status) ? to_float(*x) : 0.0f;
+    };
     const int lane = threadIdx.x & 31;
     float qf[XQ], acc[XV];
 #pragma unroll
-    for (int x = 0; x < XQ; ++x) qf[x] = lane + 32 * x < dn + dr ? to_float(q[lane + 32 * x]) : 0.0f;
+    for (int x = 0; x < XQ; ++x) qf[x] = lane + 32 * x < dn + dr ? load(q + lane + 32 * x, in.q) : 0.0f;
 #pragma unroll
     for (int x = 0; x < XV; ++x) acc[x] = 0.0f;
     float top = -INFINITY, sum = 0.0f;
@@ -39,7 +46,7 @@ __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, i
 #pragma unroll
             for (int x = 0; x < XQ; ++x) {
                 const int d = lane + 32 * x;
-                if (d < dn + dr) z = fmaf(qf[x], to_float(d < dn ? kn[d] : kr[d - dn]), z);
+                if (d < dn + dr) z = fmaf(qf[x], d < dn ? load(kn + d, in.k) : load(kr + (d - dn), in.r), z);
             }
         }
 #pragma unroll
@@ -58,13 +65,14 @@ __device__ __forceinline__ void attend_row(const T* q, int dn, int dr, int dv, i
         if (there) {
 #pragma unroll
             for (int x = 0; x < XV; ++x)
-                if (lane + 32 * x < dv) acc[x] = fmaf(w, to_float(v[lane + 32 * x]), acc[x]);
+                if (lane + 32 * x < dv) acc[x] = fmaf(w, load(v + lane + 32 * x, in.v), acc[x]);
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: zeros
 #pragma unroll
     for (int x = 0; x < XV; ++x)
-        if (lane + 32 * x < dv) o[lane + 32 * x] = from_float<T>(acc[x] * inv);
+        if (lane + 32 * x < dv && dbg_in_bytes(o + lane + 32 * x, sizeof(T), in.o, &g_status))
+            o[lane + 32 * x] = from_float<T>(acc[x] * inv);
 }
 
 template <typename T>
@@ -82,6 +90,7 @@ rows_paged_kernel(const LatentPaged a, float scale_log2) {
         const T* base = static_cast<const T*>(a.cache);
         attend_row<T>(static_cast<const T*>(a.Q) + s * a.bsQ + t * a.tsQ + h * a.hsQ, (int)a.R, (int)a.P, (int)a.R,
                       keys, scale_log2, static_cast<T*>(a.O) + s * a.bsO + t * a.tsO + h * a.hsO,
+                      Spans{a.sq, a.sc, a.sc, a.sc, a.so},
                       [&](int64_t n, const T** kn, const T** kr, const T** v) {
                           const int64_t page = a.table[s * a.max_blocks + n / a.block_size];
                           if (page < 0 || page >= a.num_blocks) {
@@ -118,6 +127,7 @@ rows_packed_kernel(const LatentPacked a, float scale_log2) {
         const int64_t keys = a.causal ? min(nk, max((int64_t)0, nk - nq + i + 1)) : nk;
         attend_row<T>(static_cast<const T*>(a.Q) + (q0 + i) * a.tsQ + h * a.hsQ, (int)a.Dn, (int)a.P, (int)a.Dv,
                       keys, scale_log2, static_cast<T*>(a.O) + (q0 + i) * a.tsO + h * a.hsO,
+                      Spans{a.sq, a.sk, a.sr, a.sv, a.so},
                       [&](int64_t n, const T** kn, const T** kr, const T** v) {
                           *kn = static_cast<const T*>(a.Kn) + (k0 + n) * a.tsK + h * a.hsK;
                           *kr = static_cast<const T*>(a.Kr) + (k0 + n) * a.tsR;

@@ -17,6 +17,7 @@
 #include <atomic>
 #include <climits>
 
+#include "debug_check.cuh"
 #include "half_util.cuh"
 #include "ptx.cuh"
 #include "serving.h"
@@ -98,8 +99,11 @@ __device__ __forceinline__ int block_exclusive(int v, int* sums, int* total) {
     return inc - v + (warp ? sums[warp - 1] : 0);
 }
 
-// `bytes` (a multiple of 16, at most kPiece) moved by one warp.
-__device__ __forceinline__ void move_piece(char* dst, const char* src, int bytes) {
+// `bytes` (a multiple of 16, at most kPiece) moved by one warp.  Debug builds:
+// between what `to` and `from` span.
+__device__ __forceinline__ void move_piece(char* dst, const char* src, int bytes, const ByteSpan& to,
+                                           const ByteSpan& from) {
+    if (!dbg_in_bytes(dst, bytes, to, &g_status) || !dbg_in_bytes(src, bytes, from, &g_status)) return;
     constexpr int kLoads = kPiece / 512;
     const int lane = threadIdx.x & 31;
     uint4 v[kLoads];
@@ -117,16 +121,33 @@ __device__ __forceinline__ void move_piece(char* dst, const char* src, int bytes
 
 __host__ __device__ __forceinline__ int64_t pieces_of(int64_t bytes) { return (bytes + kPiece - 1) / kPiece; }
 
+// What cache i occupies.
+__device__ __forceinline__ ByteSpan cache_span(const PageCaches& c, int i, int64_t num_blocks, int64_t block_size) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(c.base[i]);
+    return {base, base + (uintptr_t)(c.row_bytes[i] * block_size * num_blocks)};
+}
+
+// Debug builds: whether an entry of the counts or of the table is one.
+__device__ __forceinline__ bool a_count(const PagePool& p, const int32_t* at) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p.refs);
+    return dbg_in_bytes(at, 4, ByteSpan{base, base + (uintptr_t)(4 * p.num_blocks)}, &g_status);
+}
+__device__ __forceinline__ bool an_entry(const PagePool& p, const int32_t* at) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p.table);
+    return dbg_in_bytes(at, 4, ByteSpan{base, base + (uintptr_t)(4 * p.n_seqs * p.max_blocks)}, &g_status);
+}
+
 // Piece `j` of the first `rows` rows of a page, over all caches: moved from
 // page src to page dst by this warp.
-__device__ __forceinline__ void move_page_piece(const PageCaches& c, int64_t block_size, int64_t rows, int64_t src,
-                                                int64_t dst, int64_t j) {
+__device__ __forceinline__ void move_page_piece(const PageCaches& c, int64_t num_blocks, int64_t block_size,
+                                                int64_t rows, int64_t src, int64_t dst, int64_t j) {
     for (int i = 0; i < c.n; ++i) {
         const int64_t bytes = c.row_bytes[i] * rows, np = pieces_of(bytes);
         if (j < np) {
             const int64_t page = c.row_bytes[i] * block_size, at = j * kPiece;
             move_piece(c.base[i] + dst * page + at, c.base[i] + src * page + at,
-                       (int)min((int64_t)kPiece, bytes - at));
+                       (int)min((int64_t)kPiece, bytes - at), cache_span(c, i, num_blocks, block_size),
+                       cache_span(c, i, num_blocks, block_size));
             return;
         }
         j -= np;
@@ -175,7 +196,7 @@ copy_move_kernel(const __grid_constant__ PageCaches c, const int32_t* pairs, int
             if ((threadIdx.x & 31) == 0) record_status(&g_status, kPageRequest);
             continue;
         }
-        move_page_piece(c, block_size, block_size, src, dst, j);
+        move_page_piece(c, num_blocks, block_size, block_size, src, dst, j);
     }
 }
 
@@ -330,6 +351,7 @@ fork_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, const W
     int32_t* to = p.table + r.to * p.max_blocks;
     if (blockIdx.y == 0) {
         for (int64_t i = threadIdx.x; i < full; i += blockDim.x) {
+            if (!an_entry(p, from + i) || !an_entry(p, to + i)) continue;
             const int page = from[i];
             to[i] = page;
             if (in_pool(page, p.num_blocks)) atomicAdd(&p.refs[page], 1);
@@ -339,12 +361,12 @@ fork_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, const W
     if (r.need) {
         const int64_t src = from[full], dst = w.fresh[r.first];
         if (blockIdx.y == 0 && threadIdx.x == 0) {
-            to[full] = (int32_t)dst;
-            p.refs[dst] = 1;
+            if (an_entry(p, to + full)) to[full] = (int32_t)dst;
+            if (a_count(p, p.refs + dst)) p.refs[dst] = 1;
         }
         const int warps = (blockDim.x >> 5) * gridDim.y;
         for (int64_t j = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5); j < pieces; j += warps)
-            move_page_piece(c, p.block_size, rest, src, dst, j);
+            move_page_piece(c, p.num_blocks, p.block_size, rest, src, dst, j);
     }
 }
 
@@ -379,14 +401,19 @@ append_move_kernel(const __grid_constant__ PageCaches c, const __grid_constant__
         const int64_t page = idx < have ? *slot : w.fresh[r.first + (idx - have)];
         // The token that opens a page enters it.
         if (idx >= have && off == 0 && cache == 0 && lane == 0) {
-            *slot = (int32_t)page;
-            p.refs[page] = 1;
+            if (an_entry(p, slot)) *slot = (int32_t)page;
+            if (a_count(p, p.refs + page)) p.refs[page] = 1;
         }
         if (c.n == 0) continue;
         const int64_t rb = c.row_bytes[cache];
         char* dst = c.base[cache] + (page * p.block_size + off) * rb;
         const char* src = rows.base[cache] + j * rows.stride[cache];
-        for (int64_t at = 0; at < rb; at += kPiece) move_piece(dst + at, src + at, (int)min((int64_t)kPiece, rb - at));
+        const int64_t reach = rows.stride[cache] * (total - 1);
+        const uintptr_t first = reinterpret_cast<uintptr_t>(rows.base[cache]);
+        const ByteSpan given{first + (uintptr_t)min(reach, (int64_t)0), first + (uintptr_t)(max(reach, (int64_t)0) + rb)};
+        for (int64_t at = 0; at < rb; at += kPiece)
+            move_piece(dst + at, src + at, (int)min((int64_t)kPiece, rb - at),
+                       cache_span(c, cache, p.num_blocks, p.block_size), given);
     }
 }
 
@@ -500,6 +527,7 @@ compact_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, cons
     if (t == 0 && moved) *moved = h;
     for (int64_t k = t; k < h; k += threads) {
         const int src = w.claim[U - h + k], dst = w.fresh[k];
+        if (!a_count(p, p.refs + dst) || !a_count(p, p.refs + src)) continue;
         p.refs[dst] = p.refs[src];
         p.refs[src] = 0;
     }
@@ -514,7 +542,8 @@ compact_move_kernel(const __grid_constant__ PageCaches c, const PagePool p, cons
     }
     const int64_t warps = threads >> 5;
     for (int64_t i = t >> 5; i < h * pieces; i += warps)
-        move_page_piece(c, p.block_size, p.block_size, w.claim[U - h + i / pieces], w.fresh[i / pieces], i % pieces);
+        move_page_piece(c, p.num_blocks, p.block_size, p.block_size, w.claim[U - h + i / pieces], w.fresh[i / pieces],
+                        i % pieces);
 }
 
 int64_t page_pieces(const PageCaches& c, int64_t block_size) {

@@ -18,6 +18,7 @@ struct HalfProblem {
     int64_t M, N, K, batch;
     float alpha;
     int accumulate;
+    ByteSpan sa, sb, sc;             // debug builds: what A, B and C occupy
 };
 // Any layout, on the CUDA cores (half_gather.cu).
 cudaError_t launch_half_gather(const HalfProblem& p, cudaStream_t stream);
@@ -36,6 +37,7 @@ struct LatentPaged {
     float alpha;
     int causal;
     void* workspace; size_t workspace_bytes;
+    ByteSpan sq, sc, so;             // debug builds: what Q, the cache and O occupy
 };
 // Latent attention over packed sequences (sbgemm_latent_attention).
 struct LatentPacked {
@@ -50,6 +52,7 @@ struct LatentPacked {
     int64_t heads, Dn, P, Dv;
     float alpha;
     int causal;
+    ByteSpan sq, sk, sr, sv, so;     // debug builds: what Q, K_nope, K_rope, V and O occupy
 };
 // On the tensor cores, over a paged cache (latent_decode.cu); false for sizes
 // and alignments it does not take.

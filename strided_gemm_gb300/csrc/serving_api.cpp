@@ -57,6 +57,8 @@ bool injective(std::array<Axis, n> a) {
     return true;
 }
 
+ByteSpan span_for_kernel(const Bytes& b) { return {(uintptr_t)b.lo, (uintptr_t)b.hi}; }
+
 bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // Each span lies inside one device-accessible allocation.  An allocation seen
@@ -239,7 +241,7 @@ int sbgemm_half(int type, const void* A, int64_t rsA, int64_t csA, int64_t bsA,
     const int m = K > 0 ? in_device_memory({sa, sb, sc}) : in_device_memory({sc});
     if (m) return m;
     const HalfProblem p{type, A, rsA, csA, bsA, B, rsB, csB, bsB, C, rsC, csC, bsC,
-                        M, N, K, batch, alpha, accumulate};
+                        M, N, K, batch, alpha, accumulate, span_for_kernel(sa), span_for_kernel(sb), span_for_kernel(sc)};
     cudaError_t e = cudaSuccess;
     if (launch_half_tc(p, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_half_gather(p, static_cast<cudaStream_t>(stream)));
@@ -293,7 +295,8 @@ int sbgemm_latent_attention_paged(
         else if (const int m = in_device_memory({w})) return m;
     }
     const LatentPaged a{type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
-                        seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal, ws, ws_bytes};
+                        seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal, ws, ws_bytes,
+                        span_for_kernel(sq), span_for_kernel(sc), span_for_kernel(so)};
     cudaError_t e = cudaSuccess;
     if (launch_latent_decode(a, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_latent_rows_paged(a, static_cast<cudaStream_t>(stream)));
@@ -349,7 +352,9 @@ int sbgemm_latent_attention(
     if (!current_sms()) return SBGEMM_ERR_CUDA;
     if (const int m = in_device_memory({sq, sk, sr, sv, so, s0, s1})) return m;
     const LatentPacked a{type, Q, hsQ, tsQ, total_q, K_nope, hsK, tsK, K_rope, tsR, V, hsV, tsV, total_k,
-                         q_starts, k_starts, n_seqs, max_q, O, hsO, tsO, heads, Dn, P, Dv, alpha, causal};
+                         q_starts, k_starts, n_seqs, max_q, O, hsO, tsO, heads, Dn, P, Dv, alpha, causal,
+                         span_for_kernel(sq), span_for_kernel(sk), span_for_kernel(sr), span_for_kernel(sv),
+                         span_for_kernel(so)};
     cudaError_t e = cudaSuccess;
     if (launch_latent_prompt(a, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_latent_rows_packed(a, static_cast<cudaStream_t>(stream)));

@@ -1,6 +1,6 @@
 // The status words that kernels record codes in (bounded waits that gave up,
 // inputs that were skipped), one a kernel file: read and cleared by one launch
-// and one copy, whatever their number (a copy out and one in for each of the 14
+// and one copy, whatever their number (a copy out and one in for each of 14
 // words took 239 us on an idle GPU, this takes 22).
 #include <mutex>
 
@@ -9,7 +9,7 @@
 namespace sbg {
 namespace {
 
-constexpr int kWords = 14;
+constexpr int kWords = 15;
 struct Words { unsigned int* at[kWords]; };
 __device__ unsigned int g_first;             // of the last launch
 
@@ -29,7 +29,7 @@ bool take_status_words(cudaStream_t stream, unsigned int* code) {
     const std::lock_guard<std::mutex> lock(one_at_a_time);
     const Words w{{status_word_tma_ffma_256x128(), status_word_tma_ffma_128x256(), status_word_tma_ffma_512x64(),
                    status_word_tf32(), status_word_selftest(), status_word_attention_tc(), status_word_gather(),
-                   status_word_attention(), status_word_attention_decode(), status_word_half_tc(),
+                   status_word_attention(), status_word_attention_decode(), status_word_half_gather(), status_word_half_tc(),
                    status_word_latent_decode(), status_word_latent_prompt(), status_word_latent_rows(),
                    status_word_pages()}};
     for (const unsigned int* at : w.at)

@@ -228,3 +228,14 @@ def test_no_load_is_multicast():
             for instruction in re.split(r";|\\n", code):
                 if "multicast::cluster" in instruction:
                     assert "cp.async.bulk" not in instruction, (os.path.basename(f), instruction)
+
+
+def test_every_kernel_file_has_the_debug_build_check_its_addresses():
+    """Kernels that touch a caller's operands check the addresses in the debug
+    build (debug_check.cuh); the self-test and the status reader touch none."""
+    for f in sorted(glob.glob(os.path.join(sgbuild.CSRC, "*.cu"))):
+        with open(f) as fh:
+            text = fh.read()
+        if "__global__" in text and os.path.basename(f) not in ("selftest.cu", "status.cu",
+                                                                             "attention_tc.cu"):
+            assert "dbg_in_" in text, os.path.basename(f)
