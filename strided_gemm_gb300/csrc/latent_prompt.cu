@@ -44,6 +44,7 @@
 // against 2.6 k of the tensor pipe for both tiles.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "debug_check.cuh"
@@ -70,7 +71,11 @@ struct Params {
     int n_pieces, v_pieces, rope;            // pieces of K's nope part and of V; rope: one more piece
     int n_steps, r_steps;                    // MMA K steps of the last nope piece and of the rope piece
     int Dv;
-    float scale_log2;
+    // |alpha| log2 e, but never 0, so that a hidden score's infinity stays one: for
+    // an alpha of 0 the least float, under which the largest score is below 2^-20.
+    float scale;
+    int negative;                            // alpha < 0
+    float unit;                              // 1; NaN for an alpha that is: of rows that have a key
     int causal;
     uint32_t idesc_s, idesc_v, idesc_v_half; // P V of all columns at once; of 64 of them
     uint32_t idesc_v_tail;                   // and of V's last piece
@@ -338,10 +343,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         const int last = p.causal ? min(nk - 1, m + nk - nq) : nk - 1;   // last key the row sees
         // Blocks below this one hide nothing from any of the tile's rows.
         const int open = (p.causal ? min(nk, max(0, m0 + t * BM + nk - nq + 1)) : nk) / BN;
-        // Never 0, so that a hidden score's infinity stays one when alpha is: the
-        // least float, under which the largest score is below 2^-20.  A NaN stays.
-        const float scale = p.scale_log2 == 0.0f ? 1.0e-45f : fabsf(p.scale_log2);
-        const bool negative = p.scale_log2 < 0.0f;
+        const float scale = p.scale;
+        const bool negative = p.negative;
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
         for (int j = 0; j < n_blocks; ++j) {
@@ -487,8 +490,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tqn, const __grid_constant__ C
         ok = __all_sync(~0u, ok);
         if (ok) {
             tc_fence_after();
-            if (last < 0) sum = 0.0f;                // no key: zeros, whatever alpha is
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = sum == 0.0f ? 0.0f : p.unit / sum;
             T* out = static_cast<T*>(p.O) + (int64_t)(q0 + m) * p.tsO + (int64_t)head * p.hsO;
 #pragma unroll 1
             for (int c = 0; c < p.Dv; c += 32) {
@@ -591,7 +593,10 @@ bool launch_latent_prompt(const LatentPacked& a, cudaStream_t stream, cudaError_
     p.n_steps = a.Dn > 0 ? (int)((a.Dn - (p.n_pieces - 1) * 64 + 15) / 16) : 0;
     p.r_steps = (int)((a.P + 15) / 16);
     p.Dv = (int)a.Dv;
-    p.scale_log2 = a.alpha * 1.4426950408889634f;
+    const float scale = std::fabs(a.alpha * 1.4426950408889634f);
+    p.scale = scale > 0.0f ? scale : 1.0e-45f;
+    p.negative = a.alpha < 0.0f;
+    p.unit = std::isnan(a.alpha) ? a.alpha : 1.0f;
     p.causal = a.causal;
     p.so = a.so;
     const bool bf = a.type == SBGEMM_TYPE_BF16;
