@@ -993,6 +993,37 @@ def test_pages_of_a_large_pool_are_found(torch):
     p.compact()
 
 
+def test_pages_with_thousands_of_requests(torch):
+    """More requests than the planning CTA has threads, more sequences than its
+    shared memory has claims for, more pairs and pages than the copy's; a prompt
+    over a thousand pages in one request; invalid ones and the pool's end behind
+    the first thousand."""
+    rng = np.random.default_rng(15)
+    blocks, block, seqs = 40007, 4, 5000
+    lens = [int(x) for x in rng.integers(1, 9, seqs)]
+    kids = [int(x) for x in rng.permutation(seqs)[:2600]]
+    for s in kids:
+        lens[s] = 0
+    p = Pool(torch, rng, blocks, block, seqs, 1400, lens, [(8,)], n=10000)
+    full = [s for s in range(seqs) if lens[s]]
+    parents = [int(rng.choice(full)) for _ in kids]
+    parents[2000], kids[2100] = seqs, kids[7]                  # out of range; an earlier request's child
+    p.fork(parents, kids, code=11)
+    who = [int(x) for x in rng.permutation(full)]
+    p.append(rng, who, [5600 - 8 if i == 1500 else int(n) for i, n in enumerate(rng.integers(0, 6, len(who)))])
+    free = [int(x) for x in np.flatnonzero(p.m.refs == 0)]
+    used = np.flatnonzero(p.m.refs > 0)
+    pairs = [(int(rng.choice(used)), int(d)) for d in rng.permutation(free)[:9000]]
+    p.copy(pairs)
+    pairs[8500] = (pairs[8500][0], pairs[3][1])                # a destination for the second time
+    p.copy(pairs, code=11)
+    left = int((p.m.refs == 0).sum())
+    many = [s for s in range(seqs) if p.m.lens[s] < 40]
+    p.append(rng, many, [4 * (left // 1700)] * len(many), code=12)
+    p.free([int(x) for x in rng.permutation(seqs)[:3000]])
+    p.compact()
+
+
 def test_pages_replay(torch):
     rng = np.random.default_rng(10)
     p = Pool(torch, rng, 100, 4, 6, 10, [9, 6, 0, 0, 13, 0], [(8,), (16,)])
