@@ -346,7 +346,12 @@ SBGEMM_API int sbgemm_attention_paged(const float* Q, int64_t rsQ, int64_t csQ, 
 /* ---- 16-bit serving operators ------------------------------------------------
  * Operands below are arrays of 16-bit floats; strides count ELEMENTS (signed
  * 64-bit) as above.  Products are exact, sums and softmax statistics are fp32,
- * and each output is rounded once, to nearest even. */
+ * and each output is rounded once, to nearest even.  On the tensor cores
+ * attention rounds its softmax weights to `type` too, for their product with
+ * the values: relative to a reference within a factor of 2^8 of the row's
+ * largest weight (fp16 below 2^-14 of the reference: to a multiple of 2^-24).
+ * The paged form divides by the sum of the rounded weights, the packed form by
+ * that of the weights before. */
 enum {
     SBGEMM_TYPE_BF16 = 1,
     SBGEMM_TYPE_FP16 = 2
@@ -417,7 +422,7 @@ SBGEMM_API int sbgemm_latent_workspace_bytes(int device, size_t* bytes);
  * that belong to no sequence are left as they were.
  *   Q[i,h,:] = Q + i*tsQ + h*hsQ (Dn + P contiguous); K_nope[n,h,:] (Dn),
  *   V[n,h,:] (Dv) and O[i,h,:] (Dv) alike; K_rope[n,:] = K_rope + n*tsR (P;
- *   may be NULL when P == 0)
+ *   may be NULL when P == 0, K_nope when Dn == 0)
  *   total_q, total_k: rows of Q / O and of the keys; max_q: the most queries
  *   of a sequence
  * Starts that decrease, leave [0, total] or hold more than max_q queries are
