@@ -354,7 +354,10 @@ SBGEMM_API int sbgemm_attention_paged(const float* Q, int64_t rsQ, int64_t csQ, 
  * that of the weights before. */
 enum {
     SBGEMM_TYPE_BF16 = 1,
-    SBGEMM_TYPE_FP16 = 2
+    SBGEMM_TYPE_FP16 = 2,
+    SBGEMM_TYPE_FP32 = 3,        /* the operators below that say so */
+    SBGEMM_TYPE_E4M3 = 4,        /* 8-bit floats: 448 is the largest, no infinities */
+    SBGEMM_TYPE_E5M2 = 5         /* 57344 is the largest finite one */
 };
 
 /* The strided batched product of sbgemm on 16-bit operands:
@@ -439,6 +442,143 @@ SBGEMM_API int sbgemm_latent_attention(
     const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int64_t max_q,
     void* O, int64_t hsO, int64_t tsO,
     int64_t heads, int64_t Dn, int64_t P, int64_t Dv, float alpha, int causal, void* stream);
+
+/* Latent attention over a paged cache for a batch whose sequences share long
+ * prefixes (samples of one prompt, questions about one document, the forks of
+ * sbgemm_pages_fork).  Sequences are grouped in order: group g holds the
+ * sequences group_starts[g] .. group_starts[g+1]-1 (int32 [n_groups + 1] on the
+ * device), and its sequences read their keys n < prefix_lens[g] (int32
+ * [n_groups]) where the group's FIRST sequence has them, block_table[first],
+ * once for all of the group's query rows; the keys behind come from their own
+ * table rows, as always (entry n / block_size, also where the prefix ends
+ * inside a page).  Everything else is sbgemm_latent_attention_paged, which
+ * gives the same result up to rounding when the tables agree on the prefix.
+ * prefix_lens[g] is at most the first sequence's length; a sequence shorter
+ * than it sees its own length's keys of it.  Sequences before the first start
+ * or behind the last one, and those of a group with prefix 0, read their own
+ * keys only.  Starts that decrease or leave [0, n_seqs], and prefix lengths
+ * outside [0, the first sequence's length], are clamped and reported as code
+ * 10 (sbgemm_device_status), like block ids and lengths out of range.  NaN or
+ * infinity in a row of the prefix that some queries of the group mask and
+ * others do not may reach all of the group's queries.
+ * R, P, types and alignments of the tensor-core kernel as there; other sizes
+ * run the slower kernel, which reads the prefix once a query row.
+ * opt->workspace of sbgemm_latent_shared_workspace_bytes is required: each
+ * piece of a sequence's keys passes through it. */
+SBGEMM_API int sbgemm_latent_attention_shared(
+    int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t bsQ,
+    const void* cache, int64_t rsC, int64_t psC, int64_t num_blocks, int64_t block_size,
+    const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+    const int32_t* group_starts, const int32_t* prefix_lens, int64_t n_groups,
+    void* O, int64_t hsO, int64_t tsO, int64_t bsO,
+    int64_t q_len, int64_t heads, int64_t N, int64_t R, int64_t P, int64_t n_seqs,
+    float alpha, int causal, void* stream, const sbgemm_options* opt);
+
+/* Workspace of sbgemm_latent_attention_shared for up to these sizes. */
+SBGEMM_API int sbgemm_latent_shared_workspace_bytes(int device, int64_t n_seqs, int64_t n_groups, int64_t q_len,
+                                                    int64_t heads, int64_t R, size_t* bytes);
+
+/* ---- products of 8-bit floats -------------------------------------------------
+ * A matrix of 8-bit floats with fp32 scales, one for each `group` rows (1 or
+ * 128) and 128 elements along the contracted axis: element [r][k] stands for
+ * data[r][k] * scale[r / group][k / 128].  "Rows" are the index that is not
+ * contracted: M of A, N of B.  Strides count elements of the array they belong
+ * to, as above; operands may have any (zero ones share a matrix over the
+ * batch). */
+typedef struct {
+    int type;                    /* SBGEMM_TYPE_E4M3 or SBGEMM_TYPE_E5M2 */
+    int group;                   /* rows a scale covers: 1 or 128 */
+    void* data;
+    int64_t row_stride, k_stride, batch_stride;
+    float* scale;
+    int64_t scale_row_stride, scale_k_stride, scale_batch_stride;
+} sbgemm_fp8_matrix;
+
+/* C[b] <- alpha * A[b] * B[b] (+ C[b]) on such matrices:
+ *     C[b][m][n] = alpha * sum_j SA[m][j] SB[n][j] sum_{k in block j} A[m][k] B[n][k] (+ C_old)
+ * type_c: SBGEMM_TYPE_BF16, _FP16 or _FP32.  Products are exact; a block's sum
+ * and the sum over blocks are fp32, the output is rounded once.  A and B may be
+ * of different 8-bit types.  Operands with unit stride along k and 16-byte
+ * aligned bases, rows and batches run on the tensor cores, every other layout
+ * on a slower CUDA-core kernel.  Few output tiles with a long K are split along
+ * K inside thread-block clusters; no workspace is needed, and results repeat
+ * from run to run.  Edge cases and errors as sbgemm. */
+SBGEMM_API int sbgemm_fp8(const sbgemm_fp8_matrix* A, const sbgemm_fp8_matrix* B,
+                          int type_c, void* C, int64_t rsC, int64_t csC, int64_t bsC,
+                          int64_t M, int64_t N, int64_t K, int64_t batch,
+                          float alpha, int accumulate, void* stream);
+
+/* Quantises X [batch][M][K] (type_x: SBGEMM_TYPE_BF16, _FP16 or _FP32; any
+ * strides, so a transposed X is quantised along its other axis) into Y, whose
+ * data and scales are written: for each group x 128 elements
+ *     scale = max(largest finite |x| / largest value of Y's type, 2^-126)
+ *     y = x / scale rounded to Y's type, nearest even, largest value kept
+ * both quotients rounded to fp32; NaN and infinities become NaN and leave
+ * their block's scale alone.  Y's elements and scales must be distinct; rows
+ * past M and elements past K are not touched. */
+SBGEMM_API int sbgemm_quantize_fp8(int type_x, const void* X, int64_t rsX, int64_t csX, int64_t bsX,
+                                   const sbgemm_fp8_matrix* Y, int64_t M, int64_t K, int64_t batch, void* stream);
+
+/* ---- norms and positions of queries, keys and latents ---------------------------
+ * One pass over rows [token][head] of D elements: the RMS norm of a row's first
+ * `norm` elements (0: none), then the rotation of `dims` of its elements from
+ * `start` by their token's position.
+ *     z = x * w / sqrt(mean(x^2 over the normed ones) + eps)    (others z = x)
+ *     (y_a, y_b) = magnitude * (z_a cos - z_b sin, z_a sin + z_b cos)
+ * for each pair i < dims / 2: a = start + i, b = a + dims / 2, or when
+ * interleaved a = start + 2 i, b = a + 1.  The angle is positions[token] times
+ * steps[i], counted in 2^-64 of a turn: a frequency of f radians a position has
+ * the step f / (2 pi) * 2^64, and their product modulo 2^64 is exact, so far
+ * positions lose nothing.  Up to SBGEMM_MAX_ROPE_PARTS arrays (queries and
+ * keys; query rope parts and latent rows of the cache) go in one launch.
+ * All of `type` (SBGEMM_TYPE_BF16, _FP16 or _FP32), elements of a row
+ * contiguous; fp32 arithmetic, rounded once.  y may be x itself (same strides). */
+enum { SBGEMM_MAX_ROPE_PARTS = 4 };
+typedef struct {
+    const void* x;               /* row of token t, head h at x + t*x_token + h*x_head */
+    int64_t x_token, x_head;
+    void* y;
+    int64_t y_token, y_head;
+    int64_t heads, D, norm, start;
+    const void* weight;          /* [norm] of `type`, shared by the heads; NULL: ones */
+} sbgemm_rope_part;
+
+/* positions: int32 [tokens] (any sign), steps: uint64 [dims / 2], both on the
+ * device; dims even, 0 for norms only (both may then be NULL).  norm <= D,
+ * start + dims <= D, D <= 4096.  Rows whose elements come in aligned vectors
+ * (16 bytes; bases, strides, norm, start and dims / 2 in whole ones, else 8)
+ * take the fast kernel, others a slower one. */
+SBGEMM_API int sbgemm_norm_rope(int type, const sbgemm_rope_part* parts, int64_t n_parts,
+                                const int32_t* positions, int64_t tokens, const uint64_t* steps, int64_t dims,
+                                float magnitude, int interleaved, float eps, void* stream);
+
+/* Its gradient: dx and dweight of an upstream gradient dy.
+ *     g = dy turned back, times magnitude;   r = 1 / sqrt(mean(x^2) + eps)
+ *     dx = r (g w - x r mean(g w x r));   dweight = sum over tokens and heads of g x r
+ * (dx = g where there is no norm: without norms this is the inverse rotation,
+ * and x may be NULL).  dx may be dy itself (same strides).  dweight, fp32
+ * [norm], may be NULL; with accumulate it is added to.  opt->workspace of
+ * sbgemm_norm_rope_workspace_bytes is required when a dweight is wanted; sums
+ * are made in a fixed order, so results repeat. */
+typedef struct {
+    const void* x;
+    int64_t x_token, x_head;
+    const void* dy;
+    int64_t dy_token, dy_head;
+    void* dx;
+    int64_t dx_token, dx_head;
+    int64_t heads, D, norm, start;
+    const void* weight;
+    float* dweight;
+} sbgemm_rope_grad;
+SBGEMM_API int sbgemm_norm_rope_backward(int type, const sbgemm_rope_grad* parts, int64_t n_parts,
+                                         const int32_t* positions, int64_t tokens, const uint64_t* steps,
+                                         int64_t dims, float magnitude, int interleaved, float eps, int accumulate,
+                                         void* stream, const sbgemm_options* opt);
+
+/* Workspace of sbgemm_norm_rope_backward: norm_total is the sum of the parts'
+ * normed elements. */
+SBGEMM_API int sbgemm_norm_rope_workspace_bytes(int device, int64_t norm_total, size_t* bytes);
 
 /* A pool of pages and the sequences that hold them, all in device memory.
  * Page j of cache i is the page_bytes[i] bytes from caches[i] + j *

@@ -33,6 +33,11 @@ __all__ = [
     "sbgemm_latent_attention", "sbgemm_latent_workspace_bytes", "sbgemm_pages_workspace_bytes",
     "matmul_half", "latent_attention_paged", "latent_attention", "pages_copy", "pages_fork",
     "pages_append", "pages_free", "pages_compact",
+    "TYPE_FP32", "TYPE_E4M3", "TYPE_E5M2", "MAX_ROPE_PARTS", "sbgemm_latent_attention_shared",
+    "sbgemm_latent_shared_workspace_bytes", "latent_attention_shared", "sbgemm_fp8", "sbgemm_quantize_fp8",
+    "Fp8Matrix", "matmul_fp8", "quantize_fp8", "sbgemm_norm_rope", "sbgemm_norm_rope_backward",
+    "sbgemm_norm_rope_workspace_bytes", "RopeTable", "RopePart", "RopeGrad", "rope_steps",
+    "rope_frequencies", "rope_table", "norm_rope", "norm_rope_backward",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -64,9 +69,13 @@ EXPORTED_SYMBOLS = ("sbgemm", "sbgemm_ex", "sbgemm_fused", "sbgemm_attention",
                     "sbgemm_half", "sbgemm_latent_attention_paged", "sbgemm_latent_workspace_bytes",
                     "sbgemm_latent_attention", "sbgemm_pages_workspace_bytes", "sbgemm_pages_copy",
                     "sbgemm_pages_fork", "sbgemm_pages_append", "sbgemm_pages_free",
-                    "sbgemm_pages_compact")
-TYPE_BF16, TYPE_FP16 = 1, 2
+                    "sbgemm_pages_compact", "sbgemm_latent_attention_shared",
+                    "sbgemm_latent_shared_workspace_bytes", "sbgemm_fp8", "sbgemm_quantize_fp8",
+                    "sbgemm_norm_rope", "sbgemm_norm_rope_backward",
+                    "sbgemm_norm_rope_workspace_bytes")
+TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_E4M3, TYPE_E5M2 = 1, 2, 3, 4, 5
 MAX_CACHES = 64
+MAX_ROPE_PARTS = 4
 ACT_NONE, ACT_RELU, ACT_SIGMOID, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2, 3, 4, 5
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "sigmoid": ACT_SIGMOID, "silu": ACT_SILU,
                "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF}
@@ -170,6 +179,7 @@ def load(path: str = LIB_PATH):
         lib.sbgemm_version.restype = ctypes.c_int
         lib.sbgemm_version.argtypes = []
         _serving.declare(lib)
+        _layers.declare(lib)
         global _fast
         try:
             from . import _fastcall
@@ -478,6 +488,14 @@ def linear_backward(G, X, W, dX, dW, accumulate_dW: bool = False, stream=None,
 # The 16-bit serving operators (their own file; the same library).
 from . import serving as _serving  # noqa: E402
 from .serving import (  # noqa: E402,F401
-    latent_attention, latent_attention_paged, matmul_half, pages_append, pages_compact,
+    latent_attention, latent_attention_paged, latent_attention_shared, matmul_half, pages_append, pages_compact,
     pages_copy, pages_fork, pages_free, sbgemm_half, sbgemm_latent_attention,
-    sbgemm_latent_attention_paged, sbgemm_latent_workspace_bytes, sbgemm_pages_workspace_bytes)
+    sbgemm_latent_attention_paged, sbgemm_latent_attention_shared, sbgemm_latent_shared_workspace_bytes,
+    sbgemm_latent_workspace_bytes, sbgemm_pages_workspace_bytes)
+
+# The operators around a layer's products: 8-bit products, norms and rotations.
+from . import layers as _layers  # noqa: E402
+from .layers import (  # noqa: E402,F401
+    Fp8Matrix, RopeGrad, RopePart, RopeTable, matmul_fp8, norm_rope, norm_rope_backward, quantize_fp8,
+    rope_frequencies, rope_steps, rope_table, sbgemm_fp8, sbgemm_norm_rope, sbgemm_norm_rope_backward,
+    sbgemm_norm_rope_workspace_bytes, sbgemm_quantize_fp8)

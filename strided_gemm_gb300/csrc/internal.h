@@ -194,6 +194,10 @@ unsigned int* status_word_latent_decode();
 unsigned int* status_word_latent_prompt();
 unsigned int* status_word_latent_rows();
 unsigned int* status_word_pages();
+unsigned int* status_word_latent_shared();
+unsigned int* status_word_fp8_gather();
+unsigned int* status_word_fp8_quantize();
+unsigned int* status_word_norm_rope();
 // Clears all of them behind the work on `stream` and waits for it; *code
 // receives the first non-zero one in the order above (0 if none).  False on a
 // CUDA error.

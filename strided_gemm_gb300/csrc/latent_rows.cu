@@ -104,6 +104,34 @@ rows_paged_kernel(const LatentPaged a, float scale_log2) {
     }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+rows_shared_kernel(const __grid_constant__ LatentShared g, float scale_log2) {
+    const LatentPaged& a = g.paged;
+    const int64_t rows = a.n_seqs * a.q_len * a.heads;
+    for (int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * kWarps) {
+        const int64_t h = r % a.heads, t = r / a.heads % a.q_len, s = r / a.heads / a.q_len;
+        int64_t len = a.seq_lens ? a.seq_lens[s] : a.N;
+        len = min(max(len, (int64_t)0), a.N);            // (reported by the plan)
+        const int64_t keys = a.causal ? min(len, max((int64_t)0, len - a.q_len + t + 1)) : len;
+        const int64_t first = g.first[s], prefix = g.prefix[s];
+        const T* base = static_cast<const T*>(a.cache);
+        attend_row<T>(static_cast<const T*>(a.Q) + s * a.bsQ + t * a.tsQ + h * a.hsQ, (int)a.R, (int)a.P, (int)a.R,
+                      keys, scale_log2, static_cast<T*>(a.O) + s * a.bsO + t * a.tsO + h * a.hsO,
+                      Spans{a.sq, a.sc, a.sc, a.sc, a.so},
+                      [&](int64_t n, const T** kn, const T** kr, const T** v) {
+                          const int64_t page = a.table[(n < prefix ? first : s) * a.max_blocks + n / a.block_size];
+                          if (page < 0 || page >= a.num_blocks) {
+                              record_status(&g_status, kPagedInput);
+                              return false;
+                          }
+                          *kn = *v = base + page * a.psC + n % a.block_size * a.rsC;
+                          *kr = *kn + a.R;
+                          return true;
+                      });
+    }
+}
+
 // starts[s], starts[s + 1] as a range inside [0, total], reported when they are not.
 __device__ __forceinline__ void packed_range(const int32_t* starts, int64_t s, int64_t total, int64_t most,
                                              int64_t* lo, int64_t* n) {
@@ -145,6 +173,15 @@ cudaError_t launch_latent_rows_paged(const LatentPaged& a, cudaStream_t stream) 
     const float scale = a.alpha * 1.4426950408889634f;
     if (a.type == SBGEMM_TYPE_BF16) rows_paged_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, stream>>>(a, scale);
     else rows_paged_kernel<__half><<<grid, kWarps * 32, 0, stream>>>(a, scale);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_rows_shared(const LatentShared& g, cudaStream_t stream) {
+    const int64_t rows = g.paged.n_seqs * g.paged.q_len * g.paged.heads;
+    const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, 1 << 20);
+    const float scale = g.paged.alpha * 1.4426950408889634f;
+    if (g.paged.type == SBGEMM_TYPE_BF16) rows_shared_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, stream>>>(g, scale);
+    else rows_shared_kernel<__half><<<grid, kWarps * 32, 0, stream>>>(g, scale);
     return cudaGetLastError();
 }
 

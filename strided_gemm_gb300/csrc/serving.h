@@ -54,6 +54,24 @@ struct LatentPacked {
     int causal;
     ByteSpan sq, sk, sr, sv, so;     // debug builds: what Q, K_nope, K_rope, V and O occupy
 };
+// Latent attention over a paged cache with shared prefixes
+// (sbgemm_latent_attention_shared).  A plan kernel (latent_shared.cu) turns the
+// groups into each sequence's own first key and the row of the table that holds
+// the keys before it, once for whichever kernel follows.
+struct LatentShared {
+    LatentPaged paged;               // (its workspace is not read)
+    const int32_t* group_starts; const int32_t* prefix_lens;
+    int64_t n_groups;
+    int32_t* first;                  // [n_seqs]: the sequence whose table row has the prefix
+    int32_t* prefix;                 // [n_seqs]: keys of the prefix
+    void* rest; size_t rest_bytes;   // of the workspace
+    ByteSpan sw;                     // debug builds: what the workspace occupies
+};
+size_t latent_shared_workspace_bytes(int sms, int64_t n_seqs, int64_t n_groups, int64_t q_len, int64_t heads, int64_t R);
+cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_starts, const int32_t* prefix_lens,
+                                 int64_t n_groups, int sms, cudaStream_t stream);
+cudaError_t launch_latent_rows_shared(const LatentShared& a, cudaStream_t stream);
+
 // On the tensor cores, over a paged cache (latent_decode.cu); false for sizes
 // and alignments it does not take.
 bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err);

@@ -7,124 +7,16 @@
 
 #include <algorithm>
 #include <array>
-#include <climits>
 #include <initializer_list>
-#include <utility>
 
+#include "api_checks.h"
 #include "sbgemm.h"
 #include "serving.h"
 
 namespace sbg {
 namespace {
 
-using i128 = __int128;
-
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// Bytes [lo, hi) that an operand occupies.
-struct Bytes { i128 lo, hi; };
-
-struct Axis { int64_t stride, extent; };
-
-// The bytes of an array of `esize`-byte elements over the axes' box (extents
-// positive).  False if offsets do not fit comfortably in int64 bytes.
-bool span_of(const void* base, int64_t esize, std::initializer_list<Axis> axes, Bytes* out) {
-    i128 lo = 0, hi = 0;
-    for (const Axis& a : axes) {
-        const i128 d = (i128)a.stride * (a.extent - 1);
-        if (d < 0) lo += d;
-        else hi += d;
-    }
-    const i128 limit = (i128)1 << 60;
-    if (lo < -limit || hi > limit) return false;
-    const i128 b = (i128)reinterpret_cast<uintptr_t>(base);
-    *out = {b + lo * esize, b + (hi + 1) * esize};
-    return true;
-}
-
-// Distinct indices have distinct elements: sorted by stride, each stride
-// exceeds what the smaller ones reach (sufficient, as for the fp32 product).
-template <size_t n>
-bool injective(std::array<Axis, n> a) {
-    for (Axis& x : a) x.stride = x.stride < 0 ? -x.stride : x.stride;
-    std::sort(a.begin(), a.end(), [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
-    i128 reach = 0;
-    for (const Axis& x : a) {
-        if (x.extent <= 1) continue;
-        if ((i128)x.stride <= reach) return false;
-        reach += (i128)x.stride * (x.extent - 1);
-    }
-    return true;
-}
-
-ByteSpan span_for_kernel(const Bytes& b) { return {(uintptr_t)b.lo, (uintptr_t)b.hi}; }
-
-bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Each span lies inside one device-accessible allocation.  An allocation seen
-// before in this call is not looked up again.
-int in_device_memory(std::initializer_list<Bytes> spans) {
-    std::array<Bytes, 8> seen;
-    size_t n = 0;
-    for (const Bytes& s : spans) {
-        bool known = false;
-        for (size_t i = 0; i < n && !known; ++i) known = s.lo >= seen[i].lo && s.hi <= seen[i].hi;
-        if (known) continue;
-        uintptr_t base = 0;
-        size_t size = 0;
-        if (!device_allocation_range(reinterpret_cast<const void*>((uintptr_t)s.lo), &base, &size))
-            return SBGEMM_ERR_NOT_DEVICE_MEMORY;
-        const Bytes a{(i128)base, (i128)base + (i128)size};
-        if (s.lo < a.lo || s.hi > a.hi) return SBGEMM_ERR_NOT_DEVICE_MEMORY;
-        if (n < seen.size()) seen[n++] = a;
-    }
-    return SBGEMM_OK;
-}
-
-// The options these operators read: a workspace, and no forced path.
-int read_options(const sbgemm_options* opt, void** ws, size_t* bytes) {
-    *ws = nullptr;
-    *bytes = 0;
-    if (!opt) return SBGEMM_OK;
-    if (opt->math != SBGEMM_MATH_FP32 && opt->math != SBGEMM_MATH_TF32) return SBGEMM_ERR_INVALID_VALUE;
-    if (opt->force_path < SBGEMM_PATH_AUTO || opt->force_path > SBGEMM_PATH_TMA_TF32)
-        return SBGEMM_ERR_INVALID_VALUE;
-    if (opt->force_path != SBGEMM_PATH_AUTO) return SBGEMM_ERR_UNSUPPORTED;
-    if (opt->k_split < SBGEMM_KSPLIT_ANY || opt->k_split > SBGEMM_KSPLIT_NONE) return SBGEMM_ERR_INVALID_VALUE;
-    for (int r : opt->reserved)
-        if (r != 0) return SBGEMM_ERR_INVALID_VALUE;
-    if (opt->workspace) {
-        if (!aligned(opt->workspace, 256)) return SBGEMM_ERR_INVALID_VALUE;
-        *ws = opt->workspace;
-        *bytes = opt->workspace_bytes;
-    }
-    return SBGEMM_OK;
-}
-
-Bytes block(const void* p, int64_t bytes) {
-    const i128 b = (i128)reinterpret_cast<uintptr_t>(p);
-    return {b, b + bytes};
-}
-
 bool known_type(int type) { return type == SBGEMM_TYPE_BF16 || type == SBGEMM_TYPE_FP16; }
-
-// The SMs of the current device, 0 on a CUDA error.
-int current_sms() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess) {
-        if (const DeviceProps* d = device_props(dev)) return d->sm_count;
-    }
-    cudaGetLastError();
-    return 0;
-}
-
-int finish(cudaError_t e) {
-    if (e == cudaSuccess) return SBGEMM_OK;
-    cudaGetLastError();
-    return SBGEMM_ERR_CUDA;
-}
-
-constexpr int64_t kInt = INT_MAX;
 
 // ---- the pool ------------------------------------------------------------------
 
@@ -208,6 +100,57 @@ int check_pool_memory(const PoolView& v, std::initializer_list<Bytes> inputs, co
     return SBGEMM_OK;
 }
 
+// The arguments that sbgemm_latent_attention_paged and _shared have in common:
+// checked, and laid out in *a, with the operands' bytes (Q, cache, O, table,
+// lengths) in *spans.  *empty: there is nothing to do.
+int check_latent_paged(
+    int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t bsQ,
+    const void* cache, int64_t rsC, int64_t psC, int64_t num_blocks, int64_t block_size,
+    const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+    void* O, int64_t hsO, int64_t tsO, int64_t bsO,
+    int64_t q_len, int64_t heads, int64_t N, int64_t R, int64_t P, int64_t n_seqs,
+    float alpha, int causal, const sbgemm_options* opt, LatentPaged* a, std::array<Bytes, 5>* spans, bool* empty) {
+    *empty = false;
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (const int st = read_options(opt, &ws, &ws_bytes)) return st;
+    if (!known_type(type)) return SBGEMM_ERR_INVALID_VALUE;
+    if (q_len < 0 || heads < 0 || N < 0 || R < 0 || P < 0 || n_seqs < 0) return SBGEMM_ERR_INVALID_VALUE;
+    if (causal != 0 && causal != 1) return SBGEMM_ERR_INVALID_VALUE;
+    if (q_len == 0 || heads == 0 || n_seqs == 0 || R == 0) {
+        *empty = true;
+        return SBGEMM_OK;
+    }
+    if (num_blocks <= 0 || num_blocks >= kInt || block_size <= 0 || max_blocks <= 0)
+        return SBGEMM_ERR_INVALID_VALUE;
+    if ((i128)max_blocks * block_size < (i128)N) return SBGEMM_ERR_INVALID_VALUE;
+    if (R > kLatentMaxV || R + P > kLatentMaxQK) return SBGEMM_ERR_UNSUPPORTED;
+    // (A block of keys beyond the last one still has an int for its index.)
+    if (q_len >= kInt || heads >= kInt || N > kInt - 64 || n_seqs >= kInt || block_size >= kInt ||
+        (i128)q_len * heads >= kInt || (i128)q_len * heads * n_seqs >= kInt)
+        return SBGEMM_ERR_UNSUPPORTED;
+    if (!Q || !cache || !block_table || !O) return SBGEMM_ERR_NULL_POINTER;
+    if (!aligned(Q, 2) || !aligned(cache, 2) || !aligned(O, 2) || !aligned(block_table, 4) ||
+        (seq_lens && !aligned(seq_lens, 4)))
+        return SBGEMM_ERR_INVALID_VALUE;
+    Bytes sq{}, sc{}, so{}, st{};
+    if (!span_of(Q, 2, {{bsQ, n_seqs}, {tsQ, q_len}, {hsQ, heads}, {1, R + P}}, &sq) ||
+        !span_of(cache, 2, {{psC, num_blocks}, {rsC, block_size}, {1, R + P}}, &sc) ||
+        !span_of(O, 2, {{bsO, n_seqs}, {tsO, q_len}, {hsO, heads}, {1, R}}, &so) ||
+        !span_of(block_table, 4, {{max_blocks, n_seqs}, {1, max_blocks}}, &st))
+        return SBGEMM_ERR_INVALID_VALUE;
+    const Bytes sl = seq_lens ? block(seq_lens, n_seqs * 4) : st;
+    if (!injective(std::array<Axis, 4>{{{bsO, n_seqs}, {tsO, q_len}, {hsO, heads}, {1, R}}}))
+        return SBGEMM_ERR_OUTPUT_OVERLAP;
+    for (const Bytes& s : {sq, sc, st, sl})
+        if (meet(so, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    *a = LatentPaged{type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
+                     seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal, ws, ws_bytes,
+                     span_for_kernel(sq), span_for_kernel(sc), span_for_kernel(so)};
+    *spans = {sq, sc, so, st, sl};
+    return SBGEMM_OK;
+}
+
 }  // namespace
 
 }  // namespace sbg
@@ -254,52 +197,80 @@ int sbgemm_latent_attention_paged(
     void* O, int64_t hsO, int64_t tsO, int64_t bsO,
     int64_t q_len, int64_t heads, int64_t N, int64_t R, int64_t P, int64_t n_seqs,
     float alpha, int causal, void* stream, const sbgemm_options* opt) {
-    void* ws = nullptr;
-    size_t ws_bytes = 0;
-    if (const int st = read_options(opt, &ws, &ws_bytes)) return st;
-    if (!known_type(type)) return SBGEMM_ERR_INVALID_VALUE;
-    if (q_len < 0 || heads < 0 || N < 0 || R < 0 || P < 0 || n_seqs < 0) return SBGEMM_ERR_INVALID_VALUE;
-    if (causal != 0 && causal != 1) return SBGEMM_ERR_INVALID_VALUE;
-    if (q_len == 0 || heads == 0 || n_seqs == 0 || R == 0) return SBGEMM_OK;
-    if (num_blocks <= 0 || num_blocks >= kInt || block_size <= 0 || max_blocks <= 0)
-        return SBGEMM_ERR_INVALID_VALUE;
-    if ((i128)max_blocks * block_size < (i128)N) return SBGEMM_ERR_INVALID_VALUE;
-    if (R > kLatentMaxV || R + P > kLatentMaxQK) return SBGEMM_ERR_UNSUPPORTED;
-    // (A block of keys beyond the last one still has an int for its index.)
-    if (q_len >= kInt || heads >= kInt || N > kInt - 64 || n_seqs >= kInt || block_size >= kInt ||
-        (i128)q_len * heads >= kInt || (i128)q_len * heads * n_seqs >= kInt)
-        return SBGEMM_ERR_UNSUPPORTED;
-    if (!Q || !cache || !block_table || !O) return SBGEMM_ERR_NULL_POINTER;
-    if (!aligned(Q, 2) || !aligned(cache, 2) || !aligned(O, 2) || !aligned(block_table, 4) ||
-        (seq_lens && !aligned(seq_lens, 4)))
-        return SBGEMM_ERR_INVALID_VALUE;
-    Bytes sq{}, sc{}, so{}, st{};
-    if (!span_of(Q, 2, {{bsQ, n_seqs}, {tsQ, q_len}, {hsQ, heads}, {1, R + P}}, &sq) ||
-        !span_of(cache, 2, {{psC, num_blocks}, {rsC, block_size}, {1, R + P}}, &sc) ||
-        !span_of(O, 2, {{bsO, n_seqs}, {tsO, q_len}, {hsO, heads}, {1, R}}, &so) ||
-        !span_of(block_table, 4, {{max_blocks, n_seqs}, {1, max_blocks}}, &st))
-        return SBGEMM_ERR_INVALID_VALUE;
-    const Bytes sl = seq_lens ? block(seq_lens, n_seqs * 4) : st;
-    if (!injective(std::array<Axis, 4>{{{bsO, n_seqs}, {tsO, q_len}, {hsO, heads}, {1, R}}}))
-        return SBGEMM_ERR_OUTPUT_OVERLAP;
-    for (const Bytes& s : {sq, sc, st, sl})
-        if (meet(so, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    LatentPaged a{};
+    std::array<Bytes, 5> spans;
+    bool empty = false;
+    if (const int st = check_latent_paged(type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table,
+                                          max_blocks, seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha,
+                                          causal, opt, &a, &spans, &empty))
+        return st;
+    if (empty) return SBGEMM_OK;
     const int sms = current_sms();
     if (!sms) return SBGEMM_ERR_CUDA;
-    if (const int m = in_device_memory({sq, sc, so, st, sl})) return m;
-    if (ws) {
-        const Bytes w = block(ws, (int64_t)std::min<size_t>(ws_bytes, (size_t)1 << 60));
-        for (const Bytes& s : {sq, sc, so, st, sl})
+    if (const int m = in_device_memory({spans[0], spans[1], spans[2], spans[3], spans[4]})) return m;
+    if (a.workspace) {
+        const Bytes w = block(a.workspace, (int64_t)std::min<size_t>(a.workspace_bytes, (size_t)1 << 60));
+        for (const Bytes& s : spans)
             if (meet(w, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
-        if (ws_bytes == 0) ws = nullptr;
+        if (a.workspace_bytes == 0) a.workspace = nullptr;
         else if (const int m = in_device_memory({w})) return m;
     }
-    const LatentPaged a{type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
-                        seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal, ws, ws_bytes,
-                        span_for_kernel(sq), span_for_kernel(sc), span_for_kernel(so)};
     cudaError_t e = cudaSuccess;
     if (launch_latent_decode(a, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_latent_rows_paged(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sbgemm_latent_attention_shared(
+    int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t bsQ,
+    const void* cache, int64_t rsC, int64_t psC, int64_t num_blocks, int64_t block_size,
+    const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+    const int32_t* group_starts, const int32_t* prefix_lens, int64_t n_groups,
+    void* O, int64_t hsO, int64_t tsO, int64_t bsO,
+    int64_t q_len, int64_t heads, int64_t N, int64_t R, int64_t P, int64_t n_seqs,
+    float alpha, int causal, void* stream, const sbgemm_options* opt) {
+    LatentPaged a{};
+    std::array<Bytes, 5> spans;
+    bool empty = false;
+    if (n_groups < 0) return SBGEMM_ERR_INVALID_VALUE;
+    if (const int st = check_latent_paged(type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table,
+                                          max_blocks, seq_lens, O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha,
+                                          causal, opt, &a, &spans, &empty))
+        return st;
+    if (empty) return SBGEMM_OK;
+    if (n_groups >= kInt / 2) return SBGEMM_ERR_UNSUPPORTED;
+    if (n_groups > 0 && (!group_starts || !prefix_lens)) return SBGEMM_ERR_NULL_POINTER;
+    if (!aligned(group_starts, 4) || !aligned(prefix_lens, 4)) return SBGEMM_ERR_INVALID_VALUE;
+    // (Without groups nothing of theirs is read.)
+    const Bytes s0 = n_groups ? block(group_starts, (n_groups + 1) * 4) : spans[3];
+    const Bytes s1 = n_groups ? block(prefix_lens, n_groups * 4) : spans[3];
+    if (meet(spans[2], s0) || meet(spans[2], s1)) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    const int sms = current_sms();
+    if (!sms) return SBGEMM_ERR_CUDA;
+    const size_t need = latent_shared_workspace_bytes(sms, n_seqs, n_groups, q_len, heads, R);
+    if (!a.workspace || a.workspace_bytes < need) return SBGEMM_ERR_INVALID_VALUE;
+    a.workspace_bytes = need;
+    const Bytes w = block(a.workspace, (int64_t)need);
+    for (const Bytes& s : {spans[0], spans[1], spans[2], spans[3], spans[4], s0, s1})
+        if (meet(w, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    if (const int m = in_device_memory({spans[0], spans[1], spans[2], spans[3], spans[4], s0, s1})) return m;
+    if (const int m = in_device_memory({w})) return m;
+    return finish(launch_latent_shared(a, group_starts, prefix_lens, n_groups, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int sbgemm_latent_shared_workspace_bytes(int device, int64_t n_seqs, int64_t n_groups, int64_t q_len, int64_t heads,
+                                         int64_t R, size_t* bytes) {
+    if (!bytes) return SBGEMM_ERR_NULL_POINTER;
+    if (n_seqs < 0 || n_groups < 0 || q_len < 0 || heads < 0 || R < 0) return SBGEMM_ERR_INVALID_VALUE;
+    if (n_seqs >= kInt || n_groups >= kInt / 2 || q_len >= kInt || heads >= kInt || R > kLatentMaxV ||
+        (i128)q_len * heads >= kInt || (i128)q_len * heads * n_seqs >= kInt)
+        return SBGEMM_ERR_UNSUPPORTED;
+    const DeviceProps* d = device_props(device);
+    if (!d) {
+        cudaGetLastError();
+        return SBGEMM_ERR_CUDA;
+    }
+    *bytes = latent_shared_workspace_bytes(d->sm_count, n_seqs, n_groups, q_len, heads, R);
+    return SBGEMM_OK;
 }
 
 int sbgemm_latent_workspace_bytes(int device, size_t* bytes) {

@@ -36,6 +36,10 @@ def declare(lib) -> None:
             [_int, _vp] + [_i64] * 3 + [_vp] + [_i64] * 4 + [_vp, _i64, _vp, _vp] + [_i64] * 9 +
             [_f32, _int, _vp, opt],
         "sbgemm_latent_workspace_bytes": [_int, ctypes.POINTER(_size)],
+        "sbgemm_latent_attention_shared":
+            [_int, _vp] + [_i64] * 3 + [_vp] + [_i64] * 4 + [_vp, _i64, _vp, _vp, _vp, _i64, _vp] + [_i64] * 9 +
+            [_f32, _int, _vp, opt],
+        "sbgemm_latent_shared_workspace_bytes": [_int] + [_i64] * 5 + [ctypes.POINTER(_size)],
         "sbgemm_latent_attention":
             [_int, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp,
              _i64, _i64, _vp, _i64, _i64] + [_i64] * 4 + [_f32, _int, _vp],
@@ -107,6 +111,32 @@ def sbgemm_latent_workspace_bytes(device: int = 0) -> int:
     """Bytes of workspace with which latent_attention_paged splits keys freely."""
     n = _size(0)
     _check(_lib().sbgemm_latent_workspace_bytes(int(device), ctypes.byref(n)), "sbgemm_latent_workspace_bytes")
+    return n.value
+
+
+def sbgemm_latent_attention_shared(type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size,
+                                   block_table, max_blocks, seq_lens, group_starts, prefix_lens, n_groups,
+                                   O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal=0, stream=0,
+                                   workspace: int = 0, workspace_bytes: int = 0) -> None:
+    """Latent attention over a paged cache, each group's prefix read once."""
+    o = _sg._opts_ref(_sg.MATH_FP32, _sg.PATH_AUTO, workspace, workspace_bytes, _sg.KSPLIT_ANY)
+    _check(_lib().sbgemm_latent_attention_shared(
+        type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
+        seq_lens or None, group_starts or None, prefix_lens or None, n_groups, O, hsO, tsO, bsO, q_len, heads, N, R,
+        P, n_seqs, alpha, int(causal), stream or None, o[1]), "sbgemm_latent_attention_shared")
+
+
+def sbgemm_latent_shared_workspace_bytes(n_seqs: int, n_groups: int, q_len: int, heads: int, R: int,
+                                         device: int | None = None) -> int:
+    """Bytes of workspace for latent_attention_shared up to these sizes, on
+    `device` (default: the current one)."""
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    n = _size(0)
+    _check(_lib().sbgemm_latent_shared_workspace_bytes(int(device), int(n_seqs), int(n_groups), int(q_len), int(heads),
+                                                       int(R), ctypes.byref(n)),
+           "sbgemm_latent_shared_workspace_bytes")
     return n.value
 
 
@@ -241,16 +271,9 @@ def _paged_on(*args):
 _packed_on = sbgemm_latent_attention
 
 
-def latent_attention_paged(Q, cache, block_table, seq_lens, O, alpha, causal: bool = True,
-                           workspace=None, max_len=None, stream=None):
-    """Latent attention, absorbed form: Q [n_seqs, q_len, heads, R + P] against
-    the rows [c | k_rope] of cache [num_blocks, block_size, R + P] that
-    block_table (int32 [n_seqs, max_blocks]) and seq_lens (int32 [n_seqs]; None
-    for max_len everywhere) give each sequence; O [n_seqs, q_len, heads, R]
-    receives the averaged c.  bfloat16 or float16, unit stride along the last
-    axis.  max_len: the longest length (default: what the table can hold); a
-    workspace of sbgemm_latent_workspace_bytes splits the keys over the GPU.
-    Returns O."""
+def _paged_operands(Q, cache, block_table, seq_lens, O, max_len):
+    """(device, the C arguments up to the lengths, O's, and the sizes) of latent
+    attention over a paged cache."""
     kind, dev, dtype = _kind(O, "O"), _device(O), O.dtype
     _same(Q, "Q", dtype, dev)
     _same(cache, "cache", dtype, dev)
@@ -275,10 +298,45 @@ def latent_attention_paged(Q, cache, block_table, seq_lens, O, alpha, causal: bo
     if (wide > 1 and (eq != 1 or ec != 1)) or (R > 1 and eo != 1):
         raise ValueError("Q, cache and O need unit stride along their last axis")
     N = max_blocks * block_size if max_len is None else int(max_len)
+    return dev, (kind, Q.data_ptr(), hq, tq, bq, cache.data_ptr(), rc, pc, num_blocks, block_size, table,
+                 max_blocks, lens), (O.data_ptr(), ho, to, bo, q_len, heads, N, R, wide - R, n_seqs)
+
+
+def latent_attention_paged(Q, cache, block_table, seq_lens, O, alpha, causal: bool = True,
+                           workspace=None, max_len=None, stream=None):
+    """Latent attention, absorbed form: Q [n_seqs, q_len, heads, R + P] against
+    the rows [c | k_rope] of cache [num_blocks, block_size, R + P] that
+    block_table (int32 [n_seqs, max_blocks]) and seq_lens (int32 [n_seqs]; None
+    for max_len everywhere) give each sequence; O [n_seqs, q_len, heads, R]
+    receives the averaged c.  bfloat16 or float16, unit stride along the last
+    axis.  max_len: the longest length (default: what the table can hold); a
+    workspace of sbgemm_latent_workspace_bytes splits the keys over the GPU.
+    Returns O."""
+    dev, first, last = _paged_operands(Q, cache, block_table, seq_lens, O, max_len)
     ws, ws_bytes = _workspace(workspace, dev)
-    _run(dev, stream, _paged_on, kind, Q.data_ptr(), hq, tq, bq, cache.data_ptr(), rc, pc, num_blocks,
-         block_size, table, max_blocks, lens, O.data_ptr(), ho, to, bo, q_len, heads, N, R, wide - R, n_seqs,
-         alpha, causal, ws, ws_bytes)
+    _run(dev, stream, _paged_on, *first, *last, alpha, causal, ws, ws_bytes)
+    return O
+
+
+def _shared_on(*args):
+    sbgemm_latent_attention_shared(*args[:-3], args[-1], args[-3], args[-2])
+
+
+def latent_attention_shared(Q, cache, block_table, seq_lens, group_starts, prefix_lens, O, alpha,
+                            causal: bool = True, workspace=None, max_len=None, stream=None):
+    """latent_attention_paged for a batch whose sequences share prefixes: group
+    g's sequences group_starts[g]..group_starts[g+1] (int32 [n_groups + 1]) read
+    their first prefix_lens[g] keys (int32 [n_groups]) from the pages of its
+    first one, once for the whole group; the other arguments as there.  The
+    workspace, of sbgemm_latent_shared_workspace_bytes, is required.  Returns O."""
+    dev, first, last = _paged_operands(Q, cache, block_table, seq_lens, O, max_len)
+    n_groups = prefix_lens.numel()
+    if group_starts.numel() != n_groups + 1:
+        raise ValueError(f"group_starts{tuple(group_starts.shape)} has one entry more than "
+                         f"prefix_lens{tuple(prefix_lens.shape)}")
+    starts, prefixes = _ints(group_starts, "group_starts", dev), _ints(prefix_lens, "prefix_lens", dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run(dev, stream, _shared_on, *first, starts, prefixes, n_groups, *last, alpha, causal, ws, ws_bytes)
     return O
 
 
