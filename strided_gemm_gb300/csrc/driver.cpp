@@ -82,6 +82,11 @@ bool encode_tmap_16(CUtensorMap* map, const void* base, int rank, const uint64_t
     return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box, true);
 }
 
+bool encode_tmap_8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box) {
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides_bytes, box, true);
+}
+
 bool encode_tmap_f32_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
                         const uint64_t strides_bytes[2], const uint32_t box[3], bool swizzle128) {
     return encode_tmap_f32(map, base, 3, dims, strides_bytes, box, swizzle128);

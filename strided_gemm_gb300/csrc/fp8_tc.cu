@@ -1,0 +1,567 @@
+// The product of 8-bit floats with block scales on the tensor cores
+// (sbgemm_fp8), for operands with unit stride along K that a tensor map
+// describes.
+//
+// K goes by in blocks of 128, one 128-byte swizzled row of each operand and one
+// scale each, through a ring of TMA stages: a block's products (four MMAs of
+// K = 32, kind::f8f6f4) start a fresh accumulator in TMEM, one of two, and the
+// epilogue warps add it, times the two scales, to fp32 sums in registers while
+// the next block's MMAs run. So no scale has to be a power of two, and no more
+// than 128 products are summed by the tensor core.
+//
+// A tile is 128 rows (the MMA's M) by NT columns. Its rows are rows of C, or
+// columns of C (C^T = B^T A^T): a decode batch's few tokens are the columns and
+// the weights fill the rows. Large products run on CTA pairs, one MMA of 256 x
+// 256 x 32 over both CTAs' shared memory, which then moves 32 KB a block of K
+// and CTA, in and out, instead of 48. Few tiles with a long K are split along K
+// over the CTAs of a cluster: each sums its blocks and hands every other CTA
+// its share of the columns through distributed shared memory, added there in
+// the order of the CTAs.
+//
+// Roles: warp 8 issues the TMA loads, warp 9 the MMAs; warps 0-3 and 4-7 hold
+// the sums of the tile's two column halves, a thread one row.
+#include <algorithm>
+#include <atomic>
+
+#include "debug_check.cuh"
+#include "layers.h"
+#include "tc16.cuh"
+
+namespace sbg {
+namespace {
+
+constexpr int BX = 128, BK = kScaleBlock;
+constexpr int kGroups = 2, kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+__device__ unsigned int g_status = 0;
+
+// Scales of one operand.
+struct Scales { const float* at; int64_t rs, ks, bs, rows; int group; ByteSpan span; };
+
+struct Params {
+    void* C; int64_t cx, cy, cb;   // C's strides along the tile's rows, its columns and the batch
+    int type_c;
+    int64_t rows, cols;            // of the product's tiles: x < rows, y < cols
+    int64_t x_tiles, y_tiles, tiles;
+    int k_blocks, split;           // split: CTAs of a cluster that share a tile's blocks
+    float alpha;
+    int accumulate;
+    int vec;                       // columns go out as 16-byte vectors
+    int x_batch, y_batch;          // the batch coordinate moves (else shared)
+    uint32_t idesc;
+    Scales sx, sy;
+    ByteSpan sc;                   // debug builds: what C occupies
+};
+
+template <int NT, bool kPair>
+struct Shape {
+    static constexpr int kYRows = kPair ? NT / 2 : NT;              // this CTA's share of Y
+    static constexpr int kStage = (BX + kYRows) * BK;
+    // Two CTAs an SM for up to 64 columns: the weights' bytes want to be in flight.
+    static constexpr int kCtas = NT <= 64 ? 2 : 1;
+    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kYRows == 256 ? 4 : 6;
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr uint32_t kCols = NT >= 256 ? 512 : NT >= 128 ? 256 : NT >= 64 ? 128 : NT >= 32 ? 64 : 32;
+    static_assert(kSmem * kCtas <= 232448 - 2048 * kCtas, "shared memory");
+};
+
+// kind::f8f6f4, D fp32, both operands K-major.
+uint32_t idesc8(bool x_e5m2, bool y_e5m2, int n, int m) {
+    return (1u << 4) | ((x_e5m2 ? 1u : 0u) << 7) | ((y_e5m2 ? 1u : 0u) << 10) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// A vote and barrier of the four warps of an epilogue group.
+__device__ __forceinline__ bool all_of_group(int g, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\t"
+        "barrier.cta.red.and.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r) : "r"((uint32_t)v), "r"(1 + g) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// acc += v * f on pairs.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, float f0, float f1) {
+    uint64_t a, v, f;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(f) : "f"(f0), "f"(f1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(f));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+
+__device__ __forceinline__ float get(const float* c) { return *c; }
+template <typename T> __device__ __forceinline__ float get(const T* c) { return to_float(*c); }
+__device__ __forceinline__ void put(float* c, float v) { *c = v; }
+template <typename T> __device__ __forceinline__ void put(T* c, float v) { *c = from_float<T>(v); }
+// 16 bytes of a row.
+__device__ __forceinline__ void put_vector(float* c, const float* v, float alpha) {
+    *reinterpret_cast<float4*>(c) = make_float4(alpha * v[0], alpha * v[1], alpha * v[2], alpha * v[3]);
+}
+template <typename T> __device__ __forceinline__ void put_vector(T* c, const float* v, float alpha) {
+    *reinterpret_cast<uint4*>(c) = make_uint4(pack2<T>(alpha * v[0], alpha * v[1]), pack2<T>(alpha * v[2], alpha * v[3]),
+                                              pack2<T>(alpha * v[4], alpha * v[5]), pack2<T>(alpha * v[6], alpha * v[7]));
+}
+
+// Sums v of the columns y .. y + n - 1 of row x go out.
+template <typename T, int n>
+__device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, int64_t y, const float (&v)[n]) {
+    if (x >= p.rows) return;
+    T* c = static_cast<T*>(p.C) + b * p.cb + x * p.cx + y * p.cy;
+    constexpr int w = 16 / sizeof(T);
+    if constexpr (n % w == 0) {
+        if (p.vec) {                 // unit stride along the columns, whole vectors
+#pragma unroll
+            for (int i = 0; i < n; i += w)
+                if (y + i < p.cols && dbg_in_bytes(c + i, 16, p.sc, &g_status)) put_vector(c + i, v + i, p.alpha);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i, c += p.cy)
+        if (y + i < p.cols && dbg_in_bytes(c, sizeof(T), p.sc, &g_status))
+            put(c, p.accumulate ? fmaf(p.alpha, v[i], get(c)) : p.alpha * v[i]);
+}
+template <int n>
+__device__ __forceinline__ void emit(const Params& p, int64_t b, int64_t x, int64_t y, const float (&v)[n]) {
+    if (p.type_c == SBGEMM_TYPE_BF16) emit_as<__nv_bfloat16>(p, b, x, y, v);
+    else if (p.type_c == SBGEMM_TYPE_FP16) emit_as<__half>(p, b, x, y, v);
+    else emit_as<float>(p, b, x, y, v);
+}
+
+__device__ __forceinline__ float load_scale(const float* at, const ByteSpan& span) {
+    return dbg_in_bytes(at, 4, span, &g_status) ? __ldg(at) : 0.0f;
+}
+
+// kYScales: Y has a scale for each of its rows (the tile's columns), else one
+// for each 128 of them, which a half of the tile's columns lies in.
+template <int NT, bool kYScales, bool kPair>
+__global__ void __launch_bounds__(kThreads, Shape<NT, kPair>::kCtas)
+fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+              const __grid_constant__ Params p) {
+    using S = Shape<NT, kPair>;
+    constexpr int kCtas = kPair ? 2 : 1;
+    constexpr int CPG = NT / kGroups;            // columns of a group
+    const int rank = kPair || p.split > 1 ? (int)cluster_rank() : 0;
+    const int pair_rank = kPair ? rank : 0, k_rank = kPair ? 0 : rank;
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_free[2], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? CPG : 4];
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 4 * kGroups * kCtas);
+        }
+        mbar_init(&done, 1);
+        fence_mbar_init_cluster();
+        prefetch_tensormap(&tx);
+        prefetch_tensormap(&ty);
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (kPair) {
+            tmem_alloc_pair(&tmem_base, S::kCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&tmem_base, S::kCols);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // A cluster's barriers, TMEM and shared memory are there before another CTA uses them.
+    if (kPair || p.split > 1) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = S::kCols == kTmemAll ? kTmemBase : tmem_base;
+    const int share = kPair ? 2 : p.split;       // CTAs a tile
+    const int64_t first = blockIdx.x / share, stride = gridDim.x / share;
+    const int j0 = (int)((int64_t)k_rank * p.k_blocks / p.split), j1 = (int)((int64_t)(k_rank + 1) * p.k_blocks / p.split);
+    auto place = [&](int64_t t, int64_t* x0, int64_t* y0, int* b) {
+        *x0 = t % p.x_tiles * (BX * kCtas) + BX * pair_rank;
+        *y0 = t / p.x_tiles % p.y_tiles * NT;
+        *b = (int)(t / p.x_tiles / p.y_tiles);
+    };
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            auto load = [&](void* dst, const CUtensorMap* map, int s, int c0, int c1, int c2) {
+                if constexpr (kPair) tma_load_3d_pair(dst, map, cluster_addr(&full[s], 0), c0, c1, c2);
+                else tma_load_3d(dst, map, &full[s], c0, c1, c2);
+            };
+            int s = 0, issued = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            for (int64_t t = first; t < p.tiles && ok; t += stride) {
+                int64_t x0, y0;
+                int b;
+                place(t, &x0, &y0, &b);
+                const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
+                for (int j = j0; j < j1; ++j) {
+                    if (round > 0 && !bar_wait(&empty[s], (round - 1) & 1)) {
+                        record_status(&g_status, kWaitEmpty);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* x = ring + s * S::kStage;
+                    if (pair_rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * kCtas);
+                    load(x, &tx, s, j * BK, (int)x0, zx);
+                    load(x + BX * BK, &ty, s, j * BK, (int)y0 + S::kYRows * pair_rank, zy);
+                    if (issued < S::kStages) ++issued;
+                    if (++s == S::kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            // Copies still landing keep the CTA's shared memory (a pair's first
+            // CTA waits for both).
+            for (int q = 0; pair_rank == 0 && q < issued; ++q) {
+                if (--s < 0) {
+                    s = S::kStages - 1;
+                    --round;
+                }
+                if (!bar_wait(&full[s], round & 1)) {
+                    record_status(&g_status, kWaitDrain);
+                    break;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (pair_rank == 0 && elect_one()) {
+            int s = 0, n = 0;                      // stage; blocks begun
+            uint32_t round = 0;
+            bool ok = true;
+            for (int64_t t = first; t < p.tiles && ok; t += stride) {
+                for (int j = j0; j < j1; ++j, ++n) {
+                    if (n >= 2) {
+                        const uint32_t ph = (uint32_t)((n / 2 - 1) & 1);
+                        if (!(kPair ? mbar_wait_cluster(&acc_free[n & 1], ph) : bar_wait(&acc_free[n & 1], ph))) {
+                            record_status(&g_status, kWaitAccFree);
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!bar_wait(&full[s], round & 1)) {
+                        record_status(&g_status, kWaitFull);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + (uint32_t)(n & 1) * NT;
+                    const uint32_t x = smem_u32(ring + s * S::kStage);
+                    uint64_t dx = desc16(x), dy = desc16(x + BX * BK);
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k) {      // 32 bytes of K a step
+                        mma8<kPair>(acc, dx, dy, p.idesc, k ? 1u : 0u);
+                        dx += kStepK;
+                        dy += kStepK;
+                    }
+                    if constexpr (kPair) {
+                        mma_commit_pair_both(&empty[s]);
+                        mma_commit_pair_both(&acc_full[n & 1]);
+                    } else {
+                        mma_commit(&empty[s]);
+                        mma_commit(&acc_full[n & 1]);
+                    }
+                    if (++s == S::kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            // Nothing may still be writing TMEM when it is freed.
+            if constexpr (kPair) mma_commit_pair_local(&done);
+            else mma_commit(&done);
+            if (!bar_wait(&done, 0)) record_status(&g_status, kWaitMma);
+        }
+        __syncwarp();
+    }
+    // (Sums of a split tile's threads, kept over the cluster's barriers below.)
+    float acc[CPG];
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    int64_t x = 0, y = 0;
+    int b = 0;
+    if (warp < kTmaWarp) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        int n = 0;
+        bool ok = true;
+        for (int64_t t = first; t < p.tiles; t += stride) {
+            int64_t x0, y0;
+            place(t, &x0, &y0, &b);
+            x = x0 + row;
+            y = y0 + g * CPG;
+            // This thread's scales: its row's, and the columns' common one or, to
+            // be shared, one column's.  Rows past the end take the last one's.
+            const float* sx = p.sx.at + b * p.sx.bs + min(x, p.sx.rows - 1) / p.sx.group * p.sx.rs;
+            const float* sy = p.sy.at + b * p.sy.bs +
+                              (kYScales ? min(y + min(row, CPG - 1), p.sy.rows - 1)
+                                        : min(y, p.sy.rows - 1) / p.sy.group) * p.sy.rs;
+            float fx = 0.0f, fy = 0.0f;
+            if (j0 < j1) {
+                fx = load_scale(sx + j0 * p.sx.ks, p.sx.span);
+                fy = load_scale(sy + j0 * p.sy.ks, p.sy.span);
+            }
+#pragma unroll
+            for (int i = 0; i < CPG; ++i) acc[i] = 0.0f;
+            for (int j = j0; j < j1; ++j, ++n) {
+                const float f = kYScales ? fx : fx * fy;
+                if constexpr (kYScales)
+                    if (row < CPG) ys[g][n & 1][row] = fy;
+                if (j + 1 < j1) {
+                    fx = load_scale(sx + (j + 1) * p.sx.ks, p.sx.span);
+                    fy = load_scale(sy + (j + 1) * p.sy.ks, p.sy.span);
+                }
+                if (ok && !bar_wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1))) {
+                    record_status(&g_status, kWaitMma);
+                    ok = false;
+                }
+                // (The columns' scales meet at a barrier: all go on or none.)
+                if constexpr (kYScales) ok = all_of_group(g, ok);
+                if (!ok) break;
+                tc_fence_after();
+                constexpr int W = CPG < 32 ? CPG : CPG < 128 ? 32 : 16;   // (registers: 128 sums)
+#pragma unroll
+                for (int c = 0; c < CPG; c += W) {
+                    float v[W];
+                    tmem_ld<W>(tmem + lanes + (uint32_t)((n & 1) * NT + g * CPG + c), v);
+                    if constexpr (kYScales) {
+#pragma unroll
+                        for (int i = 0; i < W; i += 4) {
+                            const float4 s = *reinterpret_cast<const float4*>(&ys[g][n & 1][c + i]);
+                            fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f * s.x, f * s.y);
+                            fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f * s.z, f * s.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < W; i += 2)
+                            fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f, f);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair && pair_rank != 0) mbar_arrive_remote(&acc_free[n & 1], 0);
+                    else mbar_arrive(&acc_free[n & 1]);
+                }
+            }
+            if (!ok) break;
+            if (kPair || p.split == 1) emit<CPG>(p, b, x, y, acc);
+        }
+    }
+    if constexpr (!kPair) {
+        if (p.split > 1) {
+            // One tile a cluster.  Every CTA's ring is idle once all are here.
+            __syncwarp();
+            cluster_sync();
+            const int each = NT / p.split;       // columns this CTA adds up
+            if (warp < kTmaWarp) {
+#pragma unroll
+                for (int i = 0; i < CPG; ++i) {
+                    const int c = g * CPG + i, to = c / each;
+                    st_cluster(cluster_addr(ring, to) + (uint32_t)(((k_rank * each + c - to * each) * BX + row) * 4), acc[i]);
+                }
+            }
+            cluster_sync();
+            if (warp < kTmaWarp) {
+                const float* sums = reinterpret_cast<const float*>(ring);
+                const int64_t y0 = y - g * CPG;
+                for (int c = g; c < each; c += kGroups) {
+                    float v[1] = {0.0f};
+                    for (int r = 0; r < p.split; ++r) v[0] += sums[(r * each + c) * BX + row];
+                    emit<1>(p, b, x, y0 + k_rank * each + c, v);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // Neither CTA of a pair leaves while the other may use its memory.
+    if constexpr (kPair) cluster_sync();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        if constexpr (kPair) tmem_dealloc_pair(tmem, S::kCols);
+        else tmem_dealloc(tmem, S::kCols);
+    }
+}
+
+bool mappable(const Fp8Operand& o, int64_t K, int64_t batch) {
+    if (o.ks != 1 && K > 1) return false;
+    if (reinterpret_cast<uintptr_t>(o.data) % 16 != 0) return false;
+    auto ok = [](int64_t s) { return s > 0 && s % 16 == 0 && s < ((int64_t)1 << 39); };
+    if (o.rows > 1 && !ok(o.rs)) return false;
+    return batch == 1 || o.bs == 0 || ok(o.bs);
+}
+
+bool make_map(CUtensorMap* map, const Fp8Operand& o, int64_t K, int64_t batch, uint32_t box_rows) {
+    const bool moves = batch > 1 && o.bs != 0;
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)o.rows, moves ? (uint64_t)batch : 1};
+    const uint64_t rs = o.rows > 1 ? (uint64_t)o.rs : (uint64_t)(K + 15) / 16 * 16;
+    const uint64_t strides[2] = {rs, moves ? (uint64_t)o.bs : rs};
+    const uint32_t box[3] = {BK, box_rows, 1};
+    return encode_tmap_8(map, o.data, 3, dims, strides, box);
+}
+
+Scales scales_of(const Fp8Operand& o) {
+    return Scales{o.scale, o.rsS, o.ksS, o.bsS, o.rows, o.group, o.ss};
+}
+
+template <int NT, bool kYScales, bool kPair>
+cudaError_t launch(const Params& p, const CUtensorMap& tx, const CUtensorMap& ty, int sms, cudaStream_t stream) {
+    using S = Shape<NT, kPair>;
+    static std::atomic<int> ready[64];           // 0: not asked yet; else the pairs that fit (or 1)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int size = kPair ? 2 : p.split;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)size;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = size > 1 ? 1 : 0;
+    int fit = ready[dev & 63].load();
+    if (fit == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(fp8_tc_kernel<NT, kYScales, kPair>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        fit = 1;
+        if (kPair) {
+            cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+            if (cudaOccupancyMaxActiveClusters(&fit, fp8_tc_kernel<NT, kYScales, kPair>, &cfg) != cudaSuccess ||
+                fit <= 0) {
+                cudaGetLastError();
+                fit = sms / 2;
+            }
+        }
+        ready[dev & 63].store(fit);
+    }
+    // A split tile is its cluster's only one; others go round the CTAs (or pairs) that are resident.
+    const int64_t at_once = p.split > 1 ? p.tiles : kPair ? fit : (int64_t)sms * S::kCtas;
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(p.tiles, at_once) * size));
+    return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<NT, kYScales, kPair>, tx, ty, p);
+}
+
+template <bool kYScales>
+cudaError_t launch_nt(int nt, bool pair, const Params& p, const CUtensorMap& tx, const CUtensorMap& ty, int sms,
+                      cudaStream_t stream) {
+    if (pair) return launch<256, kYScales, true>(p, tx, ty, sms, stream);
+    switch (nt) {
+        case 16: return launch<16, kYScales, false>(p, tx, ty, sms, stream);
+        case 32: return launch<32, kYScales, false>(p, tx, ty, sms, stream);
+        case 64: return launch<64, kYScales, false>(p, tx, ty, sms, stream);
+        case 128: return launch<128, kYScales, false>(p, tx, ty, sms, stream);
+        default: return launch<256, kYScales, false>(p, tx, ty, sms, stream);
+    }
+}
+
+// Cycles of a block of K in a tile: its bytes through shared memory, in and
+// out, at 128 a cycle, or the MMAs.
+int block_cycles(int nt, bool pair) { return pair ? 540 : 2 * (BX + nt); }
+
+}  // namespace
+
+bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_t* err) {
+    if (p.K <= 0 || !mappable(p.a, p.K, p.batch) || !mappable(p.b, p.K, p.batch)) return false;
+    const int k_blocks = (int)((p.K + BK - 1) / BK);
+    // Orientation, columns of a tile, pairs, and the split of K: the fewest
+    // cycles, by the blocks of K that an SM goes through and 2500 cycles for a
+    // tile's start and end, 1500 for joining a split one.
+    double best = 0;
+    int nt = 0;
+    bool swapped = false, pair = false;
+    Params q{};
+    for (int s = 0; s < 2; ++s)
+        for (int n : {16, 32, 64, 128, 256, 512}) {
+            const bool two = n == 512;
+            const int64_t bx = two ? 2 * BX : BX, by = two ? 256 : n;
+            const int64_t xs = ((s ? p.b.rows : p.a.rows) + bx - 1) / bx, ys = ((s ? p.a.rows : p.b.rows) + by - 1) / by;
+            if ((double)xs * (double)ys * (double)p.batch > 1e9) continue;
+            const int64_t tiles = xs * ys * p.batch, per_sm = n <= 64 ? 2 : 1;
+            const int64_t slots = two ? sms / 2 : sms * per_sm;
+            for (int split : {1, 2, 4, 8}) {
+                if (split > 1 && (two || tiles * split > slots || split > k_blocks || by / split < 2)) break;
+                const int64_t waves = (tiles * split + slots - 1) / slots;
+                const double busy = per_sm == 2 && tiles * split > sms ? 2 : 1;
+                const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two) * busy +
+                                             2500 + (split > 1 ? 1500 : 0));
+                if (nt == 0 || cost < best) {
+                    best = cost;
+                    nt = (int)by;
+                    pair = two;
+                    swapped = s != 0;
+                    q.x_tiles = xs;
+                    q.y_tiles = ys;
+                    q.tiles = tiles;
+                    q.split = split;
+                }
+            }
+        }
+    if (nt == 0) return false;
+    const Fp8Operand& ox = swapped ? p.b : p.a;
+    const Fp8Operand& oy = swapped ? p.a : p.b;
+    CUtensorMap tx, ty;
+    if (!make_map(&tx, ox, p.K, p.batch, BX) || !make_map(&ty, oy, p.K, p.batch, (uint32_t)(pair ? nt / 2 : nt))) {
+        *err = cudaErrorInvalidValue;
+        return true;
+    }
+    q.C = p.C;
+    q.cx = swapped ? p.csC : p.rsC;
+    q.cy = swapped ? p.rsC : p.csC;
+    q.cb = p.bsC;
+    q.type_c = p.type_c;
+    q.rows = ox.rows;
+    q.cols = oy.rows;
+    q.k_blocks = k_blocks;
+    q.alpha = p.alpha;
+    q.accumulate = p.accumulate;
+    const int64_t w = p.type_c == SBGEMM_TYPE_FP32 ? 4 : 8;
+    q.vec = !p.accumulate && q.cy == 1 && q.cols % w == 0 && (q.rows == 1 || q.cx % w == 0) &&
+            (p.batch == 1 || q.cb % w == 0) && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    q.x_batch = p.batch > 1 && ox.bs != 0;
+    q.y_batch = p.batch > 1 && oy.bs != 0;
+    q.idesc = idesc8(ox.type == SBGEMM_TYPE_E5M2, oy.type == SBGEMM_TYPE_E5M2, nt, pair ? 256 : 128);
+    q.sx = scales_of(ox);
+    q.sy = scales_of(oy);
+    q.sc = p.sc;
+    *err = oy.group == 1 ? launch_nt<true>(nt, pair, q, tx, ty, sms, stream)
+                         : launch_nt<false>(nt, pair, q, tx, ty, sms, stream);
+    return true;
+}
+
+unsigned int* status_word_fp8_tc() { return word_address(&g_status); }
+
+}  // namespace sbg

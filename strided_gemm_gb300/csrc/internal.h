@@ -196,6 +196,7 @@ unsigned int* status_word_latent_rows();
 unsigned int* status_word_pages();
 unsigned int* status_word_latent_shared();
 unsigned int* status_word_fp8_gather();
+unsigned int* status_word_fp8_tc();
 unsigned int* status_word_fp8_quantize();
 unsigned int* status_word_norm_rope();
 // Clears all of them behind the work on `stream` and waits for it; *code
@@ -219,5 +220,8 @@ bool encode_tmap_f32_4d(CUtensorMap* map, const void* base, const uint64_t dims[
 // 128-byte swizzled boxes.
 bool encode_tmap_16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
+// The same with 8-bit elements.
+bool encode_tmap_8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace sbg

@@ -29,7 +29,10 @@ struct Fp8Problem {
     ByteSpan sc;                     // debug builds: what C occupies
 };
 constexpr int kScaleBlock = 128;     // elements of K a scale covers
+// Any layout, on the CUDA cores (fp8_gather.cu).
 cudaError_t launch_fp8_gather(const Fp8Problem& p, cudaStream_t stream);
+// On the tensor cores (fp8_tc.cu); false if the layout has no tensor maps.
+bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_t* err);
 
 // Quantisation (fp8_quantize.cu): X [batch][M][K] into an operand of M rows.
 struct QuantizeProblem {

@@ -148,6 +148,8 @@ int sbgemm_fp8(const sbgemm_fp8_matrix* A, const sbgemm_fp8_matrix* B, int type_
     p.alpha = alpha;
     p.accumulate = accumulate;
     p.sc = span_for_kernel(sc);
+    cudaError_t e = cudaSuccess;
+    if (launch_fp8_tc(p, sms, static_cast<cudaStream_t>(stream), &e)) return finish(e);
     return finish(launch_fp8_gather(p, static_cast<cudaStream_t>(stream)));
 }
 

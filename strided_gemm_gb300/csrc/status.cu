@@ -9,7 +9,7 @@
 namespace sbg {
 namespace {
 
-constexpr int kWords = 19;
+constexpr int kWords = 20;
 struct Words { unsigned int* at[kWords]; };
 __device__ unsigned int g_first;             // of the last launch
 
@@ -31,7 +31,7 @@ bool take_status_words(cudaStream_t stream, unsigned int* code) {
                    status_word_tf32(), status_word_selftest(), status_word_attention_tc(), status_word_gather(),
                    status_word_attention(), status_word_attention_decode(), status_word_half_gather(), status_word_half_tc(),
                    status_word_latent_decode(), status_word_latent_prompt(), status_word_latent_rows(),
-                   status_word_pages(), status_word_latent_shared(), status_word_fp8_gather(),
+                   status_word_pages(), status_word_latent_shared(), status_word_fp8_gather(), status_word_fp8_tc(),
                    status_word_fp8_quantize(), status_word_norm_rope()}};
     for (const unsigned int* at : w.at)
         if (!at) return false;
