@@ -32,7 +32,7 @@ namespace {
 
 constexpr int BX = 128, BK = kScaleBlock;
 constexpr int kGroups = 2, kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = 4 * (kGroups + 1) * 32;      // whole warpgroups: registers move between them
 __device__ unsigned int g_status = 0;
 
 // Scales of one operand.
@@ -62,6 +62,7 @@ struct Shape {
     static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kYRows == 256 ? 4 : 6;
     static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr uint32_t kCols = NT >= 256 ? 512 : NT >= 128 ? 256 : NT >= 64 ? 128 : NT >= 32 ? 64 : 32;
+    static_assert(NT > 128 || 2 * NT * BX * 4 <= kStages * kStage, "a split tile's sums, here and from the cluster");
     static_assert(kSmem * kCtas <= 232448 - 2048 * kCtas, "shared memory");
 };
 
@@ -99,15 +100,18 @@ __device__ __forceinline__ bool all_of_group(int g, bool v) {
     return r != 0;
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Shared memory of this CTA to that of a CTA of the cluster (shared::cluster
+// addresses of the destination and of its barrier).
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
-// acc += v * f on pairs.
-__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, float f0, float f1) {
+// acc += v * f on pairs; v: bits of floats.
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float f0, float f1) {
     uint64_t a, v, f;
     asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
     asm("mov.b64 %0, {%1, %2};" : "=l"(f) : "f"(f0), "f"(f1));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(f));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
@@ -169,7 +173,10 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     const int pair_rank = kPair ? rank : 0, k_rank = kPair ? 0 : rank;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_free[2], done;
+    // mma_done: a stage's MMAs are through, for the TMA warp that fills it again and
+    // for the epilogue that reads their sums (one commit a block: a second one
+    // behind it holds the issuing thread for some 360 cycles).
+    __shared__ uint64_t full[S::kStages], mma_done[S::kStages], acc_free[2], sums_full;
     __shared__ uint32_t tmem_base;
     __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? CPG : 4];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -177,13 +184,10 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&mma_done[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], 4 * kGroups * kCtas);
-        }
-        mbar_init(&done, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_free[i], 4 * kGroups * kCtas);
+        mbar_init(&sums_full, 1);
         fence_mbar_init_cluster();
         prefetch_tensormap(&tx);
         prefetch_tensormap(&ty);
@@ -212,6 +216,14 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
         *b = (int)(t / p.x_tiles / p.y_tiles);
     };
 
+    // (Sums of a split tile's threads, kept over the cluster's barriers below.)
+    float acc[CPG];
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    int64_t x = 0, y = 0;
+    int b = 0;
+    // 256 x 216 + 128 x 64 registers are within the 384 x 168 of the launch.
+    if (warp >= kTmaWarp) {
+    if constexpr (CPG == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kTmaWarp) {
         if (lane == 0) {
             auto load = [&](void* dst, const CUtensorMap* map, int s, int c0, int c1, int c2) {
@@ -227,7 +239,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 place(t, &x0, &y0, &b);
                 const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
                 for (int j = j0; j < j1; ++j) {
-                    if (round > 0 && !bar_wait(&empty[s], (round - 1) & 1)) {
+                    if (round > 0 && !bar_wait(&mma_done[s], (round - 1) & 1)) {
                         record_status(&g_status, kWaitEmpty);
                         ok = false;
                         break;
@@ -259,14 +271,14 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (pair_rank == 0 && elect_one()) {
-            int s = 0, n = 0;                      // stage; blocks begun
-            uint32_t round = 0;
+            int s = 0, n = 0, last = -1;           // stage; blocks begun; the last one's stage
+            uint32_t round = 0, last_round = 0;
             bool ok = true;
             for (int64_t t = first; t < p.tiles && ok; t += stride) {
                 for (int j = j0; j < j1; ++j, ++n) {
                     if (n >= 2) {
                         const uint32_t ph = (uint32_t)((n / 2 - 1) & 1);
-                        if (!(kPair ? mbar_wait_cluster(&acc_free[n & 1], ph) : bar_wait(&acc_free[n & 1], ph))) {
+                        if (!(kPair ? bar_wait_cluster(&acc_free[n & 1], ph) : bar_wait(&acc_free[n & 1], ph))) {
                             record_status(&g_status, kWaitAccFree);
                             ok = false;
                             break;
@@ -287,13 +299,10 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                         dx += kStepK;
                         dy += kStepK;
                     }
-                    if constexpr (kPair) {
-                        mma_commit_pair_both(&empty[s]);
-                        mma_commit_pair_both(&acc_full[n & 1]);
-                    } else {
-                        mma_commit(&empty[s]);
-                        mma_commit(&acc_full[n & 1]);
-                    }
+                    if constexpr (kPair) mma_commit_pair_both(&mma_done[s]);
+                    else mma_commit(&mma_done[s]);
+                    last = s;
+                    last_round = round;
                     if (++s == S::kStages) {
                         s = 0;
                         ++round;
@@ -301,20 +310,15 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 }
             }
             // Nothing may still be writing TMEM when it is freed.
-            if constexpr (kPair) mma_commit_pair_local(&done);
-            else mma_commit(&done);
-            if (!bar_wait(&done, 0)) record_status(&g_status, kWaitMma);
+            if (last >= 0 && !bar_wait(&mma_done[last], last_round & 1)) record_status(&g_status, kWaitMma);
         }
         __syncwarp();
     }
-    // (Sums of a split tile's threads, kept over the cluster's barriers below.)
-    float acc[CPG];
-    const int g = warp >> 2, row = threadIdx.x & 127;
-    int64_t x = 0, y = 0;
-    int b = 0;
-    if (warp < kTmaWarp) {
+    } else {
+        if constexpr (CPG == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        int n = 0;
+        int n = 0, s = 0;
+        uint32_t round = 0;
         bool ok = true;
         for (int64_t t = first; t < p.tiles; t += stride) {
             int64_t x0, y0;
@@ -342,66 +346,94 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                     fx = load_scale(sx + (j + 1) * p.sx.ks, p.sx.span);
                     fy = load_scale(sy + (j + 1) * p.sy.ks, p.sy.span);
                 }
-                if (ok && !bar_wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1))) {
+                if (ok && !bar_wait(&mma_done[s], round & 1)) {
                     record_status(&g_status, kWaitMma);
                     ok = false;
+                }
+                if (++s == S::kStages) {
+                    s = 0;
+                    ++round;
                 }
                 // (The columns' scales meet at a barrier: all go on or none.)
                 if constexpr (kYScales) ok = all_of_group(g, ok);
                 if (!ok) break;
                 tc_fence_after();
-                constexpr int W = CPG < 32 ? CPG : CPG < 128 ? 32 : 16;   // (registers: 128 sums)
+                // The accumulator in pieces, the next one on its way under a piece's sums.
+                constexpr int W = CPG <= 32 ? (CPG < 16 ? CPG : 16) : 32;      // (registers: two CTAs an SM to 64 columns)
+                uint32_t v[2][W];
+                const uint32_t at = tmem + lanes + (uint32_t)((n & 1) * NT + g * CPG);
+                tmem_ld_begin<W>(at, v[0]);
 #pragma unroll
                 for (int c = 0; c < CPG; c += W) {
-                    float v[W];
-                    tmem_ld<W>(tmem + lanes + (uint32_t)((n & 1) * NT + g * CPG + c), v);
+                    uint32_t (&now)[W] = v[c / W & 1];
+                    tmem_ld_end<W>(now);
+                    if (c + W < CPG) {
+                        tmem_ld_begin<W>(at + c + W, v[(c / W + 1) & 1]);
+                    } else {
+                        // The accumulator is read: the next block's MMAs may have it.
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (kPair && pair_rank != 0) mbar_arrive_remote_relaxed(&acc_free[n & 1], 0);
+                            else mbar_arrive(&acc_free[n & 1]);
+                        }
+                    }
                     if constexpr (kYScales) {
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
-                            const float4 s = *reinterpret_cast<const float4*>(&ys[g][n & 1][c + i]);
-                            fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f * s.x, f * s.y);
-                            fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f * s.z, f * s.w);
+                            const float4 z = *reinterpret_cast<const float4*>(&ys[g][n & 1][c + i]);
+                            fma2(acc[c + i], acc[c + i + 1], now[i], now[i + 1], f * z.x, f * z.y);
+                            fma2(acc[c + i + 2], acc[c + i + 3], now[i + 2], now[i + 3], f * z.z, f * z.w);
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < W; i += 2)
-                            fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f, f);
+                            fma2(acc[c + i], acc[c + i + 1], now[i], now[i + 1], f, f);
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair && pair_rank != 0) mbar_arrive_remote(&acc_free[n & 1], 0);
-                    else mbar_arrive(&acc_free[n & 1]);
                 }
             }
             if (!ok) break;
             if (kPair || p.split == 1) emit<CPG>(p, b, x, y, acc);
         }
     }
-    if constexpr (!kPair) {
+    if constexpr (!kPair && NT <= 128) {
         if (p.split > 1) {
-            // One tile a cluster.  Every CTA's ring is idle once all are here.
-            __syncwarp();
-            cluster_sync();
+            // One tile a cluster.  This CTA's ring is idle: its sums go there, column
+            // by column, and once every CTA's is, each one's share of the columns
+            // to it by a bulk copy, all CTAs' behind one another.
             const int each = NT / p.split;       // columns this CTA adds up
+            uint8_t* mine = ring;
+            uint8_t* theirs = ring + NT * BX * 4;
+            __syncwarp();
             if (warp < kTmaWarp) {
 #pragma unroll
-                for (int i = 0; i < CPG; ++i) {
-                    const int c = g * CPG + i, to = c / each;
-                    st_cluster(cluster_addr(ring, to) + (uint32_t)(((k_rank * each + c - to * each) * BX + row) * 4), acc[i]);
-                }
+                for (int i = 0; i < CPG; ++i)
+                    reinterpret_cast<float*>(mine)[(g * CPG + i) * BX + row] = acc[i];
+                fence_proxy_async_smem();
             }
+            __syncthreads();
             cluster_sync();
+            const uint32_t bytes = (uint32_t)(each * BX * 4);
+            if (threadIdx.x == 0) {
+                mbar_arrive_expect_tx(&sums_full, bytes * p.split);
+                for (int r = 0; r < p.split; ++r)
+                    bulk_copy_to_cta(cluster_addr(theirs + k_rank * bytes, r), mine + r * bytes, bytes,
+                                     cluster_addr(&sums_full, r));
+            }
             if (warp < kTmaWarp) {
-                const float* sums = reinterpret_cast<const float*>(ring);
+                const bool in = bar_wait(&sums_full, 0);
+                if (!in) record_status(&g_status, kWaitPartial);
+                const float* sums = reinterpret_cast<const float*>(theirs);
                 const int64_t y0 = y - g * CPG;
-                for (int c = g; c < each; c += kGroups) {
+                for (int c = g; in && c < each; c += kGroups) {
                     float v[1] = {0.0f};
                     for (int r = 0; r < p.split; ++r) v[0] += sums[(r * each + c) * BX + row];
                     emit<1>(p, b, x, y0 + k_rank * each + c, v);
                 }
             }
+            // Nobody leaves while a copy may still read its memory.
+            __syncwarp();
+            cluster_sync();
         }
     }
     tc_fence_before();
@@ -513,7 +545,7 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
             const int64_t tiles = xs * ys * p.batch, per_sm = n <= 64 ? 2 : 1;
             const int64_t slots = two ? sms / 2 : sms * per_sm;
             for (int split : {1, 2, 4, 8}) {
-                if (split > 1 && (two || tiles * split > slots || split > k_blocks || by / split < 2)) break;
+                if (split > 1 && (n > 128 || tiles * split > slots || split > k_blocks || by / split < 2)) break;
                 const int64_t waves = (tiles * split + slots - 1) / slots;
                 const double busy = per_sm == 2 && tiles * split > sms ? 2 : 1;
                 const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two) * busy +
