@@ -60,6 +60,7 @@ struct Element {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constant__ QuantizeProblem p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Element<T> x{p, p.type_y == SBGEMM_TYPE_E4M3};
     const int lane = threadIdx.x & 31;
     const int64_t kb = (p.K + kScaleBlock - 1) / kScaleBlock, items = p.batch * p.M * kb;
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
 template <typename T>
 __global__ void __launch_bounds__(kThreads) blocks_any_kernel(const __grid_constant__ QuantizeProblem p) {
     __shared__ float tops[kThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Element<T> x{p, p.type_y == SBGEMM_TYPE_E4M3};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t kb = (p.K + kScaleBlock - 1) / kScaleBlock, mb = (p.M + 127) / 128;

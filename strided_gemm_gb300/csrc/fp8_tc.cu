@@ -33,6 +33,10 @@ namespace {
 constexpr int BX = 128, BK = kScaleBlock;
 constexpr int kGroups = 2, kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1;
 constexpr int kThreads = 4 * (kGroups + 1) * 32;      // whole warpgroups: registers move between them
+// Named barriers: 0 the CTA, 1 and 2 the epilogue groups, 3 the start, of its own
+// since the TMA warp, which only arrives there, may come to the CTA's next one
+// before the others have passed it.
+constexpr int kStartBarrier = 3;
 __device__ unsigned int g_status = 0;
 
 // Scales of one operand.
@@ -47,23 +51,28 @@ struct Params {
     float alpha;
     int accumulate;
     int vec;                       // columns go out as 16-byte vectors
+    int c_tma;                     // C goes out through its tensor map
     int x_batch, y_batch;          // the batch coordinate moves (else shared)
     uint32_t idesc;
     Scales sx, sy;
     ByteSpan sc;                   // debug builds: what C occupies
 };
 
-template <int NT, bool kPair>
+template <int NT, bool kYScales, bool kPair>
 struct Shape {
     static constexpr int kYRows = kPair ? NT / 2 : NT;              // this CTA's share of Y
     static constexpr int kStage = (BX + kYRows) * BK;
     // Two CTAs an SM for up to 64 columns: the weights' bytes want to be in flight.
     static constexpr int kCtas = NT <= 64 ? 2 : 1;
-    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kYRows == 256 ? 4 : 6;
-    static constexpr int kSmem = kStages * kStage + 1024;
-    static constexpr uint32_t kCols = NT >= 256 ? 512 : NT >= 128 ? 256 : NT >= 64 ? 128 : NT >= 32 ? 64 : 32;
+    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kPair && kYScales ? 5 : 6;
+    // Accumulators in TMEM: few columns are read long after their MMAs were quick.
+    static constexpr int kAccs = NT <= 64 ? 4 : 2;
+    static constexpr uint32_t kCols = kAccs * NT;
+    // Buffers of the way out, [128 rows][128 bytes] for each group.
+    static constexpr int kOut = NT >= 128 ? kGroups * BX * 128 : 0;
+    static constexpr int kSmem = kStages * kStage + kOut + 1024;
     static_assert(NT > 128 || 2 * NT * BX * 4 <= kStages * kStage, "a split tile's sums, here and from the cluster");
-    static_assert(kSmem * kCtas <= 232448 - 2048 * kCtas, "shared memory");
+    static_assert((kSmem + (kYScales ? 8 * NT : 0) + 512) * kCtas <= 232448, "shared memory");
 };
 
 // kind::f8f6f4, D fp32, both operands K-major.
@@ -90,7 +99,8 @@ __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_
             : "memory");
 }
 
-// A vote and barrier of the four warps of an epilogue group.
+// Barriers of the four warps of an epilogue group.
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ bool all_of_group(int g, bool v) {
     uint32_t r;
     asm volatile(
@@ -107,32 +117,46 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
                  ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
-// acc += v * f on pairs; v: bits of floats.
-__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float f0, float f1) {
-    uint64_t a, v, f;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(f) : "f"(f0), "f"(f1));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(f));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+// Pairs of floats in a 64-bit register, as fma.rn.f32x2 takes them.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) { return pair_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t f) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float lower(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float upper(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 __device__ __forceinline__ float get(const float* c) { return *c; }
 template <typename T> __device__ __forceinline__ float get(const T* c) { return to_float(*c); }
 __device__ __forceinline__ void put(float* c, float v) { *c = v; }
 template <typename T> __device__ __forceinline__ void put(T* c, float v) { *c = from_float<T>(v); }
 // 16 bytes of a row.
-__device__ __forceinline__ void put_vector(float* c, const float* v, float alpha) {
-    *reinterpret_cast<float4*>(c) = make_float4(alpha * v[0], alpha * v[1], alpha * v[2], alpha * v[3]);
+__device__ __forceinline__ void put_vector(float* c, const uint64_t* v, float alpha) {
+    *reinterpret_cast<float4*>(c) =
+        make_float4(alpha * lower(v[0]), alpha * upper(v[0]), alpha * lower(v[1]), alpha * upper(v[1]));
 }
-template <typename T> __device__ __forceinline__ void put_vector(T* c, const float* v, float alpha) {
-    *reinterpret_cast<uint4*>(c) = make_uint4(pack2<T>(alpha * v[0], alpha * v[1]), pack2<T>(alpha * v[2], alpha * v[3]),
-                                              pack2<T>(alpha * v[4], alpha * v[5]), pack2<T>(alpha * v[6], alpha * v[7]));
+template <typename T> __device__ __forceinline__ void put_vector(T* c, const uint64_t* v, float alpha) {
+    *reinterpret_cast<uint4*>(c) = make_uint4(
+        pack2<T>(alpha * lower(v[0]), alpha * upper(v[0])), pack2<T>(alpha * lower(v[1]), alpha * upper(v[1])),
+        pack2<T>(alpha * lower(v[2]), alpha * upper(v[2])), pack2<T>(alpha * lower(v[3]), alpha * upper(v[3])));
+}
+template <typename T>
+__device__ __forceinline__ void put_one(const Params& p, T* c, float v) {
+    if (dbg_in_bytes(c, sizeof(T), p.sc, &g_status)) put(c, p.accumulate ? fmaf(p.alpha, v, get(c)) : p.alpha * v);
 }
 
 // Sums v of the columns y .. y + n - 1 of row x go out.
 template <typename T, int n>
-__device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, int64_t y, const float (&v)[n]) {
+__device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, int64_t y, const uint64_t (&v)[n / 2]) {
     if (x >= p.rows) return;
     T* c = static_cast<T*>(p.C) + b * p.cb + x * p.cx + y * p.cy;
     constexpr int w = 16 / sizeof(T);
@@ -140,20 +164,59 @@ __device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, i
         if (p.vec) {                 // unit stride along the columns, whole vectors
 #pragma unroll
             for (int i = 0; i < n; i += w)
-                if (y + i < p.cols && dbg_in_bytes(c + i, 16, p.sc, &g_status)) put_vector(c + i, v + i, p.alpha);
+                if (y + i < p.cols && dbg_in_bytes(c + i, 16, p.sc, &g_status)) put_vector(c + i, v + i / 2, p.alpha);
             return;
         }
     }
 #pragma unroll
     for (int i = 0; i < n; ++i, c += p.cy)
-        if (y + i < p.cols && dbg_in_bytes(c, sizeof(T), p.sc, &g_status))
-            put(c, p.accumulate ? fmaf(p.alpha, v[i], get(c)) : p.alpha * v[i]);
+        if (y + i < p.cols) put_one(p, c, i & 1 ? upper(v[i / 2]) : lower(v[i / 2]));
+}
+// One sum.
+__device__ __forceinline__ void emit_one(const Params& p, int64_t b, int64_t x, int64_t y, float v) {
+    if (x >= p.rows || y >= p.cols) return;
+    const int64_t at = b * p.cb + x * p.cx + y * p.cy;
+    if (p.type_c == SBGEMM_TYPE_BF16) put_one(p, static_cast<__nv_bfloat16*>(p.C) + at, v);
+    else if (p.type_c == SBGEMM_TYPE_FP16) put_one(p, static_cast<__half*>(p.C) + at, v);
+    else put_one(p, static_cast<float*>(p.C) + at, v);
 }
 template <int n>
-__device__ __forceinline__ void emit(const Params& p, int64_t b, int64_t x, int64_t y, const float (&v)[n]) {
-    if (p.type_c == SBGEMM_TYPE_BF16) emit_as<__nv_bfloat16>(p, b, x, y, v);
-    else if (p.type_c == SBGEMM_TYPE_FP16) emit_as<__half>(p, b, x, y, v);
-    else emit_as<float>(p, b, x, y, v);
+__device__ __forceinline__ void emit(const Params& p, int64_t b, int64_t x, int64_t y, const uint64_t (&v)[n / 2]) {
+    if (p.type_c == SBGEMM_TYPE_BF16) emit_as<__nv_bfloat16, n>(p, b, x, y, v);
+    else if (p.type_c == SBGEMM_TYPE_FP16) emit_as<__half, n>(p, b, x, y, v);
+    else emit_as<float, n>(p, b, x, y, v);
+}
+
+// The same of all 128 rows of a group's columns through shared memory and C's
+// tensor map, in boxes of 128 bytes a row: a thread's own vectors would touch 32
+// rows an instruction, half a sector each.
+template <typename T, int n>
+__device__ __forceinline__ void send_as(const Params& p, const CUtensorMap& to, uint8_t* buf, int g, int row, int b, int x0,
+                                        int y, const uint64_t (&v)[n / 2]) {
+    constexpr int w = 16 / sizeof(T), box = 128 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < n; c += box) {
+        if (row == 0) bulk_wait_read_all();              // the buffer's last store has read it
+        group_sync(g);
+#pragma unroll
+        for (int i = 0; i < box; i += w)
+            put_vector(reinterpret_cast<T*>(buf + row * 128 + ((i / w * 16) ^ ((row & 7) << 4))), v + (c + i) / 2, p.alpha);
+        fence_proxy_async_smem();
+        group_sync(g);
+        if (row == 0) {
+            if (y + c < p.cols && x0 < p.rows) tma_store_3d(&to, buf, (y + c) * (int)sizeof(T), x0, b);
+            bulk_commit();
+        }
+    }
+}
+template <int n>
+__device__ __forceinline__ void send(const Params& p, const CUtensorMap& to, uint8_t* buf, int g, int row, int b, int x0,
+                                     int y, const uint64_t (&v)[n / 2]) {
+    if constexpr (n >= 64) {
+        if (p.type_c == SBGEMM_TYPE_BF16) send_as<__nv_bfloat16, n>(p, to, buf, g, row, b, x0, y, v);
+        else if (p.type_c == SBGEMM_TYPE_FP16) send_as<__half, n>(p, to, buf, g, row, b, x0, y, v);
+        else send_as<float, n>(p, to, buf, g, row, b, x0, y, v);
+    }
 }
 
 __device__ __forceinline__ float load_scale(const float* at, const ByteSpan& span) {
@@ -163,10 +226,10 @@ __device__ __forceinline__ float load_scale(const float* at, const ByteSpan& spa
 // kYScales: Y has a scale for each of its rows (the tile's columns), else one
 // for each 128 of them, which a half of the tile's columns lies in.
 template <int NT, bool kYScales, bool kPair>
-__global__ void __launch_bounds__(kThreads, Shape<NT, kPair>::kCtas)
+__global__ void __launch_bounds__(kThreads, Shape<NT, kYScales, kPair>::kCtas)
 fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
-              const __grid_constant__ Params p) {
-    using S = Shape<NT, kPair>;
+              const __grid_constant__ CUtensorMap to, const __grid_constant__ Params p) {
+    using S = Shape<NT, kYScales, kPair>;
     constexpr int kCtas = kPair ? 2 : 1;
     constexpr int CPG = NT / kGroups;            // columns of a group
     const int rank = kPair || p.split > 1 ? (int)cluster_rank() : 0;
@@ -176,21 +239,23 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     // mma_done: a stage's MMAs are through, for the TMA warp that fills it again and
     // for the epilogue that reads their sums (one commit a block: a second one
     // behind it holds the issuing thread for some 360 cycles).
-    __shared__ uint64_t full[S::kStages], mma_done[S::kStages], acc_free[2], sums_full;
+    __shared__ uint64_t full[S::kStages], mma_done[S::kStages], acc_free[S::kAccs], sums_full;
     __shared__ uint32_t tmem_base;
     __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? CPG : 4];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == kTmaWarp * 32) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&mma_done[s], 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&acc_free[i], 4 * kGroups * kCtas);
+        for (int i = 0; i < S::kAccs; ++i) mbar_init(&acc_free[i], 4 * kGroups * kCtas);
         mbar_init(&sums_full, 1);
         fence_mbar_init_cluster();
         prefetch_tensormap(&tx);
         prefetch_tensormap(&ty);
+        if (p.c_tma) prefetch_tensormap(&to);
     }
     if (warp == kMmaWarp) {
         if constexpr (kPair) {
@@ -201,12 +266,25 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             tmem_relinquish();
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    // A cluster's barriers, TMEM and shared memory are there before another CTA uses them.
-    if (kPair || p.split > 1) cluster_sync();
-    tc_fence_after();
-    const uint32_t tmem = S::kCols == kTmemAll ? kTmemBase : tmem_base;
+    if constexpr (kPair) {
+        tc_fence_before();
+        __syncthreads();
+        // A pair's barriers and TMEM are there in both CTAs before either uses the other's.
+        cluster_sync();
+        tc_fence_after();
+    } else if (warp == kTmaWarp) {
+        // The loads need the barriers alone, which this warp has made: on without waiting.
+        __syncwarp();
+        asm volatile("bar.arrive %0, %1;" ::"n"(kStartBarrier), "n"(kThreads) : "memory");
+    } else {
+        tc_fence_before();
+        asm volatile("bar.sync %0, %1;" ::"n"(kStartBarrier), "n"(kThreads) : "memory");
+        tc_fence_after();
+    }
+    // Launched while the kernel before may still run (what it writes may be an operand).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (The TMA warp, which may be ahead of the allocation, does not use it.)
+    const uint32_t tmem = S::kCols == kTmemAll ? kTmemBase : warp == kTmaWarp ? 0 : tmem_base;
     const int share = kPair ? 2 : p.split;       // CTAs a tile
     const int64_t first = blockIdx.x / share, stride = gridDim.x / share;
     const int j0 = (int)((int64_t)k_rank * p.k_blocks / p.split), j1 = (int)((int64_t)(k_rank + 1) * p.k_blocks / p.split);
@@ -217,103 +295,104 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     };
 
     // (Sums of a split tile's threads, kept over the cluster's barriers below.)
-    float acc[CPG];
+    uint64_t acc[CPG / 2];
     const int g = warp >> 2, row = threadIdx.x & 127;
     int64_t x = 0, y = 0;
     int b = 0;
     // 256 x 216 + 128 x 64 registers are within the 384 x 168 of the launch.
     if (warp >= kTmaWarp) {
-    if constexpr (CPG == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
-            auto load = [&](void* dst, const CUtensorMap* map, int s, int c0, int c1, int c2) {
-                if constexpr (kPair) tma_load_3d_pair(dst, map, cluster_addr(&full[s], 0), c0, c1, c2);
-                else tma_load_3d(dst, map, &full[s], c0, c1, c2);
-            };
-            int s = 0, issued = 0;
-            uint32_t round = 0;
-            bool ok = true;
-            for (int64_t t = first; t < p.tiles && ok; t += stride) {
-                int64_t x0, y0;
-                int b;
-                place(t, &x0, &y0, &b);
-                const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
-                for (int j = j0; j < j1; ++j) {
-                    if (round > 0 && !bar_wait(&mma_done[s], (round - 1) & 1)) {
-                        record_status(&g_status, kWaitEmpty);
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* x = ring + s * S::kStage;
-                    if (pair_rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * kCtas);
-                    load(x, &tx, s, j * BK, (int)x0, zx);
-                    load(x + BX * BK, &ty, s, j * BK, (int)y0 + S::kYRows * pair_rank, zy);
-                    if (issued < S::kStages) ++issued;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        ++round;
-                    }
-                }
-            }
-            // Copies still landing keep the CTA's shared memory (a pair's first
-            // CTA waits for both).
-            for (int q = 0; pair_rank == 0 && q < issued; ++q) {
-                if (--s < 0) {
-                    s = S::kStages - 1;
-                    --round;
-                }
-                if (!bar_wait(&full[s], round & 1)) {
-                    record_status(&g_status, kWaitDrain);
-                    break;
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        if (pair_rank == 0 && elect_one()) {
-            int s = 0, n = 0, last = -1;           // stage; blocks begun; the last one's stage
-            uint32_t round = 0, last_round = 0;
-            bool ok = true;
-            for (int64_t t = first; t < p.tiles && ok; t += stride) {
-                for (int j = j0; j < j1; ++j, ++n) {
-                    if (n >= 2) {
-                        const uint32_t ph = (uint32_t)((n / 2 - 1) & 1);
-                        if (!(kPair ? bar_wait_cluster(&acc_free[n & 1], ph) : bar_wait(&acc_free[n & 1], ph))) {
-                            record_status(&g_status, kWaitAccFree);
+        if constexpr (CPG == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kTmaWarp) {
+            if (lane == 0) {
+                auto load = [&](void* dst, const CUtensorMap* map, int s, int c0, int c1, int c2) {
+                    if constexpr (kPair) tma_load_3d_pair(dst, map, cluster_addr(&full[s], 0), c0, c1, c2);
+                    else tma_load_3d(dst, map, &full[s], c0, c1, c2);
+                };
+                int s = 0, issued = 0;
+                uint32_t round = 0;
+                bool ok = true;
+                for (int64_t t = first; t < p.tiles && ok; t += stride) {
+                    int64_t x0, y0;
+                    int b;
+                    place(t, &x0, &y0, &b);
+                    const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
+                    for (int j = j0; j < j1; ++j) {
+                        if (round > 0 && !bar_wait(&mma_done[s], (round - 1) & 1)) {
+                            record_status(&g_status, kWaitEmpty);
                             ok = false;
                             break;
                         }
+                        uint8_t* x = ring + s * S::kStage;
+                        if (pair_rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * kCtas);
+                        load(x, &tx, s, j * BK, (int)x0, zx);
+                        load(x + BX * BK, &ty, s, j * BK, (int)y0 + S::kYRows * pair_rank, zy);
+                        if (issued < S::kStages) ++issued;
+                        if (++s == S::kStages) {
+                            s = 0;
+                            ++round;
+                        }
+                    }
+                }
+                // Copies still landing keep the CTA's shared memory (a pair's first
+                // CTA waits for both).
+                for (int q = 0; pair_rank == 0 && q < issued; ++q) {
+                    if (--s < 0) {
+                        s = S::kStages - 1;
+                        --round;
                     }
                     if (!bar_wait(&full[s], round & 1)) {
-                        record_status(&g_status, kWaitFull);
-                        ok = false;
+                        record_status(&g_status, kWaitDrain);
                         break;
-                    }
-                    tc_fence_after();
-                    const uint32_t acc = tmem + (uint32_t)(n & 1) * NT;
-                    const uint32_t x = smem_u32(ring + s * S::kStage);
-                    uint64_t dx = desc16(x), dy = desc16(x + BX * BK);
-#pragma unroll
-                    for (int k = 0; k < BK / 32; ++k) {      // 32 bytes of K a step
-                        mma8<kPair>(acc, dx, dy, p.idesc, k ? 1u : 0u);
-                        dx += kStepK;
-                        dy += kStepK;
-                    }
-                    if constexpr (kPair) mma_commit_pair_both(&mma_done[s]);
-                    else mma_commit(&mma_done[s]);
-                    last = s;
-                    last_round = round;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        ++round;
                     }
                 }
             }
-            // Nothing may still be writing TMEM when it is freed.
-            if (last >= 0 && !bar_wait(&mma_done[last], last_round & 1)) record_status(&g_status, kWaitMma);
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            if (pair_rank == 0 && elect_one()) {
+                int s = 0, n = 0, last = -1;           // stage; blocks begun; the last one's stage
+                uint32_t round = 0, last_round = 0;
+                bool ok = true;
+                for (int64_t t = first; t < p.tiles && ok; t += stride) {
+                    for (int j = j0; j < j1; ++j, ++n) {
+                        const int a = n % S::kAccs;
+                        if (n >= S::kAccs) {
+                            const uint32_t ph = (uint32_t)((n / S::kAccs - 1) & 1);
+                            if (!(kPair ? bar_wait_cluster(&acc_free[a], ph) : bar_wait(&acc_free[a], ph))) {
+                                record_status(&g_status, kWaitAccFree);
+                                ok = false;
+                                break;
+                            }
+                        }
+                        if (!bar_wait(&full[s], round & 1)) {
+                            record_status(&g_status, kWaitFull);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t acc = tmem + (uint32_t)a * NT;
+                        const uint32_t x = smem_u32(ring + s * S::kStage);
+                        uint64_t dx = desc16(x), dy = desc16(x + BX * BK);
+#pragma unroll
+                        for (int k = 0; k < BK / 32; ++k) {      // 32 bytes of K a step
+                            mma8<kPair>(acc, dx, dy, p.idesc, k ? 1u : 0u);
+                            dx += kStepK;
+                            dy += kStepK;
+                        }
+                        if constexpr (kPair) mma_commit_pair_both(&mma_done[s]);
+                        else mma_commit(&mma_done[s]);
+                        last = s;
+                        last_round = round;
+                        if (++s == S::kStages) {
+                            s = 0;
+                            ++round;
+                        }
+                    }
+                }
+                // Nothing may still be writing TMEM when it is freed.
+                if (last >= 0 && !bar_wait(&mma_done[last], last_round & 1)) record_status(&g_status, kWaitMma);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else {
         if constexpr (CPG == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -337,9 +416,9 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 fy = load_scale(sy + j0 * p.sy.ks, p.sy.span);
             }
 #pragma unroll
-            for (int i = 0; i < CPG; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < CPG / 2; ++i) acc[i] = 0;
             for (int j = j0; j < j1; ++j, ++n) {
-                const float f = kYScales ? fx : fx * fy;
+                const uint64_t ff = kYScales ? pair_of(fx, fx) : pair_of(fx * fy, fx * fy);
                 if constexpr (kYScales)
                     if (row < CPG) ys[g][n & 1][row] = fy;
                 if (j + 1 < j1) {
@@ -354,14 +433,15 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                     s = 0;
                     ++round;
                 }
-                // (The columns' scales meet at a barrier: all go on or none.)
-                if constexpr (kYScales) ok = all_of_group(g, ok);
-                if (!ok) break;
+                // (A warp whose wait ran out goes on without waiting, so that all come to
+                // the same barriers; its group's tiles are not stored from then on.)
+                if constexpr (kYScales) group_sync(g);
                 tc_fence_after();
                 // The accumulator in pieces, the next one on its way under a piece's sums.
-                constexpr int W = CPG <= 32 ? (CPG < 16 ? CPG : 16) : 32;      // (registers: two CTAs an SM to 64 columns)
+                constexpr int W = CPG < 16 ? CPG : CPG <= 32 || !kYScales ? 16 : 32;     // (as registers allow without spills)
                 uint32_t v[2][W];
-                const uint32_t at = tmem + lanes + (uint32_t)((n & 1) * NT + g * CPG);
+                const int a = n % S::kAccs;
+                const uint32_t at = tmem + lanes + (uint32_t)(a * NT + g * CPG);
                 tmem_ld_begin<W>(at, v[0]);
 #pragma unroll
                 for (int c = 0; c < CPG; c += W) {
@@ -374,27 +454,32 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if (kPair && pair_rank != 0) mbar_arrive_remote_relaxed(&acc_free[n & 1], 0);
-                            else mbar_arrive(&acc_free[n & 1]);
+                            if (kPair && pair_rank != 0) mbar_arrive_remote_relaxed(&acc_free[a], 0);
+                            else mbar_arrive(&acc_free[a]);
                         }
                     }
                     if constexpr (kYScales) {
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
                             const float4 z = *reinterpret_cast<const float4*>(&ys[g][n & 1][c + i]);
-                            fma2(acc[c + i], acc[c + i + 1], now[i], now[i + 1], f * z.x, f * z.y);
-                            fma2(acc[c + i + 2], acc[c + i + 3], now[i + 2], now[i + 3], f * z.z, f * z.w);
+                            fma2(acc[(c + i) / 2], pair_of(now[i], now[i + 1]), mul2(ff, pair_of(z.x, z.y)));
+                            fma2(acc[(c + i) / 2 + 1], pair_of(now[i + 2], now[i + 3]), mul2(ff, pair_of(z.z, z.w)));
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < W; i += 2)
-                            fma2(acc[c + i], acc[c + i + 1], now[i], now[i + 1], f, f);
+                            fma2(acc[(c + i) / 2], pair_of(now[i], now[i + 1]), ff);
                     }
                 }
             }
-            if (!ok) break;
-            if (kPair || p.split == 1) emit<CPG>(p, b, x, y, acc);
+            ok = all_of_group(g, ok);
+            if (ok && (kPair || p.split == 1)) {
+                if (S::kOut && p.c_tma) send<CPG>(p, to, ring + S::kStages * S::kStage + g * BX * 128, g, row, b, (int)x0, (int)y, acc);
+                else emit<CPG>(p, b, x, y, acc);
+            }
         }
+        if (S::kOut && p.c_tma && row == 0) bulk_wait_read_all();    // shared memory outlives the stores' reads
+
     }
     if constexpr (!kPair && NT <= 128) {
         if (p.split > 1) {
@@ -408,7 +493,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             if (warp < kTmaWarp) {
 #pragma unroll
                 for (int i = 0; i < CPG; ++i)
-                    reinterpret_cast<float*>(mine)[(g * CPG + i) * BX + row] = acc[i];
+                    reinterpret_cast<float*>(mine)[(g * CPG + i) * BX + row] = i & 1 ? upper(acc[i / 2]) : lower(acc[i / 2]);
                 fence_proxy_async_smem();
             }
             __syncthreads();
@@ -426,9 +511,9 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 const float* sums = reinterpret_cast<const float*>(theirs);
                 const int64_t y0 = y - g * CPG;
                 for (int c = g; in && c < each; c += kGroups) {
-                    float v[1] = {0.0f};
-                    for (int r = 0; r < p.split; ++r) v[0] += sums[(r * each + c) * BX + row];
-                    emit<1>(p, b, x, y0 + k_rank * each + c, v);
+                    float v = 0.0f;
+                    for (int r = 0; r < p.split; ++r) v += sums[(r * each + c) * BX + row];
+                    emit_one(p, b, x, y0 + k_rank * each + c, v);
                 }
             }
             // Nobody leaves while a copy may still read its memory.
@@ -469,8 +554,9 @@ Scales scales_of(const Fp8Operand& o) {
 }
 
 template <int NT, bool kYScales, bool kPair>
-cudaError_t launch(const Params& p, const CUtensorMap& tx, const CUtensorMap& ty, int sms, cudaStream_t stream) {
-    using S = Shape<NT, kPair>;
+cudaError_t launch(const Params& p, const CUtensorMap& tx, const CUtensorMap& ty, const CUtensorMap& to, int sms,
+                   cudaStream_t stream) {
+    using S = Shape<NT, kYScales, kPair>;
     static std::atomic<int> ready[64];           // 0: not asked yet; else the pairs that fit (or 1)
     int dev = 0;
     cudaGetDevice(&dev);
@@ -479,12 +565,14 @@ cudaError_t launch(const Params& p, const CUtensorMap& tx, const CUtensorMap& ty
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = (unsigned)size;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = size > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)size;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = size > 1 ? 2 : 1;
     int fit = ready[dev & 63].load();
     if (fit == 0) {
         const cudaError_t e = cudaFuncSetAttribute(fp8_tc_kernel<NT, kYScales, kPair>,
@@ -504,19 +592,18 @@ cudaError_t launch(const Params& p, const CUtensorMap& tx, const CUtensorMap& ty
     // A split tile is its cluster's only one; others go round the CTAs (or pairs) that are resident.
     const int64_t at_once = p.split > 1 ? p.tiles : kPair ? fit : (int64_t)sms * S::kCtas;
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(p.tiles, at_once) * size));
-    return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<NT, kYScales, kPair>, tx, ty, p);
+    return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<NT, kYScales, kPair>, tx, ty, to, p);
 }
 
 template <bool kYScales>
-cudaError_t launch_nt(int nt, bool pair, const Params& p, const CUtensorMap& tx, const CUtensorMap& ty, int sms,
-                      cudaStream_t stream) {
-    if (pair) return launch<256, kYScales, true>(p, tx, ty, sms, stream);
+cudaError_t launch_nt(int nt, bool pair, const Params& p, const CUtensorMap& tx, const CUtensorMap& ty,
+                      const CUtensorMap& to, int sms, cudaStream_t stream) {
+    if (pair) return launch<256, kYScales, true>(p, tx, ty, to, sms, stream);
     switch (nt) {
-        case 16: return launch<16, kYScales, false>(p, tx, ty, sms, stream);
-        case 32: return launch<32, kYScales, false>(p, tx, ty, sms, stream);
-        case 64: return launch<64, kYScales, false>(p, tx, ty, sms, stream);
-        case 128: return launch<128, kYScales, false>(p, tx, ty, sms, stream);
-        default: return launch<256, kYScales, false>(p, tx, ty, sms, stream);
+        case 16: return launch<16, kYScales, false>(p, tx, ty, to, sms, stream);
+        case 32: return launch<32, kYScales, false>(p, tx, ty, to, sms, stream);
+        case 64: return launch<64, kYScales, false>(p, tx, ty, to, sms, stream);
+        default: return launch<128, kYScales, false>(p, tx, ty, to, sms, stream);
     }
 }
 
@@ -537,14 +624,16 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     bool swapped = false, pair = false;
     Params q{};
     for (int s = 0; s < 2; ++s)
-        for (int n : {16, 32, 64, 128, 256, 512}) {
-            const bool two = n == 512;
-            const int64_t bx = two ? 2 * BX : BX, by = two ? 256 : n;
+        for (int n : {16, 32, 64, 128, 256}) {
+            const bool two = n == 256;       // CTA pairs, 256 x 256
+            const int64_t bx = two ? 2 * BX : BX, by = n;
             const int64_t xs = ((s ? p.b.rows : p.a.rows) + bx - 1) / bx, ys = ((s ? p.a.rows : p.b.rows) + by - 1) / by;
             if ((double)xs * (double)ys * (double)p.batch > 1e9) continue;
             const int64_t tiles = xs * ys * p.batch, per_sm = n <= 64 ? 2 : 1;
             const int64_t slots = two ? sms / 2 : sms * per_sm;
             for (int split : {1, 2, 4, 8}) {
+                // (A split tile goes out a row a lane: along C's unit stride.)
+                if (split > 1 && (s ? p.csC : p.rsC) != 1 && (s ? p.rsC : p.csC) == 1) break;
                 if (split > 1 && (n > 128 || tiles * split > slots || split > k_blocks || by / split < 2)) break;
                 const int64_t waves = (tiles * split + slots - 1) / slots;
                 const double busy = per_sm == 2 && tiles * split > sms ? 2 : 1;
@@ -565,7 +654,7 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     if (nt == 0) return false;
     const Fp8Operand& ox = swapped ? p.b : p.a;
     const Fp8Operand& oy = swapped ? p.a : p.b;
-    CUtensorMap tx, ty;
+    CUtensorMap tx, ty, to{};
     if (!make_map(&tx, ox, p.K, p.batch, BX) || !make_map(&ty, oy, p.K, p.batch, (uint32_t)(pair ? nt / 2 : nt))) {
         *err = cudaErrorInvalidValue;
         return true;
@@ -583,14 +672,28 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     const int64_t w = p.type_c == SBGEMM_TYPE_FP32 ? 4 : 8;
     q.vec = !p.accumulate && q.cy == 1 && q.cols % w == 0 && (q.rows == 1 || q.cx % w == 0) &&
             (p.batch == 1 || q.cb % w == 0) && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    // Whole vectors, and rows that a map can describe.
+    q.c_tma = q.vec && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
+              q.cx < ((int64_t)1 << 37) && q.cb < ((int64_t)1 << 37) && q.cols < ((int64_t)1 << 29);
+    if (q.c_tma) {
+        const int64_t e = 16 / w, row = q.rows > 1 ? q.cx * e : (q.cols * e + 15) / 16 * 16;
+        const uint64_t dims[3] = {(uint64_t)(q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
+        const uint64_t strides[2] = {(uint64_t)row, p.batch > 1 ? (uint64_t)(q.cb * e) : (uint64_t)row};
+        const uint32_t box[3] = {128, BX, 1};
+        // (Bytes: the map copies boxes of 128 of them whatever C's type is.)
+        if (!encode_tmap_8(&to, p.C, 3, dims, strides, box)) {
+            *err = cudaErrorInvalidValue;
+            return true;
+        }
+    }
     q.x_batch = p.batch > 1 && ox.bs != 0;
     q.y_batch = p.batch > 1 && oy.bs != 0;
     q.idesc = idesc8(ox.type == SBGEMM_TYPE_E5M2, oy.type == SBGEMM_TYPE_E5M2, nt, pair ? 256 : 128);
     q.sx = scales_of(ox);
     q.sy = scales_of(oy);
     q.sc = p.sc;
-    *err = oy.group == 1 ? launch_nt<true>(nt, pair, q, tx, ty, sms, stream)
-                         : launch_nt<false>(nt, pair, q, tx, ty, sms, stream);
+    *err = oy.group == 1 ? launch_nt<true>(nt, pair, q, tx, ty, to, sms, stream)
+                         : launch_nt<false>(nt, pair, q, tx, ty, to, sms, stream);
     return true;
 }
 
