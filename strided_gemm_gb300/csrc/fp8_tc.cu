@@ -31,7 +31,8 @@ namespace sbg {
 namespace {
 
 constexpr int BX = 128, BK = kScaleBlock;
-constexpr int kGroups = 2, kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1;
+constexpr int kGroups = 2, kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kTmaWarpY = kTmaWarp + 2;
+constexpr int kChunk = 8;        // blocks of K whose column scales come in together: a 32-byte sector of a row's
 constexpr int kThreads = 4 * (kGroups + 1) * 32;      // whole warpgroups: registers move between them
 // Named barriers: 0 the CTA, 1 and 2 the epilogue groups, 3 the start, of its own
 // since the TMA warp, which only arrives there, may come to the CTA's next one
@@ -39,18 +40,19 @@ constexpr int kThreads = 4 * (kGroups + 1) * 32;      // whole warpgroups: regis
 constexpr int kStartBarrier = 3;
 __device__ unsigned int g_status = 0;
 
-// Scales of one operand.
-struct Scales { const float* at; int64_t rs, ks, bs, rows; int group; ByteSpan span; };
+// Scales of one operand; shift: 7 where one covers 128 rows, else 0.
+struct Scales { const float* at; int64_t rs, ks, bs; int rows, shift; ByteSpan span; };
 
 struct Params {
     void* C; int64_t cx, cy, cb;   // C's strides along the tile's rows, its columns and the batch
     int type_c;
     int64_t rows, cols;            // of the product's tiles: x < rows, y < cols
-    int64_t x_tiles, y_tiles, tiles;
+    uint32_t x_tiles, y_tiles, tiles;
     int k_blocks, split;           // split: CTAs of a cluster that share a tile's blocks
     float alpha;
     int accumulate;
     int vec;                       // columns go out as 16-byte vectors
+    int vec_rows;                  // ... and a split tile's as vectors of four rows
     int c_tma;                     // C goes out through its tensor map
     int x_batch, y_batch;          // the batch coordinate moves (else shared)
     uint32_t idesc;
@@ -64,7 +66,7 @@ struct Shape {
     static constexpr int kStage = (BX + kYRows) * BK;
     // Two CTAs an SM for up to 64 columns: the weights' bytes want to be in flight.
     static constexpr int kCtas = NT <= 64 ? 2 : 1;
-    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kPair && kYScales ? 5 : 6;
+    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : kYScales ? 5 : 6;
     // Accumulators in TMEM: few columns are read long after their MMAs were quick.
     static constexpr int kAccs = NT <= 64 ? 4 : 2;
     static constexpr uint32_t kCols = kAccs * NT;
@@ -72,7 +74,7 @@ struct Shape {
     static constexpr int kOut = NT >= 128 ? kGroups * BX * 128 : 0;
     static constexpr int kSmem = kStages * kStage + kOut + 1024;
     static_assert(NT > 128 || 2 * NT * BX * 4 <= kStages * kStage, "a split tile's sums, here and from the cluster");
-    static_assert((kSmem + (kYScales ? 8 * NT : 0) + 512) * kCtas <= 232448, "shared memory");
+    static_assert((kSmem + (kYScales ? 8 * kChunk * NT : 0) + 512) * kCtas <= 232448, "shared memory");
 };
 
 // kind::f8f6f4, D fp32, both operands K-major.
@@ -115,6 +117,10 @@ __device__ __forceinline__ bool all_of_group(int g, bool v) {
 __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // Pairs of floats in a 64-bit register, as fma.rn.f32x2 takes them.
@@ -172,13 +178,29 @@ __device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, i
     for (int i = 0; i < n; ++i, c += p.cy)
         if (y + i < p.cols) put_one(p, c, i & 1 ? upper(v[i / 2]) : lower(v[i / 2]));
 }
-// One sum.
-__device__ __forceinline__ void emit_one(const Params& p, int64_t b, int64_t x, int64_t y, float v) {
-    if (x >= p.rows || y >= p.cols) return;
-    const int64_t at = b * p.cb + x * p.cx + y * p.cy;
-    if (p.type_c == SBGEMM_TYPE_BF16) put_one(p, static_cast<__nv_bfloat16*>(p.C) + at, v);
-    else if (p.type_c == SBGEMM_TYPE_FP16) put_one(p, static_cast<__half*>(p.C) + at, v);
-    else put_one(p, static_cast<float*>(p.C) + at, v);
+// The sums of four rows from x on of column y.
+template <typename T>
+__device__ __forceinline__ void emit_rows_as(const Params& p, int64_t b, int x, int y, const float4& v) {
+    T* c = static_cast<T*>(p.C) + b * p.cb + x * p.cx + y * p.cy;
+    if (p.vec_rows && x + 3 < p.rows) {
+        if (!dbg_in_bytes(c, 4 * sizeof(T), p.sc, &g_status)) return;
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(c) = make_float4(p.alpha * v.x, p.alpha * v.y, p.alpha * v.z, p.alpha * v.w);
+        else
+            *reinterpret_cast<uint2*>(c) =
+                make_uint2(pack2<T>(p.alpha * v.x, p.alpha * v.y), pack2<T>(p.alpha * v.z, p.alpha * v.w));
+        return;
+    }
+    const float each[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i, c += p.cx)
+        if (x + i < p.rows) put_one(p, c, each[i]);
+}
+__device__ __forceinline__ void emit_rows(const Params& p, int64_t b, int x, int y, const float4& v) {
+    if (y >= p.cols) return;
+    if (p.type_c == SBGEMM_TYPE_BF16) emit_rows_as<__nv_bfloat16>(p, b, x, y, v);
+    else if (p.type_c == SBGEMM_TYPE_FP16) emit_rows_as<__half>(p, b, x, y, v);
+    else emit_rows_as<float>(p, b, x, y, v);
 }
 template <int n>
 __device__ __forceinline__ void emit(const Params& p, int64_t b, int64_t x, int64_t y, const uint64_t (&v)[n / 2]) {
@@ -241,7 +263,8 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     // behind it holds the issuing thread for some 360 cycles).
     __shared__ uint64_t full[S::kStages], mma_done[S::kStages], acc_free[S::kAccs], sums_full;
     __shared__ uint32_t tmem_base;
-    __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? CPG : 4];
+    // Scales of the columns for kChunk blocks of K, two chunks a group.
+    __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? kChunk : 1][kYScales ? CPG : 4];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -283,26 +306,28 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     }
     // Launched while the kernel before may still run (what it writes may be an operand).
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // (The TMA warp, which may be ahead of the allocation, does not use it.)
+    // (That TMA warp, which may be ahead of the allocation, does not use it.)
     const uint32_t tmem = S::kCols == kTmemAll ? kTmemBase : warp == kTmaWarp ? 0 : tmem_base;
     const int share = kPair ? 2 : p.split;       // CTAs a tile
-    const int64_t first = blockIdx.x / share, stride = gridDim.x / share;
-    const int j0 = (int)((int64_t)k_rank * p.k_blocks / p.split), j1 = (int)((int64_t)(k_rank + 1) * p.k_blocks / p.split);
-    auto place = [&](int64_t t, int64_t* x0, int64_t* y0, int* b) {
-        *x0 = t % p.x_tiles * (BX * kCtas) + BX * pair_rank;
-        *y0 = t / p.x_tiles % p.y_tiles * NT;
+    const uint32_t first = blockIdx.x / share, stride = gridDim.x / share;
+    const int j0 = k_rank * p.k_blocks / p.split, j1 = (k_rank + 1) * p.k_blocks / p.split;
+    // (32 bits: a 64-bit division takes hundreds of cycles.)
+    auto place = [&](uint32_t t, int* x0, int* y0, int* b) {
+        *x0 = (int)(t % p.x_tiles) * (BX * kCtas) + BX * pair_rank;
+        *y0 = (int)(t / p.x_tiles % p.y_tiles) * NT;
         *b = (int)(t / p.x_tiles / p.y_tiles);
     };
 
     // (Sums of a split tile's threads, kept over the cluster's barriers below.)
     uint64_t acc[CPG / 2];
     const int g = warp >> 2, row = threadIdx.x & 127;
-    int64_t x = 0, y = 0;
-    int b = 0;
+    int x = 0, y = 0, b = 0;
     // 256 x 216 + 128 x 64 registers are within the 384 x 168 of the launch.
     if (warp >= kTmaWarp) {
         if constexpr (CPG == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == kTmaWarp) {
+        if (warp == kTmaWarp || warp == kTmaWarpY) {
+            // A warp an operand: a load takes its issuer some 250 cycles.
+            const bool is_x = warp == kTmaWarp;
             if (lane == 0) {
                 auto load = [&](void* dst, const CUtensorMap* map, int s, int c0, int c1, int c2) {
                     if constexpr (kPair) tma_load_3d_pair(dst, map, cluster_addr(&full[s], 0), c0, c1, c2);
@@ -311,9 +336,8 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 int s = 0, issued = 0;
                 uint32_t round = 0;
                 bool ok = true;
-                for (int64_t t = first; t < p.tiles && ok; t += stride) {
-                    int64_t x0, y0;
-                    int b;
+                for (uint32_t t = first; t < p.tiles && ok; t += stride) {
+                    int x0, y0, b;
                     place(t, &x0, &y0, &b);
                     const int zx = p.x_batch ? b : 0, zy = p.y_batch ? b : 0;
                     for (int j = j0; j < j1; ++j) {
@@ -323,9 +347,12 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                             break;
                         }
                         uint8_t* x = ring + s * S::kStage;
-                        if (pair_rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * kCtas);
-                        load(x, &tx, s, j * BK, (int)x0, zx);
-                        load(x + BX * BK, &ty, s, j * BK, (int)y0 + S::kYRows * pair_rank, zy);
+                        if (is_x) {
+                            if (pair_rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * kCtas);
+                            load(x, &tx, s, j * BK, x0, zx);
+                        } else {
+                            load(x + BX * BK, &ty, s, j * BK, y0 + S::kYRows * pair_rank, zy);
+                        }
                         if (issued < S::kStages) ++issued;
                         if (++s == S::kStages) {
                             s = 0;
@@ -335,7 +362,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 }
                 // Copies still landing keep the CTA's shared memory (a pair's first
                 // CTA waits for both).
-                for (int q = 0; pair_rank == 0 && q < issued; ++q) {
+                for (int q = 0; is_x && pair_rank == 0 && q < issued; ++q) {
                     if (--s < 0) {
                         s = S::kStages - 1;
                         --round;
@@ -352,7 +379,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 int s = 0, n = 0, last = -1;           // stage; blocks begun; the last one's stage
                 uint32_t round = 0, last_round = 0;
                 bool ok = true;
-                for (int64_t t = first; t < p.tiles && ok; t += stride) {
+                for (uint32_t t = first; t < p.tiles && ok; t += stride) {
                     for (int j = j0; j < j1; ++j, ++n) {
                         const int a = n % S::kAccs;
                         if (n >= S::kAccs) {
@@ -399,32 +426,50 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
         int n = 0, s = 0;
         uint32_t round = 0;
         bool ok = true;
-        for (int64_t t = first; t < p.tiles; t += stride) {
-            int64_t x0, y0;
+        for (uint32_t t = first; t < p.tiles; t += stride) {
+            int x0, y0;
             place(t, &x0, &y0, &b);
             x = x0 + row;
             y = y0 + g * CPG;
-            // This thread's scales: its row's, and the columns' common one or, to
-            // be shared, one column's.  Rows past the end take the last one's.
-            const float* sx = p.sx.at + b * p.sx.bs + min(x, p.sx.rows - 1) / p.sx.group * p.sx.rs;
-            const float* sy = p.sy.at + b * p.sy.bs +
-                              (kYScales ? min(y + min(row, CPG - 1), p.sy.rows - 1)
-                                        : min(y, p.sy.rows - 1) / p.sy.group) * p.sy.rs;
-            float fx = 0.0f, fy = 0.0f;
-            if (j0 < j1) {
-                fx = load_scale(sx + j0 * p.sx.ks, p.sx.span);
-                fy = load_scale(sy + j0 * p.sy.ks, p.sy.span);
+            // This thread's row's scales, two blocks ahead in registers, and the
+            // columns' common one likewise, or each column's through shared memory.
+            // Rows past the end take the last one's.
+            const float* sx = p.sx.at + b * p.sx.bs + (min(x, p.sx.rows - 1) >> p.sx.shift) * p.sx.rs;
+            const float* sy = p.sy.at + b * p.sy.bs + (kYScales ? 0 : (min(y, p.sy.rows - 1) >> p.sy.shift) * p.sy.rs);
+            // (Multiplied when they are used: a product here would wait for the loads.)
+            auto row_scale = [&](int j) { return j < j1 ? load_scale(sx + j * p.sx.ks, p.sx.span) : 0.0f; };
+            auto col_scale = [&](int j) { return !kYScales && j < j1 ? load_scale(sy + j * p.sy.ks, p.sy.span) : 1.0f; };
+            auto fetch = [&](int c) {            // the columns' scales of chunk c
+                for (int i = row; i < kChunk * CPG; i += 128) {
+                    const int k = i % kChunk, col = i / kChunk, j = j0 + c * kChunk + k;
+                    const float* at = sy + min(y + col, p.sy.rows - 1) * p.sy.rs + j * p.sy.ks;
+                    if (j < j1 && dbg_in_bytes(at, 4, p.sy.span, &g_status)) cp_async4(&ys[g][c & 1][k][col], at);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            float fx[2] = {row_scale(j0), row_scale(j0 + 1)}, fy[2] = {col_scale(j0), col_scale(j0 + 1)};
+            if constexpr (kYScales) {
+                group_sync(g);                   // the last tile's scales are read
+                fetch(0);
             }
 #pragma unroll
             for (int i = 0; i < CPG / 2; ++i) acc[i] = 0;
             for (int j = j0; j < j1; ++j, ++n) {
-                const uint64_t ff = kYScales ? pair_of(fx, fx) : pair_of(fx * fy, fx * fy);
-                if constexpr (kYScales)
-                    if (row < CPG) ys[g][n & 1][row] = fy;
-                if (j + 1 < j1) {
-                    fx = load_scale(sx + (j + 1) * p.sx.ks, p.sx.span);
-                    fy = load_scale(sy + (j + 1) * p.sy.ks, p.sy.span);
+                const float f = kYScales ? fx[0] : fx[0] * fy[0];
+                const uint64_t ff = pair_of(f, f);
+                fx[0] = fx[1];
+                fy[0] = fy[1];
+                fx[1] = row_scale(j + 2);
+                fy[1] = col_scale(j + 2);
+                if constexpr (kYScales) {
+                    if ((j - j0) % kChunk == 0) {
+                        // A chunk is in for all, and all are through with the one before.
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        group_sync(g);
+                        if (j + kChunk < j1) fetch((j - j0) / kChunk + 1);
+                    }
                 }
+                const float* yscale = ys[kYScales ? g : 0][kYScales ? (j - j0) / kChunk & 1 : 0][kYScales ? (j - j0) % kChunk : 0];
                 if (ok && !bar_wait(&mma_done[s], round & 1)) {
                     record_status(&g_status, kWaitMma);
                     ok = false;
@@ -435,7 +480,6 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 }
                 // (A warp whose wait ran out goes on without waiting, so that all come to
                 // the same barriers; its group's tiles are not stored from then on.)
-                if constexpr (kYScales) group_sync(g);
                 tc_fence_after();
                 // The accumulator in pieces, the next one on its way under a piece's sums.
                 constexpr int W = CPG < 16 ? CPG : CPG <= 32 || !kYScales ? 16 : 32;     // (as registers allow without spills)
@@ -461,7 +505,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                     if constexpr (kYScales) {
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
-                            const float4 z = *reinterpret_cast<const float4*>(&ys[g][n & 1][c + i]);
+                            const float4 z = *reinterpret_cast<const float4*>(yscale + c + i);
                             fma2(acc[(c + i) / 2], pair_of(now[i], now[i + 1]), mul2(ff, pair_of(z.x, z.y)));
                             fma2(acc[(c + i) / 2 + 1], pair_of(now[i + 2], now[i + 3]), mul2(ff, pair_of(z.z, z.w)));
                         }
@@ -474,7 +518,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             }
             ok = all_of_group(g, ok);
             if (ok && (kPair || p.split == 1)) {
-                if (S::kOut && p.c_tma) send<CPG>(p, to, ring + S::kStages * S::kStage + g * BX * 128, g, row, b, (int)x0, (int)y, acc);
+                if (S::kOut && p.c_tma) send<CPG>(p, to, ring + S::kStages * S::kStage + g * BX * 128, g, row, b, x0, y, acc);
                 else emit<CPG>(p, b, x, y, acc);
             }
         }
@@ -509,11 +553,19 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 const bool in = bar_wait(&sums_full, 0);
                 if (!in) record_status(&g_status, kWaitPartial);
                 const float* sums = reinterpret_cast<const float*>(theirs);
-                const int64_t y0 = y - g * CPG;
-                for (int c = g; in && c < each; c += kGroups) {
-                    float v = 0.0f;
-                    for (int r = 0; r < p.split; ++r) v += sums[(r * each + c) * BX + row];
-                    emit_one(p, b, x, y0 + k_rank * each + c, v);
+                // A warp a column, a lane four of its rows.
+                const int x4 = x - row + 4 * lane, y0 = y - g * CPG + k_rank * each;
+#pragma unroll 2
+                for (int c = warp; in && c < each; c += 4 * kGroups) {
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int r = 0; r < p.split; ++r) {
+                        const float4 w = *reinterpret_cast<const float4*>(sums + (r * each + c) * BX + 4 * lane);
+                        v.x += w.x;
+                        v.y += w.y;
+                        v.z += w.z;
+                        v.w += w.w;
+                    }
+                    emit_rows(p, b, x4, y0 + c, v);
                 }
             }
             // Nobody leaves while a copy may still read its memory.
@@ -550,7 +602,7 @@ bool make_map(CUtensorMap* map, const Fp8Operand& o, int64_t K, int64_t batch, u
 }
 
 Scales scales_of(const Fp8Operand& o) {
-    return Scales{o.scale, o.rsS, o.ksS, o.bsS, o.rows, o.group, o.ss};
+    return Scales{o.scale, o.rsS, o.ksS, o.bsS, (int)o.rows, o.group == 1 ? 0 : 7, o.ss};
 }
 
 template <int NT, bool kYScales, bool kPair>
@@ -609,11 +661,13 @@ cudaError_t launch_nt(int nt, bool pair, const Params& p, const CUtensorMap& tx,
 
 // Cycles of a block of K in a tile: its bytes through shared memory, in and
 // out, at 128 a cycle, or the MMAs.
-int block_cycles(int nt, bool pair) { return pair ? 540 : 2 * (BX + nt); }
+int block_cycles(int nt, bool pair, int on_sm) { return pair ? 600 : std::max(450, on_sm * 2 * (BX + nt)); }
 
 }  // namespace
 
 bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_t* err) {
+    // (Indexes of a tile past the last one still are ints.)
+    if (p.a.rows > INT32_MAX - 1024 || p.b.rows > INT32_MAX - 1024) return false;
     if (p.K <= 0 || !mappable(p.a, p.K, p.batch) || !mappable(p.b, p.K, p.batch)) return false;
     const int k_blocks = (int)((p.K + BK - 1) / BK);
     // Orientation, columns of a tile, pairs, and the split of K: the fewest
@@ -636,17 +690,17 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
                 if (split > 1 && (s ? p.csC : p.rsC) != 1 && (s ? p.rsC : p.csC) == 1) break;
                 if (split > 1 && (n > 128 || tiles * split > slots || split > k_blocks || by / split < 2)) break;
                 const int64_t waves = (tiles * split + slots - 1) / slots;
-                const double busy = per_sm == 2 && tiles * split > sms ? 2 : 1;
-                const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two) * busy +
+                const int on_sm = per_sm == 2 && tiles * split > sms ? 2 : 1;
+                const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two, on_sm) +
                                              2500 + (split > 1 ? 1500 : 0));
                 if (nt == 0 || cost < best) {
                     best = cost;
                     nt = (int)by;
                     pair = two;
                     swapped = s != 0;
-                    q.x_tiles = xs;
-                    q.y_tiles = ys;
-                    q.tiles = tiles;
+                    q.x_tiles = (uint32_t)xs;
+                    q.y_tiles = (uint32_t)ys;
+                    q.tiles = (uint32_t)tiles;
                     q.split = split;
                 }
             }
@@ -672,6 +726,8 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     const int64_t w = p.type_c == SBGEMM_TYPE_FP32 ? 4 : 8;
     q.vec = !p.accumulate && q.cy == 1 && q.cols % w == 0 && (q.rows == 1 || q.cx % w == 0) &&
             (p.batch == 1 || q.cb % w == 0) && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    q.vec_rows = !p.accumulate && q.cx == 1 && (q.cols == 1 || q.cy % 4 == 0) && (p.batch == 1 || q.cb % 4 == 0) &&
+                 reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
     // Whole vectors, and rows that a map can describe.
     q.c_tma = q.vec && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
               q.cx < ((int64_t)1 << 37) && q.cb < ((int64_t)1 << 37) && q.cols < ((int64_t)1 << 29);
