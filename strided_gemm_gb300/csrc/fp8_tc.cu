@@ -381,6 +381,13 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                 bool ok = true;
                 for (uint32_t t = first; t < p.tiles && ok; t += stride) {
                     for (int j = j0; j < j1; ++j, ++n) {
+                        // The operands first: what follows the accumulator's wait is on
+                        // the way from its last reader to the next block's sums.
+                        if (!bar_wait(&full[s], round & 1)) {
+                            record_status(&g_status, kWaitFull);
+                            ok = false;
+                            break;
+                        }
                         const int a = n % S::kAccs;
                         if (n >= S::kAccs) {
                             const uint32_t ph = (uint32_t)((n / S::kAccs - 1) & 1);
@@ -389,11 +396,6 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                                 ok = false;
                                 break;
                             }
-                        }
-                        if (!bar_wait(&full[s], round & 1)) {
-                            record_status(&g_status, kWaitFull);
-                            ok = false;
-                            break;
                         }
                         tc_fence_after();
                         const uint32_t acc = tmem + (uint32_t)a * NT;
