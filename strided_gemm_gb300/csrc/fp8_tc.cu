@@ -507,9 +507,9 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
                     if constexpr (kYScales) {
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
-                            const float4 z = *reinterpret_cast<const float4*>(yscale + c + i);
-                            fma2(acc[(c + i) / 2], pair_of(now[i], now[i + 1]), mul2(ff, pair_of(z.x, z.y)));
-                            fma2(acc[(c + i) / 2 + 1], pair_of(now[i + 2], now[i + 3]), mul2(ff, pair_of(z.z, z.w)));
+                            const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(yscale + c + i);
+                            fma2(acc[(c + i) / 2], pair_of(now[i], now[i + 1]), mul2(ff, z.x));
+                            fma2(acc[(c + i) / 2 + 1], pair_of(now[i + 2], now[i + 3]), mul2(ff, z.y));
                         }
                     } else {
 #pragma unroll
@@ -661,9 +661,21 @@ cudaError_t launch_nt(int nt, bool pair, const Params& p, const CUtensorMap& tx,
     }
 }
 
-// Cycles of a block of K in a tile: its bytes through shared memory, in and
-// out, at 128 a cycle, or the MMAs.
-int block_cycles(int nt, bool pair, int on_sm) { return pair ? 600 : std::max(450, on_sm * 2 * (BX + nt)); }
+// Cycles of a block of K in a tile, measured: with one scale for the columns or
+// one each (twice the epilogue's arithmetic), and for tiles of up to 64 columns
+// with one CTA on an SM or two. 4096 x 4096 x 4096: pairs 67 and 116 us, tiles of
+// 128 columns 74 and 122, of 64 columns 120 and 163; 2560 x 960 x 8192 with scales
+// a column: 47 us on 300 tiles of 64 columns in one wave, 58 on 40 pairs, 68 on 160
+// tiles of 128 columns in two waves.
+int block_cycles(int nt, bool pair, int on_sm, bool y_scales) {
+    if (pair) return y_scales ? 1600 : 850;
+    switch (nt) {
+        case 16: return y_scales ? (on_sm == 2 ? 900 : 610) : on_sm == 2 ? 650 : 560;
+        case 32: return y_scales ? (on_sm == 2 ? 1000 : 650) : on_sm == 2 ? 700 : 600;
+        case 64: return y_scales ? (on_sm == 2 ? 1200 : 850) : on_sm == 2 ? 920 : 760;
+        default: return y_scales ? 930 : 535;
+    }
+}
 
 }  // namespace
 
@@ -673,8 +685,10 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     if (p.K <= 0 || !mappable(p.a, p.K, p.batch) || !mappable(p.b, p.K, p.batch)) return false;
     const int k_blocks = (int)((p.K + BK - 1) / BK);
     // Orientation, columns of a tile, pairs, and the split of K: the fewest
-    // cycles, by the blocks of K that an SM goes through and 2500 cycles for a
-    // tile's start and end, 1500 for joining a split one.
+    // cycles, by the blocks of K that an SM goes through, 2500 cycles for a tile's
+    // start and end (a pair's 4000), and 4500 for joining a split one.  (16 x 7168 x
+    // 4096, 16 columns a tile: 13.7, 10.8 and 9.8 us split by 1, 2 and 4; 128 x 7168
+    // x 4096: 13.1 us upright, 16.9 turned and split by 2.)
     double best = 0;
     int nt = 0;
     bool swapped = false, pair = false;
@@ -693,8 +707,8 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
                 if (split > 1 && (n > 128 || tiles * split > slots || split > k_blocks || by / split < 2)) break;
                 const int64_t waves = (tiles * split + slots - 1) / slots;
                 const int on_sm = per_sm == 2 && tiles * split > sms ? 2 : 1;
-                const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two, on_sm) +
-                                             2500 + (split > 1 ? 1500 : 0));
+                const double cost = waves * ((double)((k_blocks + split - 1) / split) * block_cycles((int)by, two, on_sm, (s ? p.a : p.b).group == 1) +
+                                             (two ? 4000 : 2500) + (split > 1 ? 4500 : 0));
                 if (nt == 0 || cost < best) {
                     best = cost;
                     nt = (int)by;
