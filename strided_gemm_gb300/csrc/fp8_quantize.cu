@@ -132,20 +132,27 @@ __global__ void __launch_bounds__(kThreads) blocks_any_kernel(const __grid_const
     }
 }
 
-// What a block's elements are divided by.
+// fl(x / y) from inverse = fl(1 / y).
+__device__ __forceinline__ float divided(float x, float y, float inverse) {
+    const float q = x * inverse;
+    return fmaf(fmaf(-q, y, x), inverse, q);
+}
+constexpr float kLow = 8.470329472543003e-22f, kLift = 1152921504606846976.0f;     // 2^-70, 2^60
+
+// What a block's elements are divided by, and its scale.
 struct Divisor {
     float scale, lift, lifted, inverse;
-    __device__ __forceinline__ float of(float x) const {
-        const float y = x * lift, q = y * inverse;
-        return fmaf(fmaf(-q, lifted, y), inverse, q);
-    }
+    __device__ __forceinline__ float of(float x) const { return divided(x, lifted, inverse); }      // of an x times lift
+    __device__ __forceinline__ bool low() const { return lift != 1.0f; }
 };
-__device__ __forceinline__ Divisor divisor(float s) {
+__device__ __forceinline__ Divisor divisor(float amax, float largest) {
     Divisor d;
-    d.scale = s;
-    d.lift = s < 8.470329472543003e-22f ? 1152921504606846976.0f : 1.0f;      // below 2^-70: by 2^60
-    d.lifted = s * d.lift;
-    d.inverse = __fdiv_rn(1.0f, d.lifted);
+    // (A quotient of this size below fp32's normals becomes the least scale anyway.)
+    const float up = amax < kLow ? kLift : 1.0f;
+    d.scale = fmaxf(divided(amax * up, largest, largest == 448.0f ? 1.0f / 448.0f : 1.0f / 57344.0f) * (1.0f / up), kSmallest);
+    d.lift = d.scale < kLow ? kLift : 1.0f;
+    d.lifted = d.scale * d.lift;
+    d.inverse = __frcp_rn(d.lifted);
     return d;
 }
 
@@ -198,12 +205,30 @@ template <> struct Raw8<float> {
 template <typename T> struct Top8 {
     uint32_t w[4] = {};
     static constexpr uint32_t kInf2 = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
-    __device__ __forceinline__ void take(const Raw8<T>& r) {
-        const uint32_t h[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+    template <int n> __device__ __forceinline__ void take(const Raw8<T> (&r)[n]) {
 #pragma unroll
+        for (int q = 0; q < n; ++q) {
+            w[0] = __vmaxu2(w[0], r[q].w.x & 0x7fff7fffu);
+            w[1] = __vmaxu2(w[1], r[q].w.y & 0x7fff7fffu);
+            w[2] = __vmaxu2(w[2], r[q].w.z & 0x7fff7fffu);
+            w[3] = __vmaxu2(w[3], r[q].w.w & 0x7fff7fffu);
+        }
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+        if ((m & 0xffffu) < (kInf2 & 0xffffu) && m < (kInf2 & 0xffff0000u)) return;
+        // Something is not finite: again, without what is not.
+        w[0] = w[1] = w[2] = w[3] = 0;
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            const uint32_t a = h[i] & 0x7fff7fffu;
-            w[i] = __vmaxu2(w[i], a & __vcmpltu2(a, kInf2));
+            uint32_t t = 0;
+#pragma unroll
+            for (int q = 0; q < n; ++q) {
+                const uint32_t a = (i == 0 ? r[q].w.x : i == 1 ? r[q].w.y : i == 2 ? r[q].w.z : r[q].w.w) & 0x7fff7fffu;
+                t = __vmaxu2(t, a & __vcmpltu2(a, kInf2));
+            }
+            if (i == 0) w[0] = t;
+            else if (i == 1) w[1] = t;
+            else if (i == 2) w[2] = t;
+            else w[3] = t;
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -212,16 +237,17 @@ template <typename T> struct Top8 {
         r.get(v);
     }
     __device__ __forceinline__ float all() const {
-        const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-        const float2 f = unpack2<T>(m);
+        const float2 f = unpack2<T>(__vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3])));
         return fmaxf(f.x, f.y);
     }
 };
 template <> struct Top8<float> {
     float v[8] = {};
-    __device__ __forceinline__ void take(const Raw8<float>& r) {
+    template <int n> __device__ __forceinline__ void take(const Raw8<float> (&r)[n]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], finite_size(r.v[i]));
+        for (int q = 0; q < n; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], finite_size(r[q].v[i]));
     }
     __device__ __forceinline__ void get(float (&o)[8]) const {
 #pragma unroll
@@ -231,11 +257,15 @@ template <> struct Top8<float> {
         return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
     }
 };
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], const Divisor& d, bool e4m3) {
+__device__ __forceinline__ uint2 pack8(float (&v)[8], const Divisor& d, bool e4m3) {
+    if (d.low()) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= d.lift;
+    }
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = pack_fp8x2(d.of(v[2 * i]), d.of(v[2 * i + 1]), e4m3);
-    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 // 8 values of a row of Y, the first n of them.
 __device__ __forceinline__ void store8(uint8_t* y, uint2 w, int n, const ByteSpan& span) {
@@ -255,36 +285,32 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool e4m3 = p.type_y == SBGEMM_TYPE_E4M3;
     const float largest = fp8_largest(p.type_y);
-    const int lane = threadIdx.x & 31, half = lane >> 4, piece = lane & 15;
-    const int kb = (int)((p.K + kScaleBlock - 1) / kScaleBlock), per_row = (kb + 2 * n - 1) / (2 * n);
+    const int lane = threadIdx.x & 31, half = lane >> 4, piece = lane & 15, K = (int)p.K;
+    const int kb = (K + kScaleBlock - 1) / kScaleBlock, per_row = (kb + 2 * n - 1) / (2 * n);
     const int64_t items = p.batch * p.M * per_row;
     for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; it < items;
          it += (int64_t)gridDim.x * (kThreads / 32)) {
         const int64_t r = it / per_row, m = r % p.M, b = r / p.M;
-        const int j0 = (int)(it - r * per_row) * 2 * n + half;
-        const T* x = static_cast<const T*>(p.X) + b * p.bsX + m * p.rsX;
-        Raw8<T> raw[n];
+        const int j0 = (int)(it - r * per_row) * 2 * n + half, k0 = j0 * kScaleBlock + piece * 8;
+        const T* x = static_cast<const T*>(p.X) + b * p.bsX + m * p.rsX + k0;
+        uint8_t* y = p.Y + b * p.bsY + m * p.rsY + k0;
+        float* s = p.S + b * p.bsS + m * p.rsS + j0 * p.ksS;
+        Raw8<T> raw[n][1];
+#pragma unroll
+        for (int q = 0; q < n; ++q) raw[q][0].load(x + 2 * q * kScaleBlock, K - k0 - 2 * q * kScaleBlock, p.sx);
 #pragma unroll
         for (int q = 0; q < n; ++q) {
-            const int64_t k = (int64_t)(j0 + 2 * q) * kScaleBlock + piece * 8;
-            raw[q].load(x + k, k < p.K ? (int)min((int64_t)8, p.K - k) : 0, p.sx);
-        }
-#pragma unroll
-        for (int q = 0; q < n; ++q) {
-            const int j = j0 + 2 * q;
-            const int64_t k = (int64_t)j * kScaleBlock + piece * 8;
             Top8<T> tops;
             tops.take(raw[q]);
             float top = tops.all();
 #pragma unroll
             for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            const Divisor d = divisor(scale_of(top, largest));
+            const Divisor d = divisor(top, largest);
             float v[8];
-            raw[q].get(v);
-            const uint2 w = pack8(v, d, e4m3);
-            if (k < p.K) store8(p.Y + b * p.bsY + m * p.rsY + k, w, (int)min((int64_t)8, p.K - k), p.sy);
-            float* s = p.S + b * p.bsS + m * p.rsS + j * p.ksS;
-            if (piece == 0 && j < kb && dbg_in_bytes(s, 4, p.ss, &g_status)) *s = d.scale;
+            raw[q][0].get(v);
+            store8(y + 2 * q * kScaleBlock, pack8(v, d, e4m3), K - k0 - 2 * q * kScaleBlock, p.sy);
+            float* at = s + 2 * q * p.ksS;
+            if (piece == 0 && j0 + 2 * q < kb && dbg_in_bytes(at, 4, p.ss, &g_status)) *at = d.scale;
         }
     }
 }
@@ -314,9 +340,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tiles_kernel
     Top8<T> top;
 #pragma unroll
     for (int q = 0; q < 8; ++q) raw[q].load(x + (m0 + 16 * q) * p.rsX, m0 + 16 * q < p.M ? n : 0, p.sx);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) top.take(raw[q]);
-    const Divisor d = divisor(scale_of(block_max(top.all(), shared), fp8_largest(p.type_y)));
+    top.take(raw);
+    const Divisor d = divisor(block_max(top.all(), shared), fp8_largest(p.type_y));
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         float v[8];
@@ -351,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) turned_kerne
     float top[8];
     {
         Top8<T> each;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) each.take(raw[q]);
+        each.take(raw);
         each.get(top);
     }
     if (p.group == 1) {
@@ -381,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) turned_kerne
     float* s = p.S + b * p.bsS + j * p.ksS;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const Divisor d = divisor(scale_of(top[i], largest));
+        const Divisor d = divisor(top[i], largest);
         // Row m0 + i: its 8 elements of K.
         uint32_t h[4];
 #pragma unroll
@@ -389,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) turned_kerne
             float u[8], v[8];
             raw[q].get(u);
             raw[q + 1].get(v);
-            h[q / 2] = pack_fp8x2(d.of(u[i]), d.of(v[i]), e4m3);
+            h[q / 2] = pack_fp8x2(d.of(u[i] * d.lift), d.of(v[i] * d.lift), e4m3);
         }
-        out[mi * 8 + i][ki ^ mi] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        out[mi * 8 + i][ki ^ mi] = make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
         if (ki == 0 && i < n && (p.group == 1 || (mi == 0 && i == 0))) {
             float* at = s + (p.group == 1 ? m0 + i : r) * p.rsS;
             if (dbg_in_bytes(at, 4, p.ss, &g_status)) *at = d.scale;
