@@ -3,18 +3,19 @@
 //
 // Angles.  A pair turns by position * step of 2^-64 turns.  The product modulo
 // 2^64 is the angle modulo a turn without any error, for every position; its
-// top two bits are the quadrant and the rest, exact to fp32's 24 bits, an angle
-// of at most an eighth of a turn either side.
+// top bits are the nearest quarter turn and the rest, exact to fp32's 24 bits, an
+// angle of at most an eighth of a turn either side.
 //
-// vectors_kernel: rows whose elements come in whole vectors.  A unit is two
-// vectors: the two members of V pairs (i, i + dims / 2), or V interleaved pairs
-// one behind the other, or two vectors that are not rotated.  L lanes (a power of
-// two) take a row's units, one to four each, held in registers, and walk through
-// several heads of a token with its cosines, sines and weights.  Norms are sums
-// over the L lanes.  A lane alone reads and writes its elements, so that y may be
-// x (what neither changes is then not touched).  The backward kernel's groups of
-// lanes walk through (token, heads) items and keep their share of dweight in
-// registers; a CTA adds its groups' in a fixed order and leaves one partial sum.
+// vectors_kernel: rows whose elements come in whole vectors.  A lane holds one
+// unit of a row, two vectors: the two members of V pairs (i, i + dims / 2), or V
+// interleaved pairs one behind the other, or two vectors that are not rotated.  L
+// lanes (a power of two, up to the whole CTA) take a row and walk through several
+// heads of a token, with its angles: forward as the 2 x 2 coefficients of a pair
+// with the members' weights in them, so that a normed and rotated element costs
+// three operations.  Norms are sums over the L lanes.  A lane alone reads and
+// writes its elements, so that y may be x (what neither changes is then not
+// touched).  The backward kernel's lanes keep their share of dweight in registers;
+// a CTA adds its groups' in a fixed order and leaves one partial sum.
 // Bound by the bytes of x and y.
 //
 // rows_kernel: a CTA a row, any sizes and alignments.  A first pass over the
@@ -33,20 +34,30 @@ namespace {
 __device__ unsigned int g_status = 0;
 constexpr int kRowThreads = 128;
 // Blocks of the backward kernels an SM, each with its partial sums of dweight.
-constexpr int kGradBlocks = 4;
+constexpr int kGradBlocks = 2;
 
 __device__ __forceinline__ float value(float v) { return v; }
 template <typename T> __device__ __forceinline__ float value(T v) { return to_float(v); }
 __device__ __forceinline__ void put(float& o, float v) { o = v; }
 template <typename T> __device__ __forceinline__ void put(T& o, float v) { o = from_float<T>(v); }
 
-// magnitude * cosine and sine of position * step.
+// magnitude * cosine and sine of position * step.  Within an eighth of a turn the
+// Taylor polynomials of degree 9 and 10 are exact to 2^-29.
 __device__ __forceinline__ float2 turn(int position, uint64_t step, float magnitude) {
     const uint64_t phase = (uint64_t)(int64_t)position * step;
     const uint32_t q = (uint32_t)((phase + (1ull << 61)) >> 62);         // the nearest quarter turn
-    const float x = (float)(int64_t)(phase - ((uint64_t)q << 62)) * 1.0842021724855044e-19f;   // half turns: 2^-63
-    float s, c;
-    sincospif(x, &s, &c);
+    // What is left, in radians: 2 pi / 2^64.
+    const float x = (float)(int64_t)(phase - ((uint64_t)q << 62)) * 3.4061215800304626e-19f;
+    const float z = x * x;
+    float s = fmaf(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);  // 1/9!, 1/7!, 1/5!, 1/3!
+    s = fmaf(z, s, 8.3333333333333332e-3f);
+    s = fmaf(z, s, -1.6666666666666666e-1f);
+    s = fmaf(z * x, s, x);
+    float c = fmaf(z, -2.7557319223985888e-7f, 2.4801587301587302e-5f);  // 1/10!, 1/8!, 1/6!, 1/4!, 1/2!
+    c = fmaf(z, c, -1.3888888888888889e-3f);
+    c = fmaf(z, c, 4.1666666666666664e-2f);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.0f);
     const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
     return make_float2(q == 1 || q == 2 ? -magnitude * cs : magnitude * cs, q & 2 ? -magnitude * sn : magnitude * sn);
 }
@@ -202,80 +213,73 @@ template <typename T, int V> struct alignas(V * sizeof(T)) Vec {
     }
 };
 
-// (a, b) turned by the angles of V pairs, or back: b's members are the pairs'
-// second ones, or each vector holds V / 2 pairs of its own.
-template <int V, bool kBack>
-__device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float2 (&cs)[V], bool interleaved) {
-    auto pair = [&](float& u, float& v, const float2& c) {
-        const float x = u, y = v, s = kBack ? -c.y : c.y;
-        u = fmaf(x, c.x, -y * s);
-        v = fmaf(x, s, y * c.x);
-    };
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            pair(a[2 * i], a[2 * i + 1], cs[i]);
-            pair(b[2 * i], b[2 * i + 1], cs[V / 2 + i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) pair(a[i], b[i], cs[i]);
+// Sums of x and y over a row's lanes, the same in all of them.  Rows of more than a
+// warp meet in shared memory, in one of two buffers in turns.
+__device__ __forceinline__ float2 row_sums(float2 v, int L, float2 (&shared)[2][kVecThreads / 32], int& turns) {
+    for (int o = min(L, 32) >> 1; o; o >>= 1) {
+        v.x += __shfl_xor_sync(~0u, v.x, o);
+        v.y += __shfl_xor_sync(~0u, v.y, o);
     }
+    if (L > 32) {
+        float2 (&now)[kVecThreads / 32] = shared[turns++ & 1];
+        const int warp = threadIdx.x >> 5, first = warp & ~((L >> 5) - 1);
+        if ((threadIdx.x & 31) == 0) now[warp] = v;
+        __syncthreads();
+        v = now[first];
+        for (int w = 1; w < L >> 5; ++w) {
+            v.x += now[first + w].x;
+            v.y += now[first + w].y;
+        }
+    }
+    return v;
 }
 
-template <typename T, int V, int KU, bool kBackward>
-__global__ void __launch_bounds__(kVecThreads) vectors_kernel(const __grid_constant__ RopeProblem p,
-                                                              const __grid_constant__ VecPlan plan) {
+template <typename T, int V, bool kBackward>
+__global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel(const __grid_constant__ RopeProblem p,
+                                                                                 const __grid_constant__ VecPlan plan) {
     using W = Vec<T, V>;
     extern __shared__ float dsum[];
+    __shared__ float2 meet[2][kVecThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int n = 0;
+    int n = 0, turns = 0;
     while (n + 1 < p.n_parts && (int)blockIdx.x >= plan.part[n + 1].first_block) ++n;
     const RopePart& a = p.part[n];
     const PartPlan& q = plan.part[n];
-    const int L = 1 << q.log_lanes, lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5;
-    const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));
+    const int L = 1 << q.log_lanes, u = threadIdx.x & (L - 1), warp = threadIdx.x >> 5;
     const float inv_norm = a.norm ? 1.0f / a.norm : 0.0f;
-    // This lane's units: where their vectors lie, and what happens to them.
-    int o1[KU], o2[KU];
-    bool turned[KU], has1[KU], has2[KU], norm1[KU], norm2[KU];
-    W w1[KU], w2[KU];
-    float sw1[kBackward ? KU : 1][V], sw2[kBackward ? KU : 1][V];      // shares of dweight
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < KU; ++k) {
-        const int u = lane + (k << q.log_lanes);
-        turned[k] = u < q.rotated;
-        if (turned[k]) {
-            o1[k] = a.start + u * (p.interleaved ? 2 * V : V);
-            o2[k] = o1[k] + (p.interleaved ? V : p.dims / 2);
-            has1[k] = has2[k] = true;
-        } else {
-            const int e1 = 2 * (u - q.rotated) * V, e2 = e1 + V, rest = a.D - p.dims;
-            o1[k] = e1 < a.start ? e1 : e1 + p.dims;
-            o2[k] = e2 < a.start ? e2 : e2 + p.dims;
-            has1[k] = u < q.units && e1 < rest;
-            has2[k] = u < q.units && e2 < rest;
-        }
-        norm1[k] = has1[k] && o1[k] < a.norm;
-        norm2[k] = has2[k] && o2[k] < a.norm;
-        if (q.in_place && !turned[k]) {      // what stays as it is, where it is
-            has1[k] = norm1[k];
-            has2[k] = norm2[k];
-        }
-        const T* w = static_cast<const T*>(a.weight);
-        if (w && norm1[k] && dbg_in_bytes(w + o1[k], sizeof(W), a.sw, &g_status)) w1[k] = *reinterpret_cast<const W*>(w + o1[k]);
-        if (w && norm2[k] && dbg_in_bytes(w + o2[k], sizeof(W), a.sw, &g_status)) w2[k] = *reinterpret_cast<const W*>(w + o2[k]);
-        if constexpr (kBackward) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) sw1[k][i] = sw2[k][i] = 0.0f;
-        }
+    const bool interleaved = p.interleaved;
+    // This lane's unit: where its vectors lie, and what happens to them.
+    const bool turned = u < q.rotated;
+    int o1, o2;
+    bool has1, has2;
+    if (turned) {
+        o1 = a.start + u * (interleaved ? 2 * V : V);
+        o2 = o1 + (interleaved ? V : p.dims / 2);
+        has1 = has2 = true;
+    } else {
+        const int e1 = 2 * (u - q.rotated) * V, e2 = e1 + V, rest = a.D - p.dims;
+        o1 = e1 < a.start ? e1 : e1 + p.dims;
+        o2 = e2 < a.start ? e2 : e2 + p.dims;
+        has1 = u < q.units && e1 < rest;
+        has2 = u < q.units && e2 < rest;
     }
-    // Sum over a row's lanes, the same in all of them.
-    auto row_sum = [&](float v) {
-        for (int o = L >> 1; o; o >>= 1) v += __shfl_xor_sync(group_mask, v, o);
-        return v;
-    };
+    const bool norm1 = has1 && o1 < a.norm, norm2 = has2 && o2 < a.norm;
+    if (q.in_place && !turned) {             // what stays as it is, where it is
+        has1 = norm1;
+        has2 = norm2;
+    }
+    // One member of a pair normed, the other not: norms before the rotation.
+    const bool mixed = turned && !interleaved && norm1 != norm2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float w1[V], w2[V];                      // weights, 1 where there are none
+    {
+        const T* w = static_cast<const T*>(a.weight);
+#pragma unroll
+        for (int i = 0; i < V; ++i) w1[i] = w2[i] = 1.0f;
+        if (w && norm1 && dbg_in_bytes(w + o1, sizeof(W), a.sw, &g_status)) reinterpret_cast<const W*>(w + o1)->get(w1);
+        if (w && norm2 && dbg_in_bytes(w + o2, sizeof(W), a.sw, &g_status)) reinterpret_cast<const W*>(w + o2)->get(w2);
+    }
+    float sw1[V] = {}, sw2[V] = {};          // shares of dweight
     auto load = [&](const T* at, const ByteSpan& s, bool there, W& v) {
         if (there && dbg_in_bytes(at, sizeof(W), s, &g_status)) v = *reinterpret_cast<const W*>(at);
         else
@@ -288,20 +292,29 @@ __global__ void __launch_bounds__(kVecThreads) vectors_kernel(const __grid_const
         if (there && dbg_in_bytes(at, sizeof(W), a.sy, &g_status)) *reinterpret_cast<W*>(at) = v;
     };
 
-    const int64_t items = p.tokens * q.chunks, groups = (int64_t)q.blocks * (kVecThreads >> q.log_lanes);
-    for (int64_t it = (int64_t)(blockIdx.x - q.first_block) * (kVecThreads >> q.log_lanes) + (threadIdx.x >> q.log_lanes);
-         it < items; it += groups) {
-        const int64_t t = it / q.chunks;
-        const int h0 = (int)(it - t * q.chunks) * q.heads_each, h1 = min(a.heads, h0 + q.heads_each);
-        float2 cs[KU][V];
-        if (q.rotated) {
+    // (All of a CTA's groups go the same number of times round, as they meet at barriers.)
+    const int64_t items = p.tokens * q.chunks;
+    const int per = kVecThreads >> q.log_lanes, mine = threadIdx.x >> q.log_lanes;
+    for (int64_t i0 = (int64_t)(blockIdx.x - q.first_block) * per; i0 < items; i0 += (int64_t)q.blocks * per) {
+        const int64_t it = min(i0 + mine, items - 1), t = it / q.chunks;
+        const int h0 = (int)(it - t * q.chunks) * q.heads_each, h1 = i0 + mine < items ? min(a.heads, h0 + q.heads_each) : h0;
+        // A pair's first member is x.x a + x.y b, its second one x.z a + x.w b.
+        float4 m[kBackward ? 1 : V];
+        float2 cs[kBackward ? V : 1];
+        if (turned) {
             const int position = p.positions[t];
+            const uint64_t* steps = p.steps + u * V;
 #pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                if (!turned[k]) continue;
-                const uint64_t* steps = p.steps + (lane + (k << q.log_lanes)) * V;
-#pragma unroll
-                for (int i = 0; i < V; ++i) cs[k][i] = turn(position, steps[i], p.magnitude);
+            for (int i = 0; i < V; ++i) {
+                const float2 c = turn(position, steps[i], p.magnitude);
+                if constexpr (kBackward) {
+                    cs[i] = c;
+                } else {
+                    constexpr int H = V / 2;
+                    const float wa = mixed ? 1.0f : !interleaved ? w1[i] : i < H ? w1[2 * i] : w2[2 * (i - H)];
+                    const float wb = mixed ? 1.0f : !interleaved ? w2[i] : i < H ? w1[2 * i + 1] : w2[2 * (i - H) + 1];
+                    m[i] = make_float4(c.x * wa, -c.y * wb, c.y * wa, c.x * wb);
+                }
             }
         }
         const T* in = kBackward ? static_cast<const T*>(a.dy) + t * a.tsD : static_cast<const T*>(a.x) + t * a.tsX;
@@ -309,132 +322,142 @@ __global__ void __launch_bounds__(kVecThreads) vectors_kernel(const __grid_const
         const ByteSpan& span = kBackward ? a.sd : a.sx;
         const T* x = static_cast<const T*>(a.x) + t * a.tsX;
         T* y = static_cast<T*>(a.y) + t * a.tsY;
-        W r1[KU], r2[KU], x1[kBackward ? KU : 1], x2[kBackward ? KU : 1];
+        W r1, r2, x1, x2;
         auto fetch = [&](int h) {
-#pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                load(in + h * hs + o1[k], span, has1[k], r1[k]);
-                load(in + h * hs + o2[k], span, has2[k], r2[k]);
-                if constexpr (kBackward) {
-                    load(x + h * a.hsX + o1[k], a.sx, norm1[k], x1[k]);
-                    load(x + h * a.hsX + o2[k], a.sx, norm2[k], x2[k]);
-                }
+            load(in + h * hs + o1, span, has1 && h < h1, r1);
+            load(in + h * hs + o2, span, has2 && h < h1, r2);
+            if constexpr (kBackward) {
+                load(x + h * a.hsX + o1, a.sx, norm1 && h < h1, x1);
+                load(x + h * a.hsX + o2, a.sx, norm2 && h < h1, x2);
             }
         };
         fetch(h0);
-        for (int h = h0; h < h1; ++h) {
-            float f1[KU][V], f2[KU][V], g1[kBackward ? KU : 1][V], g2[kBackward ? KU : 1][V];
-#pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                r1[k].get(f1[k]);
-                r2[k].get(f2[k]);
-                if constexpr (kBackward) {
-                    x1[k].get(g1[k]);
-                    x2[k].get(g2[k]);
-                }
-            }
-            // The next head's loads under this one's work.
-            if (h + 1 < h1) fetch(h + 1);
+        for (int hh = 0; hh < q.heads_each; ++hh) {
+            const int h = h0 + hh;
+            const bool live = h < h1;
+            float f1[V], f2[V];
+            r1.get(f1);
+            r2.get(f2);
             if constexpr (!kBackward) {
+                // The next head's loads under this one's work.
+                if (hh + 1 < q.heads_each) fetch(h + 1);
+                float r = 1.0f;
                 if (a.norm) {
                     float ss = 0.0f;
+                    if (norm1)
 #pragma unroll
-                    for (int k = 0; k < KU; ++k)
+                        for (int i = 0; i < V; ++i) ss = fmaf(f1[i], f1[i], ss);
+                    if (norm2)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (norm1[k]) ss = fmaf(f1[k][i], f1[k][i], ss);
-                            if (norm2[k]) ss = fmaf(f2[k][i], f2[k][i], ss);
+                        for (int i = 0; i < V; ++i) ss = fmaf(f2[i], f2[i], ss);
+                    r = rsqrtf(fmaf(row_sums(make_float2(ss, 0.0f), L, meet, turns).x, inv_norm, p.eps));
+                }
+                if (mixed || !turned) {
+                    // (In both cases each vector is normed with its weights or not.)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        if (norm1) f1[i] *= r * w1[i];
+                        if (norm2) f2[i] *= r * w2[i];
+                    }
+                }
+                if (turned) {
+                    const float ra = norm1 && !mixed ? r : 1.0f, rb = norm2 && !mixed ? r : 1.0f;
+                    if (interleaved) {
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const float4 c = m[i], d = m[V / 2 + i];
+                            const float a0 = f1[2 * i], a1 = f1[2 * i + 1], b0 = f2[2 * i], b1 = f2[2 * i + 1];
+                            f1[2 * i] = ra * fmaf(a0, c.x, a1 * c.y);
+                            f1[2 * i + 1] = ra * fmaf(a0, c.z, a1 * c.w);
+                            f2[2 * i] = rb * fmaf(b0, d.x, b1 * d.y);
+                            f2[2 * i + 1] = rb * fmaf(b0, d.z, b1 * d.w);
                         }
-                    const float r = rsqrtf(fmaf(row_sum(ss), inv_norm, p.eps));
-#pragma unroll
-                    for (int k = 0; k < KU; ++k) {
-                        float u[V], v[V];
-                        w1[k].get(u);
-                        w2[k].get(v);
+                    } else {
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            if (norm1[k]) f1[k][i] *= a.weight ? r * u[i] : r;
-                            if (norm2[k]) f2[k][i] *= a.weight ? r * v[i] : r;
+                            const float4 c = m[i];
+                            const float a0 = f1[i], b0 = f2[i];
+                            f1[i] = ra * fmaf(a0, c.x, b0 * c.y);
+                            f2[i] = rb * fmaf(a0, c.z, b0 * c.w);
                         }
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < KU; ++k)
-                    if (turned[k]) rotate<V, false>(f1[k], f2[k], cs[k], p.interleaved);
             } else {
+                float g1[V], g2[V];
+                x1.get(g1);
+                x2.get(g2);
+                if (hh + 1 < q.heads_each) fetch(h + 1);
+                if (turned) {
+                    auto back = [](float& c, float& d, const float2& z) {
+                        const float u0 = c, v0 = d;
+                        c = fmaf(u0, z.x, v0 * z.y);
+                        d = fmaf(v0, z.x, -u0 * z.y);
+                    };
 #pragma unroll
-                for (int k = 0; k < KU; ++k)
-                    if (turned[k]) rotate<V, true>(f1[k], f2[k], cs[k], p.interleaved);
-                if (a.norm) {
-                    // x (in g) to the normed x, and the mean of g w x.
-                    float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < KU; ++k) {
-                        float u[V], v[V];
-                        w1[k].get(u);
-                        w2[k].get(v);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (norm1[k]) {
-                                ss = fmaf(g1[k][i], g1[k][i], ss);
-                                dot = fmaf(a.weight ? f1[k][i] * u[i] : f1[k][i], g1[k][i], dot);
-                            }
-                            if (norm2[k]) {
-                                ss = fmaf(g2[k][i], g2[k][i], ss);
-                                dot = fmaf(a.weight ? f2[k][i] * v[i] : f2[k][i], g2[k][i], dot);
-                            }
-                        }
-                    }
-                    const float r = rsqrtf(fmaf(row_sum(ss), inv_norm, p.eps));
-                    const float mean = row_sum(dot) * r * inv_norm;
-#pragma unroll
-                    for (int k = 0; k < KU; ++k) {
-                        float u[V], v[V];
-                        w1[k].get(u);
-                        w2[k].get(v);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (norm1[k]) {
-                                const float z = g1[k][i] * r;
-                                sw1[k][i] = fmaf(f1[k][i], z, sw1[k][i]);
-                                f1[k][i] = r * fmaf(-z, mean, a.weight ? f1[k][i] * u[i] : f1[k][i]);
-                            }
-                            if (norm2[k]) {
-                                const float z = g2[k][i] * r;
-                                sw2[k][i] = fmaf(f2[k][i], z, sw2[k][i]);
-                                f2[k][i] = r * fmaf(-z, mean, a.weight ? f2[k][i] * v[i] : f2[k][i]);
-                            }
+                    for (int i = 0; i < V / 2; ++i) {
+                        if (interleaved) {
+                            back(f1[2 * i], f1[2 * i + 1], cs[i]);
+                            back(f2[2 * i], f2[2 * i + 1], cs[V / 2 + i]);
+                        } else {
+                            back(f1[i], f2[i], cs[i]);
+                            back(f1[V / 2 + i], f2[V / 2 + i], cs[V / 2 + i]);
                         }
                     }
                 }
-            }
+                if (a.norm) {
+                    // Sums of x^2 and g w x; then dweight's share and dx.
+                    float2 sums = make_float2(0.0f, 0.0f);
+                    if (norm1)
 #pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                store(y + h * a.hsY + o1[k], has1[k], f1[k]);
-                store(y + h * a.hsY + o2[k], has2[k], f2[k]);
+                        for (int i = 0; i < V; ++i) {
+                            sums.x = fmaf(g1[i], g1[i], sums.x);
+                            sums.y = fmaf(f1[i] * w1[i], g1[i], sums.y);
+                        }
+                    if (norm2)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            sums.x = fmaf(g2[i], g2[i], sums.x);
+                            sums.y = fmaf(f2[i] * w2[i], g2[i], sums.y);
+                        }
+                    sums = row_sums(sums, L, meet, turns);
+                    const float r = rsqrtf(fmaf(sums.x, inv_norm, p.eps)), mean = sums.y * r * inv_norm;
+                    if (norm1)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float z = g1[i] * r;
+                            sw1[i] = fmaf(f1[i], z, sw1[i]);
+                            f1[i] = r * fmaf(-z, mean, f1[i] * w1[i]);
+                        }
+                    if (norm2)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float z = g2[i] * r;
+                            sw2[i] = fmaf(f2[i], z, sw2[i]);
+                            f2[i] = r * fmaf(-z, mean, f2[i] * w2[i]);
+                        }
+                }
             }
+            store(y + h * a.hsY + o1, has1 && live, f1);
+            store(y + h * a.hsY + o2, has2 && live, f2);
         }
     }
     if constexpr (kBackward) {
         if (!p.workspace || !a.norm || !a.dweight) return;
         // A warp's groups in a tree, then the warps one behind the other.
 #pragma unroll
-        for (int k = 0; k < KU; ++k)
+        for (int i = 0; i < V; ++i)
+            for (int o = L; o < 32; o <<= 1) {
+                sw1[i] += __shfl_xor_sync(~0u, sw1[i], o);
+                sw2[i] += __shfl_xor_sync(~0u, sw2[i], o);
+            }
+        const int row_warps = max(1, L >> 5);
+        for (int w = 0; w < kVecThreads / 32; w += row_warps) {
+            if (warp / row_warps * row_warps == w && (threadIdx.x & 31) < L) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                for (int o = L; o < 32; o <<= 1) {
-                    sw1[k][i] += __shfl_xor_sync(~0u, sw1[k][i], o);
-                    sw2[k][i] += __shfl_xor_sync(~0u, sw2[k][i], o);
+                for (int i = 0; i < V; ++i) {
+                    if (norm1) dsum[o1 + i] = (w ? dsum[o1 + i] : 0.0f) + sw1[i];
+                    if (norm2) dsum[o2 + i] = (w ? dsum[o2 + i] : 0.0f) + sw2[i];
                 }
-        for (int w = 0; w < kVecThreads / 32; ++w) {
-            if (warp == w && (threadIdx.x & 31) < L) {
-#pragma unroll
-                for (int k = 0; k < KU; ++k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        if (norm1[k]) dsum[o1[k] + i] = (w ? dsum[o1[k] + i] : 0.0f) + sw1[k][i];
-                        if (norm2[k]) dsum[o2[k] + i] = (w ? dsum[o2[k] + i] : 0.0f) + sw2[k][i];
-                    }
             }
             __syncthreads();
         }
@@ -445,8 +468,10 @@ __global__ void __launch_bounds__(kVecThreads) vectors_kernel(const __grid_const
 
 // dweight: the blocks' partial sums in order, in 64 bits (131072 rows of fp32
 // sums keep an error of some 2^-22 of theirs then).
-__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ RopeProblem p, const __grid_constant__ VecPlan plan) {
-    __shared__ double sums[8][32];
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ RopeProblem p,
+                                                             const __grid_constant__ VecPlan plan) {
+    __shared__ double sums[kSumWarps][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 32 + lane;
@@ -455,14 +480,20 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ RopePr
     if (e < plan.columns) {
         while (n + 1 < p.n_parts && e >= plan.part[n + 1].column) ++n;
         const int last = plan.part[n].first_block + plan.part[n].blocks;
+        const float* at = p.workspace + e;
         if (p.part[n].dweight)
-            for (int b = plan.part[n].first_block + warp; b < last; b += 8)
-                s += (double)p.workspace[(int64_t)b * plan.columns + e];
+            for (int b = plan.part[n].first_block + warp; b < last; b += 4 * kSumWarps) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = b + i * kSumWarps < last ? at[(int64_t)(b + i * kSumWarps) * plan.columns] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s += (double)v[i];
+            }
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || e >= plan.columns || !p.part[n].dweight) return;
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    for (int w = 1; w < kSumWarps; ++w) s += sums[w][lane];
     float* out = p.part[n].dweight + (e - plan.part[n].column);
     if (dbg_in_bytes(out, 4, p.part[n].sdw, &g_status)) *out = (float)(p.accumulate ? s + (double)*out : s);
 }
@@ -510,38 +541,36 @@ int columns_of(const RopeProblem& p, VecPlan* plan) {
 
 cudaError_t launch_sum(const RopeProblem& p, const VecPlan& plan, cudaStream_t stream) {
     if (!p.workspace) return cudaSuccess;
-    return start(sum_kernel, (plan.columns + 31) / 32, 256, 0, stream, p, plan);
+    return start(sum_kernel, (plan.columns + 31) / 32, kSumWarps * 32, 0, stream, p, plan);
 }
 
-template <typename T, int V, int KU>
+template <typename T, int V>
 cudaError_t launch_vectors(const RopeProblem& p, bool backward, const VecPlan& plan, int64_t blocks, cudaStream_t stream) {
-    if (!backward) return start(vectors_kernel<T, V, KU, false>, blocks, kVecThreads, 0, stream, p, plan);
+    if (!backward) return start(vectors_kernel<T, V, false>, blocks, kVecThreads, 0, stream, p, plan);
     int most = 0;
     for (int i = 0; i < p.n_parts; ++i) most = std::max(most, p.part[i].norm);
-    if (const cudaError_t e = start(vectors_kernel<T, V, KU, true>, blocks, kVecThreads, most * sizeof(float), stream, p, plan))
+    if (const cudaError_t e = start(vectors_kernel<T, V, true>, blocks, kVecThreads, most * sizeof(float), stream, p, plan))
         return e;
     return launch_sum(p, plan, stream);
 }
 
-// Lays the arrays out over CTAs; false when a row has more units than its lanes hold.
+// Lays the arrays out over CTAs; false when a row has more units than a CTA has lanes.
 template <typename T, int V>
 bool try_vectors(const RopeProblem& p, bool backward, int sms, cudaStream_t stream, cudaError_t* err) {
     VecPlan plan{};
     columns_of(p, &plan);
-    int most = 1;
     int64_t threads = 0;             // lanes of all rows
     for (int i = 0; i < p.n_parts; ++i) {
         const RopePart& a = p.part[i];
         PartPlan& q = plan.part[i];
         q.rotated = p.dims / 2 / V;
         q.units = q.rotated + ((a.D - p.dims) / V + 1) / 2;
+        if (q.units > kVecThreads) return false;
         q.log_lanes = 0;
-        while (q.log_lanes < 5 && (1 << q.log_lanes) < q.units) ++q.log_lanes;
-        most = std::max(most, (q.units + 31) / 32);
+        while ((1 << q.log_lanes) < q.units) ++q.log_lanes;
         q.in_place = backward ? a.y == a.dy : a.y == a.x;
         threads += (p.tokens * a.heads) << q.log_lanes;
     }
-    if (most > 4) return false;
     // Heads an item: as many as leave every SM its threads, since each item works out
     // its angles anew (at most 16, all of a token's rows in flight being enough).
     const int64_t want = (int64_t)sms * (backward ? kGradBlocks * kVecThreads : 2048);
@@ -564,9 +593,7 @@ bool try_vectors(const RopeProblem& p, bool backward, int sms, cudaStream_t stre
         q.blocks = (int)mine;
         blocks += mine;
     }
-    *err = most == 1 ? launch_vectors<T, V, 1>(p, backward, plan, blocks, stream)
-         : most == 2 ? launch_vectors<T, V, 2>(p, backward, plan, blocks, stream)
-                     : launch_vectors<T, V, 4>(p, backward, plan, blocks, stream);
+    *err = launch_vectors<T, V>(p, backward, plan, blocks, stream);
     return true;
 }
 
