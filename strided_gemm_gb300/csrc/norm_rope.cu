@@ -213,23 +213,22 @@ template <typename T, int V> struct alignas(V * sizeof(T)) Vec {
     }
 };
 
-// Sums of x and y over a row's lanes, the same in all of them.  Rows of more than a
-// warp meet in shared memory, in one of two buffers in turns.
-__device__ __forceinline__ float2 row_sums(float2 v, int L, float2 (&shared)[2][kVecThreads / 32], int& turns) {
-    for (int o = min(L, 32) >> 1; o; o >>= 1) {
-        v.x += __shfl_xor_sync(~0u, v.x, o);
-        v.y += __shfl_xor_sync(~0u, v.y, o);
-    }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float other(float v, int o) { return __shfl_xor_sync(~0u, v, o); }
+__device__ __forceinline__ float2 other(float2 v, int o) { return make_float2(other(v.x, o), other(v.y, o)); }
+// The sum (or two sums) over a row's lanes, the same in all of them.  Rows of more
+// than a warp meet in shared memory, in one of two buffers in turns.
+template <typename F>
+__device__ __forceinline__ F row_sums(F v, int L, float2 (&shared)[2][kVecThreads / 32], int& turns) {
+    for (int o = min(L, 32) >> 1; o; o >>= 1) v = plus(v, other(v, o));
     if (L > 32) {
-        float2 (&now)[kVecThreads / 32] = shared[turns++ & 1];
+        float2* now = shared[turns++ & 1];
         const int warp = threadIdx.x >> 5, first = warp & ~((L >> 5) - 1);
-        if ((threadIdx.x & 31) == 0) now[warp] = v;
+        if ((threadIdx.x & 31) == 0) *reinterpret_cast<F*>(&now[warp]) = v;
         __syncthreads();
-        v = now[first];
-        for (int w = 1; w < L >> 5; ++w) {
-            v.x += now[first + w].x;
-            v.y += now[first + w].y;
-        }
+        v = *reinterpret_cast<const F*>(&now[first]);
+        for (int w = 1; w < L >> 5; ++w) v = plus(v, *reinterpret_cast<const F*>(&now[first + w]));
     }
     return v;
 }
@@ -317,30 +316,38 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
                 }
             }
         }
-        const T* in = kBackward ? static_cast<const T*>(a.dy) + t * a.tsD : static_cast<const T*>(a.x) + t * a.tsX;
+        // Places of this head's vectors, moved on head by head.
         const int64_t hs = kBackward ? a.hsD : a.hsX;
+        const T* in = (kBackward ? static_cast<const T*>(a.dy) + t * a.tsD : static_cast<const T*>(a.x) + t * a.tsX) + h0 * hs;
+        const T *in1 = in + o1, *in2 = in + o2;
+        const T* x = static_cast<const T*>(a.x) + t * a.tsX + h0 * a.hsX;
+        const T *xn1 = x + o1, *xn2 = x + o2;
+        T* y = static_cast<T*>(a.y) + t * a.tsY + h0 * a.hsY;
+        T *out1 = y + o1, *out2 = y + o2;
         const ByteSpan& span = kBackward ? a.sd : a.sx;
-        const T* x = static_cast<const T*>(a.x) + t * a.tsX;
-        T* y = static_cast<T*>(a.y) + t * a.tsY;
         W r1, r2, x1, x2;
-        auto fetch = [&](int h) {
-            load(in + h * hs + o1, span, has1 && h < h1, r1);
-            load(in + h * hs + o2, span, has2 && h < h1, r2);
+        auto fetch = [&](bool there) {
+            load(in1, span, has1 && there, r1);
+            load(in2, span, has2 && there, r2);
+            in1 += hs;
+            in2 += hs;
             if constexpr (kBackward) {
-                load(x + h * a.hsX + o1, a.sx, norm1 && h < h1, x1);
-                load(x + h * a.hsX + o2, a.sx, norm2 && h < h1, x2);
+                load(xn1, a.sx, norm1 && there, x1);
+                load(xn2, a.sx, norm2 && there, x2);
+                xn1 += a.hsX;
+                xn2 += a.hsX;
             }
         };
-        fetch(h0);
-        for (int hh = 0; hh < q.heads_each; ++hh) {
-            const int h = h0 + hh;
-            const bool live = h < h1;
+        const int count = h1 - h0;
+        fetch(count > 0);
+        for (int h = 0; h < q.heads_each; ++h) {
+            const bool live = h < count;
             float f1[V], f2[V];
             r1.get(f1);
             r2.get(f2);
             if constexpr (!kBackward) {
                 // The next head's loads under this one's work.
-                if (hh + 1 < q.heads_each) fetch(h + 1);
+                if (h + 1 < q.heads_each) fetch(h + 1 < count);
                 float r = 1.0f;
                 if (a.norm) {
                     float ss = 0.0f;
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
                     if (norm2)
 #pragma unroll
                         for (int i = 0; i < V; ++i) ss = fmaf(f2[i], f2[i], ss);
-                    r = rsqrtf(fmaf(row_sums(make_float2(ss, 0.0f), L, meet, turns).x, inv_norm, p.eps));
+                    r = rsqrtf(fmaf(row_sums(ss, L, meet, turns), inv_norm, p.eps));
                 }
                 if (mixed || !turned) {
                     // (In both cases each vector is normed with its weights or not.)
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
                 float g1[V], g2[V];
                 x1.get(g1);
                 x2.get(g2);
-                if (hh + 1 < q.heads_each) fetch(h + 1);
+                if (h + 1 < q.heads_each) fetch(h + 1 < count);
                 if (turned) {
                     auto back = [](float& c, float& d, const float2& z) {
                         const float u0 = c, v0 = d;
@@ -437,8 +444,10 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
                         }
                 }
             }
-            store(y + h * a.hsY + o1, has1 && live, f1);
-            store(y + h * a.hsY + o2, has2 && live, f2);
+            store(out1, has1 && live, f1);
+            store(out2, has2 && live, f2);
+            out1 += a.hsY;
+            out2 += a.hsY;
         }
     }
     if constexpr (kBackward) {
@@ -466,16 +475,26 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
     }
 }
 
-// dweight: the blocks' partial sums in order, in 64 bits (131072 rows of fp32
-// sums keep an error of some 2^-22 of theirs then).
-constexpr int kSumWarps = 16;
+// A sum and what its rounding lost (Knuth's two-sum): 48 bits without the slow
+// 64-bit units, whose latency 300 partial sums in order would pay.
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
+        hi = s;
+    }
+};
+
+// dweight: the blocks' partial sums in order.
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ RopeProblem p,
                                                              const __grid_constant__ VecPlan plan) {
-    __shared__ double sums[kSumWarps][32];
+    __shared__ float2 sums[kSumWarps][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 32 + lane;
-    double s = 0.0;
+    Sum s;
     int n = 0;
     if (e < plan.columns) {
         while (n + 1 < p.n_parts && e >= plan.part[n + 1].column) ++n;
@@ -487,15 +506,22 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = b + i * kSumWarps < last ? at[(int64_t)(b + i * kSumWarps) * plan.columns] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s += (double)v[i];
+                for (int i = 0; i < 4; ++i) s.add(v[i]);
             }
     }
-    sums[warp][lane] = s;
+    sums[warp][lane] = make_float2(s.hi, s.lo);
     __syncthreads();
     if (warp != 0 || e >= plan.columns || !p.part[n].dweight) return;
-    for (int w = 1; w < kSumWarps; ++w) s += sums[w][lane];
+#pragma unroll 8
+    for (int w = 1; w < kSumWarps; ++w) {
+        const float2 v = sums[w][lane];
+        s.add(v.x);
+        s.add(v.y);
+    }
     float* out = p.part[n].dweight + (e - plan.part[n].column);
-    if (dbg_in_bytes(out, 4, p.part[n].sdw, &g_status)) *out = (float)(p.accumulate ? s + (double)*out : s);
+    if (!dbg_in_bytes(out, 4, p.part[n].sdw, &g_status)) return;
+    if (p.accumulate) s.add(*out);
+    *out = fabsf(s.hi) < INFINITY ? s.hi + s.lo : s.hi;
 }
 
 template <typename... Args, typename... Given>
@@ -571,9 +597,9 @@ bool try_vectors(const RopeProblem& p, bool backward, int sms, cudaStream_t stre
         q.in_place = backward ? a.y == a.dy : a.y == a.x;
         threads += (p.tokens * a.heads) << q.log_lanes;
     }
-    // Heads an item: as many as leave every SM its threads, since each item works out
-    // its angles anew (at most 16, all of a token's rows in flight being enough).
-    const int64_t want = (int64_t)sms * (backward ? kGradBlocks * kVecThreads : 2048);
+    // Heads an item: as many as leave every SM its resident threads, since each item
+    // works out its angles anew.
+    const int64_t want = (int64_t)sms * (backward ? kGradBlocks : 3) * kVecThreads;
     const int64_t each = std::max<int64_t>(1, std::min<int64_t>(16, threads / want));
     int64_t blocks = 0;
     for (int i = 0; i < p.n_parts; ++i) {
