@@ -29,6 +29,12 @@
 // joins them in order.  The lists depend on the lengths alone, which the
 // device knows; no result depends on timing.
 //
+// Groups of sequences with a shared prefix (sbgemm_latent_attention_shared) run
+// as the same kernel over another list, made by a plan in latent_shared.cu: items of
+// up to NB query rows against a run of keys, a group's rows of all its sequences
+// against the prefix and each sequence's against its own keys. Every piece goes to
+// the workspace, a slot for each, and a join of its own adds up a row's pieces.
+//
 // Roles (12 warps): a warp for each of the 2 or 3 stages loads every second
 // or third block's rows, each run of rows inside a page looked up in the table
 // and fetched by TMA, one lane a run (a bad page's coordinate lies outside the
@@ -71,7 +77,7 @@ constexpr int kMaxChunks = 9;                // 64-wide pieces of a row: R <= 51
 constexpr int kMaxTiles = 4;                 // R / 128
 // Keys a block and stages of the ring, by query rows.
 template <int NB> struct Shape {
-    static constexpr int BT = NB == 64 ? 64 : 48;
+    static constexpr int BT = latent_block_keys(NB);
     static constexpr int kStages = NB == 64 ? 2 : 3;
     static constexpr int kChunkBytes = BT * 128;             // a piece of a block: BT rows of 128 swizzled bytes
 };
@@ -100,6 +106,7 @@ struct Params {
     uint32_t idesc_s, idesc_o;
     int o_vec;                               // rows of O take 8-byte stores
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
+    LatentItems shared;                      // shared prefixes: slot item + CTA for each piece
     ByteSpan sq, sc, so, sw;                 // debug builds: what Q, the cache, O and the workspace occupy
 };
 
@@ -112,6 +119,7 @@ struct Ctl {
     int scan[kWarps], rest[kWarps];
     alignas(16) float ref[NB];               // reference maxima
     alignas(16) float factor[NB];            // a rise's factors, then 1 / sum
+    int limit[NB], least[2];                 // shared prefixes: rows' last keys, and the least of them
     union alignas(16) {
         float part[4][NB];                   // maxima or sums of the four key quarters
         int64_t out[NB];                     // element offset of a row of O (-1: none)
@@ -150,31 +158,68 @@ __device__ __forceinline__ int seq_len(const Params& p, int s, bool report) {
 template <int BT>
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + BT - 1) / BT : 1; }
 
-// A CTA's walk over its run: pieces of sequences in order.
-template <int BT>
+// A CTA's walk over its run: pieces of sequences (or of items) in order.
+template <int BT, bool kShared>
 struct Walk {
     int seq, tile, left;     // the next piece begins at block `tile` of `seq`; units left
     int len, j0, j1;         // the piece: blocks j0 .. j1 - 1 of a sequence of `len` keys
     int s, units;            // its sequence and that one's units
+    int lo, item, first, row, rows;      // shared prefixes: first key, the item, its rows
     __device__ __forceinline__ bool next(const Params& p, bool report = false) {
-        if (left <= 0 || seq >= p.n_seqs) return false;
-        s = seq;
-        len = seq_len(p, s, report);
-        units = units_of<BT>(len);
-        j0 = tile;
-        const int n = min(units - tile, left);
-        j1 = len > 0 ? j0 + n : j0;
-        left -= n;
-        tile += n;
-        if (tile >= units) {
-            seq += p.split ? 1 : p.per_group;
-            tile = 0;
+        if constexpr (kShared) {
+            while (left > 0 && seq < p.shared.most) {
+                const LatentItem it = p.shared.items[seq];
+                item = seq;
+                s = it.table;
+                lo = it.lo;
+                len = it.hi;
+                first = it.seq;
+                row = it.row;
+                rows = it.rows;
+                const int n = min(it.units - tile, left);
+                j0 = it.lo / BT + tile;
+                j1 = j0 + n;
+                left -= n;
+                tile += n;
+                if (tile >= it.units) {
+                    ++seq;
+                    tile = 0;
+                }
+                if (n > 0) return true;
+            }
+            return false;
+        } else {
+            if (left <= 0 || seq >= p.n_seqs) return false;
+            s = seq;
+            len = seq_len(p, s, report);
+            units = units_of<BT>(len);
+            j0 = tile;
+            const int n = min(units - tile, left);
+            j1 = len > 0 ? j0 + n : j0;
+            left -= n;
+            tile += n;
+            if (tile >= units) {
+                seq += p.split ? 1 : p.per_group;
+                tile = 0;
+            }
+            return true;
         }
-        return true;
+    }
+    // Where row r of the piece's rows (of group `group`) is: sequence and row in it.
+    __device__ __forceinline__ bool place(const Params& p, int group, int NB, int r, int* of, int* in) const {
+        if constexpr (kShared) {
+            *of = first + (row + r) / p.rows;
+            *in = (row + r) % p.rows;
+            return r < rows;
+        } else {
+            *of = s;
+            *in = group * NB + r;
+            return *in < p.rows;
+        }
     }
 };
 
-template <typename T, int NB>
+template <typename T, int NB, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
     constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
@@ -210,7 +255,25 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
-    if (p.split) {
+    if constexpr (kShared) {
+        // The plan is there, and its items; each thread looks at some of them.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int total = p.shared.head[0], items = p.shared.head[1];
+        const int members = min(p.per_group, total);
+        const int lo = member < members ? (int)((int64_t)member * total / members) : 0;
+        const int hi = member < members ? (int)((int64_t)(member + 1) * total / members) : 0;
+        if (tid == 0) {
+            c.count = hi - lo;
+            if (hi == lo) c.seq0 = c.tile0 = 0;
+        }
+        for (int i = tid; i < items && hi > lo; i += kThreads) {
+            const int2 at = *reinterpret_cast<const int2*>(&p.shared.items[i]);
+            if (lo >= at.x && lo < at.x + at.y) {
+                c.seq0 = i;
+                c.tile0 = lo - at.x;
+            }
+        }
+    } else if (p.split) {
         // Units of this thread's sequence of the first round, and their sum over
         // the warp's lanes up to it; pools of more sequences look again below.
         const int u0 = tid < p.n_seqs ? units_of<BT>(seq_len(p, tid, false)) : 0;
@@ -271,7 +334,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = kTmemBase;
-    Walk<BT> w{c.seq0, c.tile0, c.count};
+    using Run = Walk<BT, kShared>;
+    Run w{c.seq0, c.tile0, c.count};
 
     if (warp < kStages) {
         // ---- rows of the cache into shared memory ---------------------------------
@@ -296,7 +360,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             for (int j = w.j0; j < w.j1; ++j, ++i) {
                 if (i % kStages != st) continue;
                 const uint32_t ph_empty = (uint32_t)((i / kStages - 1) & 1);
-                if (p.run && (j + 1) * BT <= w.len) {
+                const int lowest = kShared ? w.lo : 0;       // keys before are not the piece's
+                if (p.run && j * BT >= lowest && (j + 1) * BT <= w.len) {
                     // A whole block: lane x takes run x.
                     const int runs = BT / p.run, n = j * BT + lane * p.run;
                     int page = next_page;
@@ -337,7 +402,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 for (int g = 0; g < BT / 4; ++g) {
                     const int n = j * BT + r0 + 4 * g;
                     src[g] = nullptr;
-                    if (n < w.len) {
+                    if (n >= lowest && n < w.len) {
                         const int page = table[n / p.block_size];
                         if (page >= 0 && page < p.num_blocks)
                             src[g] = cache + 2 * (page * p.psC + (n % p.block_size) * p.rsC) + piece * 16;
@@ -378,6 +443,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             const uint32_t stage_bytes = p.chunks * kChunkBytes;
             int i = 0, filled = 0;           // blocks and pieces with blocks so far
             bool ok = true;
+            // Rows in use: all of NB, or as many 16 as an item has.
+            uint32_t idesc_s = p.idesc_s, idesc_o = p.idesc_o;
             auto scores = [&](int b) {       // S^T of block number b
                 tc_fence_after();
                 const uint32_t d = tmem + kColS + (b & 1) * NB;
@@ -385,12 +452,12 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 for (int k = 0; k < p.R / 64; ++k) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, (k | x) ? 1u : 0u);
+                        mma16_ss(d, da + x * kStepK, dq + x * kStepK, idesc_s, (k | x) ? 1u : 0u);
                     da += kChunkBytes >> 4;
                     dq += NB * 128 >> 4;
                 }
                 for (int x = 0; x < p.rope_steps; ++x)
-                    mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, 1u);
+                    mma16_ss(d, da + x * kStepK, dq + x * kStepK, idesc_s, 1u);
                 mma_commit(&c.s_full[b & 1]);
             };
             auto timed_out = [&](unsigned int code) {
@@ -400,6 +467,11 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             while (ok && w.next(p)) {
                 const int n = w.j1 - w.j0;
                 if (n == 0) continue;        // an empty sequence
+                if constexpr (kShared) {
+                    const uint32_t columns = (uint32_t)((w.rows + 15) / 16 * 2) << 17;
+                    idesc_s = (p.idesc_s & ~(0x3fu << 17)) | columns;
+                    idesc_o = (p.idesc_o & ~(0x3fu << 17)) | columns;
+                }
                 if (!bar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
                     !bar_wait(&c.full[i % kStages], (uint32_t)((i / kStages) & 1))) {
                     timed_out(kWaitFull);
@@ -433,7 +505,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         const uint64_t da = desc16(rows + 2 * t * kChunkBytes, kChunkBytes), dp = desc16(p_lo);
 #pragma unroll
                         for (int x = 0; x < BT / 16; ++x)
-                            mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
+                            mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, idesc_o,
                                      (j | x) ? 1u : 0u);
                     }
                     mma_commit(&c.empty[i % kStages]);
@@ -466,14 +538,15 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         int i = 0, piece_no = 0;                             // blocks and pieces so far
         bool ok = true;
         // Queries of the walk's piece on their way into shared memory.
-        auto fetch_queries = [&](const Walk<BT>& w) {
+        auto fetch_queries = [&](const Run& w) {
             if (w.j1 > w.j0) {
                 for (int x = m; x < NB * p.chunks * 8; x += 256) {
                     const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
-                    const int gr = group * NB + r, t = gr / p.heads, h = gr % p.heads;
-                    bool read = gr < p.rows && k < row_pieces;
+                    int of, gr;
+                    bool read = w.place(p, group, NB, r, &of, &gr) && k < row_pieces;
+                    const int t = gr / p.heads, h = gr % p.heads;
                     const T* src = static_cast<const T*>(p.Q);
-                    if (read) src += w.s * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
+                    if (read) src += of * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
                     read = read && dbg_in_bytes(src, 16, p.sq, &g_wait_status);
                     cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
                 }
@@ -485,9 +558,26 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         bool more = w.next(p, group == 0);
         if (more) fetch_queries(w);
         while (more) {
-            const Walk<BT> now = w;          // this piece; the walk looks one ahead
+            const Run now = w;               // this piece; the walk looks one ahead
             const int n = now.j1 - now.j0;
             if (m < NB) c.ref[m] = -INFINITY;
+            if constexpr (kShared) {
+                // Each row's last key here, -1 for rows that are none.
+                if (m < 64) {
+                    int last = INT32_MAX;
+                    if (m < NB) {
+                        int of, in;
+                        last = -1;
+                        if (now.place(p, group, NB, m, &of, &in)) {
+                            const int len = seq_len(p, of, false);
+                            last = min(now.len - 1, p.causal ? len - p.q_len + in / p.heads : len - 1);
+                        }
+                        c.limit[m] = last;
+                    }
+                    const int least = __reduce_min_sync(~0u, last);
+                    if (lane == 0) c.least[m >> 5] = least;
+                }
+            }
             if (n > 0) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
@@ -518,15 +608,18 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     }
                 }
                 const int first = (now.j0 + j) * BT;
-                const int safe = p.causal ? now.len - p.q_len : now.len - 1;    // keys up to here: every row's
+                // Keys up to here: every row's.
+                const int safe = kShared ? min(c.least[0], c.least[1]) : p.causal ? now.len - p.q_len : now.len - 1;
+                const bool early = kShared && first < now.lo;
                 if (!mine) {
 #pragma unroll
                     for (int x = 0; x < CPT; ++x) a[x] = -INFINITY;
-                } else if (first + BT - 1 > safe) {
+                } else if (first + BT - 1 > safe || early) {
 #pragma unroll
                     for (int x = 0; x < CPT; ++x) {
-                        int limit = now.len - 1;
-                        if (p.causal) {
+                        int limit = kShared ? c.limit[col + x] : now.len - 1;
+                        if (early && first + row < now.lo) limit = -1;
+                        if (!kShared && p.causal) {
                             const int r = group * NB + col + x;
                             if (r < p.rows) limit = safe + r / p.heads;
                         }
@@ -635,9 +728,11 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 if ((lane & 15) == 0) c.part[quarter][col + x] = v;
             }
             if (math_any(!ok)) break;
-            const bool whole = now.j0 == 0 && (now.len == 0 || now.j1 == now.units);
-            // A split sequence: this CTA's first piece goes to slot 0, its last to slot 1.
-            const int slot = 2 * blockIdx.x + (piece_no > 0 ? 1 : 0);
+            const bool whole = !kShared && now.j0 == 0 && (now.len == 0 || now.j1 == now.units);
+            // A split sequence: this CTA's first piece goes to slot 0, its last to slot
+            // 1.  Pieces of items one behind the other: each has the next slot.
+            const int slot = kShared ? now.item + (int)blockIdx.x : 2 * (int)blockIdx.x + (piece_no > 0 ? 1 : 0);
+            const int used = kShared ? now.rows : NB;
             float* part = p.parts + (int64_t)slot * NB * (2 + p.R);
             if (m < NB) {
                 const float sum = c.part[0][m] + c.part[1][m] + c.part[2][m] + c.part[3][m];
@@ -648,7 +743,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 }
             }
             math_sync();
-            if (m < NB) {
+            if (!kShared && m < NB) {
                 const int r = group * NB + m, t = r / p.heads, h = r % p.heads;
                 c.out[m] = r < p.rows ? now.s * p.bsO + t * p.tsO + h * p.hsO : -1;
             }
@@ -659,7 +754,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
 #pragma unroll 1
             for (int t = half; t < tiles_o; t += 2)
 #pragma unroll 1
-                for (int x0 = 0; x0 < NB; x0 += W) {
+                for (int x0 = 0; x0 < used; x0 += W) {
                     float o[W];
                     if (n > 0) tmem_ld<W>(tmem + lanes + kColO + t * NB + x0, o);
                     const int e = t * 128 + quarter * 32 + lane;
@@ -675,7 +770,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         float* dst = part + 2 * NB + (int64_t)x0 * p.R + e;
 #pragma unroll
                         for (int x = 0; x < W; ++x, dst += p.R)
-                            if (dbg_in_bytes(dst, 4, p.sw, &g_wait_status)) *dst = o[x];
+                            if ((!kShared || x0 + x < used) && dbg_in_bytes(dst, 4, p.sw, &g_wait_status)) *dst = o[x];
                     } else {
                         T* dst = static_cast<T*>(p.O) + e;
 #pragma unroll
@@ -926,9 +1021,110 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
     }
 }
 
-int rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Joins the pieces of shared prefixes: a row's are those of its part of the prefix
+// and of its sequence's own keys.  A CTA a row; R / 8 threads hold eight columns of a
+// piece each, the CTA's groups of them take the pieces in turns, four loads in
+// flight, and meet in shared memory in their order.
+template <typename T, int NB>
+__global__ void __launch_bounds__(kJoinThreads) join_shared_kernel(const __grid_constant__ Params p) {
+    __shared__ float4 sums[kJoinThreads][2];
+    __shared__ float tops[kJoinThreads / 16], ls[kJoinThreads / 16];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per_row = p.R / 8, groups = kJoinThreads / per_row;        // 16 to 64 threads; 4 to 16 groups
+    const int g = threadIdx.x / per_row, e = threadIdx.x % per_row * 8;
+    const bool mine = g < groups;
+    const int total = p.shared.head[0], members = min(p.per_group, total);
+    const int64_t slot_floats = (int64_t)NB * (2 + p.R), rows = (int64_t)p.n_seqs * p.rows;
+    // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
+    auto member_of = [&](int unit) { return (int)(((int64_t)(unit + 1) * members + total - 1) / total) - 1; };
+    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
+        const int s = (int)(at / p.rows), r = (int)(at % p.rows);
+        // First slot, row and pieces of the row's own keys and of its prefix.
+        int slot[2], in[2], count[2];
+        {
+            const int prefix = p.shared.prefix_item[s];
+            const int64_t row = (int64_t)(s - p.shared.first[s]) * p.rows + r;
+            const int item[2] = {s * p.shared.own + r / NB, prefix < 0 ? -1 : prefix + (int)(row / NB)};
+            in[0] = r % NB;
+            in[1] = (int)(row % NB);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                count[k] = slot[k] = 0;
+                if (item[k] < 0) continue;
+                const int2 units = *reinterpret_cast<const int2*>(&p.shared.items[item[k]]);
+                if (units.y <= 0) continue;
+                const int m = member_of(units.x);
+                slot[k] = item[k] + m;
+                count[k] = member_of(units.x + units.y - 1) - m + 1;
+            }
+        }
+        const int pieces = count[0] + count[1];
+        float top = -INFINITY, l = 0.0f;
+        float4 o0 = make_float4(0, 0, 0, 0), o1 = o0;
+        for (int k0 = mine ? g : pieces; k0 < pieces; k0 += 4 * groups) {
+            float mx[4], lx[4];
+            float4 v[4][2];
+            float now = top;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + q * groups, which = k >= count[0];
+                const float* src = p.parts + (int64_t)(slot[which] + (which ? k - count[0] : k)) * slot_floats;
+                mx[q] = -INFINITY;
+                lx[q] = 0.0f;
+                v[q][0] = v[q][1] = make_float4(0, 0, 0, 0);
+                if (k < pieces && dbg_in_bytes(src, 4 * slot_floats, p.sw, &g_wait_status)) {
+                    mx[q] = src[in[which]];
+                    lx[q] = src[NB + in[which]];
+                    const float4* o = reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)in[which] * p.R + e);
+                    v[q][0] = o[0];
+                    v[q][1] = o[1];
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) now = fmaxf(now, mx[q]);
+            const float f = top == -INFINITY ? 0.0f : exp2f(top - now);
+            l *= f;
+            o0 = scale4(o0, f);
+            o1 = scale4(o1, f);
+            top = now;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float w = mx[q] == -INFINITY ? 0.0f : exp2f(mx[q] - top);
+                l = fmaf(w, lx[q], l);
+                add4(o0, w, v[q][0]);
+                add4(o1, w, v[q][1]);
+            }
+        }
+        sums[threadIdx.x][0] = o0;
+        sums[threadIdx.x][1] = o1;
+        if (mine && e == 0) {
+            tops[g] = top;
+            ls[g] = l;
+        }
+        __syncthreads();
+        if (g == 0) {
+            const int in_use = min(groups, pieces);
+            for (int k = 1; k < in_use; ++k) top = fmaxf(top, tops[k]);
+            l = 0.0f;
+            o0 = o1 = make_float4(0, 0, 0, 0);
+            for (int k = 0; k < in_use; ++k) {
+                const float w = tops[k] == -INFINITY ? 0.0f : exp2f(tops[k] - top);
+                l = fmaf(w, ls[k], l);
+                add4(o0, w, sums[k * per_row + threadIdx.x][0]);
+                add4(o1, w, sums[k * per_row + threadIdx.x][1]);
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;               // no key: zeros
+            T* out = static_cast<T*>(p.O) + s * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
+            if (dbg_in_bytes(out, 8 * sizeof(T), p.so, &g_wait_status)) {
+                store4(out, scale4(o0, inv), p.o_vec);
+                store4(out + 4, scale4(o1, inv), p.o_vec);
+            }
+        }
+        __syncthreads();
+    }
+}
 
-size_t part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
+size_t part_bytes(int nb, int64_t R) { return latent_part_bytes(nb, R); }
 
 template <typename T, int NB>
 cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
@@ -939,12 +1135,12 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_done.load() & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)most_bytes);
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
-    decode_kernel<T, NB><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
+    decode_kernel<T, NB, false><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.split) {
         cudaLaunchAttribute early{};
@@ -978,16 +1174,13 @@ bool vec16(const void* base, int64_t a, int64_t b, int64_t c) {
 
 size_t latent_decode_workspace_bytes(int sms) { return 2 * (size_t)sms * part_bytes(64, 512); }
 
-bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err) {
-    if (a.R % 128 != 0 || a.R > 512 || a.P % 8 != 0 || a.P > 64) return false;
-    if (!vec16(a.Q, a.heads > 1 ? a.hsQ : 0, a.q_len > 1 ? a.tsQ : 0, a.n_seqs > 1 ? a.bsQ : 0) ||
-        !vec16(a.cache, a.block_size > 1 ? a.rsC : 0, a.num_blocks > 1 ? a.psC : 0, 0))
-        return false;
+namespace {
+
+// What the kernels' parameters have of a call, and the tensor map of its rows, for
+// `nb` query rows a block; false on a CUDA error.
+bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map) {
+    Params& p = *out;
     const int64_t rows = a.q_len * a.heads;
-    const int nb = rows_block(rows);
-    const int64_t groups = (rows + nb - 1) / nb;
-    if (groups > 65535 || (__int128)a.n_seqs * (a.N / 32 + 1) >= INT32_MAX) return false;
-    Params p{};
     p.Q = a.Q; p.hsQ = a.hsQ; p.tsQ = a.tsQ; p.bsQ = a.bsQ;
     p.cache = a.cache; p.rsC = a.rsC; p.psC = a.psC;
     p.table = a.table; p.seq_lens = a.seq_lens;
@@ -999,7 +1192,6 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     p.o_vec = reinterpret_cast<uintptr_t>(a.O) % 8 == 0 && a.hsO % 4 == 0 && a.tsO % 4 == 0 && a.bsO % 4 == 0;
     p.chunks = (int)(a.R / 64 + (a.P > 0));
     p.rope_steps = (int)((a.P + 15) / 16);
-    p.groups = (int)groups;
     p.scale_log2 = a.alpha * 1.4426950408889634f;
     p.causal = a.causal;
     p.sq = a.sq; p.sc = a.sc; p.so = a.so;
@@ -1009,8 +1201,7 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     p.idesc_o = idesc16(bf, nb, true, true);
     // Runs of rows that lie in one page wherever a block begins; whole groups
     // of 8 rows, the swizzle's period.
-    CUtensorMap map{};
-    int run = nb == 64 ? Shape<64>::BT : Shape<32>::BT;
+    int run = latent_block_keys(nb);
     for (const int bt = run; a.block_size % run != 0 || bt % run != 0;) --run;
     const int64_t row_stride = a.block_size > 1 ? a.rsC : (a.R + a.P + 7) / 8 * 8;
     const int64_t page_stride = a.num_blocks > 1 ? a.psC : row_stride;
@@ -1019,12 +1210,71 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         const uint64_t dims[3] = {(uint64_t)(a.R + a.P), (uint64_t)a.block_size, (uint64_t)a.num_blocks};
         const uint64_t strides[2] = {(uint64_t)row_stride * 2, (uint64_t)page_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)run, 1};
-        if (!encode_tmap_16(&map, a.cache, 3, dims, strides, box)) {
-            *err = cudaErrorInvalidValue;
-            return true;
-        }
+        if (!encode_tmap_16(map, a.cache, 3, dims, strides, box)) return false;
         p.run = run;
     }
+    return true;
+}
+
+// Sizes and alignments of the tensor-core kernels.
+bool takes(const LatentPaged& a) {
+    if (a.R % 128 != 0 || a.R > 512 || a.P % 8 != 0 || a.P > 64) return false;
+    return vec16(a.Q, a.heads > 1 ? a.hsQ : 0, a.q_len > 1 ? a.tsQ : 0, a.n_seqs > 1 ? a.bsQ : 0) &&
+           vec16(a.cache, a.block_size > 1 ? a.rsC : 0, a.num_blocks > 1 ? a.psC : 0, 0);
+}
+
+template <typename T, int NB>
+cudaError_t launch_shared(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    constexpr size_t most_bytes = smem_bytes<NB>(kMaxChunks);
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load() & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, NB, true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_bytes);
+        if (e != cudaSuccess) return e;
+        attr_done.fetch_or(bit);
+    }
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.per_group);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<NB>(p.chunks);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, NB, true>, map, p)) return e;
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)p.n_seqs * p.rows, (int64_t)sms * 8));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_shared_kernel<T, NB>, p);
+}
+
+template <typename T>
+cudaError_t launch_shared_rows(int nb, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch_shared<T, 16>(map, p, sms, stream);
+    if (nb == 32) return launch_shared<T, 32>(map, p, sms, stream);
+    return launch_shared<T, 64>(map, p, sms, stream);
+}
+
+}  // namespace
+
+bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cudaError_t* err) {
+    if (!takes(a)) return false;
+    const int64_t rows = a.q_len * a.heads;
+    const int nb = latent_rows_block(rows);
+    const int64_t groups = (rows + nb - 1) / nb;
+    if (groups > 65535 || (__int128)a.n_seqs * (a.N / 32 + 1) >= INT32_MAX) return false;
+    Params p{};
+    CUtensorMap map{};
+    if (!fill(a, nb, &p, &map)) {
+        *err = cudaErrorInvalidValue;
+        return true;
+    }
+    p.groups = (int)groups;
     // CTAs for each group of rows: an SM each, as far as the workspace has two
     // slots for every one of them; without it whole sequences.
     int64_t each = std::max<int64_t>(1, sms / groups);
@@ -1037,9 +1287,25 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
         each = std::min<int64_t>(std::max<int64_t>(1, sms / groups), a.n_seqs);
     }
     p.per_group = (int)each;
-    *err = bf ? launch_rows<__nv_bfloat16>(nb, map, p, sms, stream)
-              : launch_rows<__half>(nb, map, p, sms, stream);
+    *err = a.type == SBGEMM_TYPE_BF16 ? launch_rows<__nv_bfloat16>(nb, map, p, sms, stream)
+                                      : launch_rows<__half>(nb, map, p, sms, stream);
     return true;
+}
+
+bool latent_decode_takes(const LatentPaged& a) { return takes(a); }
+
+cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems& items, int nb, void* parts, int sms,
+                                        cudaStream_t stream) {
+    Params p{};
+    CUtensorMap map{};
+    if (!fill(a, nb, &p, &map)) return cudaErrorInvalidValue;
+    p.groups = 1;
+    p.split = 1;
+    p.per_group = sms;
+    p.parts = static_cast<float*>(parts);
+    p.shared = items;
+    return a.type == SBGEMM_TYPE_BF16 ? launch_shared_rows<__nv_bfloat16>(nb, map, p, sms, stream)
+                                      : launch_shared_rows<__half>(nb, map, p, sms, stream);
 }
 
 unsigned int* status_word_latent_decode() { return word_address(&g_wait_status); }

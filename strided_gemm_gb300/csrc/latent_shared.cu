@@ -1,11 +1,19 @@
 // Latent attention over a paged cache for groups of sequences with a shared
-// prefix (sbgemm_latent_attention_shared).
+// prefix (sbgemm_latent_attention_shared): the plan.
 //
-// plan_kernel turns the groups into two numbers for each sequence: where the
-// keys below `prefix` are found (the table row of the group's first sequence),
-// and that prefix.  Starts are taken as a running maximum of their values
-// clamped to [0, n_seqs], so that every kernel sees the same, sound groups
-// whatever stands in device memory; what was clamped is reported here.
+// Starts are taken as a running maximum of their values clamped to [0, n_seqs], so
+// that every kernel sees the same, sound groups whatever stands in device memory;
+// what was clamped is reported here.  For the row kernel the plan is each
+// sequence's first key of its own and the sequence whose table row has the keys
+// before.  For the tensor cores it is a list of items besides, up to nb query rows
+// against a run of keys, and each item's place in a list of blocks of keys that the
+// CTAs share equally: items of each sequence's own keys, then those of the
+// prefixes, a group's rows of all its sequences side by side, so that a block of the
+// prefix is read once for nb rows where the sequences alone would read it each for
+// their own.  One CTA makes it (two running sums, over sequences and over groups),
+// launched before the kernel that uses it and waited for there.
+//
+// Measured on a GB300, R = 512, P = 64, plan and join included: see the kernel.
 #include <algorithm>
 
 #include "debug_check.cuh"
@@ -17,79 +25,221 @@ namespace {
 __device__ unsigned int g_status = 0;
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ int clamped(int v, int lo, int hi) {
+struct PrefixPlan {
+    LatentShared g;
+    int32_t* prefix_item;                // nullptr: no items are wanted
+    int32_t* head;
+    LatentItem* items;
+    int nb, keys, rows, own;             // query rows and keys a block; rows of a sequence; its items
+};
+
+__device__ __forceinline__ int clamped(int v, int lo, int hi, bool report) {
     const int c = min(max(v, lo), hi);
-    if (c != v) record_status(&g_status, kPagedInput);
+    if (c != v && report) record_status(&g_status, kPagedInput);
     return c;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ LatentShared g) {
-    __shared__ int tops[kPlanThreads / 32];
-    __shared__ int so_far;
+struct Pair { int a, b; };
+// Sums over the CTA's threads up to and with this one, and of all.
+__device__ __forceinline__ Pair running(Pair v, Pair (&shared)[kPlanThreads / 32], Pair* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(~0u, v.a, o), b = __shfl_up_sync(~0u, v.b, o);
+        if (lane >= o) {
+            v.a += a;
+            v.b += b;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) shared[warp] = v;
+    __syncthreads();
+    // The warps before, by each warp's lanes.
+    const Pair mine = shared[lane];
+    const int below = warp > lane;
+    Pair before{(int)__reduce_add_sync(~0u, below ? mine.a : 0), (int)__reduce_add_sync(~0u, below ? mine.b : 0)};
+    *all = Pair{(int)__reduce_add_sync(~0u, mine.a), (int)__reduce_add_sync(~0u, mine.b)};
+    return Pair{v.a + before.a, v.b + before.b};
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PrefixPlan p) {
+    struct Group { int lo, hi, prefix, item, unit; };
+    __shared__ Group group[kPlanThreads];
+    __shared__ Pair sums[kPlanThreads / 32];
+    __shared__ int tops[kPlanThreads / 32], so_far;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const LatentShared& g = p.g;
     const LatentPaged& a = g.paged;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_seqs = (int)a.n_seqs;
-    auto length = [&](int s) { return a.seq_lens ? clamped(a.seq_lens[s], 0, (int)a.N) : (int)a.N; };
-    auto put = [&](int s, int first, int prefix) {
-        if (dbg_in_bytes(g.first + s, 4, g.sw, &g_status)) g.first[s] = first;
-        if (dbg_in_bytes(g.prefix + s, 4, g.sw, &g_status)) g.prefix[s] = prefix;
+    const bool items = p.items != nullptr;
+    auto length = [&](int s, bool report) { return a.seq_lens ? clamped(a.seq_lens[s], 0, (int)a.N, report) : (int)a.N; };
+    auto put = [&](int32_t* at, int v) {
+        if (dbg_in_bytes(at, 4, g.sw, &g_status)) *at = v;
+    };
+    auto put_item = [&](int i, const LatentItem& it) {
+        if (dbg_in_bytes(p.items + i, sizeof(it), g.sw, &g_status)) p.items[i] = it;
     };
     for (int s = tid; s < n_seqs; s += kPlanThreads) {
-        length(s);                                       // reports every length
-        put(s, s, 0);
+        put(g.first + s, s);
+        put(g.prefix + s, 0);
+        if (items) put(p.prefix_item + s, -1);
     }
-    if (tid == 0) so_far = 0;
-    __syncthreads();
-    for (int64_t g0 = 0; g0 < g.n_groups; g0 += kPlanThreads) {
-        // This thread's group, from the running maximum up to its start to that
-        // up to the next one's.
-        const int64_t i = g0 + tid;
-        const bool mine = i < g.n_groups;
-        const int at = mine ? clamped(g.group_starts[i], 0, n_seqs) : 0;
-        const int next = mine ? clamped(g.group_starts[i + 1], 0, n_seqs) : 0;
-        int top = at;
+    // The groups, kPlanThreads at a time: f(how many, this thread's group).
+    auto groups = [&](bool report, auto f) {
+        if (tid == 0) so_far = 0;
+        __syncthreads();
+        for (int64_t g0 = 0; g0 < g.n_groups; g0 += kPlanThreads) {
+            const int64_t i = g0 + tid;
+            const bool mine = i < g.n_groups;
+            // From the running maximum up to this group's start to that up to the next one's.
+            const int at = mine ? clamped(g.group_starts[i], 0, n_seqs, report) : 0;
+            const int next = mine ? clamped(g.group_starts[i + 1], 0, n_seqs, report) : 0;
+            int top = at;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, top, o);
-            if (lane >= o) top = max(top, x);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(~0u, top, o);
+                if (lane >= o) top = max(top, x);
+            }
+            if (lane == 31) tops[warp] = top;
+            __syncthreads();
+            int lo = max(so_far, top);
+            for (int w = 0; w < warp; ++w) lo = max(lo, tops[w]);
+            const int hi = max(lo, next);
+            __syncthreads();
+            if (tid == kPlanThreads - 1) so_far = lo;
+            Group mine_is{lo, hi, 0, 0, 0};
+            if (mine) {
+                const int given = g.prefix_lens[i];
+                if (report && (lo != at || hi != next || given < 0)) record_status(&g_status, kPagedInput);
+                if (lo < hi) mine_is.prefix = clamped(given, 0, length(lo, false), report);
+            } else {
+                mine_is.hi = lo;
+            }
+            f((int)min((int64_t)kPlanThreads, g.n_groups - g0), mine_is);
+            __syncthreads();
         }
-        if (lane == 31) tops[warp] = top;
+    };
+    groups(true, [&](int count, const Group& mine) {
+        group[tid] = mine;
         __syncthreads();
-        int lo = max(so_far, top);
-        for (int w = 0; w < warp; ++w) lo = max(lo, tops[w]);
-        const int hi = max(lo, next);
-        if (mine && (lo != at || hi != next)) record_status(&g_status, kPagedInput);
+        for (int i = warp; i < count; i += kPlanThreads / 32)
+            for (int s = group[i].lo + lane; s < group[i].hi; s += 32) {
+                put(g.first + s, group[i].lo);
+                put(g.prefix + s, group[i].prefix);
+            }
+    });
+    __syncthreads();
+
+    // Each sequence's own keys, from its prefix on.
+    Pair total{0, n_seqs * p.own};           // units, items
+    for (int s0 = 0; s0 < n_seqs; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        const int len = s < n_seqs ? length(s, true) : 0;       // (reports every length)
+        if (!items) continue;
+        const int lo = s < n_seqs ? g.prefix[s] : 0, units = len > lo ? (len + p.keys - 1) / p.keys - lo / p.keys : 0;
+        Pair all;
+        const int at = total.a + running(Pair{units * p.own, 0}, sums, &all).a - units * p.own;
+        if (s < n_seqs)
+            for (int k = 0; k < p.own; ++k)
+                put_item(s * p.own + k, LatentItem{at + k * units, units, s, lo, len, s, k * p.nb,
+                                                   min(p.nb, p.rows - k * p.nb)});
+        total.a += all.a;
         __syncthreads();
-        if (tid == kPlanThreads - 1) so_far = lo;
-        if (mine && lo < hi) {
-            const int prefix = clamped(g.prefix_lens[i], 0, min((int)a.N, length(lo)));
-            for (int s = lo; s < hi; ++s) put(s, lo, prefix);
-        } else if (mine && g.prefix_lens[i] < 0) {
-            record_status(&g_status, kPagedInput);
+    }
+    if (!items) return;
+    groups(false, [&](int count, Group mine) {
+        const int rows = (mine.hi - mine.lo) * p.rows;
+        const int blocks = mine.prefix > 0 ? (rows + p.nb - 1) / p.nb : 0, units = (mine.prefix + p.keys - 1) / p.keys;
+        Pair all;
+        const Pair at = running(Pair{blocks * units, blocks}, sums, &all);
+        mine.unit = total.a + at.a - blocks * units;
+        mine.item = total.b + at.b - blocks;
+        group[tid] = mine;
+        __syncthreads();
+        for (int i = warp; i < count; i += kPlanThreads / 32) {
+            const Group it = group[i];
+            if (it.prefix <= 0) continue;
+            const int rows = (it.hi - it.lo) * p.rows, units = (it.prefix + p.keys - 1) / p.keys;
+            for (int s = it.lo + lane; s < it.hi; s += 32) put(p.prefix_item + s, it.item);
+            for (int k = lane; k * p.nb < rows; k += 32)
+                put_item(it.item + k, LatentItem{it.unit + k * units, units, it.lo, 0, it.prefix, it.lo, k * p.nb,
+                                                 min(p.nb, rows - k * p.nb)});
         }
-        __syncthreads();
+        total.a += all.a;
+        total.b += all.b;
+    });
+    if (tid == 0) {
+        put(p.head, total.a);
+        put(p.head + 1, total.b);
     }
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// What goes where in the workspace: arrays of a number a sequence (first, prefix,
+// prefix_item), the head, the items, and a slot for every piece: an item that begins
+// in a CTA has its index and the CTA's as its slot, so that there are as many as
+// items and CTAs together.
+struct Layout {
+    int nb;
+    int64_t own, most;                   // items of a sequence's own keys; items at most
+    size_t each, items, parts, bytes;    // bytes an array; offsets
+};
+Layout layout_of(int sms, int64_t n_seqs, int64_t n_groups, int64_t rows, int64_t R) {
+    Layout l{};
+    // Rows that a group has, were they all alike.
+    const int64_t of = n_groups > 0 ? (n_seqs + n_groups - 1) / n_groups * rows : rows;
+    l.nb = latent_rows_block(std::max(of, rows));
+    l.own = (rows + l.nb - 1) / l.nb;
+    l.most = n_seqs * l.own + n_seqs * rows / l.nb + n_groups;
+    l.each = round256((size_t)n_seqs * 4);
+    l.items = 3 * l.each + 256;
+    l.parts = l.items + round256((size_t)l.most * sizeof(LatentItem));
+    l.bytes = l.parts + (R > 0 ? (size_t)(l.most + sms) * latent_part_bytes(l.nb, R) : 0);
+    return l;
+}
+
 }  // namespace
 
 size_t latent_shared_workspace_bytes(int sms, int64_t n_seqs, int64_t n_groups, int64_t q_len, int64_t heads, int64_t R) {
-    (void)sms; (void)n_groups; (void)q_len; (void)heads; (void)R;
-    return 2 * round256((size_t)n_seqs * 4);
+    return layout_of(sms, n_seqs, n_groups, q_len * heads, R).bytes;
 }
 
 cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_starts, const int32_t* prefix_lens,
                                  int64_t n_groups, int sms, cudaStream_t stream) {
-    (void)sms;
+    const int64_t rows = a.q_len * a.heads;
+    const Layout l = layout_of(sms, a.n_seqs, n_groups, rows, a.R);
     char* ws = static_cast<char*>(a.workspace);
-    const size_t each = round256((size_t)a.n_seqs * 4);
-    LatentShared g{a, group_starts, prefix_lens, n_groups, reinterpret_cast<int32_t*>(ws),
-                   reinterpret_cast<int32_t*>(ws + each), ws + 2 * each, a.workspace_bytes - 2 * each,
-                   ByteSpan{(uintptr_t)ws, (uintptr_t)ws + a.workspace_bytes}};
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(g);
-    if (const cudaError_t e = cudaGetLastError()) return e;
-    return launch_latent_rows_shared(g, stream);
+    PrefixPlan p{};
+    p.g = LatentShared{a, group_starts, prefix_lens, n_groups, reinterpret_cast<int32_t*>(ws),
+                       reinterpret_cast<int32_t*>(ws + l.each),
+                       ByteSpan{reinterpret_cast<uintptr_t>(ws), reinterpret_cast<uintptr_t>(ws) + l.bytes}};
+    p.nb = l.nb;
+    p.keys = latent_block_keys(l.nb);
+    p.rows = (int)rows;
+    p.own = (int)l.own;
+    // (Units and slots are ints.)
+    const bool tc = latent_decode_takes(a) && (__int128)l.most * (a.N / p.keys + 2) < INT32_MAX &&
+                    a.n_seqs * rows < INT32_MAX / 2;
+    if (tc) {
+        p.prefix_item = reinterpret_cast<int32_t*>(ws + 2 * l.each);
+        p.head = reinterpret_cast<int32_t*>(ws + 3 * l.each);
+        p.items = reinterpret_cast<LatentItem*>(ws + l.items);
+    }
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, p)) return e;
+    if (!tc) return launch_latent_rows_shared(p.g, stream);
+    const LatentItems items{p.g.first, p.prefix_item, p.head, p.items, p.own, (int)l.most};
+    return launch_latent_decode_shared(a, items, l.nb, ws + l.parts, sms, stream);
 }
 
 unsigned int* status_word_latent_shared() { return word_address(&g_status); }

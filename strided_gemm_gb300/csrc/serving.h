@@ -57,20 +57,44 @@ struct LatentPacked {
 // Latent attention over a paged cache with shared prefixes
 // (sbgemm_latent_attention_shared).  A plan kernel (latent_shared.cu) turns the
 // groups into each sequence's own first key and the row of the table that holds
-// the keys before it, once for whichever kernel follows.
+// the keys before it, and for the tensor cores into a list of items.
 struct LatentShared {
     LatentPaged paged;               // (its workspace is not read)
     const int32_t* group_starts; const int32_t* prefix_lens;
     int64_t n_groups;
     int32_t* first;                  // [n_seqs]: the sequence whose table row has the prefix
     int32_t* prefix;                 // [n_seqs]: keys of the prefix
-    void* rest; size_t rest_bytes;   // of the workspace
     ByteSpan sw;                     // debug builds: what the workspace occupies
 };
+// Up to nb query rows against a run of keys.  Row r is row (row + r) % rows of
+// sequence seq + (row + r) / rows: of one sequence against its own keys, or of a
+// whole group's against the prefix, found in the first one's pages.
+struct alignas(16) LatentItem {
+    int32_t unit0, units;            // its place in the list, in blocks of keys
+    int32_t table;                   // the sequence whose table row has the keys
+    int32_t lo, hi;                  // keys
+    int32_t seq, row, rows;
+};
+static_assert(sizeof(LatentItem) == 32, "two vectors");
+struct LatentItems {
+    const int32_t* first;            // [n_seqs]: the group's first sequence
+    const int32_t* prefix_item;      // [n_seqs]: the first item of its group's prefix, -1: none
+    const int32_t* head;             // units in all, items
+    const LatentItem* items;         // a sequence's own keys: items seq * own ..; then the prefixes'
+    int own, most;                   // items of a sequence's own keys; items there is room for
+};
+// Query rows a block takes, and keys.
+inline int latent_rows_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+constexpr int latent_block_keys(int nb) { return nb == 64 ? 64 : 48; }
+inline size_t latent_part_bytes(int nb, int64_t R) { return (size_t)nb * (2 + R) * 4; }
 size_t latent_shared_workspace_bytes(int sms, int64_t n_seqs, int64_t n_groups, int64_t q_len, int64_t heads, int64_t R);
 cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_starts, const int32_t* prefix_lens,
                                  int64_t n_groups, int sms, cudaStream_t stream);
 cudaError_t launch_latent_rows_shared(const LatentShared& a, cudaStream_t stream);
+// The items' pieces and their join; sizes that latent_decode_takes.
+bool latent_decode_takes(const LatentPaged& a);
+cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems& items, int nb, void* parts, int sms,
+                                        cudaStream_t stream);
 
 // On the tensor cores, over a paged cache (latent_decode.cu); false for sizes
 // and alignments it does not take.
