@@ -186,6 +186,7 @@ def load(path: str = LIB_PATH):
             _fastcall.bind(ctypes.cast(lib.sbgemm_ex, ctypes.c_void_p).value,
                            ctypes.cast(lib.sbgemm, ctypes.c_void_p).value)
             _serving.bind(_fastcall, lib)
+            _layers.bind(_fastcall, lib)
             _fast = _fastcall
         except ImportError:
             _fast = None

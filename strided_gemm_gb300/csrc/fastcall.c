@@ -1,6 +1,6 @@
 /* A CPython extension that forwards the product entry points of the C-ABI
- * (sbgemm, sbgemm_ex) and the 16-bit serving operators with their arguments
- * converted straight from Python objects.  Argument marshalling only: the functions it calls are the
+ * (sbgemm, sbgemm_ex), the 16-bit serving operators and those around a layer's
+ * products with their arguments converted straight from Python objects.  Argument marshalling only: the functions it calls are the
  * library's own, whose addresses the Python binding hands over once with
  * bind(), so the library instance is the one the binding loaded.
  *
@@ -331,6 +331,175 @@ static PyObject* fc_pages(PyObject* self, PyObject* const* args, Py_ssize_t narg
     return PyLong_FromLong(st);
 }
 
+/* ---- the operators around a layer's products ------------------------------------ */
+
+typedef int (*shared_fn)(int, const void*, int64_t, int64_t, int64_t, const void*, int64_t, int64_t, int64_t, int64_t,
+                         const int32_t*, int64_t, const int32_t*, const int32_t*, const int32_t*, int64_t, void*, int64_t,
+                         int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, float, int, void*,
+                         const sbgemm_options*);
+typedef int (*fp8_fn)(const sbgemm_fp8_matrix*, const sbgemm_fp8_matrix*, int, void*, int64_t, int64_t, int64_t, int64_t,
+                      int64_t, int64_t, int64_t, float, int, void*);
+typedef int (*quantize_fn)(int, const void*, int64_t, int64_t, int64_t, const sbgemm_fp8_matrix*, int64_t, int64_t,
+                           int64_t, void*);
+typedef int (*rope_fn)(int, const sbgemm_rope_part*, int64_t, const int32_t*, int64_t, const uint64_t*, int64_t, float,
+                       int, float, void*);
+typedef int (*rope_back_fn)(int, const sbgemm_rope_grad*, int64_t, const int32_t*, int64_t, const uint64_t*, int64_t,
+                            float, int, float, int, void*, const sbgemm_options*);
+
+static shared_fn g_shared = NULL;
+static fp8_fn g_fp8 = NULL;
+static quantize_fn g_quantize = NULL;
+static rope_fn g_rope = NULL;
+static rope_back_fn g_rope_back = NULL;
+
+/* bind_layers(addresses of sbgemm_latent_attention_shared, sbgemm_fp8,
+ * sbgemm_quantize_fp8, sbgemm_norm_rope, sbgemm_norm_rope_backward) */
+static PyObject* fc_bind_layers(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot a[5];
+    if (!parse(args, nargs, "ppppp", "bind_layers", a)) return NULL;
+    g_shared = (shared_fn)a[0].p;
+    g_fp8 = (fp8_fn)a[1].p;
+    g_quantize = (quantize_fn)a[2].p;
+    g_rope = (rope_fn)a[3].p;
+    g_rope_back = (rope_back_fn)a[4].p;
+    Py_RETURN_NONE;
+}
+
+/* The C arguments of sbgemm_latent_attention_shared in order. */
+static PyObject* fc_shared(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot a[30];
+    int st;
+    if (!g_shared) return not_bound();
+    if (!parse(args, nargs, "ipiiipiiiipipppipiiiiiiiiifipp", "sbgemm_latent_attention_shared", a)) return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_shared((int)a[0].i, a[1].p, a[2].i, a[3].i, a[4].i, a[5].p, a[6].i, a[7].i, a[8].i, a[9].i,
+                  (const int32_t*)a[10].p, a[11].i, (const int32_t*)a[12].p, (const int32_t*)a[13].p,
+                  (const int32_t*)a[14].p, a[15].i, a[16].p, a[17].i, a[18].i, a[19].i, a[20].i, a[21].i, a[22].i,
+                  a[23].i, a[24].i, a[25].i, a[26].f, (int)a[27].i, a[28].p, (const sbgemm_options*)a[29].p);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* The ten numbers of an sbgemm_fp8_matrix: "iipiiipiii". */
+static sbgemm_fp8_matrix matrix_of(const Slot* a) {
+    sbgemm_fp8_matrix m;
+    m.type = (int)a[0].i;
+    m.group = (int)a[1].i;
+    m.data = a[2].p;
+    m.row_stride = a[3].i;
+    m.k_stride = a[4].i;
+    m.batch_stride = a[5].i;
+    m.scale = (float*)a[6].p;
+    m.scale_row_stride = a[7].i;
+    m.scale_k_stride = a[8].i;
+    m.scale_batch_stride = a[9].i;
+    return m;
+}
+
+/* fp8(A's ten numbers, B's ten, type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, stream) */
+static PyObject* fc_fp8(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot a[32];
+    int st;
+    if (!g_fp8) return not_bound();
+    if (!parse(args, nargs, "iipiiipiii" "iipiiipiii" "ipiiiiiiifbp", "sbgemm_fp8", a)) return NULL;
+    const sbgemm_fp8_matrix x = matrix_of(a), y = matrix_of(a + 10);
+    const Slot* c = a + 20;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_fp8(&x, &y, (int)c[0].i, c[1].p, c[2].i, c[3].i, c[4].i, c[5].i, c[6].i, c[7].i, c[8].i, c[9].f,
+               (int)c[10].i, c[11].p);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* quantize(type_x, X, rsX, csX, bsX, Y's ten numbers, M, K, batch, stream) */
+static PyObject* fc_quantize(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot a[19];
+    int st;
+    if (!g_quantize) return not_bound();
+    if (!parse(args, nargs, "ipiii" "iipiiipiii" "iiip", "sbgemm_quantize_fp8", a)) return NULL;
+    const sbgemm_fp8_matrix y = matrix_of(a + 5);
+    Py_BEGIN_ALLOW_THREADS
+    st = g_quantize((int)a[0].i, a[1].p, a[2].i, a[3].i, a[4].i, &y, a[15].i, a[16].i, a[17].i, a[18].p);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* A tuple of parts, each a tuple of numbers by `spec`; how many, or -1. */
+static Py_ssize_t parts_of(PyObject* t, const char* spec, const char* name, Slot (*out)[15]) {
+    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) > SBGEMM_MAX_ROPE_PARTS) {
+        PyErr_Format(PyExc_TypeError, "%s: a tuple of at most SBGEMM_MAX_ROPE_PARTS parts is wanted", name);
+        return -1;
+    }
+    const Py_ssize_t n = PyTuple_GET_SIZE(t);
+    for (Py_ssize_t k = 0; k < n; ++k) {
+        PyObject* part = PyTuple_GET_ITEM(t, k);
+        if (!PyTuple_Check(part)) {
+            PyErr_Format(PyExc_TypeError, "%s: a part is a tuple", name);
+            return -1;
+        }
+        if (!parse(((PyTupleObject*)part)->ob_item, PyTuple_GET_SIZE(part), spec, name, out[k])) return -1;
+    }
+    return n;
+}
+
+/* rope(type, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, stream) */
+static PyObject* fc_rope(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot type, e[8], p[SBGEMM_MAX_ROPE_PARTS][15];
+    sbgemm_rope_part parts[SBGEMM_MAX_ROPE_PARTS];
+    int st;
+    if (!g_rope) return not_bound();
+    if (nargs != 10) {
+        PyErr_SetString(PyExc_TypeError, "rope takes 10 arguments");
+        return NULL;
+    }
+    if (!as_i64(args[0], &type.i)) return NULL;
+    const Py_ssize_t n = parts_of(args[1], "piipiiiiiip", "sbgemm_norm_rope", p);
+    if (n < 0 || !parse(args + 2, 8, "pipifbfp", "sbgemm_norm_rope", e)) return NULL;
+    for (Py_ssize_t k = 0; k < n; ++k) {
+        const Slot* a = p[k];
+        const sbgemm_rope_part part = {a[0].p, a[1].i, a[2].i, a[3].p, a[4].i, a[5].i,
+                                       a[6].i, a[7].i, a[8].i, a[9].i, a[10].p};
+        parts[k] = part;
+    }
+    Py_BEGIN_ALLOW_THREADS
+    st = g_rope((int)type.i, parts, n, (const int32_t*)e[0].p, e[1].i, (const uint64_t*)e[2].p, e[3].i, e[4].f,
+                (int)e[5].i, e[6].f, e[7].p);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* rope_back(type, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, accumulate, stream, options) */
+static PyObject* fc_rope_back(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    Slot type, e[10], p[SBGEMM_MAX_ROPE_PARTS][15];
+    sbgemm_rope_grad parts[SBGEMM_MAX_ROPE_PARTS];
+    int st;
+    if (!g_rope_back) return not_bound();
+    if (nargs != 12) {
+        PyErr_SetString(PyExc_TypeError, "rope_back takes 12 arguments");
+        return NULL;
+    }
+    if (!as_i64(args[0], &type.i)) return NULL;
+    const Py_ssize_t n = parts_of(args[1], "piipiipiiiiiipp", "sbgemm_norm_rope_backward", p);
+    if (n < 0 || !parse(args + 2, 10, "pipifbfbpp", "sbgemm_norm_rope_backward", e)) return NULL;
+    for (Py_ssize_t k = 0; k < n; ++k) {
+        const Slot* a = p[k];
+        const sbgemm_rope_grad part = {a[0].p, a[1].i, a[2].i, a[3].p, a[4].i, a[5].i, a[6].p, a[7].i,
+                                       a[8].i, a[9].i, a[10].i, a[11].i, a[12].i, a[13].p, (float*)a[14].p};
+        parts[k] = part;
+    }
+    Py_BEGIN_ALLOW_THREADS
+    st = g_rope_back((int)type.i, parts, n, (const int32_t*)e[0].p, e[1].i, (const uint64_t*)e[2].p, e[3].i, e[4].f,
+                     (int)e[5].i, e[6].f, (int)e[7].i, e[8].p, (const sbgemm_options*)e[9].p);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
 static PyMethodDef kMethods[] = {
     {"bind", (PyCFunction)(void (*)(void))fc_bind, METH_FASTCALL, "bind the library's entry points"},
     {"sbgemm_ex", (PyCFunction)(void (*)(void))fc_sbgemm_ex, METH_FASTCALL, "sbgemm_ex; returns the status"},
@@ -339,6 +508,12 @@ static PyMethodDef kMethods[] = {
     {"half", (PyCFunction)(void (*)(void))fc_half, METH_FASTCALL, "sbgemm_half; returns the status"},
     {"paged", (PyCFunction)(void (*)(void))fc_paged, METH_FASTCALL, "sbgemm_latent_attention_paged; returns the status"},
     {"packed", (PyCFunction)(void (*)(void))fc_packed, METH_FASTCALL, "sbgemm_latent_attention; returns the status"},
+    {"bind_layers", (PyCFunction)(void (*)(void))fc_bind_layers, METH_FASTCALL, "bind the layers' entry points"},
+    {"shared", (PyCFunction)(void (*)(void))fc_shared, METH_FASTCALL, "sbgemm_latent_attention_shared; returns the status"},
+    {"fp8", (PyCFunction)(void (*)(void))fc_fp8, METH_FASTCALL, "sbgemm_fp8; returns the status"},
+    {"quantize", (PyCFunction)(void (*)(void))fc_quantize, METH_FASTCALL, "sbgemm_quantize_fp8; returns the status"},
+    {"rope", (PyCFunction)(void (*)(void))fc_rope, METH_FASTCALL, "sbgemm_norm_rope; returns the status"},
+    {"rope_back", (PyCFunction)(void (*)(void))fc_rope_back, METH_FASTCALL, "sbgemm_norm_rope_backward; returns the status"},
     {"pages", (PyCFunction)(void (*)(void))fc_pages, METH_FASTCALL, "sbgemm_pages_*; returns the status"},
     {NULL, NULL, 0, NULL},
 };

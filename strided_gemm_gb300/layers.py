@@ -54,6 +54,13 @@ def declare(lib) -> None:
         f.restype, f.argtypes = _int, types
 
 
+def bind(fast, lib) -> None:
+    """Hands the fast-call module (csrc/fastcall.c) these functions' addresses."""
+    fast.bind_layers(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
+        "sbgemm_latent_attention_shared", "sbgemm_fp8", "sbgemm_quantize_fp8", "sbgemm_norm_rope",
+        "sbgemm_norm_rope_backward")))
+
+
 def _lib():
     return _sg._lib if _sg._lib is not None else _sg.load()
 
@@ -65,35 +72,83 @@ def _check(st: int, where: str) -> None:
 
 # ---- the C functions ------------------------------------------------------------
 
+def _numbers(m):
+    """An Fp8Matrix's fields in order."""
+    return tuple(getattr(m, name) or 0 for name, _ in Fp8Matrix._fields_)
+
+
+def _fp8(a, b, type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, stream) -> None:
+    """sbgemm_fp8 of two tuples of Fp8Matrix's fields."""
+    lib = _lib()
+    if _sg._fast is not None:
+        st = _sg._fast.fp8(*a, *b, type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, stream or 0)
+    else:
+        st = lib.sbgemm_fp8(ctypes.byref(Fp8Matrix(*a)), ctypes.byref(Fp8Matrix(*b)), type_c, C, rsC, csC, bsC, M, N, K,
+                            batch, alpha, 1 if accumulate else 0, stream or None)
+    if st:
+        raise _sg.SbgemmError(st, "sbgemm_fp8")
+
+
 def sbgemm_fp8(A, B, type_c, C, rsC, csC, bsC, M, N, K, batch, alpha=1.0, accumulate=0, stream=0) -> None:
     """C <- alpha*A*B (+C) on 8-bit matrices with block scales (Fp8Matrix)."""
-    _check(_lib().sbgemm_fp8(A and ctypes.byref(A), B and ctypes.byref(B), type_c, C, rsC, csC, bsC, M, N, K, batch,
-                             alpha, 1 if accumulate else 0, stream or None), "sbgemm_fp8")
+    if A is None or B is None:
+        raise _sg.SbgemmError(_sg.SBGEMM_ERR_NULL_POINTER, "sbgemm_fp8")
+    _fp8(_numbers(A), _numbers(B), type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, stream)
+
+
+def _quantize(type_x, X, rsX, csX, bsX, y, M, K, batch, stream) -> None:
+    """sbgemm_quantize_fp8 into a tuple of Fp8Matrix's fields."""
+    lib = _lib()
+    if _sg._fast is not None:
+        st = _sg._fast.quantize(type_x, X, rsX, csX, bsX, *y, M, K, batch, stream or 0)
+    else:
+        st = lib.sbgemm_quantize_fp8(type_x, X, rsX, csX, bsX, ctypes.byref(Fp8Matrix(*y)), M, K, batch, stream or None)
+    if st:
+        raise _sg.SbgemmError(st, "sbgemm_quantize_fp8")
 
 
 def sbgemm_quantize_fp8(type_x, X, rsX, csX, bsX, Y, M, K, batch, stream=0) -> None:
     """Quantises X into the 8-bit matrix Y (Fp8Matrix), data and scales."""
-    _check(_lib().sbgemm_quantize_fp8(type_x, X, rsX, csX, bsX, Y and ctypes.byref(Y), M, K, batch, stream or None),
-           "sbgemm_quantize_fp8")
+    if Y is None:
+        raise _sg.SbgemmError(_sg.SBGEMM_ERR_NULL_POINTER, "sbgemm_quantize_fp8")
+    _quantize(type_x, X, rsX, csX, bsX, _numbers(Y), M, K, batch, stream)
 
 
 def sbgemm_norm_rope(type, parts, positions, tokens, steps, dims, magnitude=1.0, interleaved=0, eps=1e-6,
                      stream=0) -> None:
     """Norm and rotation of the arrays that `parts` (sbgemm_rope_part tuples in
     the fields' order) describe."""
-    array = (_Part * max(1, len(parts)))(*(_Part(*p) for p in parts))
-    _check(_lib().sbgemm_norm_rope(type, array, len(parts), positions, tokens, steps, dims, magnitude,
-                                   int(interleaved), eps, stream or None), "sbgemm_norm_rope")
+    lib = _lib()
+    n = len(parts)
+    if interleaved not in (0, 1) or n > _sg.MAX_ROPE_PARTS:
+        st = _sg.SBGEMM_ERR_INVALID_VALUE
+    elif _sg._fast is not None:
+        st = _sg._fast.rope(type, tuple(parts), positions, tokens, steps, dims, magnitude, interleaved, eps, stream or 0)
+    else:
+        array = (_Part * max(1, n))(*(_Part(*p) for p in parts))
+        st = lib.sbgemm_norm_rope(type, array, n, positions, tokens, steps, dims, magnitude, int(interleaved), eps,
+                                  stream or None)
+    if st:
+        raise _sg.SbgemmError(st, "sbgemm_norm_rope")
 
 
 def sbgemm_norm_rope_backward(type, parts, positions, tokens, steps, dims, magnitude=1.0, interleaved=0, eps=1e-6,
                               accumulate=0, stream=0, workspace: int = 0, workspace_bytes: int = 0) -> None:
     """The gradient of sbgemm_norm_rope (sbgemm_rope_grad tuples)."""
-    array = (_Grad * max(1, len(parts)))(*(_Grad(*p) for p in parts))
+    lib = _lib()
+    n = len(parts)
     o = _sg._opts_ref(_sg.MATH_FP32, _sg.PATH_AUTO, workspace, workspace_bytes, _sg.KSPLIT_ANY)
-    _check(_lib().sbgemm_norm_rope_backward(type, array, len(parts), positions, tokens, steps, dims, magnitude,
-                                            int(interleaved), eps, 1 if accumulate else 0, stream or None, o[1]),
-           "sbgemm_norm_rope_backward")
+    if interleaved not in (0, 1) or n > _sg.MAX_ROPE_PARTS:
+        st = _sg.SBGEMM_ERR_INVALID_VALUE
+    elif _sg._fast is not None:
+        st = _sg._fast.rope_back(type, tuple(parts), positions, tokens, steps, dims, magnitude, interleaved, eps,
+                                 accumulate, stream or 0, o[2])
+    else:
+        array = (_Grad * max(1, n))(*(_Grad(*p) for p in parts))
+        st = lib.sbgemm_norm_rope_backward(type, array, n, positions, tokens, steps, dims, magnitude, int(interleaved),
+                                           eps, 1 if accumulate else 0, stream or None, o[1])
+    if st:
+        raise _sg.SbgemmError(st, "sbgemm_norm_rope_backward")
 
 
 def sbgemm_norm_rope_workspace_bytes(norms, device: int | None = None) -> int:
@@ -145,8 +200,8 @@ def _group(rows, groups, name):
 
 
 def _matrix(x, s, name, dev, rows_at, k_at, batch):
-    """Fp8Matrix of a 3-D tensor whose rows and contracted axis are `rows_at`
-    and `k_at`, with its scales laid out alike."""
+    """Fp8Matrix's fields for a 3-D tensor whose rows and contracted axis are
+    `rows_at` and `k_at`, with its scales laid out alike."""
     kind = _fp8s.get(x.dtype)
     if kind is None:
         raise TypeError(f"{name} must be a float8_e4m3fn or float8_e5m2 tensor")
@@ -160,12 +215,8 @@ def _matrix(x, s, name, dev, rows_at, k_at, batch):
     group = _group(xs[rows_at], ss[rows_at], f"the scale of {name}")
     st, sst = x.stride(), s.stride()
     shared = xs[0] != batch
-    return Fp8Matrix(kind, group, x.data_ptr(), st[rows_at], st[k_at], 0 if shared else st[0],
-                     s.data_ptr(), sst[rows_at], sst[k_at], 0 if shared else sst[0])
-
-
-def _c_fp8(type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, A, B, stream):
-    sbgemm_fp8(A, B, type_c, C, rsC, csC, bsC, M, N, K, batch, alpha, accumulate, stream)
+    return (kind, group, x.data_ptr(), st[rows_at], st[k_at], 0 if shared else st[0],
+            s.data_ptr(), sst[rows_at], sst[k_at], 0 if shared else sst[0])
 
 
 def matmul_fp8(A, A_scale, B, B_scale, C, alpha: float = 1.0, accumulate: bool = False, stream=None):
@@ -187,7 +238,7 @@ def matmul_fp8(A, A_scale, B, B_scale, C, alpha: float = 1.0, accumulate: bool =
     a = _matrix(A3, SA, "A", dev, 1, 2, batch)
     b = _matrix(B3, SB, "B", dev, 2, 1, batch)
     bc, rc, cc = C3.stride()
-    _serving._run(dev, stream, _c_fp8, kind, C3.data_ptr(), rc, cc, bc, M, N, K, batch, alpha, accumulate, a, b)
+    _serving._run(dev, stream, _fp8, a, b, kind, C3.data_ptr(), rc, cc, bc, M, N, K, batch, alpha, accumulate)
     return C
 
 
@@ -204,7 +255,7 @@ def quantize_fp8(X, Y, scale, stream=None):
     batch, M, K = X3.shape
     y = _matrix(Y3, S3, "Y", dev, 1, 2, batch)
     bx, rx, cx = X3.stride()
-    _serving._run(dev, stream, sbgemm_quantize_fp8, kind, X3.data_ptr(), rx, cx, bx, y, M, K, batch)
+    _serving._run(dev, stream, _quantize, kind, X3.data_ptr(), rx, cx, bx, y, M, K, batch)
     return Y, scale
 
 
@@ -322,8 +373,7 @@ def _angles(positions, table, dev):
             table.magnitude)
 
 
-def _c_norm_rope(kind, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, stream):
-    sbgemm_norm_rope(kind, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, stream)
+_norm_rope_on = sbgemm_norm_rope
 
 
 def norm_rope(parts, positions, table, interleaved: bool = False, eps: float = 1e-6, stream=None):
@@ -345,13 +395,13 @@ def norm_rope(parts, positions, table, interleaved: bool = False, eps: float = 1
         y, yt, yh, _, _ = _rows(p.y, "y", x0.dtype, dev, tokens, (heads, D))
         rows.append((x, xt, xh, y, yt, yh, heads, D, p.norm, p.start,
                      _vector(p.weight, "weight", p.norm, x0.dtype, dev)))
-    _serving._run(dev, stream, _c_norm_rope, kind, rows, at, tokens, steps, dims, magnitude, bool(interleaved), eps)
+    _serving._run(dev, stream, _norm_rope_on, kind, rows, at, tokens, steps, dims, magnitude, bool(interleaved), eps)
 
 
-def _c_norm_rope_backward(kind, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, accumulate, ws,
-                          ws_bytes, stream):
-    sbgemm_norm_rope_backward(kind, parts, positions, tokens, steps, dims, magnitude, interleaved, eps, accumulate,
-                              stream, ws, ws_bytes)
+def _norm_rope_backward_on(kind, rows, at, tokens, steps, dims, magnitude, interleaved, eps, accumulate, ws, ws_bytes,
+                           stream):
+    sbgemm_norm_rope_backward(kind, rows, at, tokens, steps, dims, magnitude, interleaved, eps, accumulate, stream, ws,
+                              ws_bytes)
 
 
 def norm_rope_backward(parts, positions, table, interleaved: bool = False, eps: float = 1e-6,
@@ -380,5 +430,5 @@ def norm_rope_backward(parts, positions, table, interleaved: bool = False, eps: 
                      _vector(p.weight, "weight", p.norm, d0.dtype, dev),
                      _vector(p.dweight, "dweight", p.norm, _torch.float32, dev)))
     ws, ws_bytes = _serving._workspace(workspace, dev)
-    _serving._run(dev, stream, _c_norm_rope_backward, kind, rows, at, tokens, steps, dims, magnitude,
+    _serving._run(dev, stream, _norm_rope_backward_on, kind, rows, at, tokens, steps, dims, magnitude,
                   bool(interleaved), eps, accumulate, ws, ws_bytes)

@@ -119,11 +119,19 @@ def sbgemm_latent_attention_shared(type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_
                                    O, hsO, tsO, bsO, q_len, heads, N, R, P, n_seqs, alpha, causal=0, stream=0,
                                    workspace: int = 0, workspace_bytes: int = 0) -> None:
     """Latent attention over a paged cache, each group's prefix read once."""
+    lib = _lib()
     o = _sg._opts_ref(_sg.MATH_FP32, _sg.PATH_AUTO, workspace, workspace_bytes, _sg.KSPLIT_ANY)
-    _check(_lib().sbgemm_latent_attention_shared(
-        type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
-        seq_lens or None, group_starts or None, prefix_lens or None, n_groups, O, hsO, tsO, bsO, q_len, heads, N, R,
-        P, n_seqs, alpha, int(causal), stream or None, o[1]), "sbgemm_latent_attention_shared")
+    if _sg._fast is not None:
+        st = _sg._fast.shared(type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
+                              seq_lens or 0, group_starts or 0, prefix_lens or 0, n_groups, O, hsO, tsO, bsO, q_len,
+                              heads, N, R, P, n_seqs, alpha, int(causal), stream or 0, o[2])
+    else:
+        st = lib.sbgemm_latent_attention_shared(
+            type, Q, hsQ, tsQ, bsQ, cache, rsC, psC, num_blocks, block_size, block_table, max_blocks,
+            seq_lens or None, group_starts or None, prefix_lens or None, n_groups, O, hsO, tsO, bsO, q_len, heads, N,
+            R, P, n_seqs, alpha, int(causal), stream or None, o[1])
+    if st:
+        raise _sg.SbgemmError(st, "sbgemm_latent_attention_shared")
 
 
 def sbgemm_latent_shared_workspace_bytes(n_seqs: int, n_groups: int, q_len: int, heads: int, R: int,
