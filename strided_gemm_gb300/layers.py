@@ -199,9 +199,20 @@ def _group(rows, groups, name):
     raise ValueError(f"{name} has {groups} scales for {rows} rows: one for each, or for each 128, is wanted")
 
 
-def _matrix(x, s, name, dev, rows_at, k_at, batch):
-    """Fp8Matrix's fields for a 3-D tensor whose rows and contracted axis are
-    `rows_at` and `k_at`, with its scales laid out alike."""
+def _view(t, name):
+    """Shape and strides of a 2-D or 3-D tensor as [batch, rows, columns] (no
+    view is made: that costs more than the rest of a call)."""
+    s, st = t.shape, t.stride()
+    if len(s) == 2:
+        return 1, s[0], s[1], 0, st[0], st[1]
+    if len(s) == 3:
+        return s[0], s[1], s[2], st[0], st[1], st[2]
+    raise ValueError(f"{name} must be 2-D or 3-D, got {tuple(s)}")
+
+
+def _matrix(x, s, name, dev, turned, batch, rows, k):
+    """Fp8Matrix's fields for a tensor of `rows` x `k` over the batch (turned: k x
+    rows) with its scales laid out alike."""
     kind = _fp8s.get(x.dtype)
     if kind is None:
         raise TypeError(f"{name} must be a float8_e4m3fn or float8_e5m2 tensor")
@@ -209,14 +220,16 @@ def _matrix(x, s, name, dev, rows_at, k_at, batch):
         raise TypeError(f"the scales of {name} must be a float32 tensor")
     if x.get_device() != dev or s.get_device() != dev:
         raise TypeError(f"{name} and its scales must be on cuda:{dev}")
-    xs, ss = x.shape, s.shape
-    if xs[0] not in (1, batch) or ss[0] != xs[0] or ss[k_at] != (xs[k_at] + 127) // 128:
-        raise ValueError(f"shape mismatch: {name}{tuple(xs)} with scales {tuple(ss)} in a batch of {batch}")
-    group = _group(xs[rows_at], ss[rows_at], f"the scale of {name}")
-    st, sst = x.stride(), s.stride()
-    shared = xs[0] != batch
-    return (kind, group, x.data_ptr(), st[rows_at], st[k_at], 0 if shared else st[0],
-            s.data_ptr(), sst[rows_at], sst[k_at], 0 if shared else sst[0])
+    n, r, c, bs, rs, cs = _view(x, name)
+    ns, sr, sc, bss, rss, css = _view(s, f"the scale of {name}")
+    if turned:
+        r, c, rs, cs, sr, sc, rss, css = c, r, cs, rs, sc, sr, css, rss
+    if (n != batch and n != 1) or ns != n or r != rows or c != k or sc != (k + 127) // 128:
+        raise ValueError(f"shape mismatch: {name}{tuple(x.shape)} with scales {tuple(s.shape)} in a batch of {batch}")
+    group = _group(rows, sr, f"the scale of {name}")
+    if n != batch:
+        bs = bss = 0
+    return kind, group, x.data_ptr(), rs, cs, bs, s.data_ptr(), rss, css, bss
 
 
 def matmul_fp8(A, A_scale, B, B_scale, C, alpha: float = 1.0, accumulate: bool = False, stream=None):
@@ -228,17 +241,12 @@ def matmul_fp8(A, A_scale, B, B_scale, C, alpha: float = 1.0, accumulate: bool =
     float16 or float32.  The tensor cores take operands with unit stride along
     K, so a weight [N, K] is passed as W.t() with W_scale.t().  Returns C."""
     kind = _float_kind(C, "C")
-    A3, B3, C3 = (t if t.dim() == 3 else _sg._as3(t, n) for t, n in ((A, "A"), (B, "B"), (C, "C")))
-    SA, SB = (t if t.dim() == 3 else _sg._as3(t, n) for t, n in ((A_scale, "A_scale"), (B_scale, "B_scale")))
-    dev = _serving._device(C3)
-    batch, M, N = C3.shape
-    K = A3.shape[2]
-    if A3.shape[1] != M or B3.shape[1] != K or B3.shape[2] != N:
-        raise ValueError(f"shape mismatch: A{tuple(A3.shape)} B{tuple(B3.shape)} C{tuple(C3.shape)}")
-    a = _matrix(A3, SA, "A", dev, 1, 2, batch)
-    b = _matrix(B3, SB, "B", dev, 2, 1, batch)
-    bc, rc, cc = C3.stride()
-    _serving._run(dev, stream, _fp8, a, b, kind, C3.data_ptr(), rc, cc, bc, M, N, K, batch, alpha, accumulate)
+    dev = _serving._device(C)
+    batch, M, N, bc, rc, cc = _view(C, "C")
+    K = A.shape[-1]
+    a = _matrix(A, A_scale, "A", dev, False, batch, M, K)
+    b = _matrix(B, B_scale, "B", dev, True, batch, N, K)
+    _serving._run(dev, stream, _fp8, a, b, kind, C.data_ptr(), rc, cc, bc, M, N, K, batch, alpha, accumulate)
     return C
 
 
@@ -248,14 +256,12 @@ def quantize_fp8(X, Y, scale, stream=None):
     same shape) with the scales [batch, M or ceil(M / 128), ceil(K / 128)].
     Returns (Y, scale)."""
     kind = _float_kind(X, "X")
-    X3, Y3, S3 = (t if t.dim() == 3 else _sg._as3(t, n) for t, n in ((X, "X"), (Y, "Y"), (scale, "scale")))
-    dev = _serving._device(X3)
-    if X3.shape != Y3.shape:
-        raise ValueError(f"shape mismatch: X{tuple(X3.shape)} Y{tuple(Y3.shape)}")
-    batch, M, K = X3.shape
-    y = _matrix(Y3, S3, "Y", dev, 1, 2, batch)
-    bx, rx, cx = X3.stride()
-    _serving._run(dev, stream, _quantize, kind, X3.data_ptr(), rx, cx, bx, y, M, K, batch)
+    dev = _serving._device(X)
+    batch, M, K, bx, rx, cx = _view(X, "X")
+    y = _matrix(Y, scale, "Y", dev, False, batch, M, K)
+    if Y.dim() != X.dim() or (batch > 1 and Y.shape[0] != batch):
+        raise ValueError(f"shape mismatch: X{tuple(X.shape)} Y{tuple(Y.shape)}")
+    _serving._run(dev, stream, _quantize, kind, X.data_ptr(), rx, cx, bx, y, M, K, batch)
     return Y, scale
 
 
