@@ -106,6 +106,7 @@ struct Params {
     uint32_t idesc_s, idesc_o;
     int o_vec;                               // rows of O take 8-byte stores
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
+    int join_rows;                           // shared prefixes: rows a CTA of the join takes at once
     LatentItems shared;                      // shared prefixes: slot item + CTA for each piece
     ByteSpan sq, sc, so, sw;                 // debug builds: what Q, the cache, O and the workspace occupy
 };
@@ -176,16 +177,16 @@ struct Walk {
                 first = it.seq;
                 row = it.row;
                 rows = it.rows;
-                const int n = min(it.units - tile, left);
+                const int cost = latent_item_cost(it.units), n = min(cost - tile, left);
                 j0 = it.lo / BT + tile;
-                j1 = j0 + n;
+                j1 = it.lo / BT + min(tile + n, it.units);
                 left -= n;
                 tile += n;
-                if (tile >= it.units) {
+                if (tile >= cost) {
                     ++seq;
                     tile = 0;
                 }
-                if (n > 0) return true;
+                if (j1 > j0) return true;
             }
             return false;
         } else {
@@ -221,7 +222,8 @@ struct Walk {
 
 template <typename T, int NB, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
-decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ Params p) {
+decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap edge_map,
+              const __grid_constant__ Params p) {
     constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
     constexpr uint32_t kColO = 0, kColS = kMaxTiles * NB;
     static_assert(kColS + 2 * NB <= 512, "TMEM columns");
@@ -268,7 +270,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         }
         for (int i = tid; i < items && hi > lo; i += kThreads) {
             const int2 at = *reinterpret_cast<const int2*>(&p.shared.items[i]);
-            if (lo >= at.x && lo < at.x + at.y) {
+            if (lo >= at.x && lo < at.x + latent_item_cost(at.y)) {
                 c.seq0 = i;
                 c.tile0 = lo - at.x;
             }
@@ -396,6 +398,56 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     }
                     continue;
                 }
+                if constexpr (kShared) {
+                    if (p.run) {
+                        // A block that begins or ends inside, in boxes of 8 rows, a lane
+                        // each: those inside by TMA, those outside too, from beyond the
+                        // map (zeros), and the one or two that the piece's first or last
+                        // key lies in by cp.async.  (Every row by cp.async takes the warp
+                        // 6 us to issue, which a piece of few blocks pays twice.)
+                        const int n0 = j * BT + lane * 8;
+                        const bool is_box = lane < BT / 8, out = n0 + 8 <= w.lo || n0 >= w.len;
+                        const bool in = n0 >= w.lo && n0 + 8 <= w.len;
+                        const int page = is_box && !out ? page_of(n0) : p.num_blocks;
+                        const unsigned edges = __ballot_sync(~0u, is_box && !in && !out);
+                        if (i >= kStages && !bar_wait(&c.empty[st], ph_empty)) {
+                            record_status(&g_wait_status, kWaitEmpty);
+                            ok = false;
+                        }
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        if (lane == 0)
+                            mbar_expect_tx(&c.full[st], (uint32_t)((BT / 8 - __popc(edges)) * p.chunks * 1024));
+                        __syncwarp();
+                        if (is_box && (in || out)) {
+                            uint8_t* dst = skv + st * p.chunks * kChunkBytes + lane * 1024;
+                            for (int k = 0; k < p.chunks; ++k)
+                                tma_load_3d(dst + k * kChunkBytes, &edge_map, &c.full[st], k * 64, n0 % p.block_size, page);
+                        }
+                        for (unsigned left = edges; left; left &= left - 1) {
+                            const int box = __ffs(left) - 1, from = __shfl_sync(~0u, page, box);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const int r = box * 8 + r0 + 4 * g, n = j * BT + r;
+                                const bool there = n >= w.lo && n < w.len && from < p.num_blocks;
+                                const char* at = cache + 2 * (from * p.psC + (n % p.block_size) * p.rsC) + piece * 16;
+                                const uint32_t dst = stage + r * 128 + ((piece ^ (r & 7)) << 4);
+                                for (int k = 0; k < p.chunks; ++k) {
+                                    const bool read = there && k * 8 + piece < row_pieces &&
+                                                      dbg_in_bytes(at + k * 128, 16, p.sc, &g_wait_status);
+                                    cp_async16(dst + k * kChunkBytes, read ? at + k * 128 : cache, read);
+                                }
+                            }
+                        }
+                        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.full[st]);
+                        landing = i + 1;
+                        next = -1;
+                        continue;
+                    }
+                }
                 // The rows' places first: their table entries arrive while the stage drains.
                 const char* src[BT / 4];
 #pragma unroll
@@ -443,8 +495,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             const uint32_t stage_bytes = p.chunks * kChunkBytes;
             int i = 0, filled = 0;           // blocks and pieces with blocks so far
             bool ok = true;
-            // Rows in use: all of NB, or as many 16 as an item has.
-            uint32_t idesc_s = p.idesc_s, idesc_o = p.idesc_o;
             auto scores = [&](int b) {       // S^T of block number b
                 tc_fence_after();
                 const uint32_t d = tmem + kColS + (b & 1) * NB;
@@ -452,12 +502,12 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                 for (int k = 0; k < p.R / 64; ++k) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        mma16_ss(d, da + x * kStepK, dq + x * kStepK, idesc_s, (k | x) ? 1u : 0u);
+                        mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, (k | x) ? 1u : 0u);
                     da += kChunkBytes >> 4;
                     dq += NB * 128 >> 4;
                 }
                 for (int x = 0; x < p.rope_steps; ++x)
-                    mma16_ss(d, da + x * kStepK, dq + x * kStepK, idesc_s, 1u);
+                    mma16_ss(d, da + x * kStepK, dq + x * kStepK, p.idesc_s, 1u);
                 mma_commit(&c.s_full[b & 1]);
             };
             auto timed_out = [&](unsigned int code) {
@@ -467,11 +517,6 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             while (ok && w.next(p)) {
                 const int n = w.j1 - w.j0;
                 if (n == 0) continue;        // an empty sequence
-                if constexpr (kShared) {
-                    const uint32_t columns = (uint32_t)((w.rows + 15) / 16 * 2) << 17;
-                    idesc_s = (p.idesc_s & ~(0x3fu << 17)) | columns;
-                    idesc_o = (p.idesc_o & ~(0x3fu << 17)) | columns;
-                }
                 if (!bar_wait(&c.q_full, (uint32_t)(filled & 1)) ||
                     !bar_wait(&c.full[i % kStages], (uint32_t)((i / kStages) & 1))) {
                     timed_out(kWaitFull);
@@ -505,7 +550,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                         const uint64_t da = desc16(rows + 2 * t * kChunkBytes, kChunkBytes), dp = desc16(p_lo);
 #pragma unroll
                         for (int x = 0; x < BT / 16; ++x)
-                            mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, idesc_o,
+                            mma16_ss(tmem + kColO + t * NB, da + x * kStepMN, dp + x * kStepMN, p.idesc_o,
                                      (j | x) ? 1u : 0u);
                     }
                     mma_commit(&c.empty[i % kStages]);
@@ -540,15 +585,30 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         // Queries of the walk's piece on their way into shared memory.
         auto fetch_queries = [&](const Run& w) {
             if (w.j1 > w.j0) {
-                for (int x = m; x < NB * p.chunks * 8; x += 256) {
-                    const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
-                    int of, gr;
-                    bool read = w.place(p, group, NB, r, &of, &gr) && k < row_pieces;
-                    const int t = gr / p.heads, h = gr % p.heads;
-                    const T* src = static_cast<const T*>(p.Q);
-                    if (read) src += of * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
-                    read = read && dbg_in_bytes(src, 16, p.sq, &g_wait_status);
-                    cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
+                if constexpr (kShared) {
+                    // A warp a row: its place is worked out once.
+                    for (int r = warp - kMathWarp; r < NB; r += kMathWarps) {
+                        int of, gr;
+                        const bool there = w.place(p, group, NB, r, &of, &gr);
+                        const T* src = static_cast<const T*>(p.Q);
+                        if (there) src += of * p.bsQ + gr / p.heads * p.tsQ + gr % p.heads * p.hsQ;
+                        for (int k = lane; k < p.chunks * 8; k += 32) {
+                            const bool read = there && k < row_pieces && dbg_in_bytes(src + k * 8, 16, p.sq, &g_wait_status);
+                            cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4),
+                                       read ? src + k * 8 : static_cast<const T*>(p.Q), read);
+                        }
+                    }
+                } else {
+                    for (int x = m; x < NB * p.chunks * 8; x += 256) {
+                        const int r = x / (p.chunks * 8), k = x % (p.chunks * 8);
+                        int of, gr;
+                        bool read = w.place(p, group, NB, r, &of, &gr) && k < row_pieces;
+                        const int t = gr / p.heads, h = gr % p.heads;
+                        const T* src = static_cast<const T*>(p.Q);
+                        if (read) src += of * p.bsQ + t * p.tsQ + h * p.hsQ + k * 8;
+                        read = read && dbg_in_bytes(src, 16, p.sq, &g_wait_status);
+                        cp_async16(smem_u32(sq) + (k >> 3) * (NB * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), src, read);
+                    }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -1022,60 +1082,42 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
 }
 
 // Joins the pieces of shared prefixes: a row's are those of its part of the prefix
-// and of its sequence's own keys.  A CTA a row; R / 8 threads hold eight columns of a
-// piece each, the CTA's groups of them take the pieces in turns, four loads in
-// flight, and meet in shared memory in their order.
-template <typename T, int NB>
-__global__ void __launch_bounds__(kJoinThreads) join_shared_kernel(const __grid_constant__ Params p) {
-    __shared__ float4 sums[kJoinThreads][2];
-    __shared__ float tops[kJoinThreads / 16], ls[kJoinThreads / 16];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int per_row = p.R / 8, groups = kJoinThreads / per_row;        // 16 to 64 threads; 4 to 16 groups
-    const int g = threadIdx.x / per_row, e = threadIdx.x % per_row * 8;
-    const bool mine = g < groups;
-    const int total = p.shared.head[0], members = min(p.per_group, total);
-    const int64_t slot_floats = (int64_t)NB * (2 + p.R), rows = (int64_t)p.n_seqs * p.rows;
-    // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
-    auto member_of = [&](int unit) { return (int)(((int64_t)(unit + 1) * members + total - 1) / total) - 1; };
-    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
-        const int s = (int)(at / p.rows), r = (int)(at % p.rows);
-        // First slot, row and pieces of the row's own keys and of its prefix.
-        int slot[2], in[2], count[2];
-        {
-            const int prefix = p.shared.prefix_item[s];
-            const int64_t row = (int64_t)(s - p.shared.first[s]) * p.rows + r;
-            const int item[2] = {s * p.shared.own + r / NB, prefix < 0 ? -1 : prefix + (int)(row / NB)};
-            in[0] = r % NB;
-            in[1] = (int)(row % NB);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                count[k] = slot[k] = 0;
-                if (item[k] < 0) continue;
-                const int2 units = *reinterpret_cast<const int2*>(&p.shared.items[item[k]]);
-                if (units.y <= 0) continue;
-                const int m = member_of(units.x);
-                slot[k] = item[k] + m;
-                count[k] = member_of(units.x + units.y - 1) - m + 1;
-            }
-        }
-        const int pieces = count[0] + count[1];
-        float top = -INFINITY, l = 0.0f;
-        float4 o0 = make_float4(0, 0, 0, 0), o1 = o0;
-        for (int k0 = mine ? g : pieces; k0 < pieces; k0 += 4 * groups) {
+// and of its sequence's own keys.  R / 8 threads hold eight columns of a row each,
+// and a CTA has `groups` of them: a row for each where all of those have few pieces,
+// else the CTA's groups take one row's pieces in turns and meet in shared memory in
+// their order.  Four pieces' loads are in flight at once.
+constexpr int kSharedFew = 8;
+
+// Where a row's pieces are: two runs of slots, and the row in each.
+struct Pieces {
+    int slot[2], in[2], count[2];
+    __device__ __forceinline__ int all() const { return count[0] + count[1]; }
+};
+
+// A running maximum and sum over pieces k0, k0 + step, ... of eight columns.
+struct Joined {
+    float top = -INFINITY, l = 0.0f;
+    float4 o0 = make_float4(0, 0, 0, 0), o1 = make_float4(0, 0, 0, 0);
+    template <int NB>
+    __device__ __forceinline__ void add(const Params& p, const Pieces& at, int e, int k0, int step) {
+        const int64_t slot_floats = (int64_t)NB * (2 + p.R);
+        for (; k0 < at.all(); k0 += 4 * step) {
             float mx[4], lx[4];
             float4 v[4][2];
             float now = top;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int k = k0 + q * groups, which = k >= count[0];
-                const float* src = p.parts + (int64_t)(slot[which] + (which ? k - count[0] : k)) * slot_floats;
+                const int k = k0 + q * step;
+                const bool own = k < at.count[0];
+                const float* src = p.parts + (own ? at.slot[0] + k : at.slot[1] + (k - at.count[0])) * slot_floats;
+                const int in = own ? at.in[0] : at.in[1];
                 mx[q] = -INFINITY;
                 lx[q] = 0.0f;
                 v[q][0] = v[q][1] = make_float4(0, 0, 0, 0);
-                if (k < pieces && dbg_in_bytes(src, 4 * slot_floats, p.sw, &g_wait_status)) {
-                    mx[q] = src[in[which]];
-                    lx[q] = src[NB + in[which]];
-                    const float4* o = reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)in[which] * p.R + e);
+                if (k < at.all() && dbg_in_bytes(src, 4 * slot_floats, p.sw, &g_wait_status)) {
+                    mx[q] = src[in];
+                    lx[q] = src[NB + in];
+                    const float4* o = reinterpret_cast<const float4*>(src + 2 * NB + (int64_t)in * p.R + e);
                     v[q][0] = o[0];
                     v[q][1] = o[1];
                 }
@@ -1095,32 +1137,89 @@ __global__ void __launch_bounds__(kJoinThreads) join_shared_kernel(const __grid_
                 add4(o1, w, v[q][1]);
             }
         }
-        sums[threadIdx.x][0] = o0;
-        sums[threadIdx.x][1] = o1;
-        if (mine && e == 0) {
-            tops[g] = top;
-            ls[g] = l;
+    }
+    template <typename T>
+    __device__ __forceinline__ void write(const Params& p, int s, int r, int e) const {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;                   // no key: zeros
+        T* out = static_cast<T*>(p.O) + s * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
+        if (!dbg_in_bytes(out, 8 * sizeof(T), p.so, &g_wait_status)) return;
+        store4(out, scale4(o0, inv), p.o_vec);
+        store4(out + 4, scale4(o1, inv), p.o_vec);
+    }
+};
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(kJoinThreads, 3) join_shared_kernel(const __grid_constant__ Params p) {
+    __shared__ float4 sums[kJoinThreads][2];
+    __shared__ float tops[kJoinThreads / 16], ls[kJoinThreads / 16];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per_row = p.R / 8, groups = kJoinThreads / per_row;        // 16 to 64 threads; 4 to 16 groups
+    const int g = threadIdx.x / per_row, e = threadIdx.x % per_row * 8;
+    const int each = p.join_rows;                                        // rows a CTA takes at once
+    const int total = p.shared.head[0], members = min(p.per_group, total);
+    const int64_t rows = (int64_t)p.n_seqs * p.rows;
+    // Unit u of the list belongs to member ceil((u + 1) members / total) - 1.
+    auto member_of = [&](int unit) { return (int)(((int64_t)(unit + 1) * members + total - 1) / total) - 1; };
+    auto pieces_of = [&](int s, int r) {
+        Pieces at;
+        const int prefix = p.shared.prefix_item[s];
+        const int64_t row = (int64_t)(s - p.shared.first[s]) * p.rows + r;
+        const int item[2] = {s * p.shared.own + r / NB, prefix < 0 ? -1 : prefix + (int)(row / NB)};
+        at.in[0] = r % NB;
+        at.in[1] = (int)(row % NB);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            at.count[k] = at.slot[k] = 0;
+            if (item[k] < 0) continue;
+            const int2 units = *reinterpret_cast<const int2*>(&p.shared.items[item[k]]);
+            if (units.y <= 0) continue;
+            const int m = member_of(units.x);
+            at.slot[k] = item[k] + m;
+            at.count[k] = member_of(units.x + units.y - 1) - m + 1;
         }
-        __syncthreads();
-        if (g == 0) {
-            const int in_use = min(groups, pieces);
-            for (int k = 1; k < in_use; ++k) top = fmaxf(top, tops[k]);
-            l = 0.0f;
-            o0 = o1 = make_float4(0, 0, 0, 0);
-            for (int k = 0; k < in_use; ++k) {
-                const float w = tops[k] == -INFINITY ? 0.0f : exp2f(tops[k] - top);
-                l = fmaf(w, ls[k], l);
-                add4(o0, w, sums[k * per_row + threadIdx.x][0]);
-                add4(o1, w, sums[k * per_row + threadIdx.x][1]);
-            }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;               // no key: zeros
-            T* out = static_cast<T*>(p.O) + s * p.bsO + r / p.heads * p.tsO + r % p.heads * p.hsO + e;
-            if (dbg_in_bytes(out, 8 * sizeof(T), p.so, &g_wait_status)) {
-                store4(out, scale4(o0, inv), p.o_vec);
-                store4(out + 4, scale4(o1, inv), p.o_vec);
+        return at;
+    };
+    for (int64_t r0 = (int64_t)blockIdx.x * each; r0 < rows; r0 += (int64_t)gridDim.x * each) {
+        if (each > 1) {
+            const int64_t mine = r0 + g;
+            const bool live = g < each && mine < rows;
+            Pieces at{};
+            if (live) at = pieces_of((int)(mine / p.rows), (int)(mine % p.rows));
+            if (!__syncthreads_or(live && at.all() > kSharedFew)) {
+                if (!live) continue;
+                Joined j;
+                j.add<NB>(p, at, e, 0, 1);
+                j.write<T>(p, (int)(mine / p.rows), (int)(mine % p.rows), e);
+                continue;
             }
         }
-        __syncthreads();
+        for (int i = 0; i < each && r0 + i < rows; ++i) {
+            const int s = (int)((r0 + i) / p.rows), r = (int)((r0 + i) % p.rows);
+            const Pieces of = pieces_of(s, r);
+            Joined j;
+            if (g < groups) {
+                j.add<NB>(p, of, e, g, groups);
+                sums[threadIdx.x][0] = j.o0;
+                sums[threadIdx.x][1] = j.o1;
+                if (e == 0) {
+                    tops[g] = j.top;
+                    ls[g] = j.l;
+                }
+            }
+            __syncthreads();
+            if (g == 0) {
+                Joined o;
+                for (int k = 0; k < groups; ++k) o.top = fmaxf(o.top, tops[k]);
+                for (int k = 0; k < groups; ++k) {
+                    const float w = tops[k] == -INFINITY ? 0.0f : exp2f(tops[k] - o.top);
+                    o.l = fmaf(w, ls[k], o.l);
+                    add4(o.o0, w, sums[k * per_row + threadIdx.x][0]);
+                    add4(o.o1, w, sums[k * per_row + threadIdx.x][1]);
+                }
+                o.write<T>(p, s, r, e);
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -1140,7 +1239,7 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
-    decode_kernel<T, NB, false><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, p);
+    decode_kernel<T, NB, false><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, map, p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.split) {
         cudaLaunchAttribute early{};
@@ -1178,7 +1277,7 @@ namespace {
 
 // What the kernels' parameters have of a call, and the tensor map of its rows, for
 // `nb` query rows a block; false on a CUDA error.
-bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map) {
+bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map, CUtensorMap* edge = nullptr) {
     Params& p = *out;
     const int64_t rows = a.q_len * a.heads;
     p.Q = a.Q; p.hsQ = a.hsQ; p.tsQ = a.tsQ; p.bsQ = a.bsQ;
@@ -1211,6 +1310,8 @@ bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map) {
         const uint64_t strides[2] = {(uint64_t)row_stride * 2, (uint64_t)page_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)run, 1};
         if (!encode_tmap_16(map, a.cache, 3, dims, strides, box)) return false;
+        const uint32_t eight[3] = {64, 8, 1};
+        if (edge && !encode_tmap_16(edge, a.cache, 3, dims, strides, eight)) return false;
         p.run = run;
     }
     return true;
@@ -1224,7 +1325,7 @@ bool takes(const LatentPaged& a) {
 }
 
 template <typename T, int NB>
-cudaError_t launch_shared(const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch_shared(const CUtensorMap& map, const CUtensorMap& edge, const Params& p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     constexpr size_t most_bytes = smem_bytes<NB>(kMaxChunks);
     int dev = 0;
@@ -1246,18 +1347,21 @@ cudaError_t launch_shared(const CUtensorMap& map, const Params& p, int sms, cuda
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, NB, true>, map, p)) return e;
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)p.n_seqs * p.rows, (int64_t)sms * 8));
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, NB, true>, map, edge, p)) return e;
+    // (p.join_rows rows a CTA at once, three CTAs an SM.)
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(((int64_t)p.n_seqs * p.rows + p.join_rows - 1) / p.join_rows,
+                                                   (int64_t)sms * 3));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_shared_kernel<T, NB>, p);
 }
 
 template <typename T>
-cudaError_t launch_shared_rows(int nb, const CUtensorMap& map, const Params& p, int sms, cudaStream_t stream) {
-    if (nb == 16) return launch_shared<T, 16>(map, p, sms, stream);
-    if (nb == 32) return launch_shared<T, 32>(map, p, sms, stream);
-    return launch_shared<T, 64>(map, p, sms, stream);
+cudaError_t launch_shared_rows(int nb, const CUtensorMap& map, const CUtensorMap& edge, const Params& p, int sms,
+                               cudaStream_t stream) {
+    if (nb == 16) return launch_shared<T, 16>(map, edge, p, sms, stream);
+    if (nb == 32) return launch_shared<T, 32>(map, edge, p, sms, stream);
+    return launch_shared<T, 64>(map, edge, p, sms, stream);
 }
 
 }  // namespace
@@ -1297,15 +1401,17 @@ bool latent_decode_takes(const LatentPaged& a) { return takes(a); }
 cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems& items, int nb, void* parts, int sms,
                                         cudaStream_t stream) {
     Params p{};
-    CUtensorMap map{};
-    if (!fill(a, nb, &p, &map)) return cudaErrorInvalidValue;
+    CUtensorMap map{}, edge{};
+    if (!fill(a, nb, &p, &map, &edge)) return cudaErrorInvalidValue;
     p.groups = 1;
     p.split = 1;
     p.per_group = sms;
     p.parts = static_cast<float*>(parts);
     p.shared = items;
-    return a.type == SBGEMM_TYPE_BF16 ? launch_shared_rows<__nv_bfloat16>(nb, map, p, sms, stream)
-                                      : launch_shared_rows<__half>(nb, map, p, sms, stream);
+    // Few rows: a CTA each, whose pieces its threads share.
+    p.join_rows = (int64_t)p.n_seqs * p.rows > (int64_t)sms * 3 ? kJoinThreads / (p.R / 8) : 1;
+    return a.type == SBGEMM_TYPE_BF16 ? launch_shared_rows<__nv_bfloat16>(nb, map, edge, p, sms, stream)
+                                      : launch_shared_rows<__half>(nb, map, edge, p, sms, stream);
 }
 
 unsigned int* status_word_latent_decode() { return word_address(&g_wait_status); }

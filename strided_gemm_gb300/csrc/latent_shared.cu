@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (!items) continue;
         const int lo = s < n_seqs ? g.prefix[s] : 0, units = len > lo ? (len + p.keys - 1) / p.keys - lo / p.keys : 0;
         Pair all;
-        const int at = total.a + running(Pair{units * p.own, 0}, sums, &all).a - units * p.own;
+        const int cost = latent_item_cost(units), at = total.a + running(Pair{cost * p.own, 0}, sums, &all).a - cost * p.own;
         if (s < n_seqs)
             for (int k = 0; k < p.own; ++k)
-                put_item(s * p.own + k, LatentItem{at + k * units, units, s, lo, len, s, k * p.nb,
+                put_item(s * p.own + k, LatentItem{at + k * cost, units, s, lo, len, s, k * p.nb,
                                                    min(p.nb, p.rows - k * p.nb)});
         total.a += all.a;
         __syncthreads();
@@ -150,10 +150,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (!items) return;
     groups(false, [&](int count, Group mine) {
         const int rows = (mine.hi - mine.lo) * p.rows;
-        const int blocks = mine.prefix > 0 ? (rows + p.nb - 1) / p.nb : 0, units = (mine.prefix + p.keys - 1) / p.keys;
+        const int blocks = mine.prefix > 0 ? (rows + p.nb - 1) / p.nb : 0;
+        const int cost = latent_item_cost((mine.prefix + p.keys - 1) / p.keys);
         Pair all;
-        const Pair at = running(Pair{blocks * units, blocks}, sums, &all);
-        mine.unit = total.a + at.a - blocks * units;
+        const Pair at = running(Pair{blocks * cost, blocks}, sums, &all);
+        mine.unit = total.a + at.a - blocks * cost;
         mine.item = total.b + at.b - blocks;
         group[tid] = mine;
         __syncthreads();
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             const int rows = (it.hi - it.lo) * p.rows, units = (it.prefix + p.keys - 1) / p.keys;
             for (int s = it.lo + lane; s < it.hi; s += 32) put(p.prefix_item + s, it.item);
             for (int k = lane; k * p.nb < rows; k += 32)
-                put_item(it.item + k, LatentItem{it.unit + k * units, units, it.lo, 0, it.prefix, it.lo, k * p.nb,
+                put_item(it.item + k, LatentItem{it.unit + k * latent_item_cost(units), units, it.lo, 0, it.prefix, it.lo, k * p.nb,
                                                  min(p.nb, rows - k * p.nb)});
         }
         total.a += all.a;
@@ -172,6 +173,127 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) {
         put(p.head, total.a);
         put(p.head + 1, total.b);
+    }
+}
+
+// The same for batches of up to kPlanThreads sequences and groups, a thread each:
+// everything is loaded at once and stays in shared memory (plan_kernel's rounds
+// through global memory and its passes over the groups take twice as long).
+__global__ void __launch_bounds__(kPlanThreads) small_plan_kernel(const __grid_constant__ PrefixPlan p) {
+    struct Sums { int own, units, items; };
+    __shared__ int lens[kPlanThreads], firsts[kPlanThreads], prefixes[kPlanThreads], prefix_items[kPlanThreads];
+    __shared__ int los[kPlanThreads], his[kPlanThreads], given[kPlanThreads], tops[kPlanThreads / 32];
+    __shared__ Sums sums[kPlanThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const LatentShared& g = p.g;
+    const LatentPaged& a = g.paged;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_seqs = (int)a.n_seqs, n_groups = (int)g.n_groups;
+    const int warps = blockDim.x / 32;
+    const bool is_seq = tid < n_seqs, is_group = tid < n_groups;
+    const int len_in = is_seq && a.seq_lens ? a.seq_lens[tid] : (int)a.N;
+    const int at_in = is_group ? g.group_starts[tid] : 0, next_in = is_group ? g.group_starts[tid + 1] : 0;
+    const int prefix_in = is_group ? g.prefix_lens[tid] : 0;
+    const int len = clamped(len_in, 0, (int)a.N, true);
+    const int at = clamped(at_in, 0, n_seqs, true), next = clamped(next_in, 0, n_seqs, true);
+    lens[tid] = len;
+    firsts[tid] = tid;
+    prefixes[tid] = 0;
+    prefix_items[tid] = -1;
+    // From the running maximum up to this group's start to that up to the next one's.
+    int lo = at;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, lo, o);
+        if (lane >= o) lo = max(lo, x);
+    }
+    if (lane == 31) tops[warp] = lo;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) lo = max(lo, tops[w]);
+    const int hi = is_group ? max(lo, next) : lo;
+    int prefix = 0;
+    if (is_group) {
+        if (lo != at || hi != next || prefix_in < 0) record_status(&g_status, kPagedInput);
+        if (lo < hi) prefix = clamped(prefix_in, 0, lens[lo], true);
+        los[tid] = lo;
+        his[tid] = hi;
+        given[tid] = prefix;
+    }
+    const int group_rows = (hi - lo) * p.rows;
+    const int blocks = p.items && prefix > 0 ? (group_rows + p.nb - 1) / p.nb : 0, units = (prefix + p.keys - 1) / p.keys;
+    __syncthreads();
+    // A group's number of items and units needs no other group's; its sequences do
+    // need its prefix.
+    for (int i = warp; i < n_groups; i += warps)
+        for (int s = los[i] + lane; s < his[i]; s += 32) {
+            firsts[s] = los[i];
+            prefixes[s] = given[i];
+            prefix_items[s] = given[i] > 0 ? i : -1;         // the group, for now
+        }
+    __syncthreads();
+    const int from = prefixes[tid], own_units = is_seq && len > from ? (len + p.keys - 1) / p.keys - from / p.keys : 0;
+    if (is_seq) {
+        if (dbg_in_bytes(g.first + tid, 4, g.sw, &g_status)) g.first[tid] = firsts[tid];
+        if (dbg_in_bytes(g.prefix + tid, 4, g.sw, &g_status)) g.prefix[tid] = from;
+    }
+    if (!p.items) return;
+    // Running sums: own units over the sequences, prefix units and items over the groups.
+    const int own_cost = latent_item_cost(own_units);
+    Sums v{own_cost * p.own, blocks * latent_item_cost(units), blocks};
+    const Sums self = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, v.own, o), y = __shfl_up_sync(~0u, v.units, o), z = __shfl_up_sync(~0u, v.items, o);
+        if (lane >= o) {
+            v.own += x;
+            v.units += y;
+            v.items += z;
+        }
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    Sums all{0, 0, 0}, before{0, 0, 0};
+    for (int w = 0; w < warps; ++w) {
+        const Sums x = sums[w];
+        all.own += x.own;
+        all.units += x.units;
+        all.items += x.items;
+        if (w < warp) {
+            before.own += x.own;
+            before.units += x.units;
+            before.items += x.items;
+        }
+    }
+    auto put_item = [&](int i, const LatentItem& it) {
+        if (dbg_in_bytes(p.items + i, sizeof(it), g.sw, &g_status)) p.items[i] = it;
+    };
+    if (is_seq)
+        for (int k = 0; k < p.own; ++k)
+            put_item(tid * p.own + k, LatentItem{before.own + v.own - self.own + k * own_cost, own_units, tid, from, len, tid,
+                                                 k * p.nb, min(p.nb, p.rows - k * p.nb)});
+    // The groups' places, where their starts were.
+    __syncthreads();
+    int* unit_of = lens;
+    int* item_of = firsts;
+    if (is_group) {
+        unit_of[tid] = all.own + before.units + v.units - self.units;
+        item_of[tid] = n_seqs * p.own + before.items + v.items - self.items;
+    }
+    __syncthreads();
+    if (is_seq) {
+        const int of = prefix_items[tid];
+        if (dbg_in_bytes(p.prefix_item + tid, 4, g.sw, &g_status)) p.prefix_item[tid] = of < 0 ? -1 : item_of[of];
+    }
+    for (int i = warp; i < n_groups; i += warps) {
+        const int keys = given[i], rows = (his[i] - los[i]) * p.rows, n = (keys + p.keys - 1) / p.keys;
+        if (keys <= 0) continue;
+        for (int k = lane; k * p.nb < rows; k += 32)
+            put_item(item_of[i] + k, LatentItem{unit_of[i] + k * latent_item_cost(n), n, los[i], 0, keys, los[i], k * p.nb,
+                                                min(p.nb, rows - k * p.nb)});
+    }
+    if (tid == 0 && dbg_in_bytes(p.head, 8, g.sw, &g_status)) {
+        p.head[0] = all.own + all.units;
+        p.head[1] = n_seqs * p.own + all.items;
     }
 }
 
@@ -220,7 +342,7 @@ cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_star
     p.rows = (int)rows;
     p.own = (int)l.own;
     // (Units and slots are ints.)
-    const bool tc = latent_decode_takes(a) && (__int128)l.most * (a.N / p.keys + 2) < INT32_MAX &&
+    const bool tc = latent_decode_takes(a) && (__int128)l.most * (a.N / p.keys + 2 + kLatentItemPad) < INT32_MAX &&
                     a.n_seqs * rows < INT32_MAX / 2;
     if (tc) {
         p.prefix_item = reinterpret_cast<int32_t*>(ws + 2 * l.each);
@@ -232,11 +354,13 @@ cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_star
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(kPlanThreads);
+    const int64_t most = std::max(a.n_seqs, n_groups);
+    const bool small = most <= kPlanThreads;
+    cfg.blockDim = dim3(small ? (unsigned)(most + 31) / 32 * 32 : kPlanThreads);
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, p)) return e;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, small ? small_plan_kernel : plan_kernel, p)) return e;
     if (!tc) return launch_latent_rows_shared(p.g, stream);
     const LatentItems items{p.g.first, p.prefix_item, p.head, p.items, p.own, (int)l.most};
     return launch_latent_decode_shared(a, items, l.nb, ws + l.parts, sms, stream);

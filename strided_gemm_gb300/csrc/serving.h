@@ -70,12 +70,17 @@ struct LatentShared {
 // sequence seq + (row + r) / rows: of one sequence against its own keys, or of a
 // whole group's against the prefix, found in the first one's pages.
 struct alignas(16) LatentItem {
-    int32_t unit0, units;            // its place in the list, in blocks of keys
+    int32_t unit0, units;            // its place in the list, and its blocks of keys
     int32_t table;                   // the sequence whose table row has the keys
     int32_t lo, hi;                  // keys
     int32_t seq, row, rows;
 };
 static_assert(sizeof(LatentItem) == 32, "two vectors");
+// An item's part of the list: its blocks, and what its queries' way in and its sums'
+// way out take, as blocks.  (Counted without it, the CTAs with the sequences' own
+// keys, a few blocks each, took twice the others' time.)
+constexpr int kLatentItemPad = 5;
+__host__ __device__ constexpr int latent_item_cost(int units) { return units > 0 ? units + kLatentItemPad : 0; }
 struct LatentItems {
     const int32_t* first;            // [n_seqs]: the group's first sequence
     const int32_t* prefix_item;      // [n_seqs]: the first item of its group's prefix, -1: none

@@ -58,6 +58,11 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity)
     return false;
 }
 
+// Bytes that a barrier's phase waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Arrival on a barrier of another CTA that hands over TMEM alone (its reads
 // ordered by tcgen05.wait::ld and the tcgen05 fence before): nothing in memory
 // is released by it, so no fence waits for the thread's global loads.

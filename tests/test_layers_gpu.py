@@ -778,6 +778,27 @@ def test_shared_sequences_shorter_than_the_prefix(torch):
     status_is(0)
 
 
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+def test_shared_by_many(torch, t):
+    # More sequences than a planning thread each, in groups of many sizes.
+    sizes = [1, 2, 3, 700, 5, 6, 400, 31]
+    c = Shared(torch, t, [(10 * n % 97, *((i * 7 + n) % 40 for i in range(n))) for n in sizes], 2, 1, 128, 64, 16, seed=1)
+    assert len(c.lens) > 1024
+    c.run()
+    c.check(torch)
+    status_is(0)
+    # More groups than that, most of them empty.
+    empty = c.starts[1:2].repeat(2000)
+    c.starts = torch.cat([c.starts[:1], empty, c.starts[2:]])
+    c.prefixes = torch.cat([c.prefixes[:1], torch.full((1999,), 5, device="cuda", dtype=torch.int32), c.prefixes[1:]])
+    c.workspace = torch.empty(sg.sbgemm_latent_shared_workspace_bytes(len(c.lens), len(c.prefixes), 1, 2, 128),
+                              device="cuda", dtype=torch.uint8)
+    c.o.fill_(math.nan)
+    c.run()
+    c.check(torch)
+    status_is(0)
+
+
 def test_shared_capture_and_two_streams(torch):
     c = Shared(torch, "bf16", [(640, 100, 30, 7), (64, 5, 300)], 16, 1, 512, 64, 64)
     d = Shared(torch, "bf16", [(900, 10, 3)], 16, 1, 512, 64, 64, seed=9)
