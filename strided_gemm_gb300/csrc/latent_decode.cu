@@ -106,6 +106,7 @@ struct Params {
     uint32_t idesc_s, idesc_o;
     int o_vec;                               // rows of O take 8-byte stores
     float* parts;                            // [2 * CTAs][NB][2 + R]: maxima, sums, then O rows
+    int q_tma;                               // shared prefixes: heads a box of queries takes; 0: no TMA
     int join_rows;                           // shared prefixes: rows a CTA of the join takes at once
     LatentItems shared;                      // shared prefixes: slot item + CTA for each piece
     ByteSpan sq, sc, so, sw;                 // debug builds: what Q, the cache, O and the workspace occupy
@@ -223,7 +224,7 @@ struct Walk {
 template <typename T, int NB, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap edge_map,
-              const __grid_constant__ Params p) {
+              const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Params p) {
     constexpr int BT = Shape<NB>::BT, kStages = Shape<NB>::kStages, kChunkBytes = Shape<NB>::kChunkBytes;
     constexpr uint32_t kColO = 0, kColS = kMaxTiles * NB;
     static_assert(kColS + 2 * NB <= 512, "TMEM columns");
@@ -242,7 +243,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             mbar_init(&c.full[i], 1);
             mbar_init(&c.empty[i], 1);
         }
-        mbar_init(&c.q_full, kMathWarps);
+        mbar_init(&c.q_full, kShared && p.q_tma ? 1 : kMathWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&c.s_full[i], 1);
         mbar_init(&c.p_full, kMathWarps);
         mbar_init(&c.o_free, kMathWarps);
@@ -582,8 +583,27 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
         const int row_pieces = (p.R + p.P) / 8;
         int i = 0, piece_no = 0;                             // blocks and pieces so far
         bool ok = true;
+        int q_boxes = 0;                                     // pieces whose queries come by TMA
         // Queries of the walk's piece on their way into shared memory.
         auto fetch_queries = [&](const Run& w) {
+            if (kShared && p.q_tma) {
+                // A box takes rows of one token, a power of two from 8 on that divides
+                // its heads; rows that are none from beyond the map.
+                if (warp == kMathWarp) {
+                    if (lane == 0) mbar_arrive_expect_tx(&c.q_full, (uint32_t)(NB * 128 * p.chunks));
+                    __syncwarp();
+                    if (lane < NB / p.q_tma) {
+                        int of, gr;
+                        const bool there = w.place(p, group, NB, lane * p.q_tma, &of, &gr);
+                        const int h = there ? gr % p.heads : 0, t = there ? gr / p.heads : 0;
+                        for (int k = 0; k < p.chunks; ++k)
+                            tma_load_4d(sq + k * (NB * 128) + lane * p.q_tma * 128, &q_map, &c.q_full, k * 64, h, t,
+                                        there ? of : p.n_seqs);
+                    }
+                    ++q_boxes;
+                }
+                return;
+            }
             if (w.j1 > w.j0) {
                 if constexpr (kShared) {
                     // A warp takes every eighth row, whose places its lanes work out at
@@ -647,7 +667,7 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
                     if (lane == 0) c.least[m >> 5] = least;
                 }
             }
-            if (n > 0) {
+            if (n > 0 && !(kShared && p.q_tma)) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -859,6 +879,8 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
             ++piece_no;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");   // on a failure too: shared memory outlives them
+        if (kShared && warp == kMathWarp && q_boxes > 0 && !bar_wait(&c.q_full, (uint32_t)((q_boxes - 1) & 1)))
+            record_status(&g_wait_status, kWaitDrain);
     }
     tc_fence_before();
     __syncthreads();
@@ -1248,7 +1270,7 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, int sms, cudaStream_
         if (e != cudaSuccess) return e;
         attr_done.fetch_or(bit);
     }
-    decode_kernel<T, NB, false><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, map, p);
+    decode_kernel<T, NB, false><<<(unsigned)(p.groups * p.per_group), kThreads, smem_bytes<NB>(p.chunks), stream>>>(map, map, map, p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.split) {
         cudaLaunchAttribute early{};
@@ -1334,7 +1356,7 @@ bool takes(const LatentPaged& a) {
 }
 
 template <typename T, int NB>
-cudaError_t launch_shared(const CUtensorMap& map, const CUtensorMap& edge, const Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch_shared(const CUtensorMap (&maps)[3], const Params& p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     constexpr size_t most_bytes = smem_bytes<NB>(kMaxChunks);
     int dev = 0;
@@ -1356,7 +1378,8 @@ cudaError_t launch_shared(const CUtensorMap& map, const CUtensorMap& edge, const
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, NB, true>, map, edge, p)) return e;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, NB, true>, maps[0], maps[1], maps[2], p))
+        return e;
     // (p.join_rows rows a CTA at once, three CTAs an SM.)
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(((int64_t)p.n_seqs * p.rows + p.join_rows - 1) / p.join_rows,
                                                    (int64_t)sms * 3));
@@ -1366,11 +1389,10 @@ cudaError_t launch_shared(const CUtensorMap& map, const CUtensorMap& edge, const
 }
 
 template <typename T>
-cudaError_t launch_shared_rows(int nb, const CUtensorMap& map, const CUtensorMap& edge, const Params& p, int sms,
-                               cudaStream_t stream) {
-    if (nb == 16) return launch_shared<T, 16>(map, edge, p, sms, stream);
-    if (nb == 32) return launch_shared<T, 32>(map, edge, p, sms, stream);
-    return launch_shared<T, 64>(map, edge, p, sms, stream);
+cudaError_t launch_shared_rows(int nb, const CUtensorMap (&maps)[3], const Params& p, int sms, cudaStream_t stream) {
+    if (nb == 16) return launch_shared<T, 16>(maps, p, sms, stream);
+    if (nb == 32) return launch_shared<T, 32>(maps, p, sms, stream);
+    return launch_shared<T, 64>(maps, p, sms, stream);
 }
 
 }  // namespace
@@ -1410,8 +1432,18 @@ bool latent_decode_takes(const LatentPaged& a) { return takes(a); }
 cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems& items, int nb, void* parts, int sms,
                                         cudaStream_t stream) {
     Params p{};
-    CUtensorMap map{}, edge{};
-    if (!fill(a, nb, &p, &map, &edge)) return cudaErrorInvalidValue;
+    CUtensorMap maps[3] = {};                // the cache's rows, in boxes of 8 too, and the queries
+    if (!fill(a, nb, &p, &maps[0], &maps[1])) return cudaErrorInvalidValue;
+    const int64_t lim = (int64_t)1 << 39, wide = (a.R + a.P + 7) / 8 * 8;
+    const int64_t hs = a.heads > 1 ? a.hsQ : wide, ts = a.q_len > 1 ? a.tsQ : hs, bs = a.n_seqs > 1 ? a.bsQ : ts;
+    if (a.heads % 8 == 0 && hs > 0 && ts > 0 && bs > 0 && hs < lim && ts < lim && bs < lim) {
+        const uint64_t dims[4] = {(uint64_t)(a.R + a.P), (uint64_t)a.heads, (uint64_t)a.q_len, (uint64_t)a.n_seqs};
+        const uint64_t strides[3] = {(uint64_t)hs * 2, (uint64_t)ts * 2, (uint64_t)bs * 2};
+        p.q_tma = 8;
+        while (p.q_tma < nb && a.heads % (2 * p.q_tma) == 0) p.q_tma *= 2;
+        const uint32_t box[4] = {64, (uint32_t)p.q_tma, 1, 1};
+        if (!encode_tmap_16(&maps[2], a.Q, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    }
     p.groups = 1;
     p.split = 1;
     p.per_group = sms;
@@ -1419,8 +1451,8 @@ cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems&
     p.shared = items;
     // Few rows: a CTA each, whose pieces its threads share.
     p.join_rows = (int64_t)p.n_seqs * p.rows > (int64_t)sms * 3 ? kJoinThreads / (p.R / 8) : 1;
-    return a.type == SBGEMM_TYPE_BF16 ? launch_shared_rows<__nv_bfloat16>(nb, map, edge, p, sms, stream)
-                                      : launch_shared_rows<__half>(nb, map, edge, p, sms, stream);
+    return a.type == SBGEMM_TYPE_BF16 ? launch_shared_rows<__nv_bfloat16>(nb, maps, p, sms, stream)
+                                      : launch_shared_rows<__half>(nb, maps, p, sms, stream);
 }
 
 unsigned int* status_word_latent_decode() { return word_address(&g_wait_status); }
