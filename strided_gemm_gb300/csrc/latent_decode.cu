@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks<NB>) join_kernel(con
 // and a CTA has `groups` of them: a row for each where all of those have few pieces,
 // else the CTA's groups take one row's pieces in turns and meet in shared memory in
 // their order.  Four pieces' loads are in flight at once.
-constexpr int kSharedFew = 8;
+constexpr int kSharedFew = 16;
 
 // Where a row's pieces are: two runs of slots, and the row in each.
 struct Pieces {
