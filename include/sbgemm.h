@@ -464,7 +464,8 @@ SBGEMM_API int sbgemm_latent_attention(
  * R, P, types and alignments of the tensor-core kernel as there; other sizes
  * run the slower kernel, which reads the prefix once a query row.
  * opt->workspace of sbgemm_latent_shared_workspace_bytes is required: each
- * piece of a sequence's keys passes through it. */
+ * piece of a sequence's keys passes through it (calls that may run at the same
+ * time need workspaces of their own). */
 SBGEMM_API int sbgemm_latent_attention_shared(
     int type, const void* Q, int64_t hsQ, int64_t tsQ, int64_t bsQ,
     const void* cache, int64_t rsC, int64_t psC, int64_t num_blocks, int64_t block_size,
@@ -556,10 +557,11 @@ SBGEMM_API int sbgemm_norm_rope(int type, const sbgemm_rope_part* parts, int64_t
  *     g = dy turned back, times magnitude;   r = 1 / sqrt(mean(x^2) + eps)
  *     dx = r (g w - x r mean(g w x r));   dweight = sum over tokens and heads of g x r
  * (dx = g where there is no norm: without norms this is the inverse rotation,
- * and x may be NULL).  dx may be dy itself (same strides).  dweight, fp32
+ * and x may be NULL).  dx may be dy or x itself (same strides).  dweight, fp32
  * [norm], may be NULL; with accumulate it is added to.  opt->workspace of
- * sbgemm_norm_rope_workspace_bytes is required when a dweight is wanted; sums
- * are made in a fixed order, so results repeat. */
+ * sbgemm_norm_rope_workspace_bytes is required when a dweight is wanted (calls
+ * that may run at the same time need workspaces of their own); sums are made in
+ * a fixed order, so results repeat. */
 typedef struct {
     const void* x;
     int64_t x_token, x_head;
@@ -723,7 +725,8 @@ SBGEMM_API int sbgemm_noalloc(const float* A, int64_t rsA, int64_t csA, int64_t 
  * a tile, 5 a free accumulator, 6 a stream-K partial sum, 7 / 8 the
  * self-test's mbarrier / flag, 9 an address outside its operand's span (debug
  * builds only; the access was skipped), 10 a paged-attention block id or
- * sequence length (or a packed sequence's start) out of range, 11 a page
+ * sequence length (or a packed sequence's start, or a group's start or prefix)
+ * out of range, 11 a page
  * request that is not valid, 12 one that found no free page. */
 SBGEMM_API int sbgemm_device_status(void* stream, int* where_out);
 

@@ -611,9 +611,11 @@ bool try_vectors(const RopeProblem& p, bool backward, int sms, cudaStream_t stre
         const int64_t per = kVecThreads >> q.log_lanes;
         int64_t mine = (p.tokens * q.chunks + per - 1) / per;
         if (backward) {
-            // Its share of the partial sums' slots, by its rows' lanes.
-            const int64_t share = (int64_t)((double)sms * kGradBlocks * (double)((p.tokens * a.heads) << q.log_lanes) / (double)threads);
-            mine = std::min(mine, std::max<int64_t>(1, share - 1));
+            // Its share of the partial sums' slots, by its rows' lanes, one at least: so
+            // that all of them are no more than there are, but for one each to spare.
+            const int64_t slots = (int64_t)sms * kGradBlocks - p.n_parts;
+            const int64_t share = (int64_t)((double)slots * (double)((p.tokens * a.heads) << q.log_lanes) / (double)threads);
+            mine = std::min(mine, std::max<int64_t>(1, share));
         }
         if (blocks + mine >= ((int64_t)1 << 31)) return false;
         q.first_block = (int)blocks;

@@ -516,6 +516,42 @@ def test_rope_gradient_accumulates_and_repeats(torch):
     assert all(torch.equal(x, y) for x, y in zip(first, dx))
 
 
+def test_workspaces_are_kept_to(torch):
+    """Nothing is written behind a workspace of the size that is asked for."""
+    for tokens, parts in ((2000, [(64, 128, 128, 0), (1, 16, 16, 0), (1, 16, 16, 0), (1, 16, 16, 0)]),
+                          (900, [(9, 9, 9, 0), (1, 7, 7, 0)]), (5000, [(1, 64, 64, 0)])):
+        r = Rope(torch, "bf16", tokens, 0, False, parts)
+        need = sg.sbgemm_norm_rope_workspace_bytes([p[2] for p in parts])
+        whole = torch.full((need + 65536,), 77, device="cuda", dtype=torch.uint8)
+        dx = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in r.x]
+        dw = [torch.empty(p[2], device="cuda") for p in parts]
+        sg.norm_rope_backward([sg.RopeGrad(x, dy, o, norm=p[2], weight=w, dweight=d)
+                               for x, dy, o, w, d, p in zip(r.x, r.dy, dx, r.w, dw, parts)], None, None,
+                              workspace=whole[:need])
+        assert bool((whole[need:] == 77).all())
+        for i in range(len(parts)):
+            _, _, rw, lw = r.gradient(i)
+            assert_within(torch, dw[i], rw, lw)
+    for groups, heads, R in (([(300, *range(1, 50))], 16, 512), ([(n, n) for n in range(1, 90)], 5, 128), ([(1, 1)], 1, 40)):
+        c = Shared(torch, "bf16", groups, heads, 1, R, 8, 16)
+        need = c.workspace.numel()
+        whole = torch.full((need + 65536,), 77, device="cuda", dtype=torch.uint8)
+        c.workspace = whole[:need]
+        c.run()
+        c.check(torch)
+        assert bool((whole[need:] == 77).all())
+
+
+def test_rope_gradient_in_place_of_its_input(torch):
+    r = Rope(torch, "fp32", 37, 64, True, [(4, 128, 128, 0), (1, 96, 64, 32)], gap=8)
+    want = [r.gradient(i) for i in range(2)]
+    dw = [torch.empty(128, device="cuda"), torch.empty(64, device="cuda")]
+    r.backward(r.x, dw)
+    for i in range(2):
+        assert_within(torch, r.x[i], *want[i][:2])
+        assert_within(torch, dw[i], *want[i][2:])
+
+
 def test_rope_gradient_against_differences(torch):
     r = Rope(torch, "fp32", 7, 32, True, [(3, 64, 48, 16)], factor=4.0)
     x0 = r.x[0].clone()
