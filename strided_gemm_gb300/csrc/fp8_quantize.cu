@@ -458,7 +458,7 @@ cudaError_t launch(const QuantizeProblem& p, cudaStream_t stream) {
     const bool y = (p.ksY == 1 || p.K == 1) && whole(p.Y, 8, p.rsY, p.M, p.bsY, p.batch, 8);
     const bool along_k = (p.csX == 1 || p.K == 1) && whole(p.X, 16, p.rsX, p.M, p.bsX, p.batch, 8);
     const bool along_m = p.rsX == 1 && whole(p.X, 16, p.csX, p.K, p.bsX, p.batch, 8);
-    if (y && along_k && p.group == 1) {
+    if (y && along_k && p.group == 1 && p.K < ((int64_t)1 << 30)) {        // (its indexes are ints)
         // 8 blocks a warp where a row has them, else 2: short rows and few of them want more warps.
         const int n = kb >= 8 && p.batch * p.M * kb >= 8192 ? 4 : 1;
         const int64_t items = p.batch * p.M * ((kb + 2 * n - 1) / (2 * n)), blocks = std::min((items + 7) / 8, most);
