@@ -267,7 +267,6 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
     __shared__ alignas(16) float ys[kYScales ? kGroups : 1][2][kYScales ? kChunk : 1][kYScales ? CPG : 4];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == kTmaWarp * 32) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -288,6 +287,9 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             tmem_alloc(&tmem_base, S::kCols);
             tmem_relinquish();
         }
+        // From here on: a kernel that starts early and waits for this one may hold TMEM
+        // on this SM, which this one must not wait for.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     if constexpr (kPair) {
         tc_fence_before();

@@ -253,9 +253,10 @@ decode_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constan
     if (warp == kMmaWarp) {
         tmem_alloc(&c.tmem_base, kTmemAll);
         tmem_relinquish();
+        // From here on: a kernel that starts early and waits for this one may hold TMEM
+        // on this SM, which this one must not wait for.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // This CTA's run: units [lo, hi) of the list, lo located in a sequence.
     if constexpr (kShared) {
