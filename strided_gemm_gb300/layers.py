@@ -373,6 +373,8 @@ def _angles(positions, table, dev):
         raise TypeError("the table's steps must be an int64 tensor")
     if table.steps.get_device() != dev or not table.steps.is_contiguous():
         raise ValueError(f"the table must be contiguous on cuda:{dev}")
+    if positions is None:
+        raise TypeError("a rotation needs positions")
     if positions.dim() != 1:
         raise ValueError("positions must be [tokens]")
     return (_serving._ints(positions, "positions", dev), positions.shape[0], table.steps.data_ptr(), table.dims,
