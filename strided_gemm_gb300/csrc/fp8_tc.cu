@@ -24,6 +24,7 @@
 #include <atomic>
 
 #include "debug_check.cuh"
+#include "f32x2.cuh"
 #include "layers.h"
 #include "tc16.cuh"
 
@@ -122,24 +123,6 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
 __device__ __forceinline__ void cp_async4(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-
-// Pairs of floats in a 64-bit register, as fma.rn.f32x2 takes them.
-__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) { return pair_of(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t f) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float lower(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float upper(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 __device__ __forceinline__ float get(const float* c) { return *c; }
 template <typename T> __device__ __forceinline__ float get(const T* c) { return to_float(*c); }

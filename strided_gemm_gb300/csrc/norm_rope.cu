@@ -2,21 +2,29 @@
 // one pass, and the gradient (sbgemm_norm_rope, sbgemm_norm_rope_backward).
 //
 // Angles.  A pair turns by position * step of 2^-64 turns.  The product modulo
-// 2^64 is the angle modulo a turn without any error, for every position; its
-// top bits are the nearest quarter turn and the rest, exact to fp32's 24 bits, an
-// angle of at most an eighth of a turn either side.
+// 2^64 is the angle modulo a turn, for every position; its top 32 bits leave out
+// less than 2^-29 radians.  They are the nearest quarter turn and the rest, an angle
+// of at most an eighth of a turn either side.
 //
 // vectors_kernel: rows whose elements come in whole vectors.  A lane holds one
 // unit of a row, two vectors: the two members of V pairs (i, i + dims / 2), or V
 // interleaved pairs one behind the other, or two vectors that are not rotated.  L
-// lanes (a power of two, up to the whole CTA) take a row and walk through several
-// heads of a token, with its angles: forward as the 2 x 2 coefficients of a pair
-// with the members' weights in them, so that a normed and rotated element costs
-// three operations.  Norms are sums over the L lanes.  A lane alone reads and
-// writes its elements, so that y may be x (what neither changes is then not
-// touched).  The backward kernel's lanes keep their share of dweight in registers;
-// a CTA adds its groups' in a fixed order and leaves one partial sum.
-// Bound by the bytes of x and y.
+// lanes (a power of two, up to the whole CTA) take a row and walk through a run of
+// rows, head by head and token by token, with a token's angles: forward as the 2 x 2
+// coefficients of a pair with the members' weights in them, so that a normed and
+// rotated element costs three operations, two elements an instruction.  Norms are
+// sums over the L lanes.  A lane alone reads and writes its elements, so that y may be
+// x (what neither changes is then not touched).  The backward kernel's lanes keep
+// their share of dweight in registers; a CTA adds its warps' in a fixed order and
+// leaves one partial sum.
+//
+// Measured on a GB300, device time in a graph: 8192 tokens of 40 heads of 128, bf16,
+// normed and rotated, 37 us, 4.5 TB/s (20000 tokens without norms 72 us, 5.6 TB/s);
+// the gradient of 4096 of them 31.7 us, 4.0 TB/s, where one element an instruction,
+// angles from 64-bit arithmetic and a walk of four heads took 39.  Bound by
+// instructions as much as by the bytes of x and y: unpacking, sums over lanes and
+// addresses take as many as the arithmetic.  (Angles made once a warp in shared
+// memory, for rows taken in the order of memory: 45 and 44 us, by its bookkeeping.)
 //
 // rows_kernel: a CTA a row, any sizes and alignments.  A first pass over the
 // row makes its sums, a second one the outputs; a thread has a pair, or an
@@ -25,6 +33,7 @@
 #include <algorithm>
 
 #include "debug_check.cuh"
+#include "f32x2.cuh"
 #include "half_util.cuh"
 #include "layers.h"
 
@@ -41,13 +50,21 @@ template <typename T> __device__ __forceinline__ float value(T v) { return to_fl
 __device__ __forceinline__ void put(float& o, float v) { o = v; }
 template <typename T> __device__ __forceinline__ void put(T& o, float v) { o = from_float<T>(v); }
 
-// magnitude * cosine and sine of position * step.  Within an eighth of a turn the
-// Taylor polynomials of degree 9 and 10 are exact to 2^-29.
-__device__ __forceinline__ float2 turn(int position, uint64_t step, float magnitude) {
-    const uint64_t phase = (uint64_t)(int64_t)position * step;
-    const uint32_t q = (uint32_t)((phase + (1ull << 61)) >> 62);         // the nearest quarter turn
-    // What is left, in radians: 2 pi / 2^64.
-    const float x = (float)(int64_t)(phase - ((uint64_t)q << 62)) * 3.4061215800304626e-19f;
+// A token's position without its sign, and the factors of cosine and sine (which the
+// sign belongs to).
+struct Place {
+    uint32_t at;
+    float c, s;
+    __device__ __forceinline__ Place(int position, float magnitude)
+        : at(position < 0 ? 0u - (uint32_t)position : (uint32_t)position), c(magnitude), s(position < 0 ? -magnitude : magnitude) {}
+};
+// Cosine and sine of position * step, times their factors.  Within an eighth of a turn
+// the Taylor polynomials of degree 9 and 10 are exact to 2^-29.
+__device__ __forceinline__ float2 turn(const Place& p, uint64_t step) {
+    const uint32_t phase = p.at * (uint32_t)(step >> 32) + __umulhi(p.at, (uint32_t)step);   // in 2^-32 turns
+    const uint32_t q = phase + (1u << 29);                               // the nearest quarter turn on top
+    // What is left, in radians: 2 pi / 2^32.
+    const float x = (float)(int)(phase - (q & 0xc0000000u)) * 1.4629180792671596e-09f;
     const float z = x * x;
     float s = fmaf(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);  // 1/9!, 1/7!, 1/5!, 1/3!
     s = fmaf(z, s, 8.3333333333333332e-3f);
@@ -58,8 +75,10 @@ __device__ __forceinline__ float2 turn(int position, uint64_t step, float magnit
     c = fmaf(z, c, 4.1666666666666664e-2f);
     c = fmaf(z, c, -0.5f);
     c = fmaf(z, c, 1.0f);
-    const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
-    return make_float2(q == 1 || q == 2 ? -magnitude * cs : magnitude * cs, q & 2 ? -magnitude * sn : magnitude * sn);
+    const bool odd = q & 0x40000000u;
+    const uint32_t cs = __float_as_uint(odd ? s : c) ^ ((q + 0x40000000u) & 0x80000000u);    // minus in quarters 1 and 2
+    const uint32_t sn = __float_as_uint(odd ? c : s) ^ (q & 0x80000000u);                    // ... 2 and 3
+    return make_float2(p.c * __uint_as_float(cs), p.s * __uint_as_float(sn));
 }
 
 // Sum over the CTA's threads, the same in all of them.
@@ -108,7 +127,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         }
         const RopePart& a = p.part[n];
         const int64_t t = r / a.heads, h = r % a.heads;
-        const int position = p.positions ? p.positions[t] : 0;
+        const Place place(p.positions ? p.positions[t] : 0, p.magnitude);
         const T* x = static_cast<const T*>(a.x) + t * a.tsX + h * a.hsX;
         const T* dy = static_cast<const T*>(a.dy) + t * a.tsD + h * a.hsD;
         T* y = static_cast<T*>(a.y) + t * a.tsY + h * a.hsY;
@@ -120,7 +139,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         // The gradient of item i's elements before the rotation.
         auto gradient = [&](int i) {
             if (i >= items.pairs) return make_float2(load(dy + items.first(i), a.sd), 0.0f);
-            const float2 cs = turn(position, p.steps[i], p.magnitude);
+            const float2 cs = turn(place, p.steps[i]);
             const float u = load(dy + items.first(i), a.sd), v = load(dy + items.second(i), a.sd);
             return make_float2(fmaf(u, cs.x, v * cs.y), fmaf(v, cs.x, -u * cs.y));
         };
@@ -159,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
             const float2 g = kBackward ? gradient(i) : make_float2(0.0f, 0.0f);
             float u = element(e, g.x), v = i < items.pairs ? element(f, g.y) : 0.0f;
             if (!kBackward && i < items.pairs) {
-                const float2 cs = turn(position, p.steps[i], p.magnitude);
+                const float2 cs = turn(place, p.steps[i]);
                 const float a0 = u, b0 = v;
                 u = fmaf(a0, cs.x, -b0 * cs.y);
                 v = fmaf(a0, cs.y, b0 * cs.x);
@@ -174,13 +193,15 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 // ---- rows in vectors -----------------------------------------------------------------
 
 constexpr int kVecThreads = 256;
+// Rows on their way to a group of lanes, and CTAs an SM, forward.
+constexpr int kForwardAhead = 3, kForwardBlocks = 2;
 
 // How a launch goes through one array.
 struct PartPlan {
     int first_block, blocks;         // its CTAs
     int log_lanes;                   // lanes a row, log2
     int rotated, units;              // units that are rotated, and all
-    int heads_each, chunks;          // heads an item, items a token
+    int span;                        // rows, head by head, that a group of lanes walks through
     int column;                      // of its first normed element among all arrays'
     int in_place;                    // y is x (dx is dy)
 };
@@ -189,26 +210,26 @@ struct VecPlan { PartPlan part[SBGEMM_MAX_ROPE_PARTS]; int columns; };
 // V elements as they lie in memory.
 template <typename T, int V> struct alignas(V * sizeof(T)) Vec {
     uint32_t w[V * sizeof(T) / 4];
-    __device__ __forceinline__ void get(float (&f)[V]) const {
-        if constexpr (sizeof(T) == 4) {
+    __device__ __forceinline__ void get(uint64_t (&f)[V / 2]) const {
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = pair_of(w[2 * i], w[2 * i + 1]);
+            } else {
                 const float2 x = unpack2<T>(w[i]);
-                f[2 * i] = x.x;
-                f[2 * i + 1] = x.y;
+                f[i] = pair_of(x.x, x.y);
             }
         }
     }
-    __device__ __forceinline__ void set(const float (&f)[V]) {
-        if constexpr (sizeof(T) == 4) {
+    __device__ __forceinline__ void set(const uint64_t (&f)[V / 2]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(f[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[2 * i] = __float_as_uint(lower(f[i]));
+                w[2 * i + 1] = __float_as_uint(upper(f[i]));
+            } else {
+                w[i] = pack2<T>(lower(f[i]), upper(f[i]));
+            }
         }
     }
 };
@@ -234,7 +255,7 @@ __device__ __forceinline__ F row_sums(F v, int L, float2 (&shared)[2][kVecThread
 }
 
 template <typename T, int V, bool kBackward>
-__global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel(const __grid_constant__ RopeProblem p,
+__global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : kForwardBlocks) vectors_kernel(const __grid_constant__ RopeProblem p,
                                                                                  const __grid_constant__ VecPlan plan) {
     using W = Vec<T, V>;
     extern __shared__ float dsum[];
@@ -270,208 +291,267 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : 3) vectors_kernel
     // One member of a pair normed, the other not: norms before the rotation.
     const bool mixed = turned && !interleaved && norm1 != norm2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float w1[V], w2[V];                      // weights, 1 where there are none
-    {
+    constexpr int H = V / 2;                 // pairs of elements a vector
+    const uint64_t one = pair_of(1.0f, 1.0f);
+    // Weights, 1 where there are none.
+    auto weights = [&](uint64_t (&w1)[H], uint64_t (&w2)[H]) {
         const T* w = static_cast<const T*>(a.weight);
 #pragma unroll
-        for (int i = 0; i < V; ++i) w1[i] = w2[i] = 1.0f;
+        for (int i = 0; i < H; ++i) w1[i] = w2[i] = one;
         if (w && norm1 && dbg_in_bytes(w + o1, sizeof(W), a.sw, &g_status)) reinterpret_cast<const W*>(w + o1)->get(w1);
         if (w && norm2 && dbg_in_bytes(w + o2, sizeof(W), a.sw, &g_status)) reinterpret_cast<const W*>(w + o2)->get(w2);
-    }
-    float sw1[V] = {}, sw2[V] = {};          // shares of dweight
+    };
+    uint64_t w1[kBackward ? H : 1], w2[kBackward ? H : 1];
+    if constexpr (kBackward) weights(w1, w2);
+    uint64_t sw1[H] = {}, sw2[H] = {};       // shares of dweight
     auto load = [&](const T* at, const ByteSpan& s, bool there, W& v) {
         if (there && dbg_in_bytes(at, sizeof(W), s, &g_status)) v = *reinterpret_cast<const W*>(at);
         else
 #pragma unroll
             for (uint32_t& x : v.w) x = 0;
     };
-    auto store = [&](T* at, bool there, const float (&f)[V]) {
+    auto store = [&](T* at, bool there, const uint64_t (&f)[H]) {
         W v;
         v.set(f);
         if (there && dbg_in_bytes(at, sizeof(W), a.sy, &g_status)) *reinterpret_cast<W*>(at) = v;
     };
 
-    // (All of a CTA's groups go the same number of times round, as they meet at barriers.)
-    const int64_t items = p.tokens * q.chunks;
-    const int per = kVecThreads >> q.log_lanes, mine = threadIdx.x >> q.log_lanes;
-    for (int64_t i0 = (int64_t)(blockIdx.x - q.first_block) * per; i0 < items; i0 += (int64_t)q.blocks * per) {
-        const int64_t it = min(i0 + mine, items - 1), t = it / q.chunks;
-        const int h0 = (int)(it - t * q.chunks) * q.heads_each, h1 = i0 + mine < items ? min(a.heads, h0 + q.heads_each) : h0;
-        // A pair's first member is x.x a + x.y b, its second one x.z a + x.w b.
-        float4 m[kBackward ? 1 : V];
-        float2 cs[kBackward ? V : 1];
-        if (turned) {
-            const int position = p.positions[t];
-            const uint64_t* steps = p.steps + u * V;
+    // This group's rows, a token's heads one behind the other. (All of a CTA's groups
+    // go the same number of times round, as they meet at barriers.)
+    const int per = kVecThreads >> q.log_lanes;
+    const int64_t lo = ((int64_t)(blockIdx.x - q.first_block) * per + (threadIdx.x >> q.log_lanes)) * q.span;
+    const int count = (int)max((int64_t)0, min(p.tokens * a.heads - lo, (int64_t)q.span));
+    int64_t t = count > 0 ? lo / a.heads : 0;
+    int h = count > 0 ? (int)(lo - t * a.heads) : 0;
+    // Places of the next row to come in and of the next one to go out, moved on row by
+    // row: by a head, or from the last one to the next token's first.
+    const int64_t hs = kBackward ? a.hsD : a.hsX, ts = kBackward ? a.tsD : a.tsX;
+    const T* in = (kBackward ? static_cast<const T*>(a.dy) : static_cast<const T*>(a.x)) + t * ts + h * hs;
+    const T* x = static_cast<const T*>(a.x) + t * a.tsX + h * a.hsX;
+    T* out = static_cast<T*>(a.y) + t * a.tsY + h * a.hsY;
+    const int64_t in_wrap = ts - (a.heads - 1) * hs, x_wrap = a.tsX - (a.heads - 1) * a.hsX, out_wrap = a.tsY - (a.heads - 1) * a.hsY;
+    const ByteSpan& span = kBackward ? a.sd : a.sx;
+    constexpr int kAhead = kBackward ? 1 : kForwardAhead;
+    W r1[kAhead], r2[kAhead], x1, x2;
+    int hf = h, left = count;
+    auto fetch = [&](W& r1, W& r2) {
+        const bool there = left > 0, wrap = hf + 1 == a.heads;
+        load(in + o1, span, has1 && there, r1);
+        load(in + o2, span, has2 && there, r2);
+        if constexpr (kBackward) {
+            load(x + o1, a.sx, norm1 && there, x1);
+            load(x + o2, a.sx, norm2 && there, x2);
+            x += wrap ? x_wrap : a.hsX;
+        }
+        in += wrap ? in_wrap : hs;
+        hf = wrap ? 0 : hf + 1;
+        --left;
+    };
+    // A token's rotation.  Forward, with the weights in it: the elements i of the two
+    // vectors (or the two elements of a pair i) are m[i] a + n[i] b and m[H + i] a +
+    // n[H + i] b; of vectors that are not turned m and n are the weights.  Backward:
+    // cosines and sines by elements (or by pairs).
+    // (Zeros for groups without rows, which go round with the others.)
+    uint64_t m[V] = {}, n2[kBackward ? 1 : V] = {};
+    if constexpr (!kBackward) {
+        if (!turned) {
+            uint64_t v1[H], v2[H];
+            weights(v1, v2);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float2 c = turn(position, steps[i], p.magnitude);
-                if constexpr (kBackward) {
-                    cs[i] = c;
+            for (int i = 0; i < H; ++i) {
+                m[i] = v1[i];
+                n2[i] = v2[i];
+            }
+        }
+    }
+    int next = turned && count > 0 ? p.positions[t] : 0;     // (the next token's, ahead of its rows)
+    bool fresh = true;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(r1[k], r2[k]);
+    for (int i0 = 0; i0 < q.span; i0 += kAhead)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        if (kAhead > 1 && i0 + k >= q.span) break;
+        const bool live = i0 + k < count;
+        if (turned && live && fresh) {
+            const Place place(next, p.magnitude);
+            next = t + 1 < p.tokens ? p.positions[t + 1] : 0;
+            const uint64_t* steps = p.steps + u * V;
+            // (Two angles at a time: all of them would not leave their registers free.)
+            uint64_t v1[H], v2[H];
+            if constexpr (!kBackward) weights(v1, v2);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 c = turn(place, steps[interleaved ? i : 2 * i]);
+                const float2 d = turn(place, steps[interleaved ? H + i : 2 * i + 1]);
+                if (interleaved) {
+                    if constexpr (kBackward) {
+                        m[i] = pair_of(c.x, c.y);
+                        m[H + i] = pair_of(d.x, d.y);
+                    } else {
+                        m[i] = mul2(pair_of(c.x, c.y), pair_of(lower(v1[i]), lower(v1[i])));
+                        n2[i] = mul2(pair_of(-c.y, c.x), pair_of(upper(v1[i]), upper(v1[i])));
+                        m[H + i] = mul2(pair_of(d.x, d.y), pair_of(lower(v2[i]), lower(v2[i])));
+                        n2[H + i] = mul2(pair_of(-d.y, d.x), pair_of(upper(v2[i]), upper(v2[i])));
+                    }
                 } else {
-                    constexpr int H = V / 2;
-                    const float wa = mixed ? 1.0f : !interleaved ? w1[i] : i < H ? w1[2 * i] : w2[2 * (i - H)];
-                    const float wb = mixed ? 1.0f : !interleaved ? w2[i] : i < H ? w1[2 * i + 1] : w2[2 * (i - H) + 1];
-                    m[i] = make_float4(c.x * wa, -c.y * wb, c.y * wa, c.x * wb);
+                    m[i] = pair_of(c.x, d.x);
+                    m[H + i] = pair_of(c.y, d.y);
+                    if constexpr (!kBackward) {
+                        const uint64_t wa = mixed ? one : v1[i], wb = mixed ? one : v2[i];
+                        n2[i] = mul2(pair_of(-c.y, -d.y), wb);
+                        n2[H + i] = mul2(m[i], wb);
+                        m[i] = mul2(m[i], wa);
+                        m[H + i] = mul2(m[H + i], wa);
+                    }
                 }
             }
         }
-        // Places of this head's vectors, moved on head by head.
-        const int64_t hs = kBackward ? a.hsD : a.hsX;
-        const T* in = (kBackward ? static_cast<const T*>(a.dy) + t * a.tsD : static_cast<const T*>(a.x) + t * a.tsX) + h0 * hs;
-        const T *in1 = in + o1, *in2 = in + o2;
-        const T* x = static_cast<const T*>(a.x) + t * a.tsX + h0 * a.hsX;
-        const T *xn1 = x + o1, *xn2 = x + o2;
-        T* y = static_cast<T*>(a.y) + t * a.tsY + h0 * a.hsY;
-        T *out1 = y + o1, *out2 = y + o2;
-        const ByteSpan& span = kBackward ? a.sd : a.sx;
-        W r1, r2, x1, x2;
-        auto fetch = [&](bool there) {
-            load(in1, span, has1 && there, r1);
-            load(in2, span, has2 && there, r2);
-            in1 += hs;
-            in2 += hs;
-            if constexpr (kBackward) {
-                load(xn1, a.sx, norm1 && there, x1);
-                load(xn2, a.sx, norm2 && there, x2);
-                xn1 += a.hsX;
-                xn2 += a.hsX;
+        uint64_t f1[H], f2[H];
+        r1[k].get(f1);
+        r2[k].get(f2);
+        if constexpr (!kBackward) {
+            fetch(r1[k], r2[k]);             // rows ahead on their way under this one's work
+            float r = 1.0f;
+            if (a.norm) {
+                uint64_t ss = 0;
+                if (norm1)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) fma2(ss, f1[i], f1[i]);
+                if (norm2)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) fma2(ss, f2[i], f2[i]);
+                r = rsqrtf(fmaf(row_sums(lower(ss) + upper(ss), L, meet, turns), inv_norm, p.eps));
             }
-        };
-        const int count = h1 - h0;
-        fetch(count > 0);
-        for (int h = 0; h < q.heads_each; ++h) {
-            const bool live = h < count;
-            float f1[V], f2[V];
-            r1.get(f1);
-            r2.get(f2);
-            if constexpr (!kBackward) {
-                // The next head's loads under this one's work.
-                if (h + 1 < q.heads_each) fetch(h + 1 < count);
-                float r = 1.0f;
-                if (a.norm) {
-                    float ss = 0.0f;
-                    if (norm1)
+            const uint64_t rr = pair_of(r, r);
+            if (!turned) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) ss = fmaf(f1[i], f1[i], ss);
-                    if (norm2)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) ss = fmaf(f2[i], f2[i], ss);
-                    r = rsqrtf(fmaf(row_sums(ss, L, meet, turns), inv_norm, p.eps));
+                for (int i = 0; i < H; ++i) {
+                    if (norm1) f1[i] = mul2(f1[i], mul2(rr, m[i]));
+                    if (norm2) f2[i] = mul2(f2[i], mul2(rr, n2[i]));
                 }
-                if (mixed || !turned) {
-                    // (In both cases each vector is normed with its weights or not.)
+            } else if (mixed) {
+                uint64_t w1[H], w2[H];
+                weights(w1, w2);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        if (norm1) f1[i] *= r * w1[i];
-                        if (norm2) f2[i] *= r * w2[i];
+                for (int i = 0; i < H; ++i) {
+                    if (norm1) f1[i] = mul2(f1[i], mul2(rr, w1[i]));
+                    if (norm2) f2[i] = mul2(f2[i], mul2(rr, w2[i]));
+                }
+            }
+            if (turned) {
+                const uint64_t ra = norm1 && !mixed ? rr : one, rb = norm2 && !mixed ? rr : one;
+                if (interleaved) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        auto both = [](float v) { return pair_of(v, v); };
+                        f1[i] = mul2(ra, mad2(m[i], both(lower(f1[i])), mul2(n2[i], both(upper(f1[i])))));
+                        f2[i] = mul2(rb, mad2(m[H + i], both(lower(f2[i])), mul2(n2[H + i], both(upper(f2[i])))));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const uint64_t c = f1[i], d = f2[i];
+                        f1[i] = mul2(ra, mad2(m[i], c, mul2(n2[i], d)));
+                        f2[i] = mul2(rb, mad2(m[H + i], c, mul2(n2[H + i], d)));
                     }
                 }
-                if (turned) {
-                    const float ra = norm1 && !mixed ? r : 1.0f, rb = norm2 && !mixed ? r : 1.0f;
-                    if (interleaved) {
-#pragma unroll
-                        for (int i = 0; i < V / 2; ++i) {
-                            const float4 c = m[i], d = m[V / 2 + i];
-                            const float a0 = f1[2 * i], a1 = f1[2 * i + 1], b0 = f2[2 * i], b1 = f2[2 * i + 1];
-                            f1[2 * i] = ra * fmaf(a0, c.x, a1 * c.y);
-                            f1[2 * i + 1] = ra * fmaf(a0, c.z, a1 * c.w);
-                            f2[2 * i] = rb * fmaf(b0, d.x, b1 * d.y);
-                            f2[2 * i + 1] = rb * fmaf(b0, d.z, b1 * d.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float4 c = m[i];
-                            const float a0 = f1[i], b0 = f2[i];
-                            f1[i] = ra * fmaf(a0, c.x, b0 * c.y);
-                            f2[i] = rb * fmaf(a0, c.z, b0 * c.w);
-                        }
-                    }
-                }
-            } else {
-                float g1[V], g2[V];
-                x1.get(g1);
-                x2.get(g2);
-                if (h + 1 < q.heads_each) fetch(h + 1 < count);
-                if (turned) {
-                    auto back = [](float& c, float& d, const float2& z) {
-                        const float u0 = c, v0 = d;
-                        c = fmaf(u0, z.x, v0 * z.y);
-                        d = fmaf(v0, z.x, -u0 * z.y);
+            }
+        } else {
+            uint64_t g1[H], g2[H];
+            x1.get(g1);
+            x2.get(g2);
+            fetch(r1[k], r2[k]);
+            if (turned) {
+                if (interleaved) {
+                    auto back = [](uint64_t f, uint64_t z) {
+                        return pair_of(fmaf(lower(f), lower(z), upper(f) * upper(z)), fmaf(upper(f), lower(z), -lower(f) * upper(z)));
                     };
 #pragma unroll
-                    for (int i = 0; i < V / 2; ++i) {
-                        if (interleaved) {
-                            back(f1[2 * i], f1[2 * i + 1], cs[i]);
-                            back(f2[2 * i], f2[2 * i + 1], cs[V / 2 + i]);
-                        } else {
-                            back(f1[i], f2[i], cs[i]);
-                            back(f1[V / 2 + i], f2[V / 2 + i], cs[V / 2 + i]);
-                        }
+                    for (int i = 0; i < H; ++i) {
+                        f1[i] = back(f1[i], m[i]);
+                        f2[i] = back(f2[i], m[H + i]);
+                    }
+                } else {
+                    const uint64_t minus = pair_of(-1.0f, -1.0f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const uint64_t c = f1[i], d = f2[i];
+                        f1[i] = mad2(c, m[i], mul2(d, m[H + i]));
+                        f2[i] = mad2(mul2(c, m[H + i]), minus, mul2(d, m[i]));
                     }
                 }
-                if (a.norm) {
-                    // Sums of x^2 and g w x; then dweight's share and dx.
-                    float2 sums = make_float2(0.0f, 0.0f);
-                    if (norm1)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            sums.x = fmaf(g1[i], g1[i], sums.x);
-                            sums.y = fmaf(f1[i] * w1[i], g1[i], sums.y);
-                        }
-                    if (norm2)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            sums.x = fmaf(g2[i], g2[i], sums.x);
-                            sums.y = fmaf(f2[i] * w2[i], g2[i], sums.y);
-                        }
-                    sums = row_sums(sums, L, meet, turns);
-                    const float r = rsqrtf(fmaf(sums.x, inv_norm, p.eps)), mean = sums.y * r * inv_norm;
-                    if (norm1)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float z = g1[i] * r;
-                            sw1[i] = fmaf(f1[i], z, sw1[i]);
-                            f1[i] = r * fmaf(-z, mean, f1[i] * w1[i]);
-                        }
-                    if (norm2)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float z = g2[i] * r;
-                            sw2[i] = fmaf(f2[i], z, sw2[i]);
-                            f2[i] = r * fmaf(-z, mean, f2[i] * w2[i]);
-                        }
-                }
             }
-            store(out1, has1 && live, f1);
-            store(out2, has2 && live, f2);
-            out1 += a.hsY;
-            out2 += a.hsY;
+            if (a.norm) {
+                // Sums of x^2 and g w x; then dweight's share and dx.
+                uint64_t xx = 0, gx = 0;
+                if (norm1)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        fma2(xx, g1[i], g1[i]);
+                        fma2(gx, mul2(f1[i], w1[i]), g1[i]);
+                    }
+                if (norm2)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        fma2(xx, g2[i], g2[i]);
+                        fma2(gx, mul2(f2[i], w2[i]), g2[i]);
+                    }
+                const float2 sums = row_sums(make_float2(lower(xx) + upper(xx), lower(gx) + upper(gx)), L, meet, turns);
+                const float r = rsqrtf(fmaf(sums.x, inv_norm, p.eps)), mean = sums.y * r * inv_norm;
+                const uint64_t rr = pair_of(r, r), mm = pair_of(-mean, -mean);
+                if (norm1)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const uint64_t z = mul2(g1[i], rr);
+                        fma2(sw1[i], f1[i], z);
+                        f1[i] = mul2(rr, mad2(z, mm, mul2(f1[i], w1[i])));
+                    }
+                if (norm2)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const uint64_t z = mul2(g2[i], rr);
+                        fma2(sw2[i], f2[i], z);
+                        f2[i] = mul2(rr, mad2(z, mm, mul2(f2[i], w2[i])));
+                    }
+            }
         }
+        store(out + o1, has1 && live, f1);
+        store(out + o2, has2 && live, f2);
+        fresh = h + 1 == a.heads;
+        out += fresh ? out_wrap : a.hsY;
+        t += fresh;
+        h = fresh ? 0 : h + 1;
     }
     if constexpr (kBackward) {
         if (!p.workspace || !a.norm || !a.dweight) return;
         // A warp's groups in a tree, then the warps one behind the other.
+        float s1[V], s2[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            s1[i] = i & 1 ? upper(sw1[i / 2]) : lower(sw1[i / 2]);
+            s2[i] = i & 1 ? upper(sw2[i / 2]) : lower(sw2[i / 2]);
             for (int o = L; o < 32; o <<= 1) {
-                sw1[i] += __shfl_xor_sync(~0u, sw1[i], o);
-                sw2[i] += __shfl_xor_sync(~0u, sw2[i], o);
+                s1[i] += __shfl_xor_sync(~0u, s1[i], o);
+                s2[i] += __shfl_xor_sync(~0u, s2[i], o);
             }
-        const int row_warps = max(1, L >> 5);
-        for (int w = 0; w < kVecThreads / 32; w += row_warps) {
-            if (warp / row_warps * row_warps == w && (threadIdx.x & 31) < L) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (norm1) dsum[o1 + i] = (w ? dsum[o1 + i] : 0.0f) + sw1[i];
-                    if (norm2) dsum[o2 + i] = (w ? dsum[o2 + i] : 0.0f) + sw2[i];
-                }
-            }
-            __syncthreads();
         }
+        const int row_warps = max(1, L >> 5), sets = kVecThreads / 32 / row_warps;
+        float* mine = dsum + warp / row_warps * a.norm;
+        if ((threadIdx.x & 31) < L) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (norm1) mine[o1 + i] = s1[i];
+                if (norm2) mine[o2 + i] = s2[i];
+            }
+        }
+        __syncthreads();
         float* slot = p.workspace + (int64_t)blockIdx.x * plan.columns + q.column;
-        for (int e = threadIdx.x; e < a.norm; e += kVecThreads) slot[e] = dsum[e];
+        for (int e = threadIdx.x; e < a.norm; e += kVecThreads) {
+            float sum = dsum[e];
+            for (int w = 1; w < sets; ++w) sum += dsum[w * a.norm + e];
+            slot[e] = sum;
+        }
     }
 }
 
@@ -574,7 +654,8 @@ template <typename T, int V>
 cudaError_t launch_vectors(const RopeProblem& p, bool backward, const VecPlan& plan, int64_t blocks, cudaStream_t stream) {
     if (!backward) return start(vectors_kernel<T, V, false>, blocks, kVecThreads, 0, stream, p, plan);
     int most = 0;
-    for (int i = 0; i < p.n_parts; ++i) most = std::max(most, p.part[i].norm);
+    for (int i = 0; i < p.n_parts; ++i)      // (a warp's lanes hold 32 x 2 V elements at most: 16 KB in all)
+        most = std::max(most, p.part[i].norm * (kVecThreads / 32 / std::max(1, (1 << plan.part[i].log_lanes) / 32)));
     if (const cudaError_t e = start(vectors_kernel<T, V, true>, blocks, kVecThreads, most * sizeof(float), stream, p, plan))
         return e;
     return launch_sum(p, plan, stream);
@@ -597,26 +678,27 @@ bool try_vectors(const RopeProblem& p, bool backward, int sms, cudaStream_t stre
         q.in_place = backward ? a.y == a.dy : a.y == a.x;
         threads += (p.tokens * a.heads) << q.log_lanes;
     }
-    // Heads an item: as many as leave every SM its resident threads, since each item
-    // works out its angles anew.
-    const int64_t want = (int64_t)sms * (backward ? kGradBlocks : 3) * kVecThreads;
-    // (Backward at most 4: 4096 tokens of 40 heads take 39 us so, 44 with up to 16.)
-    const int64_t each = std::max<int64_t>(1, std::min<int64_t>(backward ? 4 : 16, threads / want));
+    // As many CTAs as are resident, so that a group has the angles of a token for all
+    // the heads that it has of it; the arrays' shares by their rows' lanes, one at
+    // least, which for the gradient all fit the partial sums' slots.  Forward, groups
+    // that would have more than 16 rows take some 8, a part of a token or some tokens,
+    // and the CTAs come in waves: 8192 tokens of 40 heads of 128 take 37 us so, 39 with
+    // 16 rows each and 47 in one wave of 45.
+    const int64_t slots = (int64_t)sms * (backward ? kGradBlocks : kForwardBlocks) - p.n_parts;
     int64_t blocks = 0;
     for (int i = 0; i < p.n_parts; ++i) {
         const RopePart& a = p.part[i];
         PartPlan& q = plan.part[i];
-        q.chunks = (int)((a.heads + std::min<int64_t>(each, a.heads) - 1) / std::min<int64_t>(each, a.heads));
-        q.heads_each = (a.heads + q.chunks - 1) / q.chunks;
-        const int64_t per = kVecThreads >> q.log_lanes;
-        int64_t mine = (p.tokens * q.chunks + per - 1) / per;
-        if (backward) {
-            // Its share of the partial sums' slots, by its rows' lanes, one at least: so
-            // that all of them are no more than there are, but for one each to spare.
-            const int64_t slots = (int64_t)sms * kGradBlocks - p.n_parts;
-            const int64_t share = (int64_t)((double)slots * (double)((p.tokens * a.heads) << q.log_lanes) / (double)threads);
-            mine = std::min(mine, std::max<int64_t>(1, share));
+        const int64_t per = kVecThreads >> q.log_lanes, rows = p.tokens * a.heads;
+        const int64_t share = std::max<int64_t>(1, (int64_t)((double)slots * (double)(rows << q.log_lanes) / (double)threads));
+        int64_t span = (rows + share * per - 1) / (share * per);
+        if (!backward && span > 16) {
+            const int64_t pieces = (a.heads + 9) / 10;
+            span = a.heads < 8 ? 8 / a.heads * a.heads : (a.heads + pieces - 1) / pieces;
         }
+        if (span >= ((int64_t)1 << 31)) return false;
+        q.span = (int)span;
+        const int64_t mine = (rows + span * per - 1) / (span * per);
         if (blocks + mine >= ((int64_t)1 << 31)) return false;
         q.first_block = (int)blocks;
         q.blocks = (int)mine;
