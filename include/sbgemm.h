@@ -529,8 +529,8 @@ SBGEMM_API int sbgemm_quantize_fp8(int type_x, const void* X, int64_t rsX, int64
  * for each pair i < dims / 2: a = start + i, b = a + dims / 2, or when
  * interleaved a = start + 2 i, b = a + 1.  The angle is positions[token] times
  * steps[i], counted in 2^-64 of a turn: a frequency of f radians a position has
- * the step f / (2 pi) * 2^64, and their product modulo 2^64 is exact, so far
- * positions lose nothing.  Up to SBGEMM_MAX_ROPE_PARTS arrays (queries and
+ * the step f / (2 pi) * 2^64, and of their product modulo 2^64 the top 32 bits
+ * are used, 2^-29 radians, however far the position.  Up to SBGEMM_MAX_ROPE_PARTS arrays (queries and
  * keys; query rope parts and latent rows of the cache) go in one launch.
  * All of `type` (SBGEMM_TYPE_BF16, _FP16 or _FP32), elements of a row
  * contiguous; fp32 arithmetic, rounded once.  y may be x itself (same strides). */

@@ -21,6 +21,13 @@
 // 2^-70 both x and the scale are multiplied by 2^60 first. Infinities and NaN come
 // out as NaN. (64 divisions a thread take 26 us for 7100 x 4096 fp16, their code
 // alone being more than the instruction cache holds.)
+//
+// Measured on a GB300, device time in a graph: rows 4099 x 4096 bf16 12.9 us (3.9
+// TB/s), fp32 14.0 (6.0 TB/s); tiles 7100 x 4096 fp16 16.1 us (5.4 TB/s); turned 2560
+// x 8192 bf16 19.6 us (3.2 TB/s); any 4099 x 4095 bf16 45 us. Bound: fp32 and tiles by
+// the bytes; bf16 rows by instructions (a maximum, a quotient's three operations and a
+// conversion an element); turned by its two passes over shared memory between loads
+// and stores that all of a CTA's threads wait for.
 #include <algorithm>
 #include <type_traits>
 

@@ -18,8 +18,22 @@
 // its share of the columns through distributed shared memory, added there in
 // the order of the CTAs.
 //
-// Roles: warp 8 issues the TMA loads, warp 9 the MMAs; warps 0-3 and 4-7 hold
-// the sums of the tile's two column halves, a thread one row.
+// Roles: warps 8 and 10 issue the TMA loads of an operand each, warp 9 the MMAs; warps
+// 0-3 and 4-7 hold the sums of the tile's two column halves, a thread one row.
+// C goes out through shared memory and its tensor map (fp32 sums added to C by the
+// same boxes), else in 16-byte vectors, else by the element.
+//
+// Measured on a GB300, device time in a graph, bf16 out, a scale a row of A and
+// 128 x 128 of B: 4099 x 7168 x 4096 113 us (2.13 PFLOP/s), 4096 x 4096 x 4096 67 us,
+// a scale a row of both 116; 1024 x 4096 x 4096 19.1 us; 2560 x 960 x 8192, a scale a
+// row of both, fp32 47.5 us, added to C 51.7; 4099 x 7168 x 4096 fp32 127 us, added
+// to C 138 (702 by the element); 16 x 7168 x 4096 7.4 us from L2, 9.7 from memory.
+// Bound: large products by the epilogue. A block's 256 x 256 x 128 take the
+// tensor cores 513 cycles and the eight warps that scale it 850, of which 270 wait for
+// their loads from TMEM; with a scale for each column twice the arithmetic, 1600.
+// (Without effect or slower: two commits a block for half the columns each 118 us,
+// scales' addresses moved on 147, scales staged in shared memory 140 to 146.) Few rows
+// by the weights' bytes and the start and end of a cluster's CTAs.
 #include <algorithm>
 #include <atomic>
 
@@ -120,6 +134,14 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
                  ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
+// A box of shared memory added to fp32 global memory, each element once (its sum with
+// alpha's product rounded on its own: a rounding more than a fused one; below 2^-126
+// it may be zero).
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+
 __device__ __forceinline__ void cp_async4(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -138,6 +160,20 @@ template <typename T> __device__ __forceinline__ void put_vector(T* c, const uin
         pack2<T>(alpha * lower(v[0]), alpha * upper(v[0])), pack2<T>(alpha * lower(v[1]), alpha * upper(v[1])),
         pack2<T>(alpha * lower(v[2]), alpha * upper(v[2])), pack2<T>(alpha * lower(v[3]), alpha * upper(v[3])));
 }
+// The same added to what is there.
+__device__ __forceinline__ void add_vector(float* c, const uint64_t* v, float alpha) {
+    const float4 o = *reinterpret_cast<const float4*>(c);
+    *reinterpret_cast<float4*>(c) = make_float4(fmaf(alpha, lower(v[0]), o.x), fmaf(alpha, upper(v[0]), o.y),
+                                                fmaf(alpha, lower(v[1]), o.z), fmaf(alpha, upper(v[1]), o.w));
+}
+template <typename T> __device__ __forceinline__ void add_vector(T* c, const uint64_t* v, float alpha) {
+    const uint4 o = *reinterpret_cast<const uint4*>(c);
+    auto added = [&](uint32_t w, uint64_t x) {
+        const float2 f = unpack2<T>(w);
+        return pack2<T>(fmaf(alpha, lower(x), f.x), fmaf(alpha, upper(x), f.y));
+    };
+    *reinterpret_cast<uint4*>(c) = make_uint4(added(o.x, v[0]), added(o.y, v[1]), added(o.z, v[2]), added(o.w, v[3]));
+}
 template <typename T>
 __device__ __forceinline__ void put_one(const Params& p, T* c, float v) {
     if (dbg_in_bytes(c, sizeof(T), p.sc, &g_status)) put(c, p.accumulate ? fmaf(p.alpha, v, get(c)) : p.alpha * v);
@@ -153,7 +189,10 @@ __device__ __forceinline__ void emit_as(const Params& p, int64_t b, int64_t x, i
         if (p.vec) {                 // unit stride along the columns, whole vectors
 #pragma unroll
             for (int i = 0; i < n; i += w)
-                if (y + i < p.cols && dbg_in_bytes(c + i, 16, p.sc, &g_status)) put_vector(c + i, v + i / 2, p.alpha);
+                if (y + i < p.cols && dbg_in_bytes(c + i, 16, p.sc, &g_status)) {
+                    if (p.accumulate) add_vector(c + i, v + i / 2, p.alpha);
+                    else put_vector(c + i, v + i / 2, p.alpha);
+                }
             return;
         }
     }
@@ -167,11 +206,21 @@ __device__ __forceinline__ void emit_rows_as(const Params& p, int64_t b, int x, 
     T* c = static_cast<T*>(p.C) + b * p.cb + x * p.cx + y * p.cy;
     if (p.vec_rows && x + 3 < p.rows) {
         if (!dbg_in_bytes(c, 4 * sizeof(T), p.sc, &g_status)) return;
-        if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4*>(c) = make_float4(p.alpha * v.x, p.alpha * v.y, p.alpha * v.z, p.alpha * v.w);
-        else
-            *reinterpret_cast<uint2*>(c) =
-                make_uint2(pack2<T>(p.alpha * v.x, p.alpha * v.y), pack2<T>(p.alpha * v.z, p.alpha * v.w));
+        float4 o = make_float4(p.alpha * v.x, p.alpha * v.y, p.alpha * v.z, p.alpha * v.w);
+        if (p.accumulate) {
+            float4 old;
+            if constexpr (sizeof(T) == 4) {
+                old = *reinterpret_cast<const float4*>(c);
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(c);
+                const float2 a = unpack2<T>(w.x), d = unpack2<T>(w.y);
+                old = make_float4(a.x, a.y, d.x, d.y);
+            }
+            o = make_float4(fmaf(p.alpha, v.x, old.x), fmaf(p.alpha, v.y, old.y), fmaf(p.alpha, v.z, old.z),
+                            fmaf(p.alpha, v.w, old.w));
+        }
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(c) = o;
+        else *reinterpret_cast<uint2*>(c) = make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
         return;
     }
     const float each[4] = {v.x, v.y, v.z, v.w};
@@ -209,7 +258,10 @@ __device__ __forceinline__ void send_as(const Params& p, const CUtensorMap& to, 
         fence_proxy_async_smem();
         group_sync(g);
         if (row == 0) {
-            if (y + c < p.cols && x0 < p.rows) tma_store_3d(&to, buf, (y + c) * (int)sizeof(T), x0, b);
+            if (y + c < p.cols && x0 < p.rows) {
+                if (sizeof(T) == 4 && p.accumulate) tma_add_3d(&to, buf, y + c, x0, b);
+                else tma_store_3d(&to, buf, (y + c) * (int)sizeof(T), x0, b);
+            }
             bulk_commit();
         }
     }
@@ -725,20 +777,21 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     q.alpha = p.alpha;
     q.accumulate = p.accumulate;
     const int64_t w = p.type_c == SBGEMM_TYPE_FP32 ? 4 : 8;
-    q.vec = !p.accumulate && q.cy == 1 && q.cols % w == 0 && (q.rows == 1 || q.cx % w == 0) &&
+    q.vec = q.cy == 1 && q.cols % w == 0 && (q.rows == 1 || q.cx % w == 0) &&
             (p.batch == 1 || q.cb % w == 0) && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    q.vec_rows = !p.accumulate && q.cx == 1 && (q.cols == 1 || q.cy % 4 == 0) && (p.batch == 1 || q.cb % 4 == 0) &&
+    q.vec_rows = q.cx == 1 && (q.cols == 1 || q.cy % 4 == 0) && (p.batch == 1 || q.cb % 4 == 0) &&
                  reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    // Whole vectors, and rows that a map can describe.
-    q.c_tma = q.vec && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
+    // Whole vectors, and rows that a map can describe.  (What is added to 16-bit
+    // elements is not rounded before: they are read here.)
+    q.c_tma = q.vec && (!p.accumulate || p.type_c == SBGEMM_TYPE_FP32) && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
               q.cx < ((int64_t)1 << 37) && q.cb < ((int64_t)1 << 37) && q.cols < ((int64_t)1 << 29);
     if (q.c_tma) {
         const int64_t e = 16 / w, row = q.rows > 1 ? q.cx * e : (q.cols * e + 15) / 16 * 16;
-        const uint64_t dims[3] = {(uint64_t)(q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
         const uint64_t strides[2] = {(uint64_t)row, p.batch > 1 ? (uint64_t)(q.cb * e) : (uint64_t)row};
-        const uint32_t box[3] = {128, BX, 1};
-        // (Bytes: the map copies boxes of 128 of them whatever C's type is.)
-        if (!encode_tmap_8(&to, p.C, 3, dims, strides, box)) {
+        // Bytes: the map copies boxes of 128 of them whatever C's type is.  Additions want floats.
+        const uint64_t dims[3] = {(uint64_t)(p.accumulate ? q.cols : q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
+        const uint32_t box[3] = {p.accumulate ? 32u : 128u, BX, 1};
+        if (!(p.accumulate ? encode_tmap_f32_3d(&to, p.C, dims, strides, box, true) : encode_tmap_8(&to, p.C, 3, dims, strides, box))) {
             *err = cudaErrorInvalidValue;
             return true;
         }

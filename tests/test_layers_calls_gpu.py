@@ -9,7 +9,7 @@ import math
 import pytest
 
 import strided_gemm_gb300 as sg
-from tests.test_layers_gpu import HALF, TINY, U, Rope, Shared, clean_status, fp8_operand, gen, torch  # noqa: F401
+from tests.test_layers_gpu import HALF, TINY, U, Rope, Shared, check_fp8, clean_status, fp8_operand, gen, torch  # noqa: F401
 from tests.test_serving_gpu import assert_within, status_is
 
 pytestmark = pytest.mark.gpu
@@ -218,3 +218,11 @@ def test_refusals_on_a_device(torch):
     host = torch.zeros(8, 256).bfloat16()
     with pytest.raises(TypeError):
         sg.quantize_fp8(host, y, torch.empty(8, 2, device="cuda"))
+
+
+@pytest.mark.parametrize("tc", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("lc", ["c", "t", "o"])
+@pytest.mark.parametrize("size", [(1, 700, 1000, 640), (3, 260, 264, 256), (1, 16, 2048, 2000), (1, 2600, 1032, 384), (2, 4, 6, 300)])
+def test_fp8_added_to_c(torch, tc, lc, size):
+    """Tiles of every shape added to C, whose rows are vectors, in either order, or not."""
+    check_fp8(torch, *size, lc=lc, tc=tc, alpha=1.5, accumulate=True)
