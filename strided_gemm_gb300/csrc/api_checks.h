@@ -60,10 +60,11 @@ inline bool meet(const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < 
 
 // Each span lies inside one device-accessible allocation.  An allocation seen
 // before in this call is not looked up again.
-inline int in_device_memory(std::initializer_list<Bytes> spans) {
+inline int in_device_memory(const Bytes* spans, size_t count) {
     std::array<Bytes, 8> seen;
     size_t n = 0;
-    for (const Bytes& s : spans) {
+    for (size_t k = 0; k < count; ++k) {
+        const Bytes& s = spans[k];
         bool known = false;
         for (size_t i = 0; i < n && !known; ++i) known = s.lo >= seen[i].lo && s.hi <= seen[i].hi;
         if (known) continue;
@@ -77,6 +78,8 @@ inline int in_device_memory(std::initializer_list<Bytes> spans) {
     }
     return SBGEMM_OK;
 }
+
+inline int in_device_memory(std::initializer_list<Bytes> spans) { return in_device_memory(spans.begin(), spans.size()); }
 
 // The options these operators read: a workspace, and no forced path.
 inline int read_options(const sbgemm_options* opt, void** ws, size_t* bytes) {

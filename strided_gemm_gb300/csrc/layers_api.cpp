@@ -63,6 +63,12 @@ bool same_rows(const Rows& a, const Rows& b) {
     return a.base == b.base && (a.ts == b.ts || a.tokens <= 1) && (a.hs == b.hs || a.heads <= 1);
 }
 
+template <size_t most> struct SpanList {
+    Bytes at[most];
+    size_t n = 0;
+    void add(const Bytes& s) { at[n++] = s; }
+};
+
 // What both directions check; in: x (or dy and x) of each part, out: y or dx.
 struct RopeArrays {
     Rows in[SBGEMM_MAX_ROPE_PARTS][2];
@@ -222,10 +228,13 @@ int sbgemm_norm_rope(int type, const sbgemm_rope_part* parts, int64_t n_parts, c
     if (const int st = check_rope_overlaps(a, p, extra, n_extra)) return st;
     const int sms = current_sms();
     if (!sms) return SBGEMM_ERR_CUDA;
-    for (int i = 0; i < p.n_parts; ++i)
-        if (const int m = in_device_memory({a.in[i][0].span, a.out[i].span})) return m;
-    for (size_t k = 0; k < n_extra; ++k)
-        if (const int m = in_device_memory({extra[k]})) return m;
+    SpanList<2 * SBGEMM_MAX_ROPE_PARTS + 2 + SBGEMM_MAX_ROPE_PARTS> used;
+    for (int i = 0; i < p.n_parts; ++i) {
+        used.add(a.in[i][0].span);
+        used.add(a.out[i].span);
+    }
+    for (size_t k = 0; k < n_extra; ++k) used.add(extra[k]);
+    if (const int m = in_device_memory(used.at, used.n)) return m;
     p.type = type;
     p.positions = dims > 0 ? positions : nullptr;
     p.tokens = tokens;
@@ -340,17 +349,16 @@ int sbgemm_norm_rope_backward(int type, const sbgemm_rope_grad* parts, int64_t n
     }
     for (size_t k = 0; wanted && k < n_extra; ++k)
         if (meet(w, extra[k])) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    SpanList<4 * SBGEMM_MAX_ROPE_PARTS + 3 + 2 * SBGEMM_MAX_ROPE_PARTS + 1> used;
     for (int i = 0; i < p.n_parts; ++i) {
-        if (const int m = in_device_memory({a.in[i][0].span, a.out[i].span})) return m;
-        if (a.n_in[i] > 1)
-            if (const int m = in_device_memory({a.in[i][1].span})) return m;
-        if (p.part[i].dweight)
-            if (const int m = in_device_memory({weights[i]})) return m;
+        used.add(a.in[i][0].span);
+        used.add(a.out[i].span);
+        if (a.n_in[i] > 1) used.add(a.in[i][1].span);
+        if (p.part[i].dweight) used.add(weights[i]);
     }
-    for (size_t k = 0; k < n_extra; ++k)
-        if (const int m = in_device_memory({extra[k]})) return m;
-    if (wanted)
-        if (const int m = in_device_memory({w})) return m;
+    for (size_t k = 0; k < n_extra; ++k) used.add(extra[k]);
+    if (wanted) used.add(w);
+    if (const int m = in_device_memory(used.at, used.n)) return m;
     p.type = type;
     p.positions = dims > 0 ? positions : nullptr;
     p.tokens = tokens;

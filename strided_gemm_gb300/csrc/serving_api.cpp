@@ -252,8 +252,7 @@ int sbgemm_latent_attention_shared(
     const Bytes w = block(a.workspace, (int64_t)need);
     for (const Bytes& s : {spans[0], spans[1], spans[2], spans[3], spans[4], s0, s1})
         if (meet(w, s)) return SBGEMM_ERR_OUTPUT_OVERLAP;
-    if (const int m = in_device_memory({spans[0], spans[1], spans[2], spans[3], spans[4], s0, s1})) return m;
-    if (const int m = in_device_memory({w})) return m;
+    if (const int m = in_device_memory({spans[0], spans[1], spans[2], spans[3], spans[4], s0, s1, w})) return m;
     return finish(launch_latent_shared(a, group_starts, prefix_lens, n_groups, sms, static_cast<cudaStream_t>(stream)));
 }
 
