@@ -21,13 +21,14 @@
 // Roles: warps 8 and 10 issue the TMA loads of an operand each, warp 9 the MMAs; warps
 // 0-3 and 4-7 hold the sums of the tile's two column halves, a thread one row.
 // C goes out through shared memory and its tensor map (fp32 sums added to C by the
-// same boxes), else in 16-byte vectors, else by the element.
+// same boxes), else in 16-byte vectors, else from shared memory row by row, or by the
+// element.
 //
 // Measured on a GB300, device time in a graph, bf16 out, a scale a row of A and
-// 128 x 128 of B: 4099 x 7168 x 4096 113 us (2.13 PFLOP/s), 4096 x 4096 x 4096 67 us,
-// a scale a row of both 116; 1024 x 4096 x 4096 19.1 us; 2560 x 960 x 8192, a scale a
-// row of both, fp32 47.5 us, added to C 51.7; 4099 x 7168 x 4096 fp32 127 us, added
-// to C 138 (702 by the element); 16 x 7168 x 4096 7.4 us from L2, 9.7 from memory.
+// 128 x 128 of B: 4099 x 7168 x 4096 110 us (2.18 PFLOP/s), 4096 x 4096 x 4096 64 us,
+// a scale a row of both 118; 1024 x 4096 x 4096 19.1 us; 2560 x 960 x 8192, a scale a
+// row of both, fp32 47.5 us, added to C 51.7; 4099 x 7168 x 4096 fp32 123 us, added
+// to C 132 (702 by the element), bf16 added to C 177; 16 x 7168 x 4096 7.4 us from L2, 9.7 from memory.
 // Bound: large products by the epilogue. A block's 256 x 256 x 128 take the
 // tensor cores 513 cycles and the eight warps that scale it 850, of which 270 wait for
 // their loads from TMEM; with a scale for each column twice the arithmetic, 1600.
@@ -69,6 +70,7 @@ struct Params {
     int vec;                       // columns go out as 16-byte vectors
     int vec_rows;                  // ... and a split tile's as vectors of four rows
     int c_tma;                     // C goes out through its tensor map
+    int c_rows;                    // rows that are not whole vectors: a row's columns by a warp's lanes
     int x_batch, y_batch;          // the batch coordinate moves (else shared)
     uint32_t idesc;
     Scales sx, sy;
@@ -273,6 +275,46 @@ __device__ __forceinline__ void send(const Params& p, const CUtensorMap& to, uin
         if (p.type_c == SBGEMM_TYPE_BF16) send_as<__nv_bfloat16, n>(p, to, buf, g, row, b, x0, y, v);
         else if (p.type_c == SBGEMM_TYPE_FP16) send_as<__half, n>(p, to, buf, g, row, b, x0, y, v);
         else send_as<float, n>(p, to, buf, g, row, b, x0, y, v);
+    }
+}
+
+// Where rows of C are not whole vectors: 32 columns of the sums at a time through
+// shared memory, then a row's by a warp's lanes. (4099 x 7168 x 4096, rows of 7169: 134
+// us, 377 by a thread a row.)
+template <typename T, int n>
+__device__ __forceinline__ void spread_as(const Params& p, uint8_t* buf, int g, int row, int b, int x0, int y,
+                                          const uint64_t (&v)[n / 2]) {
+    const int lane = row & 31, r0 = row & ~31;
+#pragma unroll
+    for (int c = 0; c < n; c += 32) {
+        group_sync(g);                                   // the buffer's last columns are read
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            put_vector(reinterpret_cast<float*>(buf + row * 128 + ((i * 4) ^ ((row & 7) << 4))), v + (c + i) / 2, 1.0f);
+        group_sync(g);
+        T* at = static_cast<T*>(p.C) + b * p.cb + (int64_t)(x0 + r0) * p.cx + (y + c + lane);
+        if (y + c + lane < p.cols) {
+            for (int r = 0; r < 32; r += 16, at += 16 * p.cx) {
+                auto mine = [&](int q) { return x0 + r0 + r + q < p.rows && dbg_in_bytes(at + q * p.cx, sizeof(T), p.sc, &g_status); };
+                float old[16];                           // (all on their way before the first store)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) old[q] = p.accumulate && mine(q) ? get(at + q * p.cx) : 0.0f;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const float v = *reinterpret_cast<const float*>(buf + (r0 + r + q) * 128 + ((lane * 4) ^ ((q & 7) << 4)));
+                    if (mine(q)) put(at + q * p.cx, p.accumulate ? fmaf(p.alpha, v, old[q]) : p.alpha * v);
+                }
+            }
+        }
+    }
+}
+template <int n>
+__device__ __forceinline__ void spread(const Params& p, uint8_t* buf, int g, int row, int b, int x0, int y,
+                                       const uint64_t (&v)[n / 2]) {
+    if constexpr (n >= 64) {
+        if (p.type_c == SBGEMM_TYPE_BF16) spread_as<__nv_bfloat16, n>(p, buf, g, row, b, x0, y, v);
+        else if (p.type_c == SBGEMM_TYPE_FP16) spread_as<__half, n>(p, buf, g, row, b, x0, y, v);
+        else spread_as<float, n>(p, buf, g, row, b, x0, y, v);
     }
 }
 
@@ -558,6 +600,7 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             ok = all_of_group(g, ok);
             if (ok && (kPair || p.split == 1)) {
                 if (S::kOut && p.c_tma) send<CPG>(p, to, ring + S::kStages * S::kStage + g * BX * 128, g, row, b, x0, y, acc);
+                else if (S::kOut && p.c_rows) spread<CPG>(p, ring + S::kStages * S::kStage + g * BX * 128, g, row, b, x0, y, acc);
                 else emit<CPG>(p, b, x, y, acc);
             }
         }
@@ -785,6 +828,7 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     // elements is not rounded before: they are read here.)
     q.c_tma = q.vec && (!p.accumulate || p.type_c == SBGEMM_TYPE_FP32) && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
               q.cx < ((int64_t)1 << 37) && q.cb < ((int64_t)1 << 37) && q.cols < ((int64_t)1 << 29);
+    q.c_rows = !q.vec && nt >= 128 && q.cy == 1;
     if (q.c_tma) {
         const int64_t e = 16 / w, row = q.rows > 1 ? q.cx * e : (q.cols * e + 15) / 16 * 16;
         const uint64_t strides[2] = {(uint64_t)row, p.batch > 1 ? (uint64_t)(q.cb * e) : (uint64_t)row};

@@ -226,3 +226,11 @@ def test_refusals_on_a_device(torch):
 def test_fp8_added_to_c(torch, tc, lc, size):
     """Tiles of every shape added to C, whose rows are vectors, in either order, or not."""
     check_fp8(torch, *size, lc=lc, tc=tc, alpha=1.5, accumulate=True)
+
+
+@pytest.mark.parametrize("tc", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("size", [(1, 700, 1000, 640), (2, 2600, 1033, 384), (1, 130, 4099, 128)])
+def test_fp8_rows_of_c_that_are_not_vectors(torch, tc, size):
+    check_fp8(torch, *size, lc="o", tc=tc, alpha=1.5)
+    check_fp8(torch, *size, lc="c", tc=tc, accumulate=True)
+    check_fp8(torch, *size, lc="t", tc=tc)
