@@ -318,8 +318,10 @@ __device__ __forceinline__ void spread(const Params& p, uint8_t* buf, int g, int
     }
 }
 
+// (An ordinary load: the kernel before may write scales while this one is resident
+// already, and what comes by the read-only path is not ordered behind the wait for it.)
 __device__ __forceinline__ float load_scale(const float* at, const ByteSpan& span) {
-    return dbg_in_bytes(at, 4, span, &g_status) ? __ldg(at) : 0.0f;
+    return dbg_in_bytes(at, 4, span, &g_status) ? *at : 0.0f;
 }
 
 // kYScales: Y has a scale for each of its rows (the tile's columns), else one
