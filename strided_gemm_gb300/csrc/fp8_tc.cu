@@ -20,15 +20,17 @@
 //
 // Roles: warps 8 and 10 issue the TMA loads of an operand each, warp 9 the MMAs; warps
 // 0-3 and 4-7 hold the sums of the tile's two column halves, a thread one row.
-// C goes out through shared memory and its tensor map (fp32 sums added to C by the
-// same boxes), else in 16-byte vectors, else from shared memory row by row, or by the
-// element.
+// C goes out through shared memory and its tensor map (what fp32 sums are added to is
+// brought there first, so that every output is rounded once; boxes added by the map's
+// own additions would round alpha's product before them and lose what is below 2^-126:
+// 131 us for the 146 below), else in 16-byte vectors, else from shared memory row by row,
+// or by the element.
 //
 // Measured on a GB300, device time in a graph, bf16 out, a scale a row of A and
 // 128 x 128 of B: 4099 x 7168 x 4096 110 us (2.18 PFLOP/s), 4096 x 4096 x 4096 64 us,
 // a scale a row of both 118; 1024 x 4096 x 4096 19.1 us; 2560 x 960 x 8192, a scale a
 // row of both, fp32 47.5 us, added to C 51.7; 4099 x 7168 x 4096 fp32 123 us, added
-// to C 132 (702 by the element), bf16 added to C 177; 16 x 7168 x 4096 7.4 us from L2, 9.7 from memory.
+// to C 146 (702 by the element), bf16 added to C 179; 16 x 7168 x 4096 7.4 us from L2, 9.7 from memory.
 // Bound: large products by the epilogue. A block's 256 x 256 x 128 take the
 // tensor cores 513 cycles and the eight warps that scale it 850, of which 270 wait for
 // their loads from TMEM; with a scale for each column twice the arithmetic, 1600.
@@ -136,16 +138,13 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, const void* src, 
                  ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
-// A box of shared memory added to fp32 global memory, each element once (its sum with
-// alpha's product rounded on its own: a rounding more than a fused one; below 2^-126
-// it may be zero).
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2) : "memory");
-}
-
 __device__ __forceinline__ void cp_async4(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// 16 bytes, or zeros.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ float get(const float* c) { return *c; }
@@ -246,7 +245,7 @@ __device__ __forceinline__ void emit(const Params& p, int64_t b, int64_t x, int6
 // The same of all 128 rows of a group's columns through shared memory and C's
 // tensor map, in boxes of 128 bytes a row: a thread's own vectors would touch 32
 // rows an instruction, half a sector each.
-template <typename T, int n>
+template <typename T, int n, bool kAdded>
 __device__ __forceinline__ void send_as(const Params& p, const CUtensorMap& to, uint8_t* buf, int g, int row, int b, int x0,
                                         int y, const uint64_t (&v)[n / 2]) {
     constexpr int w = 16 / sizeof(T), box = 128 / sizeof(T);
@@ -254,16 +253,28 @@ __device__ __forceinline__ void send_as(const Params& p, const CUtensorMap& to, 
     for (int c = 0; c < n; c += box) {
         if (row == 0) bulk_wait_read_all();              // the buffer's last store has read it
         group_sync(g);
+        if constexpr (kAdded) {
+            // What the sums are added to comes in first, 8 threads a row.
 #pragma unroll
-        for (int i = 0; i < box; i += w)
-            put_vector(reinterpret_cast<T*>(buf + row * 128 + ((i / w * 16) ^ ((row & 7) << 4))), v + (c + i) / 2, p.alpha);
+            for (int i = 0; i < 8; ++i) {
+                const int r = 16 * i + (row >> 3), e = (row & 7) * w;
+                const T* at = static_cast<const T*>(p.C) + b * p.cb + (int64_t)(x0 + r) * p.cx + (y + c + e);
+                const bool there = x0 + r < p.rows && y + c + e < p.cols && dbg_in_bytes(at, 16, p.sc, &g_status);
+                cp_async16(buf + r * 128 + ((e * 4) ^ ((r & 7) << 4)), there ? at : static_cast<const T*>(p.C), there);
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            group_sync(g);
+        }
+#pragma unroll
+        for (int i = 0; i < box; i += w) {
+            T* at = reinterpret_cast<T*>(buf + row * 128 + ((i / w * 16) ^ ((row & 7) << 4)));
+            if constexpr (kAdded) add_vector(at, v + (c + i) / 2, p.alpha);
+            else put_vector(at, v + (c + i) / 2, p.alpha);
+        }
         fence_proxy_async_smem();
         group_sync(g);
         if (row == 0) {
-            if (y + c < p.cols && x0 < p.rows) {
-                if (sizeof(T) == 4 && p.accumulate) tma_add_3d(&to, buf, y + c, x0, b);
-                else tma_store_3d(&to, buf, (y + c) * (int)sizeof(T), x0, b);
-            }
+            if (y + c < p.cols && x0 < p.rows) tma_store_3d(&to, buf, (y + c) * (int)sizeof(T), x0, b);
             bulk_commit();
         }
     }
@@ -272,9 +283,10 @@ template <int n>
 __device__ __forceinline__ void send(const Params& p, const CUtensorMap& to, uint8_t* buf, int g, int row, int b, int x0,
                                      int y, const uint64_t (&v)[n / 2]) {
     if constexpr (n >= 64) {
-        if (p.type_c == SBGEMM_TYPE_BF16) send_as<__nv_bfloat16, n>(p, to, buf, g, row, b, x0, y, v);
-        else if (p.type_c == SBGEMM_TYPE_FP16) send_as<__half, n>(p, to, buf, g, row, b, x0, y, v);
-        else send_as<float, n>(p, to, buf, g, row, b, x0, y, v);
+        if (p.type_c == SBGEMM_TYPE_BF16) send_as<__nv_bfloat16, n, false>(p, to, buf, g, row, b, x0, y, v);
+        else if (p.type_c == SBGEMM_TYPE_FP16) send_as<__half, n, false>(p, to, buf, g, row, b, x0, y, v);
+        else if (p.accumulate) send_as<float, n, true>(p, to, buf, g, row, b, x0, y, v);
+        else send_as<float, n, false>(p, to, buf, g, row, b, x0, y, v);
     }
 }
 
@@ -534,6 +546,12 @@ fp8_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CU
             if constexpr (kYScales) {
                 group_sync(g);                   // the last tile's scales are read
                 fetch(0);
+            }
+            if (S::kOut && p.c_tma && p.accumulate && x < p.rows) {
+                // What the sums are added to, on its way into L2 under the products.  (Without:
+                // 157 us, for 149 at the time.)
+                const float* at = static_cast<const float*>(p.C) + b * p.cb + x * p.cx + y;
+                for (int i = 0; i < CPG && y + i < p.cols; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i) : "memory");
             }
 #pragma unroll
             for (int i = 0; i < CPG / 2; ++i) acc[i] = 0;
@@ -826,18 +844,18 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
             (p.batch == 1 || q.cb % w == 0) && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
     q.vec_rows = q.cx == 1 && (q.cols == 1 || q.cy % 4 == 0) && (p.batch == 1 || q.cb % 4 == 0) &&
                  reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    // Whole vectors, and rows that a map can describe.  (What is added to 16-bit
-    // elements is not rounded before: they are read here.)
+    // Whole vectors, and rows that a map can describe.  (What is added to 16-bit elements
+    // goes by a thread's own vectors.)
     q.c_tma = q.vec && (!p.accumulate || p.type_c == SBGEMM_TYPE_FP32) && nt >= 128 && q.split == 1 && (q.rows == 1 || q.cx > 0) && (p.batch == 1 || q.cb > 0) &&
               q.cx < ((int64_t)1 << 37) && q.cb < ((int64_t)1 << 37) && q.cols < ((int64_t)1 << 29);
     q.c_rows = !q.vec && nt >= 128 && q.cy == 1;
     if (q.c_tma) {
         const int64_t e = 16 / w, row = q.rows > 1 ? q.cx * e : (q.cols * e + 15) / 16 * 16;
         const uint64_t strides[2] = {(uint64_t)row, p.batch > 1 ? (uint64_t)(q.cb * e) : (uint64_t)row};
-        // Bytes: the map copies boxes of 128 of them whatever C's type is.  Additions want floats.
-        const uint64_t dims[3] = {(uint64_t)(p.accumulate ? q.cols : q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
-        const uint32_t box[3] = {p.accumulate ? 32u : 128u, BX, 1};
-        if (!(p.accumulate ? encode_tmap_f32_3d(&to, p.C, dims, strides, box, true) : encode_tmap_8(&to, p.C, 3, dims, strides, box))) {
+        // Bytes: the map copies boxes of 128 of them whatever C's type is.
+        const uint64_t dims[3] = {(uint64_t)(q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
+        const uint32_t box[3] = {128, BX, 1};
+        if (!encode_tmap_8(&to, p.C, 3, dims, strides, box)) {
             *err = cudaErrorInvalidValue;
             return true;
         }
