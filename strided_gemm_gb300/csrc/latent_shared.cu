@@ -313,11 +313,9 @@ struct Layout {
     int64_t own, most;                   // items of a sequence's own keys; items at most
     size_t each, items, parts, bytes;    // bytes an array; offsets
 };
-Layout layout_of(int sms, int64_t n_seqs, int64_t n_groups, int64_t rows, int64_t R) {
+Layout layout_with(int nb, int sms, int64_t n_seqs, int64_t n_groups, int64_t rows, int64_t R) {
     Layout l{};
-    // Rows that a group has, were they all alike.
-    const int64_t of = n_groups > 0 ? (n_seqs + n_groups - 1) / n_groups * rows : rows;
-    l.nb = latent_rows_block(std::max(of, rows));
+    l.nb = nb;
     l.own = (rows + l.nb - 1) / l.nb;
     l.most = n_seqs * l.own + n_seqs * rows / l.nb + n_groups;
     l.each = round256((size_t)n_seqs * 4);
@@ -326,11 +324,25 @@ Layout layout_of(int sms, int64_t n_seqs, int64_t n_groups, int64_t rows, int64_
     l.bytes = l.parts + (R > 0 ? (size_t)(l.most + sms) * latent_part_bytes(l.nb, R) : 0);
     return l;
 }
+Layout layout_of(int sms, int64_t n_seqs, int64_t n_groups, int64_t rows, int64_t R) {
+    // Rows that a group has, were they all alike.
+    const int64_t of = n_groups > 0 ? (n_seqs + n_groups - 1) / n_groups * rows : rows;
+    return layout_with(latent_rows_block(std::max(of, rows)), sms, n_seqs, n_groups, rows, R);
+}
 
 }  // namespace
 
+// What any call of up to these sizes needs: a block's query rows follow from the sizes
+// (fewer groups have more rows each, and larger slots), and for one number of them
+// nothing shrinks as the sizes grow.
 size_t latent_shared_workspace_bytes(int sms, int64_t n_seqs, int64_t n_groups, int64_t q_len, int64_t heads, int64_t R) {
-    return layout_of(sms, n_seqs, n_groups, q_len * heads, R).bytes;
+    const int64_t rows = q_len * heads;
+    size_t most = 0;
+    for (const int nb : {16, 32, 64}) {
+        if (nb > latent_rows_block(n_seqs * rows)) break;
+        most = std::max(most, layout_with(nb, sms, n_seqs, n_groups, rows, R).bytes);
+    }
+    return most;
 }
 
 cudaError_t launch_latent_shared(const LatentPaged& a, const int32_t* group_starts, const int32_t* prefix_lens,
