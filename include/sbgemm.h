@@ -533,7 +533,11 @@ SBGEMM_API int sbgemm_quantize_fp8(int type_x, const void* X, int64_t rsX, int64
  * are used, 2^-29 radians, however far the position.  Up to SBGEMM_MAX_ROPE_PARTS arrays (queries and
  * keys; query rope parts and latent rows of the cache) go in one launch.
  * All of `type` (SBGEMM_TYPE_BF16, _FP16 or _FP32), elements of a row
- * contiguous; fp32 arithmetic, rounded once.  y may be x itself (same strides). */
+ * contiguous; fp32 arithmetic, rounded once.  y may be x itself (same strides).
+ * Arrays may lie in one another's gaps, one behind the other in each token or in
+ * each head's place (one projection's queries and keys, in place); with different
+ * token strides, or inside a token different head strides, they count as
+ * SBGEMM_ERR_OUTPUT_OVERLAP where their spans meet. */
 enum { SBGEMM_MAX_ROPE_PARTS = 4 };
 typedef struct {
     const void* x;               /* row of token t, head h at x + t*x_token + h*x_head */

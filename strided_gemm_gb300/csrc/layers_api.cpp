@@ -45,18 +45,39 @@ bool rows_span(Rows* r) {
     return span_of(r->base, r->esize, {{r->ts, r->tokens}, {r->hs, r->heads}, {1, r->D}}, &r->span);
 }
 
-// Whether two arrays share an element, or may: packed arrays (one projection's
-// queries and keys side by side) have spans that meet, but one token stride and
-// parts of a token that do not.
+// v modulo a positive pitch.
+i128 modulo(i128 v, i128 pitch) {
+    const i128 r = v % pitch;
+    return r < 0 ? r + pitch : r;
+}
+
+// Whether two arrays share an element, or may: packed arrays have spans that meet,
+// but parts of a token that do not (one projection's queries and keys side by side)
+// or, token by token, parts of a head's place that do not (queries, keys and values
+// head by head).
 bool rows_meet(const Rows& a, const Rows& b) {
     if (!meet(a.span, b.span)) return false;
-    const i128 pitch = (i128)a.ts * a.esize;
-    if (a.ts != b.ts || a.esize != b.esize || pitch <= 0 || a.tokens <= 1 || a.hs < 0 || b.hs < 0) return true;
-    const i128 wa = ((i128)a.hs * (a.heads - 1) + a.D) * a.esize, wb = ((i128)b.hs * (b.heads - 1) + b.D) * b.esize;
-    // b's part of a token behind a's start, modulo the pitch.
-    i128 off = ((i128)reinterpret_cast<uintptr_t>(b.base) - (i128)reinterpret_cast<uintptr_t>(a.base)) % pitch;
-    if (off < 0) off += pitch;
-    return !(off >= wa && off + wb <= pitch);
+    if (a.esize != b.esize || a.hs < 0 || b.hs < 0) return true;
+    i128 off = (i128)reinterpret_cast<uintptr_t>(b.base) - (i128)reinterpret_cast<uintptr_t>(a.base);
+    if (a.tokens > 1) {
+        const i128 pitch = (i128)a.ts * a.esize;
+        if (a.ts != b.ts || pitch <= 0) return true;
+        const i128 wa = ((i128)a.hs * (a.heads - 1) + a.D) * a.esize, wb = ((i128)b.hs * (b.heads - 1) + b.D) * b.esize;
+        off = modulo(off, pitch);
+        if (off >= wa && off + wb <= pitch) return false;
+        // A part of a token of each in every pitch from a's start on, or from b's: then
+        // no others can meet.
+        if (wa > pitch || off + wb > pitch) {
+            if (wb > pitch || pitch - off + wa > pitch) return true;
+            off -= pitch;
+        }
+    }
+    // Heads in step (a single one is in step with any).
+    if (a.heads > 1 && b.heads > 1 && a.hs != b.hs) return true;
+    const i128 step = (i128)(a.heads > 1 ? a.hs : b.hs) * a.esize;
+    if (step <= 0) return true;
+    off = modulo(off, step);
+    return !(off >= a.D * a.esize && off + b.D * b.esize <= step);
 }
 
 bool same_rows(const Rows& a, const Rows& b) {
