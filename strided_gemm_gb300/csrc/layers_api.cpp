@@ -338,15 +338,21 @@ int sbgemm_norm_rope_backward(int type, const sbgemm_rope_grad* parts, int64_t n
     }
     if (p.n_parts == 0 && n_zeros == 0) return SBGEMM_OK;
     if (const int st = check_rope_overlaps(a, p, extra, n_extra)) return st;
+    // (A part has no rows because the others have none either, or has no heads: its
+    // gradient, which is zeroed first, meets nothing of theirs.)
+    for (int i = 0; i < n_zeros; ++i) {
+        for (int j = 0; j < p.n_parts; ++j) {
+            if (meet(zeros[i], a.out[j].span) || meet(zeros[i], weights[j])) return SBGEMM_ERR_OUTPUT_OVERLAP;
+            for (int k = 0; k < a.n_in[j]; ++k)
+                if (meet(zeros[i], a.in[j][k].span)) return SBGEMM_ERR_OUTPUT_OVERLAP;
+        }
+        for (size_t k = 0; p.n_parts > 0 && k < n_extra; ++k)
+            if (meet(zeros[i], extra[k])) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    }
     const int sms = current_sms();
     if (!sms) return SBGEMM_ERR_CUDA;
-    // (A part has no rows because the others have none either, or has no heads:
-    // its gradient's place is checked against the others' outputs.)
-    for (int i = 0; i < n_zeros; ++i) {
-        for (int j = 0; j < p.n_parts; ++j)
-            if (meet(zeros[i], a.out[j].span) || meet(zeros[i], weights[j])) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    for (int i = 0; i < n_zeros; ++i)
         if (const int m = in_device_memory({zeros[i]})) return m;
-    }
     Bytes w{};
     if (wanted) {
         const size_t need = norm_rope_workspace_bytes(sms, total);
@@ -370,6 +376,8 @@ int sbgemm_norm_rope_backward(int type, const sbgemm_rope_grad* parts, int64_t n
     }
     for (size_t k = 0; wanted && k < n_extra; ++k)
         if (meet(w, extra[k])) return SBGEMM_ERR_OUTPUT_OVERLAP;
+    for (int i = 0; wanted && i < n_zeros; ++i)
+        if (meet(w, zeros[i])) return SBGEMM_ERR_OUTPUT_OVERLAP;
     SpanList<4 * SBGEMM_MAX_ROPE_PARTS + 3 + 2 * SBGEMM_MAX_ROPE_PARTS + 1> used;
     for (int i = 0; i < p.n_parts; ++i) {
         used.add(a.in[i][0].span);

@@ -67,3 +67,14 @@ def test_the_check_against_every_address():
             apart += 1
             passed += st != OVERLAP
     assert apart > 1000 and passed > 0.6 * apart, (passed, apart)
+
+
+@pytest.mark.parametrize("want,at", [
+    (OVERLAP, dict(dweight=A)), (OVERLAP, dict(dweight=A + 2 * 1024 * 7)), (OVERLAP, dict(dweight=B + 64)),
+    (OVERLAP, dict(dweight=C)), (OVERLAP, dict(dweight=D)), (OVERLAP, dict(dweight=E + 28)), (OVERLAP, dict(dweight=F)),
+    (None, dict(dweight=F + 4096)),
+])
+def test_the_gradient_of_a_part_without_heads_meets_nothing_of_the_others(want, at):
+    """It is zeroed first: x, dy, dx, the weight, positions and steps of the others."""
+    st = rope_back(part=dict(weight=D), second=dict(heads=0, weight=0, **at))
+    assert st == want if want is not None else st in PAST
