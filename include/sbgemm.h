@@ -496,9 +496,12 @@ typedef struct {
 } sbgemm_fp8_matrix;
 
 /* C[b] <- alpha * A[b] * B[b] (+ C[b]) on such matrices:
- *     C[b][m][n] = alpha * sum_j SA[m][j] SB[n][j] sum_{k in block j} A[m][k] B[n][k] (+ C_old)
+ *     C[b][m][n] = alpha * sum_j (SA[m][j] SB[n][j]) sum_{k in block j} A[m][k] B[n][k] (+ C_old)
  * type_c: SBGEMM_TYPE_BF16, _FP16 or _FP32.  Products are exact; a block's sum
- * and the sum over blocks are fp32, the output is rounded once.  A and B may be
+ * and the sum over blocks are fp32, the output is rounded once.  The two scales of
+ * a block are multiplied first, in fp32: where their product is subnormal (below
+ * 2^-126) it has fewer bits, and where it is infinite (from 2^128 on) the outputs
+ * are infinite or NaN, whatever alpha is.  A and B may be
  * of different 8-bit types.  Operands with unit stride along k and 16-byte
  * aligned bases, rows and batches run on the tensor cores, every other layout
  * on a slower CUDA-core kernel.  Few output tiles with a long K are split along
