@@ -825,10 +825,7 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
     const Fp8Operand& ox = swapped ? p.b : p.a;
     const Fp8Operand& oy = swapped ? p.a : p.b;
     CUtensorMap tx, ty, to{};
-    if (!make_map(&tx, ox, p.K, p.batch, BX) || !make_map(&ty, oy, p.K, p.batch, (uint32_t)(pair ? nt / 2 : nt))) {
-        *err = cudaErrorInvalidValue;
-        return true;
-    }
+    if (!make_map(&tx, ox, p.K, p.batch, BX) || !make_map(&ty, oy, p.K, p.batch, (uint32_t)(pair ? nt / 2 : nt))) return false;
     q.C = p.C;
     q.cx = swapped ? p.csC : p.rsC;
     q.cy = swapped ? p.rsC : p.csC;
@@ -855,10 +852,7 @@ bool launch_fp8_tc(const Fp8Problem& p, int sms, cudaStream_t stream, cudaError_
         // Bytes: the map copies boxes of 128 of them whatever C's type is.
         const uint64_t dims[3] = {(uint64_t)(q.cols * e), (uint64_t)q.rows, (uint64_t)p.batch};
         const uint32_t box[3] = {128, BX, 1};
-        if (!encode_tmap_8(&to, p.C, 3, dims, strides, box)) {
-            *err = cudaErrorInvalidValue;
-            return true;
-        }
+        q.c_tma = encode_tmap_8(&to, p.C, 3, dims, strides, box);        // (else by vectors)
     }
     q.x_batch = p.batch > 1 && ox.bs != 0;
     q.y_batch = p.batch > 1 && oy.bs != 0;

@@ -1310,8 +1310,8 @@ size_t latent_decode_workspace_bytes(int sms) { return 2 * (size_t)sms * part_by
 namespace {
 
 // What the kernels' parameters have of a call, and the tensor map of its rows, for
-// `nb` query rows a block; false on a CUDA error.
-bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map, CUtensorMap* edge = nullptr) {
+// `nb` query rows a block.  (Rows that the driver makes no map of come by cp.async.)
+void fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map, CUtensorMap* edge = nullptr) {
     Params& p = *out;
     const int64_t rows = a.q_len * a.heads;
     p.Q = a.Q; p.hsQ = a.hsQ; p.tsQ = a.tsQ; p.bsQ = a.bsQ;
@@ -1343,12 +1343,10 @@ bool fill(const LatentPaged& a, int nb, Params* out, CUtensorMap* map, CUtensorM
         const uint64_t dims[3] = {(uint64_t)(a.R + a.P), (uint64_t)a.block_size, (uint64_t)a.num_blocks};
         const uint64_t strides[2] = {(uint64_t)row_stride * 2, (uint64_t)page_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)run, 1};
-        if (!encode_tmap_16(map, a.cache, 3, dims, strides, box)) return false;
         const uint32_t eight[3] = {64, 8, 1};
-        if (edge && !encode_tmap_16(edge, a.cache, 3, dims, strides, eight)) return false;
-        p.run = run;
+        if (encode_tmap_16(map, a.cache, 3, dims, strides, box) && (!edge || encode_tmap_16(edge, a.cache, 3, dims, strides, eight)))
+            p.run = run;
     }
-    return true;
 }
 
 // Sizes and alignments of the tensor-core kernels.
@@ -1408,10 +1406,7 @@ bool launch_latent_decode(const LatentPaged& a, int sms, cudaStream_t stream, cu
     if (groups > 65535 || (__int128)a.n_seqs * (a.N / 32 + 1) >= INT32_MAX) return false;
     Params p{};
     CUtensorMap map{};
-    if (!fill(a, nb, &p, &map)) {
-        *err = cudaErrorInvalidValue;
-        return true;
-    }
+    fill(a, nb, &p, &map);
     p.groups = (int)groups;
     // CTAs for each group of rows: an SM each, as far as the workspace has two
     // slots for every one of them; without it whole sequences.
@@ -1436,7 +1431,7 @@ cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems&
                                         cudaStream_t stream) {
     Params p{};
     CUtensorMap maps[3] = {};                // the cache's rows, in boxes of 8 too, and the queries
-    if (!fill(a, nb, &p, &maps[0], &maps[1])) return cudaErrorInvalidValue;
+    fill(a, nb, &p, &maps[0], &maps[1]);
     const int64_t lim = (int64_t)1 << 39, wide = (a.R + a.P + 7) / 8 * 8;
     const int64_t hs = a.heads > 1 ? a.hsQ : wide, ts = a.q_len > 1 ? a.tsQ : hs, bs = a.n_seqs > 1 ? a.bsQ : ts;
     if (a.heads % 8 == 0 && hs > 0 && ts > 0 && bs > 0 && hs < lim && ts < lim && bs < lim) {
@@ -1445,7 +1440,7 @@ cudaError_t launch_latent_decode_shared(const LatentPaged& a, const LatentItems&
         p.q_tma = 8;
         while (p.q_tma < nb && a.heads % (2 * p.q_tma) == 0) p.q_tma *= 2;
         const uint32_t box[4] = {64, (uint32_t)p.q_tma, 1, 1};
-        if (!encode_tmap_16(&maps[2], a.Q, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!encode_tmap_16(&maps[2], a.Q, 4, dims, strides, box)) p.q_tma = 0;
     }
     p.groups = 1;
     p.split = 1;
