@@ -94,6 +94,18 @@ __device__ __forceinline__ float block_sum(float v, float* shared) {
     return r;
 }
 
+// A sum and what its rounding lost (Knuth's two-sum): 48 bits without the slow
+// 64-bit units, whose latency 300 partial sums in order would pay.
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ float all() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
+};
+
 // Items of a row: first its pairs, then the elements that are not rotated.
 struct Items {
     int pairs, dims, start, interleaved, count;
@@ -113,9 +125,12 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     const int tid = threadIdx.x;
     int64_t rows = 0;
     for (int n = 0; n < p.n_parts; ++n) rows += p.tokens * p.part[n].heads;
+    // This CTA's sums of dweight, and behind all CTAs' what their roundings lost: it
+    // adds up rows / CTAs of them one behind the other.
     float* slot = kBackward && p.workspace ? p.workspace + blockIdx.x * norm_total : nullptr;
+    float* lost = slot + gridDim.x * norm_total;
     if (slot)
-        for (int64_t e = tid; e < norm_total; e += kRowThreads) slot[e] = 0.0f;
+        for (int64_t e = tid; e < norm_total; e += kRowThreads) slot[e] = lost[e] = 0.0f;
     __syncthreads();
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         int64_t r = row, before = 0;
@@ -169,7 +184,12 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
             } else {
                 if (e >= a.norm) return g;
                 const float v = load(x + e, a.sx) * r_norm;
-                if (slot && a.dweight) slot[before + e] += g * v;
+                if (slot && a.dweight) {
+                    Sum sum{slot[before + e], lost[before + e]};
+                    sum.add(g * v);
+                    slot[before + e] = sum.hi;
+                    lost[before + e] = sum.lo;
+                }
                 return r_norm * (g * weight(e) - v * mean);
             }
         };
@@ -188,6 +208,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         }
         __syncthreads();
     }
+    if (slot)
+        for (int64_t e = tid; e < norm_total; e += kRowThreads) slot[e] = Sum{slot[e], lost[e]}.all();
 }
 
 // ---- rows in vectors -----------------------------------------------------------------
@@ -555,17 +577,6 @@ __global__ void __launch_bounds__(kVecThreads, kBackward ? 2 : kForwardBlocks) v
     }
 }
 
-// A sum and what its rounding lost (Knuth's two-sum): 48 bits without the slow
-// 64-bit units, whose latency 300 partial sums in order would pay.
-struct Sum {
-    float hi = 0.0f, lo = 0.0f;
-    __device__ __forceinline__ void add(float v) {
-        const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
-        hi = s;
-    }
-};
-
 // dweight: the blocks' partial sums in order.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ RopeProblem p,
@@ -601,7 +612,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
     float* out = p.part[n].dweight + (e - plan.part[n].column);
     if (!dbg_in_bytes(out, 4, p.part[n].sdw, &g_status)) return;
     if (p.accumulate) s.add(*out);
-    *out = fabsf(s.hi) < INFINITY ? s.hi + s.lo : s.hi;
+    *out = s.all();
 }
 
 template <typename... Args, typename... Given>
@@ -744,7 +755,8 @@ cudaError_t launch_norm_rope_backward(const RopeProblem& p, int sms, cudaStream_
     return launch_any(p, true, sms, stream);
 }
 size_t norm_rope_workspace_bytes(int sms, int64_t norm_total) {
-    return ((size_t)sms * kGradBlocks * (size_t)norm_total * 4 + 255) / 256 * 256;
+    // (Twice: the kernel of any alignment keeps what its sums' roundings lost.)
+    return ((size_t)sms * kGradBlocks * (size_t)norm_total * 8 + 255) / 256 * 256;
 }
 
 unsigned int* status_word_norm_rope() { return word_address(&g_status); }

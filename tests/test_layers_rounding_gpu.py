@@ -52,3 +52,35 @@ def test_sums_added_to_c_are_rounded_once(torch, size, pad, gb):
     A.zero_()
     assert torch.equal(added_to(tiny, 1.0), tiny)
     status_is(0)
+
+
+def gradient_of_ones(torch, t, tokens, heads, D):
+    """(relative error of dweight, depth): x = 1 and dy = c for every element, so that
+    dweight is rows c / sqrt(1 + eps)."""
+    dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[t]
+    x = torch.ones(1, 1, D, device="cuda", dtype=dt).expand(tokens, heads, D)
+    dy = torch.full((1, 1, D), 1.1, device="cuda", dtype=dt).expand(tokens, heads, D)
+    dx, dw = torch.empty(tokens, heads, D, device="cuda", dtype=dt), torch.empty(D, device="cuda")
+    ws = torch.empty(sg.sbgemm_norm_rope_workspace_bytes([D]), device="cuda", dtype=torch.uint8)
+    sg.norm_rope_backward([sg.RopeGrad(x, dy, dx, norm=D, dweight=dw)], None, None, workspace=ws)
+    status_is(0)
+    ref = tokens * heads * float(dy[0, 0, 0]) * (1 + 1e-6) ** -0.5
+    return float((dw.double() - ref).abs().max()) / ref
+
+
+@pytest.mark.parametrize("t,D", [("bf16", 33), ("fp32", 7), ("fp32", 300)])
+def test_long_sums_of_one_sign_at_any_alignment(torch, t, D):
+    """2^20 rows, some 3400 a CTA one behind the other: every addend is off by
+    (D / 2 + 8) 2^-24 of itself as every normed element is, the CTAs' sums and the
+    whole by a rounding each, and nothing grows with the rows."""
+    assert gradient_of_ones(torch, t, 1 << 16, 16, D) <= (D / 2 + 10) * 2.0 ** -24
+
+
+def test_long_sums_of_one_sign_in_vectors(torch):
+    """Rows of 64 bf16 elements are 4 lanes' work, so that 64 groups of lanes a CTA and
+    two CTAs an SM (less one) share them: that many additions, then 3 over a warp's
+    groups and 8 over the warps."""
+    tokens, heads, D = 1 << 16, 16, 64
+    groups = (2 * torch.cuda.get_device_properties(0).multi_processor_count - 1) * 64
+    depth = -(-tokens * heads // groups) + 3 + 8
+    assert gradient_of_ones(torch, "bf16", tokens, heads, D) <= (D / 2 + 10 + depth) * 2.0 ** -24
