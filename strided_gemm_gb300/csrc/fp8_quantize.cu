@@ -22,12 +22,13 @@
 // out as NaN. (64 divisions a thread take 26 us for 7100 x 4096 fp16, their code
 // alone being more than the instruction cache holds.)
 //
-// Measured on a GB300, device time in a graph: rows 4099 x 4096 bf16 12.9 us (3.9
-// TB/s), fp32 14.0 (6.0 TB/s); tiles 7100 x 4096 fp16 16.1 us (5.4 TB/s); turned 2560
-// x 8192 bf16 19.6 us (3.2 TB/s); any 4099 x 4095 bf16 45 us. Bound: fp32 and tiles by
-// the bytes; bf16 rows by instructions (a maximum, a quotient's three operations and a
-// conversion an element); turned by its two passes over shared memory between loads
-// and stores that all of a CTA's threads wait for.
+// Measured on a GB300, device time in a graph whose replays find these arrays in L2,
+// and behind a flushed L2: rows 4099 x 4096 bf16 12.9 and 16.3 us (3.1 TB/s from memory),
+// fp32 14.0 and 18.8 (4.5 TB/s); tiles 7100 x 4096 fp16 16.3 and 22 (4.0 TB/s); turned
+// 2560 x 8192 bf16 19.7 and 25 (2.5 TB/s); any 4099 x 4095 bf16 45 and 46. Bound: by what
+// is in flight. Of bf16 rows from memory the counters show 53 % of the SMs' peak, 25 % of
+// DRAM's and 42 % of the warps, which wait for their own loads and for fixed latencies; a
+// thread of the turned kernel loads nothing while its CTA converts and stores.
 #include <algorithm>
 #include <type_traits>
 

@@ -58,7 +58,7 @@
 // sequences of 2048 to 8192 keys with 128 heads 171 us (399 MB: 2.3 TB/s, 539
 // TFLOP/s); 32 sequences of up to 8191 keys with 16 heads 54 us (193 MB: 3.6
 // TB/s, in the loop 5.5 to 5.9); one of 701 keys with 16 heads 14.5 us.
-// Shared prefixes: 64 sequences of 1000 keys behind 16001, 16 heads, 76 us, bound by the
+// Shared prefixes: 64 sequences of 250 to 1000 keys behind 16001, 16 heads, 76 us, bound by the
 // chain of 64 rows above and by the pieces' way to the join.
 // Bound: few heads by the cache's bytes and a start of 7 us; 128 heads by the
 // chain above and, at a sequence's end, the way of 64 x 512 sums to the workspace

@@ -14,10 +14,11 @@
 // launched before the kernel that uses it and waited for there.
 //
 // Measured on a GB300, R = 512, P = 64, plan and join included, device time in a
-// graph: 64 sequences with 1000 keys each of their own behind 16001, 16 heads, bf16 76
-// us (each for itself 180); 4 documents of 8192 keys with 16 questions of 700, 128
-// heads, fp16, pages of 64 228 us, of 16 270; 4 samples of 200 behind 1500 20 us; 64
-// sequences of 1000 and no prefix 32 us; 300 groups of 5 with 60 behind 500 270 us. The
+// graph: 64 sequences with 250 to 1000 keys of their own behind 16001, 16 heads, bf16 76
+// us (each for itself 180; with 1000 each 84); 4 documents of 8192 keys with 16 questions
+// of 175 to 700, 128 heads, fp16, pages of 64 235 us, of 16 277; 4 samples of 50 to 200
+// behind 1500 20 us; 64 sequences of 250 to 1000 and no prefix 31 us, of 1000 35; 300
+// groups of 5 with 60 behind 500 270 us. The
 // plan of up to 1024 sequences takes 5.5 us on its own, caches cold.
 #include <algorithm>
 

@@ -18,13 +18,14 @@
 // their share of dweight in registers; a CTA adds its warps' in a fixed order and
 // leaves one partial sum.
 //
-// Measured on a GB300, device time in a graph: 8192 tokens of 40 heads of 128, bf16,
-// normed and rotated, 37 us, 4.5 TB/s (20000 tokens without norms 72 us, 5.6 TB/s);
-// the gradient of 4096 of them 31.7 us, 4.0 TB/s, where one element an instruction,
-// angles from 64-bit arithmetic and a walk of four heads took 39.  Bound by
-// instructions as much as by the bytes of x and y: unpacking, sums over lanes and
-// addresses take as many as the arithmetic.  (Angles made once a warp in shared
-// memory, for rows taken in the order of memory: 45 and 44 us, by its bookkeeping.)
+// Measured on a GB300, device time in a graph and behind a flushed L2: 8192 tokens of 40
+// heads of 128, bf16, normed and rotated, 37 and 39 us, 4.5 and 4.3 TB/s (20000 tokens
+// without norms 74 us, 5.5 TB/s); the gradient of 4096 of them 31.8 and 34.8 us, 4.0 and 3.6
+// TB/s, where one element an instruction, angles from 64-bit arithmetic and a walk of
+// four heads took 39.  Bound by what is in flight: the counters show 49 % of the SMs' peak
+// and 40 % of DRAM's, the gradient's 52 and 52, with 23 % of the warps, since two CTAs of
+// 118 and 128 registers a thread fill an SM.  (Angles made once a warp in shared memory,
+// for rows taken in the order of memory: 45 and 44 us, by its bookkeeping.)
 //
 // rows_kernel: a CTA a row, any sizes and alignments.  A first pass over the
 // row makes its sums, a second one the outputs; a thread has a pair, or an
